@@ -106,6 +106,44 @@ typedef struct {
 
 typedef void* moe_stream_t; /* cudaStream_t */
 
+/* What follows a block (the MoE FFN, an attention block, a dense MLP), per
+ * token row.  With f the block's output,
+ *   g     = f / sqrt(mean(f^2) + post_eps) * post_w   (g = f when post_w is NULL)
+ *   h     = residual + scale * gate * g               (a NULL part drops out)
+ *   out   = h, rounded once to out's type
+ *   x_hat = h / sqrt(mean(h^2) + next_eps) * next_w   from the unrounded h: the
+ *           next block's rms_norm ([V100] "rewrite on torch::stable::Tensor")
+ *   xq    = e4m3_satfinite_rne(x_hat / xscale), xscale = max|x_hat| / 448 of the
+ *           token (or of its 128-column group; 1 where that maximum is 0), from
+ *           the unrounded x_hat
+ * in fp32.  The pages name rms_norm only; the norm after the block, the gate
+ * and the residual scale are the plain reading of models that have them.
+ * A host struct; its pointers are device pointers.  `residual` may be the
+ * `out` of the call (the update in place); no other buffer may overlap an
+ * output. */
+typedef struct {
+  const void* residual;     /* [T, H], bf16 or fp32 (residual_f32), or NULL     */
+  const void* post_w;       /* bf16 [H] norm after the block, or NULL           */
+  const void* gate;         /* [gate_rows, gate_cols], bf16 or fp32 (gate_f32),
+                               or NULL                                          */
+  const int32_t* gate_row;  /* int32 [T] gate row of each token; NULL: row 0
+                               when gate_rows is 1, else token t uses row t
+                               (gate_rows must be T).  An index outside
+                               [0, gate_rows) is flagged in the device status
+                               word and that token's out is the residual alone  */
+  const void* next_w;       /* bf16 [H] norm before the next block, or NULL     */
+  void* xhat;               /* bf16 [T, H] or NULL                              */
+  void* xq;                 /* e4m3 [T, H] or NULL (xhat or xq with next_w)     */
+  float* xscale;            /* fp32 [T], or [T, H/128] when q_group is 128      */
+  float post_eps, next_eps; /* >= 0                                             */
+  float scale;              /* residual scale of the block's output             */
+  int32_t residual_f32;
+  int32_t gate_f32;
+  int32_t gate_cols;        /* H, or 1 (one factor per gate row)                */
+  int32_t gate_rows;
+  int32_t q_group;          /* 0 (a scale per token) or 128 (H % 128 == 0)      */
+} moe_block_tail;
+
 /* ---------------------------------------------------------------- misc -- */
 
 /* MOE_ABI_VERSION of the built library. */
@@ -394,6 +432,26 @@ moe_status moe_silu_and_mul(const void* h, int32_t R, int32_t I, void* a, moe_st
 moe_status moe_combine(const void* y, int32_t y_bf16, int32_t y_pair_order,
                        const int32_t* row_of_pair, int32_t T, int32_t k, int32_t H, void* out,
                        moe_stream_t stream);
+
+/* moe_combine and what follows the block, in one pass:
+ *   f_t = sum_{j=0..k-1} y_{t,j}, fp32, in slot order, then the tail
+ * (moe_block_tail above).  y rows as in moe_combine (y_bf16, y_pair_order,
+ * pairs whose row_of_pair is negative are skipped); row_of_pair may be NULL
+ * with y_pair_order = 1 (no pair is skipped).  k = 1 with pair-ordered rows is
+ * the tail of any block with one output row per token (attention, dense MLP).
+ * A row_of_pair entry >= T*k is skipped and flagged in the device status word.
+ *   y [T*k, H] bf16 (y_bf16 = 1) or fp32; out [T, H] bf16 or fp32 (out_f32).
+ * Each input is read once and each output written once.  T = 0 returns MOE_OK
+ * without looking at the tensor pointers.
+ * Errors: INVALID_ARG (null or misaligned pointers, eps < 0, gate_rows /
+ * gate_cols / q_group outside the values above, next_w without xhat and xq, or
+ * xhat / xq without next_w, xq without xscale or the reverse);
+ * UNSUPPORTED_SHAPE unless H % 8 == 0 (H % 128 == 0 with q_group = 128),
+ * H <= 32768, 0 < k <= 8 and T*k <= 2^24. */
+moe_status moe_combine_norm(const void* y, int32_t y_bf16, int32_t y_pair_order,
+                            const int32_t* row_of_pair, int32_t T, int32_t k, int32_t H,
+                            const moe_block_tail* tail, void* out, int32_t out_f32,
+                            moe_stream_t stream);
 
 /* Row-wise dynamic E4M3 quantisation ([SM] 3.2, W8A8):
  *   scale[r] = max|x[r, :]| / 448 (1 for a zero row), fp32;

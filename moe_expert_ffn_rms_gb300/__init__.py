@@ -39,6 +39,17 @@ class MoeShape(ctypes.Structure):
                 ("wdtype", ctypes.c_int32), ("engine", ctypes.c_int32)]
 
 
+class MoeBlockTail(ctypes.Structure):
+    _fields_ = [("residual", ctypes.c_void_p), ("post_w", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_row", ctypes.c_void_p),
+                ("next_w", ctypes.c_void_p), ("xhat", ctypes.c_void_p), ("xq", ctypes.c_void_p),
+                ("xscale", ctypes.c_void_p), ("post_eps", ctypes.c_float),
+                ("next_eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("residual_f32", ctypes.c_int32), ("gate_f32", ctypes.c_int32),
+                ("gate_cols", ctypes.c_int32), ("gate_rows", ctypes.c_int32),
+                ("q_group", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(msg)
@@ -79,6 +90,8 @@ _SIGS = {
                                        _P, _P, _P, _SZ, _P]),
     "moe_silu_and_mul": (ctypes.c_int, [_P, _I32, _I32, _P, _P]),
     "moe_combine": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _I32, _I32, _P, _P]),
+    "moe_combine_norm": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _I32, _I32,
+                                        ctypes.POINTER(MoeBlockTail), _P, _I32, _P]),
     "moe_quantize_fp8_rows": (ctypes.c_int, [_P, ctypes.c_int64, _I32, _P, _P, _P]),
     "moe_ffn_forward_nvfp4": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _P, _P, _P, _P,
                                              _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -296,6 +309,148 @@ def moe_quantize_nvfp4(w, q, sb, sg, stream=None):
     N = w.shape[-2]
     M = w.numel() // (N * K) if w.numel() else 0
     _check(lib.moe_quantize_nvfp4(_ptr(w), M, N, K, _ptr(q), _ptr(sb), _ptr(sg), _stream(stream)))
+
+
+def _check_tensor(t, name, shape, dtypes, device):
+    """Raises ValueError unless t is a contiguous tensor of this shape, one of
+    these types, on this device."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, need {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, need {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+
+
+_BF16 = (torch.bfloat16,)
+_FLOATS = (torch.bfloat16, torch.float32)
+_I32S = (torch.int32,)
+_F32S = (torch.float32,)
+
+
+class BlockTail:
+    """A moe_block_tail and the tensors it points to (kept alive by it).  T is
+    None while none of them fixes the number of tokens."""
+
+    def __init__(self, struct, tensors, T, H, device, rows):
+        self.struct = struct
+        self.ref = ctypes.byref(struct)
+        self.tensors = tensors
+        self.T, self.H, self.device, self.rows = T, H, device, rows
+
+
+def make_block_tail(residual=None, post_w=None, post_eps=1e-6, gate=None, gate_row=None, scale=1.0,
+                    next_w=None, next_eps=1e-6, xhat=None, xq=None, xscale=None) -> BlockTail:
+    """What follows a block (moe_block_tail in include/moe_ffn.h):
+    h = residual + scale * gate * rms_norm(f; post_w); x_hat = rms_norm(h; next_w).
+
+    residual bf16 / fp32 [T, H]; post_w, next_w bf16 [H]; gate bf16 / fp32: [H]
+    (one factor per column), [T, 1] (one per token), [T, H], or [G, H] / [G, 1]
+    with gate_row int32 [T]; xhat bf16 [T, H], xq uint8 or float8_e4m3fn [T, H]
+    with xscale fp32 [T] (a scale per token) or [T, H/128] (per 128 columns).
+
+    The result can be used for any number of calls; it holds pointers to the
+    tensors it was made from."""
+    ts = {n: t for n, t in (("residual", residual), ("post_w", post_w), ("gate", gate),
+                            ("gate_row", gate_row), ("next_w", next_w), ("xhat", xhat), ("xq", xq),
+                            ("xscale", xscale)) if t is not None}
+    T = H = device = None
+    for n in ("residual", "xhat", "xq"):
+        if n in ts:
+            if ts[n].dim() != 2:
+                raise ValueError(f"{n}: must be [T, H]")
+            T, H = ts[n].shape
+            break
+    for n in ("post_w", "next_w"):
+        if H is None and n in ts:
+            H = ts[n].numel()
+    if gate is not None and gate.dim() not in (1, 2):
+        raise ValueError("gate: must be [H] or [rows, H or 1]")
+    if H is None and gate is not None and gate.shape[-1] != 1:
+        H = gate.shape[-1]
+    if T is None and gate_row is not None:
+        T = gate_row.numel()
+    for t in ts.values():
+        device = t.device
+        break
+    s = MoeBlockTail()
+    s.post_eps, s.next_eps, s.scale = post_eps, next_eps, scale
+    rows = 1
+    if residual is not None:
+        _check_tensor(residual, "residual", (T, H), _FLOATS, device)
+        s.residual_f32 = residual.dtype == torch.float32
+    for n in ("post_w", "next_w"):
+        if n in ts:
+            _check_tensor(ts[n], n, (H,), _BF16, device)
+    if gate is not None:
+        g = gate if gate.dim() == 2 else gate[None]
+        rows, cols = g.shape
+        if cols != 1 and cols != H:
+            raise ValueError(f"gate: {cols} columns, need 1 or {H}")
+        _check_tensor(gate, "gate", gate.shape, _FLOATS, device)
+        s.gate_rows, s.gate_cols, s.gate_f32 = rows, cols, gate.dtype == torch.float32
+        if gate_row is None and rows != 1:
+            if T is None:
+                T = rows
+            elif rows != T:
+                raise ValueError(f"gate: {rows} rows without gate_row, need 1 or {T}")
+    if gate_row is not None:
+        if gate is None:
+            raise ValueError("gate_row: needs gate")
+        _check_tensor(gate_row, "gate_row", (T,), _I32S, device)
+    if xhat is not None:
+        _check_tensor(xhat, "xhat", (T, H), _BF16, device)
+    if xq is not None:
+        _check_tensor(xq, "xq", (T, H), (torch.uint8, torch.float8_e4m3fn), device)
+    if xscale is not None:
+        if xscale.dim() == 2:
+            s.q_group = 128
+            _check_tensor(xscale, "xscale", (T, H // 128), _F32S, device)
+        else:
+            _check_tensor(xscale, "xscale", (T,), _F32S, device)
+    for n, t in ts.items():
+        setattr(s, n, t.data_ptr())
+    return BlockTail(s, tuple(ts.values()), T, H, device, rows)
+
+
+def _check_current(device):
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _check_tail(tail, T, H, device):
+    if tail.T is not None and tail.T != T:
+        raise ValueError(f"tail: made for {tail.T} tokens, need {T}")
+    if tail.H is not None and tail.H != H:
+        raise ValueError(f"tail: made for H={tail.H}, need {H}")
+    if tail.device is not None and tail.device != device:
+        raise ValueError(f"tail: tensors on {tail.device}, need {device}")
+
+
+def moe_combine_norm(y, out, T, k, tail: BlockTail, row_of_pair=None, pair_order=True, stream=None):
+    """Sum of each token's k expert rows and what follows the block, in one
+    pass.  y bf16 / fp32 [T*k, H], out bf16 / fp32 [T, H]; rows in (token, slot)
+    order, or (pair_order=False) at row_of_pair int32 [T*k]."""
+    H = y.shape[-1]
+    device = y.device
+    _check_current(device)
+    _check_tensor(y, "y", (T * k, H), _FLOATS, device)
+    _check_tensor(out, "out", (T, H), _FLOATS, device)
+    if row_of_pair is not None:
+        if row_of_pair.numel() != T * k:
+            raise ValueError(f"row_of_pair: {row_of_pair.numel()} entries, need {T * k}")
+        _check_tensor(row_of_pair, "row_of_pair", row_of_pair.shape, _I32S, device)
+    _check_tail(tail, T, H, device)
+    _check(lib.moe_combine_norm(y.data_ptr(), y.dtype == torch.bfloat16, 1 if pair_order else 0,
+                                None if row_of_pair is None else row_of_pair.data_ptr(), T, k, H,
+                                tail.ref, out.data_ptr(), out.dtype == torch.float32,
+                                _stream(stream)))
+    return out
 
 
 def moe_quantize_fp8_rows(x, q, scale, stream=None):

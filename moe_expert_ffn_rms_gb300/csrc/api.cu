@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "engine.h"
 #include "kernels.h"
+#include "tail.h"
 #include "api_internal.h"
 
 // Device status word: MOE_OK, or the first error a kernel flagged.
@@ -505,6 +506,55 @@ moe_status forward_impl(const moe_shape* s, const void* x, const void* norm_w, c
   return MOE_OK;
 }
 
+// Checks a moe_block_tail for T rows of H columns and copies it to the
+// kernels' form.
+moe_status make_tail(const moe_block_tail* b, int T, int H, void* out, int out_f32, moe::TailP* p) {
+  MOE_REQ(out != nullptr && aligned16(out), MOE_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
+  MOE_REQ(aligned16(b->residual) && aligned16(b->post_w) && aligned16(b->next_w) &&
+              aligned16(b->xhat) && aligned16(b->xq) && ((uintptr_t)b->xscale & 3u) == 0 &&
+              ((uintptr_t)b->gate_row & 3u) == 0,
+          MOE_ERR_INVALID_ARG, "misaligned pointer in the block tail");
+  MOE_REQ(b->post_eps >= 0.f && b->next_eps >= 0.f, MOE_ERR_INVALID_ARG, "eps < 0");
+  MOE_REQ((b->next_w != nullptr) == (b->xhat != nullptr || b->xq != nullptr), MOE_ERR_INVALID_ARG,
+          "next_w goes with xhat or xq");
+  MOE_REQ((b->xq == nullptr) == (b->xscale == nullptr), MOE_ERR_INVALID_ARG,
+          "xq and xscale must both be given or both NULL");
+  MOE_REQ(b->q_group == 0 || b->q_group == 128, MOE_ERR_INVALID_ARG, "q_group=%d (0 or 128)", b->q_group);
+  MOE_REQ(!b->xq || b->q_group == 0 || H % 128 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
+          "H=%d must be a multiple of 128 for scales per 128 columns", H);
+  if (b->gate) {
+    MOE_REQ(b->gate_cols == H || b->gate_cols == 1, MOE_ERR_INVALID_ARG, "gate_cols=%d (H or 1)",
+            b->gate_cols);
+    MOE_REQ(b->gate_cols != 1 || ((uintptr_t)b->gate & (b->gate_f32 ? 3u : 1u)) == 0,
+            MOE_ERR_INVALID_ARG, "misaligned gate");
+    MOE_REQ(b->gate_cols == 1 || aligned16(b->gate), MOE_ERR_INVALID_ARG, "gate must be 16-byte aligned");
+    MOE_REQ(b->gate_rows > 0 && (b->gate_row || b->gate_rows == 1 || b->gate_rows == T),
+            MOE_ERR_INVALID_ARG, "gate_rows=%d without gate_row must be 1 or T=%d", b->gate_rows, T);
+  } else {
+    MOE_REQ(!b->gate_row, MOE_ERR_INVALID_ARG, "gate_row without gate");
+  }
+  *p = moe::TailP{};
+  p->residual = b->residual;
+  p->post_w = static_cast<const bf16*>(b->post_w);
+  p->gate = b->gate;
+  p->gate_row = b->gate_row;
+  p->next_w = static_cast<const bf16*>(b->next_w);
+  p->xhat = static_cast<bf16*>(b->xhat);
+  p->xq = static_cast<uint8_t*>(b->xq);
+  p->xscale = b->xscale;
+  p->out = out;
+  p->post_eps = b->post_eps;
+  p->next_eps = b->next_eps;
+  p->scale = b->scale;
+  p->res_f32 = b->residual_f32 != 0;
+  p->out_f32 = out_f32 != 0;
+  p->gate_f32 = b->gate_f32 != 0;
+  p->gate_cols = b->gate_cols;
+  p->gate_rows = b->gate_rows;
+  p->q_group = b->q_group;
+  return MOE_OK;
+}
+
 }  // namespace
 
 namespace moe {
@@ -868,6 +918,30 @@ moe_status moe_combine(const void* y, int32_t y_bf16, int32_t y_pair_order,
   MOE_CUDA(moe::launch_combine(y, y_bf16 != 0, y_pair_order != 0, row_of_pair, T, k, H, out,
                                (cudaStream_t)stream),
            "combine launch");
+  return MOE_OK;
+}
+
+moe_status moe_combine_norm(const void* y, int32_t y_bf16, int32_t y_pair_order,
+                            const int32_t* row_of_pair, int32_t T, int32_t k, int32_t H,
+                            const moe_block_tail* tail, void* out, int32_t out_f32,
+                            moe_stream_t stream) {
+  MOE_REQ(tail, MOE_ERR_INVALID_ARG, "tail must be non-NULL");
+  MOE_REQ(T >= 0 && k > 0 && k <= kMaxTopK && H > 0 && H % 8 == 0 && H <= moe::kTailMaxH &&
+              (int64_t)T * k <= (1 << 24),
+          MOE_ERR_UNSUPPORTED_SHAPE, "T=%d k=%d H=%d (k <= %d, H %% 8 == 0, H <= %d, T*k <= 2^24)", T, k,
+          H, kMaxTopK, moe::kTailMaxH);
+  if (T == 0) return MOE_OK;
+  MOE_REQ(y, MOE_ERR_INVALID_ARG, "y must be non-NULL");
+  MOE_REQ(row_of_pair || y_pair_order, MOE_ERR_INVALID_ARG, "rows in expert order need row_of_pair");
+  MOE_REQ(aligned16(y) && ((uintptr_t)row_of_pair & 3u) == 0, MOE_ERR_INVALID_ARG, "misaligned pointer");
+  moe::TailP p;
+  moe_status rc = make_tail(tail, T, H, out, out_f32, &p);
+  if (rc != MOE_OK) return rc;
+  DevInfo* d = nullptr;
+  if ((rc = device_info(&d)) != MOE_OK) return rc;
+  MOE_CUDA(moe::launch_combine_norm(y, y_bf16 == 0, y_pair_order != 0, row_of_pair, T, k, H, p,
+                                    d->status, (cudaStream_t)stream),
+           "combine_norm launch");
   return MOE_OK;
 }
 

@@ -1,0 +1,124 @@
+// What follows a block, per token row (shared by moe_combine_norm and the
+// tail of moe_layer_forward):
+//   g = f / sqrt(mean(f^2) + post_eps) * post_w          (g = f without post_w)
+//   h = residual + scale * gate * g                      (out = h rounded once)
+//   x_hat = h / sqrt(mean(h^2) + next_eps) * next_w      (from the unrounded h)
+//   xq = e4m3(x_hat / s), s = max|x_hat| / 448           (per token or 128 columns)
+// f, h, x_hat and the row statistics stay in fp32; every output is rounded
+// once, from the fp32 value.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// Device-side copy of moe_block_tail plus the output (host: make_tail).
+struct TailP {
+  const void* residual;
+  const bf16* post_w;
+  const void* gate;
+  const int32_t* gate_row;
+  const bf16* next_w;
+  bf16* xhat;
+  uint8_t* xq;
+  float* xscale;
+  void* out;
+  float post_eps, next_eps, scale;
+  int res_f32, out_f32, gate_f32, gate_cols, gate_rows, q_group;
+};
+
+// Eight consecutive columns as fp32.
+MOE_DEV void load8(const void* p, bool f32, size_t at, float (&v)[8]) {
+  if (f32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 a = s[0], b = s[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    unpack8_bf16(*reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + at), v);
+  }
+}
+
+MOE_DEV void store8_bf16(bf16* p, const float (&v)[8]) {
+  uint4 o;
+  o.x = pack2_bf16(v[0], v[1]);
+  o.y = pack2_bf16(v[2], v[3]);
+  o.z = pack2_bf16(v[4], v[5]);
+  o.w = pack2_bf16(v[6], v[7]);
+  *reinterpret_cast<uint4*>(p) = o;
+}
+
+MOE_DEV void store8(void* p, bool f32, size_t at, const float (&v)[8]) {
+  if (f32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    store8_bf16(static_cast<bf16*>(p) + at, v);
+  }
+}
+
+// Row of the gate that token t uses, or -1 for an index outside the gate
+// (flagged; the row then counts as a zero gate).
+MOE_DEV int tail_gate_row(const TailP& p, int t, int* status) {
+  if (!p.gate) return 0;
+  if (!p.gate_row) return p.gate_rows == 1 ? 0 : t;
+  const int r = p.gate_row[t];
+  if (r < 0 || r >= p.gate_rows) {
+    flag_status(status, MOE_ERR_INVALID_ARG);
+    return -1;
+  }
+  return r;
+}
+
+// The token's scalar factor: scale, times the gate when it is one per token.
+MOE_DEV float tail_row_factor(const TailP& p, int grow) {
+  if (!p.gate || p.gate_cols != 1) return grow < 0 ? 0.f : p.scale;
+  if (grow < 0) return 0.f;
+  const float g = p.gate_f32 ? static_cast<const float*>(p.gate)[grow]
+                             : __bfloat162float(static_cast<const bf16*>(p.gate)[grow]);
+  return p.scale * g;
+}
+
+// h of eight columns at column c of token t.  A row whose gate index is out
+// of range (grow < 0) is the residual alone, whatever f holds.
+MOE_DEV void tail_h8(const TailP& p, int t, int H, int c, const float (&f)[8], float r, int grow,
+                     float factor, float (&h)[8]) {
+  float g[8];
+  if (p.post_w) {
+    float w[8];
+    load8(p.post_w, false, c, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = (f[i] * r) * w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = f[i];
+  }
+  if (p.gate && p.gate_cols != 1 && grow >= 0) {
+    float a[8];
+    load8(p.gate, p.gate_f32 != 0, (size_t)grow * H + c, a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] *= a[i];
+  }
+  if (p.residual) {
+    load8(p.residual, p.res_f32 != 0, (size_t)t * H + c, h);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = 0.f;
+  }
+  if (grow >= 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = fmaf(factor, g[i], h[i]);
+  }
+}
+
+MOE_DEV uint2 tail_e4m3x8(const float (&v)[8], float s) {
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) lo |= (uint32_t)f_to_e4m3(__fdiv_rn(v[i], s)) << (8 * i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) hi |= (uint32_t)f_to_e4m3(__fdiv_rn(v[4 + i], s)) << (8 * i);
+  return make_uint2(lo, hi);
+}
+
+}  // namespace moe
