@@ -940,7 +940,7 @@ moe_status moe_combine_norm(const void* y, int32_t y_bf16, int32_t y_pair_order,
   DevInfo* d = nullptr;
   if ((rc = device_info(&d)) != MOE_OK) return rc;
   MOE_CUDA(moe::launch_combine_norm(y, y_bf16 == 0, y_pair_order != 0, row_of_pair, T, k, H, p,
-                                    d->status, (cudaStream_t)stream),
+                                    d->status, d->sms, (cudaStream_t)stream),
            "combine_norm launch");
   return MOE_OK;
 }

@@ -3,84 +3,63 @@
 #include "block_tail.cuh"
 #include "kernels.h"
 #include "tail.h"
+#include "tc_ptx.cuh"
+
+#include <stdlib.h>
 
 namespace moe {
 namespace {
 
-// One CTA per token; thread `tid` holds the 8-column chunks tid, tid +
-// blockDim, ... (at most VPT) in registers from the first read to the last
-// write, so each input is read once and each output written once.
+// ---------------------------------------------------------- per-token parts --
+// The tail of one token for a thread that owns VPT 8-column chunks (tid, tid +
+// blockDim, ...).  Weights and a per-column gate are read from global memory
+// (L1 / L2 resident); the callers supply the sum and the residual.
+
+// Sum (or maximum) over the first nt threads of the CTA (nt a multiple of 32,
+// at most 512) with one barrier among them.  `red` (16 floats) must not be
+// written again before another such barrier has passed.
+template <bool MAX>
+MOE_DEV float rows_reduce(float v, int nt, float* red) {
+  v = MAX ? warp_max(v) : warp_sum(v);
+  if (nt == 32) return v;
+  const int lane = threadIdx.x & 31, nw = nt >> 5;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync 1, %0;" ::"r"(nt) : "memory");
+  v = (lane & 15) < nw ? red[lane & 15] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, u) : v + u;
+  }
+  return v;
+}
+
+// 1 / norm of the row held in f.
 template <int VPT>
-__global__ void __launch_bounds__(1024) combine_norm_kernel(
-    const void* __restrict__ y, int y_f32, int pair_order, const int32_t* __restrict__ row_of_pair,
-    int T, int k, int H, const TailP p, int* status) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ float red[32];
-  const int t = blockIdx.x;
-  const int nv = H >> 3;
-  float f[VPT][8];
+MOE_DEV float row_rnorm(const float (&f)[VPT][8], int nt, int H, float eps, float* red) {
+  float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
-  for (int j = 0; j < k; ++j) {  // summed in slot order, skipped pairs excluded
-    const int64_t pair = (int64_t)t * k + j;
-    int64_t row = pair;
-    if (row_of_pair) {
-      const int r = row_of_pair[pair];
-      if (r < 0) continue;
-      if (r >= T * k) {
-        if (threadIdx.x == 0) flag_status(status, MOE_ERR_INVALID_ARG);
-        continue;
-      }
-      if (!pair_order) row = r;
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nv) break;
-      float a[8];
-      load8(y, y_f32 != 0, (size_t)row * H + v * 8, a);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) f[i][q] += a[q];
-    }
-  }
-  float r = 1.f;
-  if (p.post_w) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int q = 0; q < 8; ++q) ss = fmaf(f[i][q], f[i][q], ss);
-    r = 1.0f / sqrtf(block_sum(ss, red) / (float)H + p.post_eps);
-  }
-  const int grow = tail_gate_row(p, t, threadIdx.x == 0 ? status : nullptr);
-  const float factor = tail_row_factor(p, grow);
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
-    if (v >= nv) break;
-    float h[8];
-    tail_h8(p, t, H, v * 8, f[i], r, grow, factor, h);
-    store8(p.out, p.out_f32 != 0, (size_t)t * H + v * 8, h);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      f[i][q] = h[q];
-      ss = fmaf(h[q], h[q], ss);
-    }
-  }
-  if (!p.next_w) return;
-  r = 1.0f / sqrtf(block_sum(ss, red) / (float)H + p.next_eps);
+    for (int q = 0; q < 8; ++q) ss = fmaf(f[i][q], f[i][q], ss);
+  return 1.0f / sqrtf(rows_reduce<false>(ss, nt, red) / (float)H + eps);
+}
+
+// x_hat (and its quantisation) of the row h held in f; chunks beyond the row
+// hold zeros.  KEPT: next_w holds this thread's (one) chunk of the weights.
+template <int VPT, bool KEPT = false>
+MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], float r, int nt,
+                        const uint4& next_w, float* red) {
+  const int tid = threadIdx.x, nv = H >> 3;
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
+    const int v = tid + i * nt;
     float m = 0.f;
     if (v < nv) {
       float w[8];
-      load8(p.next_w, false, v * 8, w);
+      if (KEPT) unpack8_bf16(next_w, w);
+      else load8(p.next_w, false, v * 8, w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         f[i][q] = (f[i][q] * r) * w[q];
@@ -89,8 +68,8 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(
       if (p.xhat) store8_bf16(p.xhat + (size_t)t * H + v * 8, f[i]);
     }
     if (p.xq && p.q_group) {
-      // a group of 128 columns is 16 consecutive lanes (blockDim is a
-      // multiple of 32, H of 128)
+      // a group of 128 columns is 16 consecutive lanes (nt is a multiple of 32,
+      // H of 128)
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float s = m > 0.f ? __fdiv_rn(m, 448.0f) : 1.0f;
@@ -102,33 +81,436 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(
     amax = fmaxf(amax, m);
   }
   if (p.xq && !p.q_group) {
-    amax = block_max(amax, red);
+    amax = rows_reduce<true>(amax, nt, red);
     const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
+      const int v = tid + i * nt;
       if (v < nv) *reinterpret_cast<uint2*>(p.xq + (size_t)t * H + v * 8) = tail_e4m3x8(f[i], s);
     }
-    if (threadIdx.x == 0) p.xscale[t] = s;
+    if (tid == 0) p.xscale[t] = s;
   }
+}
+
+// --------------------------------------------------------- one CTA per token --
+// Few tokens (latency) and rows too long for the streaming form: every load of
+// a chunk (its k expert rows, residual, weights) is issued before the first
+// use, so the chain is one round of loads, two row reductions, the stores.
+struct Raw8 {
+  uint4 a, b;  // 8 columns: bf16 in a, or fp32 in a and b
+};
+
+MOE_DEV Raw8 ldg8(const void* p, bool f32, size_t at) {
+  Raw8 r;
+  if (f32) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+    r.a = s[0];
+    r.b = s[1];
+  } else {
+    r.a = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + at);
+    r.b = make_uint4(0u, 0u, 0u, 0u);
+  }
+  return r;
+}
+
+MOE_DEV void raw_to_f(const Raw8& r, bool f32, float (&v)[8]) {
+  if (f32) {
+    v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y);
+    v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
+    v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
+    v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
+  } else {
+    unpack8_bf16(r.a, v);
+  }
+}
+
+constexpr int kRowThreads = 512;
+
+template <int VPT, bool YF32>
+__global__ void __launch_bounds__(kRowThreads) combine_norm_row_kernel(
+    const void* __restrict__ y, int pair_order, const int32_t* __restrict__ row_of_pair, int T, int k,
+    int H, const TailP p, int* status) {
+  constexpr int BJ = VPT <= 2 ? 8 : 4;  // rows in flight per chunk
+  constexpr bool EARLY = VPT <= 2;      // residual held from the start (registers)
+  __shared__ float red[3][16];
+  pdl_trigger();
+  pdl_wait();
+  const int t = blockIdx.x;
+  const int tid = threadIdx.x, nt = blockDim.x, nv = H >> 3;
+  int64_t row[kMaxTopK];  // row of each slot, -1 when skipped
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    row[j] = j < k ? (int64_t)t * k + j : -1;
+    if (row_of_pair && j < k) {
+      const int r = row_of_pair[row[j]];
+      if (r >= T * k && tid == 0) flag_status(status, MOE_ERR_INVALID_ARG);
+      if (r < 0 || r >= T * k) row[j] = -1;
+      else if (!pair_order) row[j] = r;
+    }
+  }
+  float f[VPT][8];
+  Raw8 res[EARLY ? VPT : 1];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * nt;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
+    if (EARLY) {
+      res[i].a = res[i].b = make_uint4(0u, 0u, 0u, 0u);
+      if (v < nv && p.residual) res[i] = ldg8(p.residual, p.res_f32 != 0, (size_t)t * H + v * 8);
+    }
+    if (v >= nv) continue;
+#pragma unroll
+    for (int j0 = 0; j0 < kMaxTopK; j0 += BJ) {
+      Raw8 a[BJ];
+#pragma unroll
+      for (int j = 0; j < BJ; ++j)
+        if (row[j0 + j] >= 0) a[j] = ldg8(y, YF32, (size_t)row[j0 + j] * H + v * 8);
+#pragma unroll
+      for (int j = 0; j < BJ; ++j) {  // summed in slot order, skipped pairs excluded
+        if (row[j0 + j] >= 0) {
+          float b[8];
+          raw_to_f(a[j], YF32, b);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) f[i][q] += b[q];
+        }
+      }
+    }
+  }
+  const int grow = tail_gate_row(p, t, tid == 0 ? status : nullptr);
+  const float factor = tail_row_factor(p, grow);
+  const float r = p.post_w ? row_rnorm(f, nt, H, p.post_eps, red[0]) : 1.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * nt;
+    if (v >= nv) continue;
+    float h[8], b[8];
+    if (EARLY) {
+      raw_to_f(res[i], p.res_f32 != 0, b);
+    } else if (p.residual) {
+      load8(p.residual, p.res_f32 != 0, (size_t)t * H + v * 8, b);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) b[q] = 0.f;
+    }
+    tail_h8(p, H, v * 8, f[i], r, grow, factor, b, h);
+    store8(p.out, p.out_f32 != 0, (size_t)t * H + v * 8, h);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[i][q] = h[q];
+  }
+  if (!p.next_w) return;
+  write_next(p, t, H, f, row_rnorm(f, nt, H, p.next_eps, red[1]), nt, make_uint4(0u, 0u, 0u, 0u), red[2]);
+}
+
+// ----------------------------------------------------------- streaming form --
+// Persistent CTAs, a token per pass.  The rows a token needs are brought to
+// shared memory by bulk copies that a producer warp issues up to S stages
+// ahead, so the next rows are in flight while the consumer warps take a token
+// through its row reductions.  A stage holds R of the token's k expert rows
+// (one copy when they are consecutive); the token's last stage also holds its
+// residual and its gate row.  The producer reads the token's indices and
+// leaves them beside the rows.
+struct StreamMeta {
+  unsigned use;   // slots whose row is present
+  float factor;   // tail_row_factor
+  int gate_ok;    // 0: gate index out of range
+};
+
+template <int VPT, bool YF32, bool SPLIT>
+__global__ void __launch_bounds__(kRowThreads + 32, VPT <= 2 ? 2 : 1)
+    combine_norm_stream_kernel(const void* __restrict__ y, int pair_order,
+                               const int32_t* __restrict__ row_of_pair, int T, int k, int H,
+                               const TailP p, int* status, int S, int stage_bytes, int R_) {
+  extern __shared__ __align__(128) unsigned char stages[];
+  __shared__ uint64_t full[kStreamStages], empty[kStreamStages];
+  __shared__ StreamMeta meta[kStreamStages];
+  __shared__ float red[2][3][16];
+  __shared__ int s_abort;
+  const int R = SPLIT ? R_ : k;
+  const int tid = threadIdx.x, nt = blockDim.x - 32, nv = H >> 3;
+  const bool gate_rows = p.gate && p.gate_cols != 1 && !(p.gate_rows == 1 && !p.gate_row);
+  const int yb = H * (YF32 ? 4 : 2), rb = p.residual ? H * (p.res_f32 ? 4 : 2) : 0;
+  const int gb = gate_rows ? H * (p.gate_f32 ? 4 : 2) : 0;
+  pdl_trigger();
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < S; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], nt >> 5);
+    }
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+
+  if (tid >= nt) {
+    // ------------------------------------------------------------ producer --
+    if (tid != nt) return;
+    auto copy = [&](unsigned char* dst, const unsigned char* src, int bytes, uint64_t* bar) {
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              ptx::smem_u32(dst)),
+          "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+          : "memory");
+    };
+    const unsigned char* yc = static_cast<const unsigned char*>(y);
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+      int rows[kMaxTopK];
+      unsigned use = 0;
+      if (row_of_pair) {
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j) rows[j] = j < k ? row_of_pair[(int64_t)t * k + j] : -1;
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j) {
+          if (rows[j] >= T * k) flag_status(status, MOE_ERR_INVALID_ARG);
+          if (rows[j] >= 0 && rows[j] < T * k) use |= 1u << j;
+          if (pair_order) rows[j] = t * k + j;
+        }
+      } else {
+        use = (1u << k) - 1;
+      }
+      const int grow = tail_gate_row(p, t, status);
+      const float factor = tail_row_factor(p, grow);
+      const bool with_gate = gate_rows && grow >= 0;
+      for (int j0 = 0; ok && j0 < k; j0 += R, ++n) {
+        if (!(ok = ptx::mbar_wait(&empty[s], ph ^ 1, &s_abort))) break;
+        meta[s].use = use;
+        meta[s].factor = factor;
+        meta[s].gate_ok = grow >= 0;
+        unsigned char* st = stages + (size_t)s * stage_bytes;
+        const int nr = min(R, k - j0);
+        const bool last = j0 + R >= k;
+        const unsigned mine = (use >> j0) & ((1u << nr) - 1);
+        ptx::mbar_arrive_expect_tx(&full[s], __popc(mine) * yb + (last ? rb + (with_gate ? gb : 0) : 0));
+        if (row_of_pair) {
+#pragma unroll
+          for (int j = 0; j < kMaxTopK; ++j)
+            if (j >= j0 && ((mine >> (j - j0)) & 1u))
+              copy(st + (size_t)(j - j0) * yb, yc + (size_t)rows[j] * yb, yb, &full[s]);
+        } else {
+          copy(st, yc + ((size_t)t * k + j0) * yb, nr * yb, &full[s]);
+        }
+        if (last && rb)
+          copy(st + (size_t)R * yb, static_cast<const unsigned char*>(p.residual) + (size_t)t * rb, rb,
+               &full[s]);
+        if (last && with_gate)
+          copy(st + (size_t)R * yb + rb, static_cast<const unsigned char*>(p.gate) + (size_t)grow * gb, gb,
+               &full[s]);
+        if (++s == S) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok) {
+      flag_status(status, MOE_ERR_TIMEOUT);
+      // copies in flight must land before the shared memory is given up
+      for (int i = n > S ? n - S : 0; i < n; ++i) {
+        const long long t0 = clock64();
+        while (!ptx::mbar_try_wait(&full[i % S], (uint32_t)((i / S) & 1)) &&
+               clock64() - t0 < ptx::kSpinLimitCycles) {
+        }
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers --
+  constexpr int BJ = YF32 ? 2 : 4;
+  constexpr bool KEEP = VPT == 1;  // the norm weights stay in registers over the tokens
+  uint4 pw = make_uint4(0u, 0u, 0u, 0u), nw = pw;
+  if (KEEP && tid < nv) {
+    if (p.post_w) pw = reinterpret_cast<const uint4*>(p.post_w)[tid];
+    if (p.next_w) nw = reinterpret_cast<const uint4*>(p.next_w)[tid];
+  }
+  int s = 0, n = 0;
+  uint32_t ph = 0;
+  bool ok = true;
+  for (int t = blockIdx.x; t < T; t += gridDim.x, ++n) {
+    // a wait that runs out leaves garbage in the outputs and is reported
+    ok = ptx::mbar_wait(&full[s], ph, &s_abort) && ok;
+    const unsigned char* st = stages + (size_t)s * stage_bytes;
+    const unsigned use = meta[s].use;
+    const float factor = meta[s].factor;
+    const bool gate_ok = meta[s].gate_ok != 0;
+    float f[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
+    }
+    if (k == 1) {  // one row per token: no loop, no additions
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (use && tid + i * nt < nv) load8(st, YF32, (tid + i * nt) * 8, f[i]);
+    } else {
+      // summed in slot order, BJ rows' loads at a time; a skipped slot adds 0
+#pragma unroll 1
+      for (int j0 = 0; SPLIT ? j0 < k : j0 == 0; j0 += R) {
+        if (SPLIT && j0 > 0) {  // the stage before this one has been read
+          __syncwarp();
+          if ((tid & 31) == 0) ptx::mbar_arrive(&empty[s]);
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
+          ok = ptx::mbar_wait(&full[s], ph, &s_abort) && ok;
+          st = stages + (size_t)s * stage_bytes;
+        }
+        const unsigned mine = SPLIT ? (use >> j0) & ((1u << R) - 1) : use;
+        const int nr = SPLIT ? min(R, k - j0) : k;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int v = tid + i * nt;
+          if (v >= nv) continue;
+#pragma unroll 1
+          for (int j1 = 0; j1 < nr; j1 += BJ) {
+            Raw8 a[BJ];
+#pragma unroll
+            for (int j = 0; j < BJ; ++j) {
+              a[j].a = a[j].b = make_uint4(0u, 0u, 0u, 0u);
+              if ((mine >> (j1 + j)) & 1u) a[j] = ldg8(st + (size_t)(j1 + j) * yb, YF32, v * 8);
+            }
+#pragma unroll
+            for (int j = 0; j < BJ; ++j) {
+              float b[8];
+              raw_to_f(a[j], YF32, b);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) f[i][q] += b[q];
+            }
+          }
+        }
+      }
+    }
+    const float r = p.post_w ? row_rnorm(f, nt, H, p.post_eps, red[n & 1][0]) : 1.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = tid + i * nt;
+      if (v >= nv) continue;
+      float a[8];
+      if (p.post_w) {
+        if (KEEP) unpack8_bf16(pw, a);
+        else load8(p.post_w, false, v * 8, a);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[i][q] = (f[i][q] * r) * a[q];
+      }
+      if (p.gate && p.gate_cols != 1 && gate_ok) {
+        if (gate_rows) load8(st + (size_t)R * yb + rb, p.gate_f32 != 0, v * 8, a);
+        else load8(p.gate, p.gate_f32 != 0, v * 8, a);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[i][q] *= a[q];
+      }
+      float h[8];
+      if (rb) {
+        load8(st + (size_t)R * yb, p.res_f32 != 0, v * 8, h);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) h[q] = 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (gate_ok) h[q] = fmaf(factor, f[i][q], h[q]);
+        f[i][q] = h[q];
+      }
+      store8(p.out, p.out_f32 != 0, (size_t)t * H + v * 8, h);
+    }
+    // this warp has read the stage
+    __syncwarp();
+    if ((tid & 31) == 0) ptx::mbar_arrive(&empty[s]);
+    if (p.next_w)
+      write_next<VPT, KEEP>(p, t, H, f, row_rnorm(f, nt, H, p.next_eps, red[n & 1][1]), nt, nw,
+                            red[n & 1][2]);
+    if (++s == S) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+  if (!ok) flag_status(status, MOE_ERR_TIMEOUT);
+}
+
+template <int VPT, bool YF32>
+cudaError_t launch_row(const void* y, bool pair_order, const int32_t* row_of_pair, int T, int k, int H,
+                       const TailP& p, int* status, int threads, cudaStream_t st) {
+  return launch_kernel(combine_norm_row_kernel<VPT, YF32>, dim3(T), dim3(threads), 0, st, y,
+                       (int)pair_order, row_of_pair, T, k, H, p, status);
+}
+
+// cudaErrorNotSupported when even one expert row per stage does not fit twice.
+template <int VPT, bool YF32>
+cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_pair, int T, int k, int H,
+                          const TailP& p, int* status, int sms, int threads, cudaStream_t st) {
+  auto kern = combine_norm_stream_kernel<VPT, YF32, false>;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  const int64_t yb = (int64_t)H * (YF32 ? 4 : 2);
+  const int64_t extra = (p.residual ? (int64_t)H * (p.res_f32 ? 4 : 2) : 0) +
+                        (p.gate && p.gate_cols != 1 ? (int64_t)H * (p.gate_f32 ? 4 : 2) : 0);
+  auto bytes = [&](int rows) { return (rows * yb + extra + 127) / 128 * 128; };
+  // CTAs an SM holds by registers (given out to four warps at a time) and threads
+  const int warps = (threads / 32 + 1 + 3) / 4 * 4;
+  int by_regs = 65536 / ((fa.numRegs + 7) / 8 * 8 * 32 * warps);
+  if (by_regs > 2048 / (threads + 32)) by_regs = 2048 / (threads + 32);
+  if (by_regs > kStreamCtas) by_regs = kStreamCtas;
+  if (by_regs < 1) return cudaErrorNotSupported;
+  auto by_smem = [&](int64_t b) { return (int)(kStreamSmem / (b + kStreamStatic)); };
+  int R = k, S, per_sm = by_smem(bytes(k)) < by_regs ? by_smem(bytes(k)) : by_regs;
+  if (per_sm > 0 && T <= sms * per_sm) {
+    // every token gets a CTA of its own at once: one stage each
+    S = 1;
+  } else {
+    // two or more stages, each as much of a token as fits; then as many CTAs as
+    // fit, then the memory that is left goes to more stages
+    while (R > 1 && by_smem(2 * bytes(R)) < 1) R = (R + 1) / 2;
+    per_sm = by_smem(2 * bytes(R));
+    if (per_sm < 1) return cudaErrorNotSupported;
+    if (per_sm > by_regs) per_sm = by_regs;
+    S = (int)((kStreamSmem / per_sm - kStreamStatic) / bytes(R));
+    if (S > kStreamStages) S = kStreamStages;
+    if (R < k) kern = combine_norm_stream_kernel<VPT, YF32, true>;
+  }
+  const size_t smem = (size_t)S * bytes(R);
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int grid = T < sms * per_sm ? T : sms * per_sm;
+  return launch_kernel(kern, dim3(grid), dim3(threads + 32), smem, st, y, (int)pair_order, row_of_pair, T,
+                       k, H, p, status, S, (int)bytes(R), R);
 }
 
 }  // namespace
 
 cudaError_t launch_combine_norm(const void* y, bool y_f32, bool pair_order,
                                 const int32_t* row_of_pair, int T, int k, int H, const TailP& p,
-                                int* status, cudaStream_t st) {
+                                int* status, int sms, cudaStream_t st) {
   if (T == 0) return cudaSuccess;
   const int nv = H / 8;
-  int threads = rmsnorm_threads(T, nv);
-  if (threads * 4 < nv) threads = ((nv + 3) / 4 + 31) / 32 * 32;
-  const int vpt = (nv + threads - 1) / threads;
-#define MOE_CN(V)                                                                              \
-  return launch_kernel(combine_norm_kernel<V>, dim3(T), dim3(threads), 0, st, y, (int)y_f32,   \
-                       (int)pair_order, row_of_pair, T, k, H, p, status)
-  if (vpt <= 1) MOE_CN(1);
-  if (vpt <= 2) MOE_CN(2);
-  MOE_CN(4);
+  const char* env = getenv("MOE_CN_STREAM");
+  if (nv <= 2048 && (env ? env[0] == '1' : T > sms)) {
+    const int vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);
+    const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+    cudaError_t e;
+#define MOE_CN(V)                                                                                     \
+  e = y_f32 ? launch_stream<V, true>(y, pair_order, row_of_pair, T, k, H, p, status, sms, threads, st) \
+            : launch_stream<V, false>(y, pair_order, row_of_pair, T, k, H, p, status, sms, threads, st)
+    if (vpt == 1) MOE_CN(1);
+    else if (vpt == 2) MOE_CN(2);
+    else MOE_CN(4);
+#undef MOE_CN
+    if (e != cudaErrorNotSupported) return e;
+  }
+  const int vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : (nv <= 2048 ? 4 : 8));
+  const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+#define MOE_CN(V)                                                                                     \
+  return y_f32 ? launch_row<V, true>(y, pair_order, row_of_pair, T, k, H, p, status, threads, st)     \
+               : launch_row<V, false>(y, pair_order, row_of_pair, T, k, H, p, status, threads, st)
+  if (vpt == 1) MOE_CN(1);
+  if (vpt == 2) MOE_CN(2);
+  if (vpt == 4) MOE_CN(4);
+  MOE_CN(8);
 #undef MOE_CN
 }
 

@@ -48,11 +48,21 @@ MOE_DEV void store8_bf16(bf16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = o;
 }
 
+// fp32 columns go out in one 32-byte store where the address allows it (whole
+// sectors; two 16-byte stores write every sector in two halves).
 MOE_DEV void store8(void* p, bool f32, size_t at, const float (&v)[8]) {
   if (f32) {
     float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    if (((uintptr_t)d & 31u) == 0) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d),
+                   "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                   "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+                   "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                   : "memory");
+    } else {
+      d[0] = make_float4(v[0], v[1], v[2], v[3]);
+      d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
   } else {
     store8_bf16(static_cast<bf16*>(p) + at, v);
   }
@@ -80,10 +90,11 @@ MOE_DEV float tail_row_factor(const TailP& p, int grow) {
   return p.scale * g;
 }
 
-// h of eight columns at column c of token t.  A row whose gate index is out
-// of range (grow < 0) is the residual alone, whatever f holds.
-MOE_DEV void tail_h8(const TailP& p, int t, int H, int c, const float (&f)[8], float r, int grow,
-                     float factor, float (&h)[8]) {
+// h of eight columns from column c: f the block's output, r its norm factor,
+// res the residual (zeros without one).  A row whose gate index is out of range
+// (grow < 0) is the residual alone, whatever f holds.
+MOE_DEV void tail_h8(const TailP& p, int H, int c, const float (&f)[8], float r, int grow, float factor,
+                     const float (&res)[8], float (&h)[8]) {
   float g[8];
   if (p.post_w) {
     float w[8];
@@ -100,25 +111,29 @@ MOE_DEV void tail_h8(const TailP& p, int t, int H, int c, const float (&f)[8], f
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] *= a[i];
   }
-  if (p.residual) {
-    load8(p.residual, p.res_f32 != 0, (size_t)t * H + c, h);
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = 0.f;
-  }
-  if (grow >= 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = fmaf(factor, g[i], h[i]);
-  }
+  for (int i = 0; i < 8; ++i) h[i] = grow >= 0 ? fmaf(factor, g[i], res[i]) : res[i];
 }
 
+// E4M3 codes of v / s.  The quotient is taken as a product with 1 / s (one
+// division per row or group instead of eight per thread; within two roundings
+// of the quotient, which is of the size of x_hat's own), except for scales so
+// small that 1 / s could overflow.
 MOE_DEV uint2 tail_e4m3x8(const float (&v)[8], float s) {
-  uint32_t lo = 0, hi = 0;
+  float q[8];
+  if (s >= 1e-30f) {
+    const float inv = __fdiv_rn(1.0f, s);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) lo |= (uint32_t)f_to_e4m3(__fdiv_rn(v[i], s)) << (8 * i);
+    for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) hi |= (uint32_t)f_to_e4m3(__fdiv_rn(v[4 + i], s)) << (8 * i);
-  return make_uint2(lo, hi);
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+  }
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 }  // namespace moe

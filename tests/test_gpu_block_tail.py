@@ -30,6 +30,14 @@ def M():
     return M
 
 
+@pytest.fixture(params=["auto", "row", "stream"])
+def form(request, monkeypatch):
+    """The launcher's own choice, and both kernels wherever their rows fit."""
+    if request.param != "auto":
+        monkeypatch.setenv("MOE_CN_STREAM", "1" if request.param == "stream" else "0")
+    return request.param
+
+
 def randn(g, *shape, std=1.0, mean=0.0, dtype=torch.bfloat16):
     return torch.randn(shape, generator=g, device=DEV).mul_(std).add_(mean).to(dtype)
 
@@ -183,12 +191,12 @@ def check_outputs(d, o, h, dh, x, dx):
 
 
 SIZES = [(1, 8), (3, 24), (5, 64), (2, 1000), (7, 2048), (4, 4096), (3, 7168), (2, 8200), (1, 16392),
-         (2, 32768), (600, 264), (513, 4096), (640, 8192)]
+         (2, 32768), (600, 264), (513, 4096), (640, 8192), (170, 16384), (1300, 7168)]
 
 
 @pytest.mark.parametrize("T,H", SIZES)
 @pytest.mark.parametrize("k", [1, 8])
-def test_sizes(M, T, H, k):
+def test_sizes(M, form, T, H, k):
     d = make(T, H, k, nxt="both", gate="channel", seed=T + H)
     check(d, call(M, d))
 
@@ -196,7 +204,7 @@ def test_sizes(M, T, H, k):
 @pytest.mark.parametrize("y,order,res", list(itertools.product(
     [torch.bfloat16, torch.float32], ["pair", "pair_idx", "expert"],
     [None, torch.bfloat16, torch.float32])))
-def test_types_and_orders(M, y, order, res):
+def test_types_and_orders(M, form, y, order, res):
     for T, H, k in ((6, 512, 4), (530, 1032, 3)):
         d = make(T, H, k, y=y, order=order, res=res, nxt="bf16", drop=0.0, seed=k)
         check(d, call(M, d))
@@ -206,14 +214,14 @@ def test_types_and_orders(M, y, order, res):
                                   "row_scalars"])
 @pytest.mark.parametrize("post", [False, True])
 @pytest.mark.parametrize("nxt", ["none", "bf16", "e4m3", "e4m3g", "both"])
-def test_gates_and_outputs(M, gate, post, nxt):
+def test_gates_and_outputs(M, form, gate, post, nxt):
     for T, H, k in ((1, 128, 1), (9, 640, 2), (515, 384, 1)):
         d = make(T, H, k, post=post, gate=gate, nxt=nxt, seed=T)
         check(d, call(M, d))
 
 
 @pytest.mark.parametrize("order", ["pair_idx", "expert"])
-def test_skipped_pairs(M, order):
+def test_skipped_pairs(M, form, order):
     d = make(40, 256, 4, order=order, drop=0.5, nxt="bf16", seed=3)
     d["row_of_pair"][8:12] = -1  # token 2 has no row at all: f = 0, out = residual
     o = call(M, d)
@@ -221,7 +229,7 @@ def test_skipped_pairs(M, order):
     assert torch.equal(o["out"][2], d["residual"][2])
 
 
-def test_empty_rows_and_zero_input(M):
+def test_empty_rows_and_zero_input(M, form):
     d = make(4, 256, 2, order="pair_idx", res=None, nxt="e4m3", seed=4)
     d["row_of_pair"].fill_(-1)  # f = 0 everywhere and no residual: h = 0
     o = call(M, d)
@@ -232,7 +240,7 @@ def test_empty_rows_and_zero_input(M):
     assert (o["out"] == 0).all() and (o["xq"] & 0x7f == 0).all() and (o["xscale"] == 1).all()
 
 
-def test_non_finite_rows_stay_in_their_token(M):
+def test_non_finite_rows_stay_in_their_token(M, form):
     d = make(6, 512, 2, nxt="both", gate="rows", seed=5)
     clean = call(M, d)
     d["y"][4] = float("nan")       # token 2
@@ -245,7 +253,7 @@ def test_non_finite_rows_stay_in_their_token(M):
     assert torch.isinf(o["out"][4, 7])
 
 
-def test_bad_indices_are_flagged_and_skipped(M):
+def test_bad_indices_are_flagged_and_skipped(M, form):
     M.device_status(clear=True)
     d = make(8, 256, 2, order="expert", gate="rows", nxt="bf16", seed=6)
     want = dict(d, row_of_pair=d["row_of_pair"].clone())
@@ -268,7 +276,7 @@ def test_bad_indices_are_flagged_and_skipped(M):
     assert M.device_status(clear=True) == 0
 
 
-def test_in_place_and_rows_behind_the_last(M):
+def test_in_place_and_rows_behind_the_last(M, form):
     d = make(5, 512, 2, nxt="bf16", seed=7)
     want = call(M, d)
     keep = d["residual"].clone()
