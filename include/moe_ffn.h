@@ -292,6 +292,50 @@ moe_status moe_ffn_forward_nvfp4(const moe_shape* shape, const void* x, const vo
                                  float* topk_w_out, void* workspace, size_t workspace_bytes,
                                  moe_stream_t stream);
 
+/* Device workspace bytes moe_layer_forward needs for this shape (0 and an
+ * error message when the shape is invalid or outside its limits). */
+size_t moe_layer_workspace_size(const moe_shape* shape);
+
+/* The whole MoE block for a few tokens (1 <= T <= 8: one user, a small batch,
+ * a speculative draft) in two launches: rms_norm, router, top-k, the experts'
+ * FC1 + silu_and_mul + FC2, the weighted sum, and with a tail (moe_block_tail)
+ * the norm after the block, gate, residual and the next block's norm ([SM] 4.3:
+ * small batches want few launches).
+ *   x_hat, router, top-k, FFN and combine as in moe_ffn_forward, with the
+ *   arguments x, norm_w, router_w, router_logits, router_bias, w13, w2,
+ *   w13_scale, w2_scale, topk_ids_out, topk_w_out as described there; or with
+ *   topk_ids int32 [T, top_k] and topk_w fp32 [T, top_k] given as in
+ *   moe_ffn_forward_routed (exactly one of router_w, router_logits and
+ *   topk_ids; an expert id outside [0, E) is skipped and flagged, an id given
+ *   twice for a token counts with the sum of its weights).
+ *   wdtype: MOE_W_BF16, MOE_W_FP8_E4M3 or MOE_W_FP8_BLOCK.  Only the weights
+ *   are quantised here: x_hat and the intermediate are not rounded to E4M3 or
+ *   bf16 but enter the products with 16 bits of mantissa, products accumulate
+ *   in fp32, and the only other rounding is that of the outputs.  (So the
+ *   result is nearer to the exact one than moe_ffn_forward's, and not
+ *   bit-equal to it.)
+ *   tail NULL: out bf16 [T, H] = f (out_f32 must be 0).  Otherwise out [T, H]
+ *   (bf16, or fp32 when out_f32) = h, and the tail's other outputs.  The
+ *   block's own residual connection is tail->residual = x.
+ *   workspace >= moe_layer_workspace_size(shape) bytes, 256-byte aligned, not
+ *   used by other work while this call runs; nothing in it has to be
+ *   initialised or kept between calls.
+ * Weights must be finite for the experts a token uses: an infinite weight
+ * gives NaN in its output column of those tokens (other tokens are not
+ * affected).  The result does not depend on what else runs: sums are taken in
+ * a fixed order.
+ * T = 0 returns MOE_OK without looking at the tensor pointers.
+ * Errors: as moe_ffn_forward and moe_combine_norm; UNSUPPORTED_SHAPE for
+ * T > 8, H > 16384 or wdtype = MOE_W_NVFP4 (use moe_ffn_forward_nvfp4). */
+moe_status moe_layer_forward(const moe_shape* shape, const void* x, const void* norm_w,
+                             const float* router_w, const float* router_logits,
+                             const float* router_bias, const int32_t* topk_ids,
+                             const float* topk_w, const void* w13, const void* w2,
+                             const float* w13_scale, const float* w2_scale,
+                             const moe_block_tail* tail, void* out, int32_t out_f32,
+                             int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                             size_t workspace_bytes, moe_stream_t stream);
+
 /* ------------------------------------------------------------ the steps -- */
 
 /* rms_norm ([V100] "rewrite on torch::stable::Tensor"):

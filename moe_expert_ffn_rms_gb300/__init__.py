@@ -90,6 +90,10 @@ _SIGS = {
                                        _P, _P, _P, _SZ, _P]),
     "moe_silu_and_mul": (ctypes.c_int, [_P, _I32, _I32, _P, _P]),
     "moe_combine": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _I32, _I32, _P, _P]),
+    "moe_layer_workspace_size": (_SZ, [ctypes.POINTER(MoeShape)]),
+    "moe_layer_forward": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                         _P, _P, ctypes.POINTER(MoeBlockTail), _P, _I32, _P, _P, _P,
+                                         _SZ, _P]),
     "moe_combine_norm": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _I32, _I32,
                                         ctypes.POINTER(MoeBlockTail), _P, _I32, _P]),
     "moe_quantize_fp8_rows": (ctypes.c_int, [_P, ctypes.c_int64, _I32, _P, _P, _P]),
@@ -457,6 +461,64 @@ def moe_combine_norm(y, out, T, k, tail: BlockTail, row_of_pair=None, pair_order
                                 None if row_of_pair is None else row_of_pair.data_ptr(), T, k, H,
                                 tail.ref, out.data_ptr(), out.dtype == torch.float32,
                                 _stream(stream)))
+    return out
+
+
+def moe_layer_workspace_size(shape: MoeShape) -> int:
+    n = lib.moe_layer_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise MoeError(2, last_error())
+    return n
+
+
+def _opt(t, name, shape, dtypes, device):
+    if t is None:
+        return None
+    _check_tensor(t, name, shape, dtypes, device)
+    return t.data_ptr()
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def moe_layer_forward(shape: MoeShape, x, norm_w, w13, w2, out, workspace, router_w=None,
+                      router_logits=None, router_bias=None, topk_ids=None, topk_w=None,
+                      w13_scale=None, w2_scale=None, tail: BlockTail = None, topk_ids_out=None,
+                      topk_w_out=None, stream=None):
+    """The whole MoE block for 1..8 tokens in two launches: norm, router (or
+    given logits, or given topk_ids / topk_w), experts, weighted sum, and with a
+    tail (make_block_tail) what follows the block.  Tensors as in
+    moe_ffn_forward; out bf16 [T, H], or the type of the residual stream (bf16 /
+    fp32) with a tail; workspace of moe_layer_workspace_size(shape) bytes."""
+    T, H, E, I, k, wd = shape.T, shape.H, shape.E, shape.I, shape.top_k, shape.wdtype
+    device = x.device
+    _check_current(device)
+    wt = _BF16 if wd == W_BF16 else _CODES
+    if wd == W_FP8_BLOCK:
+        s13, s2 = (E, 2 * I // 128, H // 128), (E, H // 128, I // 128)
+    else:
+        s13, s2 = (E, 2 * I), (E, H)
+    _check_tensor(x, "x", (T, H), _BF16, device)
+    _check_tensor(norm_w, "norm_w", (H,), _BF16, device)
+    _check_tensor(w13, "w13", (E, 2 * I, H), wt, device)
+    _check_tensor(w2, "w2", (E, H, I), wt, device)
+    _check_tensor(out, "out", (T, H), _BF16 if tail is None else _FLOATS, device)
+    if workspace.device != device:
+        raise ValueError(f"workspace: on {workspace.device}, need {device}")
+    if tail is not None:
+        _check_tail(tail, T, H, device)
+    _check(lib.moe_layer_forward(
+        ctypes.byref(shape), x.data_ptr(), norm_w.data_ptr(),
+        _opt(router_w, "router_w", (H, E), _F32S, device),
+        _opt(router_logits, "router_logits", (T, E), _F32S, device),
+        _opt(router_bias, "router_bias", (E,), _F32S, device),
+        _opt(topk_ids, "topk_ids", (T, k), _I32S, device), _opt(topk_w, "topk_w", (T, k), _F32S, device),
+        w13.data_ptr(), w2.data_ptr(), _opt(w13_scale, "w13_scale", s13, _F32S, device),
+        _opt(w2_scale, "w2_scale", s2, _F32S, device), None if tail is None else tail.ref,
+        out.data_ptr(), out.dtype == torch.float32,
+        _opt(topk_ids_out, "topk_ids_out", (T, k), _I32S, device),
+        _opt(topk_w_out, "topk_w_out", (T, k), _F32S, device), _ws_ptr(workspace),
+        _ws_bytes(workspace), _stream(stream)))
     return out
 
 

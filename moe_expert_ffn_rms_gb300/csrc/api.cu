@@ -555,6 +555,18 @@ moe_status make_tail(const moe_block_tail* b, int T, int H, void* out, int out_f
   return MOE_OK;
 }
 
+// Limits of the few-token layer beside check_shape's.
+moe_status check_layer_shape(const moe_shape* s) {
+  moe_status rc = check_shape(s);
+  if (rc != MOE_OK) return rc;
+  MOE_REQ(s->T <= moe::kLayerMaxT, MOE_ERR_UNSUPPORTED_SHAPE, "T=%d > %d (moe_ffn_forward takes more)",
+          s->T, moe::kLayerMaxT);
+  MOE_REQ(s->H <= moe::kLayerMaxH, MOE_ERR_UNSUPPORTED_SHAPE, "H=%d > %d", s->H, moe::kLayerMaxH);
+  MOE_REQ(s->wdtype != MOE_W_NVFP4, MOE_ERR_UNSUPPORTED_SHAPE,
+          "NVFP4 weights run through moe_ffn_forward_nvfp4");
+  return MOE_OK;
+}
+
 }  // namespace
 
 namespace moe {
@@ -918,6 +930,77 @@ moe_status moe_combine(const void* y, int32_t y_bf16, int32_t y_pair_order,
   MOE_CUDA(moe::launch_combine(y, y_bf16 != 0, y_pair_order != 0, row_of_pair, T, k, H, out,
                                (cudaStream_t)stream),
            "combine launch");
+  return MOE_OK;
+}
+
+size_t moe_layer_workspace_size(const moe_shape* shape) {
+  if (check_layer_shape(shape) != MOE_OK) return 0;
+  return moe::layer_workspace_bytes(shape->T, shape->H, shape->E, shape->I, shape->top_k);
+}
+
+moe_status moe_layer_forward(const moe_shape* shape, const void* x, const void* norm_w,
+                             const float* router_w, const float* router_logits,
+                             const float* router_bias, const int32_t* topk_ids,
+                             const float* topk_w, const void* w13, const void* w2,
+                             const float* w13_scale, const float* w2_scale,
+                             const moe_block_tail* tail, void* out, int32_t out_f32,
+                             int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                             size_t workspace_bytes, moe_stream_t stream) {
+  moe_status rc = check_layer_shape(shape);
+  if (rc != MOE_OK) return rc;
+  if (shape->T == 0) return MOE_OK;
+  const bool f8 = shape->wdtype != MOE_W_BF16;
+  MOE_REQ(x && norm_w && w13 && w2 && out && workspace, MOE_ERR_INVALID_ARG,
+          "x, norm_w, w13, w2, out and workspace must be non-NULL");
+  MOE_REQ((router_w != nullptr) + (router_logits != nullptr) + (topk_ids != nullptr) == 1,
+          MOE_ERR_INVALID_ARG, "give exactly one of router_w, router_logits and topk_ids");
+  MOE_REQ((topk_ids != nullptr) == (topk_w != nullptr), MOE_ERR_INVALID_ARG,
+          "topk_ids and topk_w must both be given or both NULL");
+  MOE_REQ(!topk_ids || !router_bias, MOE_ERR_INVALID_ARG, "router_bias without a router");
+  MOE_REQ(!f8 || (w13_scale && w2_scale), MOE_ERR_INVALID_ARG, "FP8 weights need w13_scale and w2_scale");
+  MOE_REQ(aligned16(x) && aligned16(norm_w) && aligned16(w13) && aligned16(w2) && aligned16(out),
+          MOE_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  MOE_REQ(!f8 || (aligned16(w13_scale) && aligned16(w2_scale)), MOE_ERR_INVALID_ARG,
+          "FP8 weight scales must be 16-byte aligned");
+  for (const void* q : {(const void*)router_w, (const void*)router_logits, (const void*)router_bias,
+                        (const void*)topk_ids, (const void*)topk_w, (const void*)topk_ids_out,
+                        (const void*)topk_w_out})
+    MOE_REQ(((uintptr_t)q & 3u) == 0, MOE_ERR_INVALID_ARG, "misaligned router or routing pointer");
+  MOE_REQ(((uintptr_t)workspace & 255u) == 0, MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const size_t need = moe_layer_workspace_size(shape);
+  MOE_REQ(workspace_bytes >= need, MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes",
+          workspace_bytes, need);
+  MOE_REQ(tail || !out_f32, MOE_ERR_INVALID_ARG, "out is bf16 without a tail");
+  moe::TailP tp;
+  if (tail && (rc = make_tail(tail, shape->T, shape->H, out, out_f32, &tp)) != MOE_OK) return rc;
+  DevInfo* dev = nullptr;
+  if ((rc = device_info(&dev)) != MOE_OK) return rc;
+  moe::LayerArgs a{};
+  a.x = x;
+  a.norm_w = norm_w;
+  a.router_w = router_w;
+  a.logits = router_logits;
+  a.bias = router_bias;
+  a.ids_in = topk_ids;
+  a.tw_in = topk_w;
+  a.w13 = w13;
+  a.w2 = w2;
+  a.s13 = w13_scale;
+  a.s2 = w2_scale;
+  a.ids_out = topk_ids_out;
+  a.tw_out = topk_w_out;
+  a.out = out;
+  a.workspace = workspace;
+  a.T = shape->T;
+  a.H = shape->H;
+  a.E = shape->E;
+  a.I = shape->I;
+  a.k = shape->top_k;
+  a.fp8 = f8;
+  a.block_scales = shape->wdtype == MOE_W_FP8_BLOCK;
+  a.eps = shape->eps;
+  MOE_CUDA(moe::launch_layer(a, tail ? &tp : nullptr, dev->sms, dev->status, (cudaStream_t)stream),
+           "layer launch");
   return MOE_OK;
 }
 
