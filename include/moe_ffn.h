@@ -326,7 +326,8 @@ size_t moe_layer_workspace_size(const moe_shape* shape);
  * a fixed order.
  * T = 0 returns MOE_OK without looking at the tensor pointers.
  * Errors: as moe_ffn_forward and moe_combine_norm; UNSUPPORTED_SHAPE for
- * T > 8, H > 16384 or wdtype = MOE_W_NVFP4 (use moe_ffn_forward_nvfp4). */
+ * T > 8, H > 16384, 2 * I * H >= 2^31 or wdtype = MOE_W_NVFP4 (use
+ * moe_ffn_forward_nvfp4). */
 moe_status moe_layer_forward(const moe_shape* shape, const void* x, const void* norm_w,
                              const float* router_w, const float* router_logits,
                              const float* router_bias, const int32_t* topk_ids,

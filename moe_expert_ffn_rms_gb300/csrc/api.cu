@@ -564,6 +564,9 @@ moe_status check_layer_shape(const moe_shape* s) {
   MOE_REQ(s->H <= moe::kLayerMaxH, MOE_ERR_UNSUPPORTED_SHAPE, "H=%d > %d", s->H, moe::kLayerMaxH);
   MOE_REQ(s->wdtype != MOE_W_NVFP4, MOE_ERR_UNSUPPORTED_SHAPE,
           "NVFP4 weights run through moe_ffn_forward_nvfp4");
+  // the kernels' offsets within one expert's matrix are 32-bit
+  MOE_REQ((int64_t)2 * s->I * s->H < (int64_t)1 << 31, MOE_ERR_UNSUPPORTED_SHAPE,
+          "H=%d, I=%d: an expert's matrix is too large", s->H, s->I);
   return MOE_OK;
 }
 

@@ -26,12 +26,14 @@
 // Products: the weights are the 16 x 16 operand of m16n8k16 bf16 MMAs, the (at
 // most 8) tokens the 8 columns.  Activations enter as two bf16 terms hi + lo
 // (16 bits of mantissa), so neither x_hat nor the intermediate is rounded to
-// bf16; accumulation is fp32.  A warp reads its own weights: each lane copies
+// bf16; accumulation is fp32.  A warp reads its own operands: each lane copies
 // exactly the 16-byte pieces it will feed to its MMAs into its own part of
-// shared memory (cp.async, kStages steps ahead) and reads them back, so the
+// shared memory (cp.async, a few steps ahead) and reads them back, so the
 // stream needs no barrier, and the first W2 pieces are already on their way
 // while the CTA waits for the other CTAs' FC1 tiles.  The order of the K
 // elements inside a piece is the same for both operands and therefore free.
+// The activations go the same way as the weights: a plain load of them would
+// wait behind the copies in flight (4 us of them with 160 KB per SM).
 //
 // mma.sync and not tcgen05: at 8 columns the tensor work is 1/16 of what the
 // legacy instruction sustains at this memory rate, a fragment load straight from
@@ -47,9 +49,9 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreadsL = 32 * kWarps;
-constexpr int kStages = 6;                      // steps in flight per warp
-constexpr int kStepBytes = 4096;                // per warp: 2 tiles x 2 row halves x 2 K blocks x 512 B
-constexpr int kRingBytes = kWarps * kStages * kStepBytes;
+constexpr int kMaxStages = 6;                   // steps in flight per warp, at most
+constexpr int kStepA = 4096;                    // weights: 2 tiles x 2 row halves x 2 K blocks x 512 B
+constexpr int kRingBytes = 200 << 10;           // shared memory of the CTA's copies
 constexpr int kRedFloats = kWarps * 2 * 16 * 8; // partial sums of two row tiles
 constexpr int kMaxPairs = kLayerMaxT * kMaxTopK;
 
@@ -79,9 +81,13 @@ struct LayerP {
 
 // ------------------------------------------------------------------ launch 1 --
 // Grid (kLayerChunks, groups of 32 experts): K chunk c, experts 32y .. 32y+31.
-__global__ void __launch_bounds__(kThreadsL) layer_route_kernel(const LayerP p) {
+// Latency is all there is: each warp has its rows of W_r (16 at H = 4096) on
+// their way before it waits for anything.
+constexpr int kRouteWarps = 16;
+
+__global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const LayerP p) {
   extern __shared__ __align__(16) float xw[];  // [rows of the chunk][8 tokens]
-  __shared__ float red[kWarps][kLayerMaxT][32];
+  __shared__ float red[kRouteWarps][kLayerMaxT][32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -91,62 +97,55 @@ __global__ void __launch_bounds__(kThreadsL) layer_route_kernel(const LayerP p) 
   if (c == 0 && blockIdx.y == 0 && tid < 4) p.ctr[tid] = 0;
   const int e = blockIdx.y * 32 + lane;
   const float* wr = p.router_w ? p.router_w + (size_t)k0 * p.E + e : nullptr;
-  constexpr int U = 8;
+  constexpr int U = 16;
   float wv[U];
-  if (wr) {  // the first rows of W_r are on their way while x is prepared
+  if (wr) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = warp + kWarps * u;
+      const int r = warp + kRouteWarps * u;
       wv[u] = (r < rows && e < p.E) ? wr[(size_t)r * p.E] : 0.f;
     }
   }
-  // warp t: token t
-  float ss = 0.f;
-  for (int v = lane; v < b1 - b0; v += 32) {
-    float a[8], hi[8], lo[8];
-    if (warp < p.T) {
-      float w[8];
-      load8(p.x, false, (size_t)warp * p.H + k0 + v * 8, a);
-      load8(p.norm_w, false, k0 + v * 8, w);
+  // warp t: token t (zeros beyond the last)
+  if (warp < kLayerMaxT) {
+    float ss = 0.f;
+    for (int v = lane; v < b1 - b0; v += 32) {
+      float a[8] = {}, hi[8], lo[8];
+      if (warp < p.T) {
+        float w[8];
+        load8(p.x, false, (size_t)warp * p.H + k0 + v * 8, a);
+        load8(p.norm_w, false, k0 + v * 8, w);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        ss = fmaf(a[q], a[q], ss);
-        a[q] *= w[q];
-        hi[q] = bf16_round_f(a[q]);
-        lo[q] = a[q] - hi[q];
+        for (int q = 0; q < 8; ++q) {
+          ss = fmaf(a[q], a[q], ss);
+          a[q] *= w[q];
+          hi[q] = bf16_round_f(a[q]);
+          lo[q] = a[q] - hi[q];
+        }
+        if (blockIdx.y == 0) {
+          store8_bf16(p.hi + (size_t)warp * p.H + k0 + v * 8, hi);
+          store8_bf16(p.lo + (size_t)warp * p.H + k0 + v * 8, lo);
+        }
       }
-      if (blockIdx.y == 0) {
-        store8_bf16(p.hi + (size_t)warp * p.H + k0 + v * 8, hi);
-        store8_bf16(p.lo + (size_t)warp * p.H + k0 + v * 8, lo);
+      if (wr) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) xw[(v * 8 + q) * kLayerMaxT + warp] = a[q];
       }
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) a[q] = 0.f;
     }
-    if (wr) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) xw[(v * 8 + q) * kLayerMaxT + warp] = a[q];
+    if (blockIdx.y == 0) {
+      ss = warp_sum(ss);
+      if (lane == 0 && warp < p.T) p.ssq[c * kLayerMaxT + warp] = ss;
     }
-  }
-  if (blockIdx.y == 0) {
-    ss = warp_sum(ss);
-    if (lane == 0 && warp < p.T) p.ssq[c * kLayerMaxT + warp] = ss;
   }
   if (!wr) return;
   __syncthreads();
   float acc[kLayerMaxT];
 #pragma unroll
   for (int t = 0; t < kLayerMaxT; ++t) acc[t] = 0.f;
-  for (int r0 = warp; r0 < rows; r0 += kWarps * U) {
-    float nx[U];
+  for (int r0 = warp; r0 < rows; r0 += kRouteWarps * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = r0 + kWarps * (U + u);
-      nx[u] = (r < rows && e < p.E) ? wr[(size_t)r * p.E] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + kWarps * u;
+      const int r = r0 + kRouteWarps * u;
       if (r < rows) {
         const float4 a = *reinterpret_cast<const float4*>(&xw[r * kLayerMaxT]);
         const float4 b = *reinterpret_cast<const float4*>(&xw[r * kLayerMaxT + 4]);
@@ -159,7 +158,8 @@ __global__ void __launch_bounds__(kThreadsL) layer_route_kernel(const LayerP p) 
         acc[6] = fmaf(b.z, wv[u], acc[6]);
         acc[7] = fmaf(b.w, wv[u], acc[7]);
       }
-      wv[u] = nx[u];
+      const int rn = r + kRouteWarps * U;
+      wv[u] = (rn < rows && e < p.E) ? wr[(size_t)rn * p.E] : 0.f;
     }
   }
 #pragma unroll
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreadsL) layer_route_kernel(const LayerP p) 
   if (warp < p.T && e < p.E) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += red[w][warp][lane];
+    for (int w = 0; w < kRouteWarps; ++w) s += red[w][warp][lane];
     p.part[((size_t)c * p.T + warp) * p.E + e] = s;
   }
 }
@@ -177,16 +177,19 @@ __global__ void __launch_bounds__(kThreadsL) layer_route_kernel(const LayerP p) 
 MOE_DEV void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+MOE_DEV void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 MOE_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most n of the newest groups are in flight.
-MOE_DEV void cp_wait(int n) {
+// Waits for the oldest of n groups in flight.
+MOE_DEV void cp_wait_oldest(int n) {
   switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
   }
 }
 
@@ -208,36 +211,34 @@ MOE_DEV void e4m3x4_bf16(uint32_t q, uint32_t& lo, uint32_t& hi) {
   hi = pack2_bf16(fb.x, fb.y);
 }
 
-// A lane's activations for one step: two K blocks of EPC elements in two bf16
-// terms, for the token of the lane's column.
-template <int EPC>
-struct StepB {
-  uint4 hi[2][EPC / 8], lo[2][EPC / 8];
-  float s[2][2];  // FP8: weight scales of the lane's four rows
-};
-
 struct LayerSmem {
   int32_t ids[kLayerMaxT][kMaxTopK];
   float w[kLayerMaxT][kMaxTopK];
   float r[kLayerMaxT];
+  unsigned used[kMaxExperts];  // tokens of each expert, as a bit mask
+  int slot[kMaxExperts];       // its place among the active experts
   int expert[kMaxPairs];
   unsigned mask[kMaxPairs];
   int pair[kMaxPairs][kLayerMaxT];
   float wt[kMaxPairs][kLayerMaxT];
   int warp_cnt[kWarps];
   int claim[4];
-  int n_act;
   int flag;
   float sum[kWarps];
 };
 
+// Top-k of one token by one warp with the results of warp_topk (common.cuh):
+// larger logit first, ties to the lower expert, NaN as -inf, softmax over the
+// selected (summed in slot order), weights 0 when all of them are -inf.  Here
+// the arg-max is two warp reductions of integers: the logits' bits in an
+// order-preserving form, then the lowest expert that has the maximum.
 template <int PER>
 MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float r, LayerSmem* sm) {
-  float v[PER];
+  unsigned key[PER];  // 0: taken or beyond E
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 32 * i;
-    v[i] = -INFINITY;
+    key[i] = 0;
     if (e < p.E) {
       float z = 0.f;
       if (p.logits) {
@@ -247,37 +248,97 @@ MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float r, LayerSmem* sm
         for (int c = 0; c < kLayerChunks; ++c) z += __ldcg(&p.part[((size_t)c * p.T + t) * p.E + e]);
         z *= r;
       }
-      v[i] = p.bias ? z + p.bias[e] : z;
+      if (p.bias) z += p.bias[e];
+      z = (z != z) ? -INFINITY : z + 0.0f;  // (-0 counts as 0)
+      const unsigned u = __float_as_uint(z);
+      key[i] = (u & 0x80000000u) ? ~u : u | 0x80000000u;  // -inf: 0x007fffff
     }
   }
-  warp_topk<PER>(v, p.E, p.k, lane, sm->ids[t], sm->w[t]);
+  float sel = -INFINITY;
+  int sel_e = 0;
+  for (int j = 0; j < p.k; ++j) {
+    unsigned m = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = max(m, key[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    unsigned at = 0xffffffffu;
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i)
+      if (key[i] == m) at = lane + 32 * i;
+    at = __reduce_min_sync(0xffffffffu, at);
+    if ((at & 31u) == (unsigned)lane) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if ((int)(at >> 5) == i) key[i] = 0;
+    }
+    if (lane == j) {
+      sel = __uint_as_float((m & 0x80000000u) ? m & 0x7fffffffu : ~m);
+      sel_e = (int)at;
+    }
+  }
+  const float top = __shfl_sync(0xffffffffu, sel, 0);
+  const bool some = top > -INFINITY;
+  const float e = (some && lane < p.k) ? expf(sel - top) : 0.f;
+  float s = 0.f;
+  for (int j = 0; j < p.k; ++j) s += __shfl_sync(0xffffffffu, e, j);
+  if (lane < p.k) {
+    sm->ids[t][lane] = sel_e;
+    sm->w[t][lane] = some ? e / s : 0.f;
+  }
 }
 
-// FP8: E4M3 weights with scales, one per (row >> rs, K step * ks).
+// Per-warp stage: weights [2 tiles][2 row halves][2 K blocks][32 lanes] of 16
+// bytes; activations [2 K blocks][hi, lo][pieces][T tokens][4 lanes] of 16 bytes;
+// FP8: the scales of the 32 rows.
+struct LayerRing {
+  int stage, depth;  // bytes, steps
+};
+__host__ __device__ inline LayerRing layer_ring(int T, bool fp8) {
+  LayerRing r;
+  r.stage = kStepA + T * (fp8 ? 512 : 256) + (fp8 ? 128 : 0);
+  r.depth = kRingBytes / (kWarps * r.stage);
+  if (r.depth > kMaxStages) r.depth = kMaxStages;
+  return r;
+}
+
+// FP8: E4M3 weights, one scale per (row >> rs) and K step * ks.
 template <bool FP8>
 __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
                                                                      int has_tail) {
   constexpr int EB = FP8 ? 1 : 2;   // bytes per weight
   constexpr int EPC = 16 / EB;      // weights per 16-byte piece
   constexpr int KE = 64 / EB;       // K elements of a K block (64 bytes of a row)
+  constexpr int Q = EPC / 8;        // 16-byte pieces of activations per K block and term
   extern __shared__ __align__(128) unsigned char ring_all[];
   __shared__ LayerSmem sm;
   __shared__ __align__(16) float red[2][kRedFloats];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, tq = lane & 3;  // MMA fragment row / column group, K group
+  const int g = lane >> 2, tq = lane & 3;  // MMA fragment row / column, K group
   const int T = p.T, H = p.H, E = p.E, I = p.I, k = p.k;
+  sm.used[tid] = 0;
   pdl_trigger();
+  __syncthreads();
   pdl_wait();
 
   // ---- routing (every CTA by itself; warp t: token t)
   if (tid == 0) {
     sm.claim[0] = atomicAdd(&p.ctr[0], 1);
     sm.claim[1] = atomicAdd(&p.ctr[0], 1);
-    sm.n_act = 0;
+  }
+  if (has_tail) {  // what the tail will read is brought to L2 meanwhile
+    const int64_t line = (int64_t)blockIdx.x * kThreadsL + tid;
+    auto warm = [&](const void* q, int64_t bytes) {
+      if (q && line * 128 < bytes)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(q) + line * 128));
+    };
+    warm(tail.residual, (int64_t)T * H * (tail.res_f32 ? 4 : 2));
+    warm(tail.post_w, 2 * H);
+    warm(tail.next_w, 2 * H);
+    if (tail.gate_cols == H && tail.gate_rows == 1) warm(tail.gate, (int64_t)H * (tail.gate_f32 ? 4 : 2));
   }
   if (warp < T) {
-    float ss = lane < kLayerChunks ? __ldcg(&p.ssq[lane * kLayerMaxT + warp]) : 0.f;
+    const float ss = lane < kLayerChunks ? __ldcg(&p.ssq[lane * kLayerMaxT + warp]) : 0.f;
     const float r = 1.0f / sqrtf(warp_sum(ss) / (float)H + p.eps);
     if (lane == 0) sm.r[warp] = r;
     if (p.ids_in) {
@@ -294,19 +355,20 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     } else {
       layer_topk<8>(p, warp, lane, r, &sm);
     }
+    // the token's experts: lane j, its j-th
+    __syncwarp();
+    const int id = lane < k ? sm.ids[warp][lane] : -1;
+    if (id >= 0 && id < E) atomicOr(&sm.used[id], 1u << warp);
+    if (blockIdx.x == 0 && lane < k) {
+      if (p.ids_out) p.ids_out[warp * k + lane] = id;
+      if (p.tw_out) p.tw_out[warp * k + lane] = sm.w[warp][lane];
+      if (id < 0 || id >= E) flag_status(p.status, MOE_ERR_INVALID_ARG);
+    }
   }
   __syncthreads();
-  if (blockIdx.x == 0 && tid < T * k) {
-    const int id = sm.ids[tid / k][tid % k];
-    if (p.ids_out) p.ids_out[tid] = id;
-    if (p.tw_out) p.tw_out[tid] = sm.w[tid / k][tid % k];
-    if (id < 0 || id >= E) flag_status(p.status, MOE_ERR_INVALID_ARG);
-  }
   // active experts in ascending order (thread e: expert e; E <= 256)
   {
-    unsigned mask = 0;
-    for (int i = 0; i < T * k; ++i)
-      if (tid < E && sm.ids[i / k][i % k] == tid) mask |= 1u << (i / k);
+    const unsigned mask = sm.used[tid];
     const unsigned act = __ballot_sync(0xffffffffu, mask != 0);
     if (lane == 0) sm.warp_cnt[warp] = __popc(act);
     __syncthreads();
@@ -315,27 +377,33 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       for (int w = 0; w < warp; ++w) at += sm.warp_cnt[w];
       sm.expert[at] = tid;
       sm.mask[at] = mask;
-      for (int t = 0; t < kLayerMaxT; ++t) {
-        int pr = -1;
-        float w = 0.f;
-        if ((mask >> t) & 1u)
-          for (int j = 0; j < k; ++j)
-            if (sm.ids[t][j] == tid) {  // (an expert given twice counts with both weights)
-              if (pr < 0) pr = t * k + j;
-              w += sm.w[t][j];
-            }
-        sm.pair[at][t] = pr;
-        sm.wt[at][t] = w;
-      }
+      sm.slot[tid] = at;
+      *reinterpret_cast<int4*>(&sm.pair[at][0]) = make_int4(-1, -1, -1, -1);
+      *reinterpret_cast<int4*>(&sm.pair[at][4]) = make_int4(-1, -1, -1, -1);
     }
-    if (tid == 0) {
-      int n = 0;
-      for (int w = 0; w < kWarps; ++w) n += sm.warp_cnt[w];
-      sm.n_act = n;
+    __syncthreads();
+    if (warp < T && lane < k) {
+      const int id = sm.ids[warp][lane];
+      if (id >= 0 && id < E) {
+        // an expert given twice counts once, with the sum of its weights
+        bool first = true;
+        float w = 0.f;
+        for (int j = 0; j < k; ++j)
+          if (sm.ids[warp][j] == id) {
+            if (j < lane) first = false;
+            w += sm.w[warp][j];
+          }
+        if (first) {
+          sm.pair[sm.slot[id]][warp] = warp * k + lane;
+          sm.wt[sm.slot[id]][warp] = w;
+        }
+      }
     }
     __syncthreads();
   }
-  const int n_act = sm.n_act;
+  int n_act = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) n_act += sm.warp_cnt[w];
 
   // ---- work: FC1 row tiles (8 gate + 8 up rows) in claims of two, the last
   // ones (one per CTA) single; FC2 output rows [n0, n1) in units of 32
@@ -346,171 +414,209 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   const int claims = pairs + singles;
   const int n0 = (int)((int64_t)blockIdx.x * H / gridDim.x);
   const int n1 = (int)((int64_t)(blockIdx.x + 1) * H / gridDim.x);
-  const size_t rb1 = (size_t)H * EB, rb2 = (size_t)I * EB;  // bytes of a weight row
+  const uint32_t rb1 = (uint32_t)H * EB, rb2 = (uint32_t)I * EB;  // bytes of a weight row
   const int S1 = (int)((rb1 + 127) >> 7), S2 = (int)((rb2 + 127) >> 7);  // 128-byte steps of a row
   const int kb1 = (int)(rb1 >> 6), kb2 = (int)(rb2 >> 6);                // 64-byte K blocks
-  const unsigned char* w13 = static_cast<const unsigned char*>(p.w13);
-  const unsigned char* w2 = static_cast<const unsigned char*>(p.w2);
-
-  unsigned char* ring = ring_all + warp * (kStages * kStepBytes);
-  const uint32_t ring_u = ptx::smem_u32(ring) + lane * 16;
-
-  // ---- producer: the warp's steps in the order it will use them
-  int pn = 0;           // FC1 claim being produced (index into this CTA's claims)
-  int p_step = warp;    // next step of it
-  int pu = 0, pa = 0;   // FC2 unit and active expert being produced
-  bool p_fc2 = false;
-  int known = 1;        // newest claim index published to this warp
-  int issued = 0, used = 0;
   auto claim_tile = [&](int c) { return c < pairs ? 2 * c : c + pairs; };
 
-  // Copies the next step if it is known; false when nothing can be copied yet.
-  auto produce = [&]() -> bool {
+  const LayerRing rg = layer_ring(T, FP8);
+  unsigned char* ring = ring_all + warp * (rg.depth * rg.stage);
+  const uint32_t ring_u = ptx::smem_u32(ring);
+  const uint32_t ring_end = (uint32_t)rg.depth * rg.stage;
+  const bool col = g < T;                       // this lane's column is a token
+  const uint32_t b_lane = kStepA + (g * 4 + tq) * 16;
+  const uint32_t b_piece = T * 64;              // bytes of one piece of all tokens
+  const uint32_t s_at = kStepA + 4 * Q * b_piece;
+  // block scales: one row of the scale matrix per 128 weight rows, one column
+  // per K step; channel scales: one per row
+  const int rs = p.block_scales ? 7 : 0;
+  const int kg1 = p.block_scales ? H >> 7 : 1, kg2 = p.block_scales ? I >> 7 : 1;
+  const int ks = p.block_scales ? 1 : 0;
+
+  // ---- producer: the warp's steps in the order it will use them.  A segment is
+  // the warp's steps of one FC1 claim, or of one expert for one FC2 unit; step
+  // q of all experts' steps goes to warp q mod 8.
+  const unsigned char* p_src = nullptr;  // this lane's first row at the next step
+  uint32_t p_ts = 0, p_hs = 0;           // to the second tile, to a tile's lower 8 rows (bytes)
+  unsigned p_ok = 0;                     // bit 2 * tile + half: this lane's row is wanted
+  const bf16* p_b = nullptr;             // hi term of this lane's token at the next step
+  int64_t p_lo = 0;                      // to the lo term (elements)
+  bool p_on = false;                     // the lane's token uses the expert (and may be read)
+  const float* p_sc = nullptr;           // FP8: scale of row `lane` of the step's 32 rows
+  bool p_sok = false;
+  int p_step = 0, p_end = 0, p_kb = 0;   // next step, steps and K blocks of a row
+  int pn = -1, pu = 0, pa = -1;          // claim; FC2 unit and active expert
+  int known = 1;                         // newest claim index published to this warp
+  bool p_fc2 = false, fc1_done = false;
+  int flying = 0;                        // steps issued and not yet used
+  int ready = 0;                         // of these, steps known to have arrived
+  uint32_t p_at = 0, c_at = 0;           // ring offsets of the next step to issue / to use
+
+  // Moves to the next segment that has a step for this warp.
+  auto next_segment = [&]() -> bool {
     while (!p_fc2) {
-      if (pn > known) return false;
-      if (sm.claim[pn & 3] >= claims) {
+      if (pn + 1 > known) return false;
+      const int c = sm.claim[(pn + 1) & 3];
+      if (c >= claims) {
         p_fc2 = true;
-        p_step = warp;
-      } else if (p_step >= S1) {
-        ++pn;
-        p_step = warp;
-      } else {
         break;
       }
-    }
-    const unsigned char* src;
-    size_t ts, hs;       // byte strides of the second tile and of a tile's lower 8 rows
-    unsigned ok;         // bit 2*tile + half: this lane's row is wanted
-    bool two;            // the step's second K block exists
-    if (!p_fc2) {
-      const int c = sm.claim[pn & 3];
-      const int tile = claim_tile(c);
-      const int a = tile / tiles_e;
-      const int row = (tile - a * tiles_e) * 8 + g;
-      src = w13 + ((size_t)sm.expert[a] * 2 * I + row) * rb1;
-      ts = 8 * rb1;
-      hs = (size_t)I * rb1;
-      ok = c < pairs ? 15u : 3u;
-      two = 2 * p_step + 1 < kb1;
-    } else {
-      while (p_step >= S2) {
-        p_step -= S2;
-        ++pa;
+      ++pn;
+      if (warp >= S1) continue;
+      const int tile = claim_tile(c), a = tile / tiles_e;
+      const int i0 = (tile - a * tiles_e) * 8;
+      const int e = sm.expert[a];
+      p_step = warp;
+      p_end = S1;
+      p_kb = kb1;
+      p_src = static_cast<const unsigned char*>(p.w13) + ((size_t)e * 2 * I + i0 + g) * rb1 + p_step * 128 +
+              tq * 16;
+      p_ts = 8 * rb1;
+      p_hs = (uint32_t)I * rb1;
+      p_ok = c < pairs ? 15u : 3u;
+      p_on = col && ((sm.mask[a] >> g) & 1u);
+      p_b = p.hi + (size_t)(p_on ? g : 0) * H + p_step * 2 * KE + tq * EPC;
+      p_lo = p.lo - p.hi;
+      if constexpr (FP8) {
+        const int row = i0 + (lane & 7) + ((lane & 8) ? I : 0) + ((lane & 16) ? 8 : 0);
+        p_sok = c < pairs || lane < 16;
+        p_sc = p.s13 + ((size_t)e * (2 * I >> rs) + ((p_sok ? row : 0) >> rs)) * kg1 + p_step * ks;
       }
-      while (pa >= n_act) {  // next unit of output rows
-        if (n_act == 0 || n0 + 32 * (pu + 1) >= n1) {
-          pa = n_act;
-          return false;
-        }
+      return true;
+    }
+    while (n0 + 32 * pu < n1) {
+      if (++pa >= n_act) {
+        if (n_act == 0) return false;
+        pa = -1;
         ++pu;
-        pa = 0;
-        p_step = warp;
-        while (p_step >= S2) {
-          p_step -= S2;
-          ++pa;
+        continue;
+      }
+      p_step = (warp - pa * S2) & (kWarps - 1);
+      if (p_step >= S2) continue;
+      const int row0 = n0 + 32 * pu, e = sm.expert[pa];
+      p_end = S2;
+      p_kb = kb2;
+      p_src = static_cast<const unsigned char*>(p.w2) + ((size_t)e * H + row0 + g) * rb2 + p_step * 128 +
+              tq * 16;
+      p_ts = 16 * rb2;
+      p_hs = 8 * rb2;
+      p_ok = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p_ok |= (row0 + g + 8 * i < n1 ? 1u : 0u) << i;
+      const int pr = sm.pair[pa][g];
+      p_on = pr >= 0 && fc1_done;
+      p_b = p.act_hi + (size_t)(pr >= 0 ? pr : 0) * I + p_step * 2 * KE + tq * EPC;
+      p_lo = p.act_lo - p.act_hi;
+      if constexpr (FP8) {
+        p_sok = row0 + lane < n1;
+        p_sc = p.s2 + ((size_t)e * (H >> rs) + ((p_sok ? row0 + lane : 0) >> rs)) * kg2 + p_step * ks;
+      }
+      return true;
+    }
+    p_end = 0;
+    return false;
+  };
+  // This lane's activations of a step into the stage at ring offset `at`.
+  auto copy_b = [&](uint32_t at, const bf16* b, int64_t lo, bool two) {
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if (FP8 && kb && !two) break;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const bf16* src = b + kb * KE + q * 8;
+        const uint32_t dst = ring_u + at + b_lane + (kb * 2 * Q + q) * b_piece;
+        cp_async16(dst, src);
+        cp_async16(dst + Q * b_piece, src + lo);
+      }
+    }
+  };
+  // Keeps the ring full as far as the steps are known.
+  auto top_up = [&]() {
+    while (flying < rg.depth) {
+      if (p_step >= p_end && !next_segment()) break;
+      const uint32_t dst = ring_u + p_at + lane * 16;
+      const bool two = !FP8 || 2 * p_step + 1 < p_kb;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((p_ok >> i) & 1u) {
+          const unsigned char* src = p_src + (i >> 1) * p_ts + (i & 1) * p_hs;
+          cp_async16(dst + (2 * i) * 512, src);
+          if (two) cp_async16(dst + (2 * i + 1) * 512, src + 64);
         }
       }
-      const int row = n0 + 32 * pu + g;
-      src = w2 + ((size_t)sm.expert[pa] * H + row) * rb2;
-      ts = 16 * rb2;
-      hs = 8 * rb2;
-      ok = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ok |= (row + 8 * i < n1 ? 1u : 0u) << i;
-      two = 2 * p_step + 1 < kb2;
-    }
-    src += (size_t)p_step * 128 + tq * 16;
-    const uint32_t dst = ring_u + (issued % kStages) * kStepBytes;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if ((ok >> i) & 1u) {
-        const unsigned char* s = src + (i >> 1) * ts + (i & 1) * hs;
-        cp_async16(dst + (2 * i) * 512, s);
-        if (two) cp_async16(dst + (2 * i + 1) * 512, s + 64);
-      }
-    }
-    cp_commit();
-    ++issued;
-    p_step += kWarps;
-    return true;
-  };
-  auto top_up = [&]() {
-    while (issued - used < kStages && produce()) {
+      if (p_on) copy_b(p_at, p_b, p_lo, two);
+      if (FP8 && p_sok) cp_async4(ring_u + p_at + s_at + lane * 4, p_sc);
+      cp_commit();
+      ++flying;
+      p_at += rg.stage;
+      if (p_at == ring_end) p_at = 0;
+      p_src += kWarps * 128;
+      p_b += kWarps * 2 * KE;
+      p_sc += kWarps * ks;
+      p_step += kWarps;
     }
   };
 
-  // One step: acc[tile] += weights of the step * activations b.
-  auto multiply = [&](float (&acc)[2][4], const StepB<EPC>& b, bool second_tile, bool two) {
-    cp_wait(issued - used - 1);
-    const uint4* sp = reinterpret_cast<const uint4*>(ring + (used % kStages) * kStepBytes) + lane;
+  // One step: h/l[tile] += weights of the step * the hi / lo activations.  What
+  // a lane did not copy (rows that are not wanted, tokens that do not use the
+  // expert) is whatever the ring held: it only reaches sums that are not used.
+  struct Acc {
+    float h[2][4], l[2][4];
+  };
+  auto clear = [](Acc& a) {
 #pragma unroll
-    for (int tl = 0; tl < 2; ++tl) {
-      if (tl && !second_tile) break;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (kb && !two) break;
+      for (int j = 0; j < 4; ++j) a.h[i][j] = a.l[i][j] = 0.f;
+  };
+  auto multiply = [&](Acc& acc, float (&sc)[4], bool second_tile, bool two) {
+    if (ready > 0) --ready;
+    else cp_wait_oldest(flying);
+    const unsigned char* st = ring + c_at;
+    const uint4* sp = reinterpret_cast<const uint4*>(st) + lane;
+    // (columns beyond the last token read a token's piece again; they are not used)
+    const unsigned char* bp = st + (col ? b_lane : (uint32_t)kStepA + tq * 16);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if (FP8 && kb && !two) break;
+      uint4 h[Q], l[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        h[q] = *reinterpret_cast<const uint4*>(bp + (kb * 2 * Q + q) * b_piece);
+        l[q] = *reinterpret_cast<const uint4*>(bp + (kb * 2 * Q + Q + q) * b_piece);
+      }
+#pragma unroll
+      for (int tl = 0; tl < 2; ++tl) {
+        if (tl && !second_tile) break;
         const uint4 u0 = sp[((tl * 2 + 0) * 2 + kb) * 32], u1 = sp[((tl * 2 + 1) * 2 + kb) * 32];
-        const uint32_t q0[4] = {u0.x, u0.y, u0.z, u0.w}, q1[4] = {u1.x, u1.y, u1.z, u1.w};
         if constexpr (!FP8) {
-          const uint4 h = b.hi[kb][0], l = b.lo[kb][0];
-          mma_16816(acc[tl], q0[0], q1[0], q0[1], q1[1], h.x, h.y);
-          mma_16816(acc[tl], q0[0], q1[0], q0[1], q1[1], l.x, l.y);
-          mma_16816(acc[tl], q0[2], q1[2], q0[3], q1[3], h.z, h.w);
-          mma_16816(acc[tl], q0[2], q1[2], q0[3], q1[3], l.z, l.w);
+          mma_16816(acc.h[tl], u0.x, u1.x, u0.y, u1.y, h[0].x, h[0].y);
+          mma_16816(acc.l[tl], u0.x, u1.x, u0.y, u1.y, l[0].x, l[0].y);
+          mma_16816(acc.h[tl], u0.z, u1.z, u0.w, u1.w, h[0].z, h[0].w);
+          mma_16816(acc.l[tl], u0.z, u1.z, u0.w, u1.w, l[0].z, l[0].w);
         } else {
+          const uint32_t q0[4] = {u0.x, u0.y, u0.z, u0.w}, q1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             uint32_t a0, a1, a2, a3;
             e4m3x4_bf16(q0[m], a0, a2);
             e4m3x4_bf16(q1[m], a1, a3);
-            const uint4 h = b.hi[kb][m >> 1], l = b.lo[kb][m >> 1];
-            mma_16816(acc[tl], a0, a1, a2, a3, (m & 1) ? h.z : h.x, (m & 1) ? h.w : h.y);
-            mma_16816(acc[tl], a0, a1, a2, a3, (m & 1) ? l.z : l.x, (m & 1) ? l.w : l.y);
+            const uint4 hm = h[(m >> 1) % Q], lm = l[(m >> 1) % Q];
+            mma_16816(acc.h[tl], a0, a1, a2, a3, (m & 1) ? hm.z : hm.x, (m & 1) ? hm.w : hm.y);
+            mma_16816(acc.l[tl], a0, a1, a2, a3, (m & 1) ? lm.z : lm.x, (m & 1) ? lm.w : lm.y);
           }
         }
       }
     }
-    ++used;
-  };
-  // Activations of K blocks 2*step, 2*step + 1 from row `row` (negative: zeros).
-  auto load_b = [&](StepB<EPC>& b, const bf16* hi, const bf16* lo, int64_t row, int K, int step, int nkb) {
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-      for (int q = 0; q < EPC / 8; ++q) {
-        b.hi[kb][q] = b.lo[kb][q] = make_uint4(0u, 0u, 0u, 0u);
-        if (row >= 0 && 2 * step + kb < nkb) {
-          const size_t at = (size_t)row * K + (size_t)(2 * step + kb) * KE + tq * EPC + q * 8;
-          b.hi[kb][q] = __ldcg(reinterpret_cast<const uint4*>(hi + at));
-          b.lo[kb][q] = __ldcg(reinterpret_cast<const uint4*>(lo + at));
-        }
-      }
-    }
-  };
-  // FP8 scales of the lane's rows row, row + hs (and a tile further, + ts) at a step.
-  auto load_s = [&](StepB<EPC>& b, const float* s, int e, int N, int K, int row, int ts, int hs, unsigned ok,
-                    int step) {
     if constexpr (FP8) {
+      __syncwarp();  // the scales were copied by other lanes of the warp
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rw = row + (i >> 1) * ts + (i & 1) * hs;
-        b.s[i >> 1][i & 1] = 0.f;
-        if ((ok >> i) & 1u)
-          b.s[i >> 1][i & 1] = p.block_scales
-                                   ? s[((size_t)e * (N >> 7) + (rw >> 7)) * (K >> 7) + step]
-                                   : s[(size_t)e * N + rw];
-      }
+      for (int i = 0; i < 4; ++i) sc[i] = *reinterpret_cast<const float*>(st + s_at + (g + 8 * i) * 4);
+      __syncwarp();  // and are overwritten by them once all have read
     }
-  };
-  // tot += scale * acc for the tokens in mask; a column outside it adds nothing
-  // (not 0 times a weight that may not be finite).
-  auto fold = [&](float (&tot)[2][4], const float (&acc)[2][4], const StepB<EPC>& b, unsigned mask) {
-#pragma unroll
-    for (int tl = 0; tl < 2; ++tl)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((mask >> (2 * tq + (i & 1))) & 1u)
-          tot[tl][i] = FP8 ? fmaf(b.s[tl][i >> 1], acc[tl][i], tot[tl][i]) : tot[tl][i] + acc[tl][i];
+    --flying;
+    c_at += rg.stage;
+    if (c_at == ring_end) c_at = 0;
   };
   auto store_red = [&](float* rd, const float (&tot)[2][4]) {
 #pragma unroll
@@ -520,10 +626,22 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       *reinterpret_cast<float2*>(d + 64) = make_float2(tot[tl][2], tot[tl][3]);
     }
   };
+  // tot += s * acc, s per row (bit i of `mask`: token i counts).  A token outside
+  // the mask gets nothing (not 0 times a weight that may not be finite).
+  auto fold = [&](float (&tot)[2][4], const Acc& acc, const float (&s)[4], unsigned mask) {
+#pragma unroll
+    for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((mask >> (2 * tq + (i & 1))) & 1u) {
+          const float v = acc.h[tl][i] + acc.l[tl][i];
+          tot[tl][i] = FP8 ? fmaf(s[tl * 2 + (i >> 1)], v, tot[tl][i]) : tot[tl][i] + v;
+        }
+  };
 
-  top_up();
   int buf = 0;
   int my_tiles = 0;
+  float sc[4] = {};
 
   // ---- FC1
   for (int n = 0;; ++n) {
@@ -531,65 +649,56 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     if (c >= claims) break;
     int next_claim = claims;
     if (tid == 0) next_claim = atomicAdd(&p.ctr[0], 1);  // used two claims from here
-    const int tile = claim_tile(c);
-    const int nt = c < pairs ? 2 : 1;
-    const int a = tile / tiles_e;
+    const int tile = claim_tile(c), a = tile / tiles_e;
+    const bool two_tiles = c < pairs;
     const int i0 = (tile - a * tiles_e) * 8;
-    const int e = sm.expert[a];
     const unsigned mask = sm.mask[a];
-    const int64_t brow = ((mask >> g) & 1u) ? g : -1;
     float tot[2][4] = {};
-    StepB<EPC> b;
-    if (warp < S1) {
-      load_b(b, p.hi, p.lo, brow, H, warp, kb1);
-      load_s(b, p.s13, e, 2 * I, H, i0 + g, 8, I, nt == 2 ? 15u : 3u, warp);
-    }
+    Acc acc;
+    clear(acc);
     for (int step = warp; step < S1; step += kWarps) {
-      StepB<EPC> nb;
-      if (step + kWarps < S1) {
-        load_b(nb, p.hi, p.lo, brow, H, step + kWarps, kb1);
-        load_s(nb, p.s13, e, 2 * I, H, i0 + g, 8, I, nt == 2 ? 15u : 3u, step + kWarps);
-      }
-      if constexpr (FP8) {
-        float acc[2][4] = {};
-        multiply(acc, b, nt == 2, 2 * step + 1 < kb1);
-        fold(tot, acc, b, mask);
-      } else {
-        multiply(tot, b, nt == 2, 2 * step + 1 < kb1);
-      }
       top_up();
-      b = nb;
+      multiply(acc, sc, two_tiles, 2 * step + 1 < kb1);
+      if constexpr (FP8) {
+        fold(tot, acc, sc, mask);
+        clear(acc);
+      }
     }
+    if constexpr (!FP8) fold(tot, acc, sc, mask);
     store_red(red[buf], tot);
     if (tid == 0) sm.claim[(n + 2) & 3] = next_claim;
     __syncthreads();
     known = n + 2;
-    // 16 consecutive threads: the 16 intermediate columns of one token
-    if (tid < 128) {
-      const int t = tid >> 4, il = tid & 15;
-      if (((mask >> t) & 1u) && (il >> 3) < nt) {
-        const float* s = red[buf] + ((il >> 3) * 16 + (il & 7)) * 8 + t;
-        float gate = 0.f, up = 0.f;
+    // warp t: the 16 intermediate columns of token t (each half warp adds four
+    // warps' partial sums)
+    if ((mask >> warp) & 1u) {
+      const int il = lane & 15;
+      const float* s = red[buf] + ((il >> 3) * 16 + (il & 7)) * 8 + warp + (lane >> 4) * 1024;
+      float gate = 0.f, up = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          gate += s[w * 256];
-          up += s[w * 256 + 64];
-        }
-        const float r = sm.r[t];
+      for (int w = 0; w < 4; ++w) {
+        gate += s[w * 256];
+        up += s[w * 256 + 64];
+      }
+      gate += __shfl_xor_sync(0xffffffffu, gate, 16);
+      up += __shfl_xor_sync(0xffffffffu, up, 16);
+      if (lane < (two_tiles ? 16 : 8)) {
+        const float r = sm.r[warp];
         // the routing weight goes into the intermediate, so FC2 adds the
         // token's experts without a factor
-        const float v = silu_f(gate * r) * (up * r) * sm.wt[a][t];
+        const float v = silu_f(gate * r) * (up * r) * sm.wt[a][warp];
         const float hi = bf16_round_f(v);
-        const size_t at = (size_t)sm.pair[a][t] * I + i0 + il;
+        const size_t at = (size_t)sm.pair[a][warp] * I + i0 + il;
         p.act_hi[at] = __float2bfloat16_rn(hi);
         p.act_lo[at] = __float2bfloat16_rn(v - hi);
       }
     }
-    my_tiles += nt;
+    my_tiles += two_tiles ? 2 : 1;
     buf ^= 1;
-    top_up();
   }
-  // ---- all FC1 tiles done (each CTA's writes are visible before its count)
+  // ---- all FC1 tiles done (each CTA's writes are visible before its count);
+  // the first W2 steps are copied meanwhile
+  top_up();
   __syncthreads();
   if (tid == 0) {
     __threadfence();
@@ -611,47 +720,54 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
+  // the activations of the steps already in flight (the warp's first ones)
+  fc1_done = true;
+  if (p_step < p_end) p_on = sm.pair[pa][g] >= 0;
+  {
+    int a = -1, step = S2;
+    uint32_t at = c_at;
+    for (int left = flying; left > 0; --left) {
+      step += kWarps;
+      while (step >= S2) {
+        if (++a == n_act) a = 0;  // (a short unit: the next one's steps follow)
+        step = (warp - a * S2) & (kWarps - 1);
+      }
+      const int pr = sm.pair[a][g];
+      if (pr >= 0)
+        copy_b(at, p.act_hi + (size_t)pr * I + step * 2 * KE + tq * EPC, p.act_lo - p.act_hi,
+               2 * step + 1 < kb2);
+      at += rg.stage;
+      if (at == ring_end) at = 0;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    ready = flying;
+  }
 
   // ---- FC2: this CTA's output rows over all active experts
   for (int u = 0; n0 + 32 * u < n1; ++u) {
     const int row0 = n0 + 32 * u;
-    unsigned ok = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ok |= (row0 + g + 8 * i < n1 ? 1u : 0u) << i;
     const bool second = row0 + 16 < n1;
     float tot[2][4] = {};
-    StepB<EPC> b;
-    int a = 0, step = warp;
-    while (step >= S2) {
-      step -= S2;
-      ++a;
-    }
-    if (a < n_act) {
-      load_b(b, p.act_hi, p.act_lo, sm.pair[a][g], I, step, kb2);
-      load_s(b, p.s2, sm.expert[a], H, I, row0 + g, 16, 8, ok, step);
-    }
-    while (a < n_act) {
-      int na = a, ns = step + kWarps;
-      while (ns >= S2) {
-        ns -= S2;
-        ++na;
+    Acc acc;
+    clear(acc);
+    for (int a = 0; a < n_act; ++a) {
+      const unsigned mask = sm.mask[a];
+      for (int step = (warp - a * S2) & (kWarps - 1); step < S2; step += kWarps) {
+        top_up();
+        multiply(acc, sc, second, 2 * step + 1 < kb2);
+        if constexpr (FP8) {
+          fold(tot, acc, sc, mask);
+          clear(acc);
+        }
       }
-      StepB<EPC> nb;
-      if (na < n_act) {
-        load_b(nb, p.act_hi, p.act_lo, sm.pair[na][g], I, ns, kb2);
-        load_s(nb, p.s2, sm.expert[na], H, I, row0 + g, 16, 8, ok, ns);
+      if constexpr (!FP8) {
+        fold(tot, acc, sc, mask);
+        clear(acc);
       }
-      float acc[2][4] = {};
-      multiply(acc, b, second, 2 * step + 1 < kb2);
-      fold(tot, acc, b, sm.mask[a]);
-      top_up();
-      b = nb;
-      a = na;
-      step = ns;
     }
     store_red(red[buf], tot);
     __syncthreads();
-    const int row = tid & 31, t = tid >> 5;
+    const int row = lane, t = warp;
     if (t < T && row0 + row < n1) {
       const float* s = red[buf] + row * 8 + t;
       float v = 0.f;
@@ -675,12 +791,14 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   }
   __syncthreads();
   if (!sm.flag) return;
-  // 256 / Tp threads per row (Tp: T rounded up to a power of two)
+  // 256 / Tp threads per row (Tp: T rounded up to a power of two).  The rows are
+  // kept in the weights' shared memory between the passes where they fit.
   const int tp = T <= 1 ? 1 : (T <= 2 ? 2 : (T <= 4 ? 4 : 8));
   const int ntr = kThreadsL / tp, wpr = kWarps / tp;
   const int t = tid / ntr, sub = tid - t * ntr;
   const bool on = t < T;
   const int nv = H >> 3;
+  float* keep = (size_t)T * H * 4 <= (size_t)kRingBytes ? reinterpret_cast<float*>(ring_all) : p.f;
   auto row_reduce = [&](float v, bool mx) {
     v = mx ? warp_max(v) : warp_sum(v);
     if (lane == 0) sm.sum[warp] = v;
@@ -690,61 +808,48 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     __syncthreads();
     return v;
   };
-  auto load_f = [&](int c, float (&v)[8]) {
-    const float4* s = reinterpret_cast<const float4*>(p.f + (size_t)t * H + c);
-    const float4 a = __ldcg(s), b = __ldcg(s + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  };
-  float r = 1.f;
-  if (tail.post_w) {
-    float ss = 0.f;
-    if (on) {
-#pragma unroll 4
-      for (int v = sub; v < nv; v += ntr) {
-        float f[8];
-        load_f(v * 8, f);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) ss = fmaf(f[q], f[q], ss);
-      }
-    }
-    r = 1.0f / sqrtf(row_reduce(ss, false) / (float)H + tail.post_eps);
-  }
+  // (a thread reads back only what it wrote)
+  auto kept = [&](int v) { return reinterpret_cast<float4*>(keep + (size_t)t * H + v * 8); };
   const int grow = on ? tail_gate_row(tail, t, sub == 0 ? p.status : nullptr) : 0;
   const float factor = on ? tail_row_factor(tail, grow) : 0.f;
   float ss = 0.f;
   if (on) {
+#pragma unroll 4
+    for (int v = sub; v < nv; v += ntr) {
+      const float4* s = reinterpret_cast<const float4*>(p.f + (size_t)t * H + v * 8);
+      const float4 a = __ldcg(s), b = __ldcg(s + 1);
+      kept(v)[0] = a;
+      kept(v)[1] = b;
+      ss += a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w + b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
+    }
+  }
+  const float r = tail.post_w ? 1.0f / sqrtf(row_reduce(ss, false) / (float)H + tail.post_eps) : 1.f;
+  ss = 0.f;
+  if (on) {
 #pragma unroll 2
     for (int v = sub; v < nv; v += ntr) {
-      float f[8], h[8], res[8];
-      load_f(v * 8, f);
-      if (tail.residual) {
-        load8(tail.residual, tail.res_f32 != 0, (size_t)t * H + v * 8, res);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) res[q] = 0.f;
-      }
+      float f[8], h[8], res[8] = {};
+      load8(kept(v), true, 0, f);
+      if (tail.residual) load8(tail.residual, tail.res_f32 != 0, (size_t)t * H + v * 8, res);
       tail_h8(tail, H, v * 8, f, r, grow, factor, res, h);
       store8(tail.out, tail.out_f32 != 0, (size_t)t * H + v * 8, h);
-      if (tail.next_w) {
-        float4* d = reinterpret_cast<float4*>(p.f + (size_t)t * H + v * 8);  // read back by this thread
-        __stcg(d, make_float4(h[0], h[1], h[2], h[3]));
-        __stcg(d + 1, make_float4(h[4], h[5], h[6], h[7]));
+      kept(v)[0] = make_float4(h[0], h[1], h[2], h[3]);
+      kept(v)[1] = make_float4(h[4], h[5], h[6], h[7]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) ss = fmaf(h[q], h[q], ss);
-      }
+      for (int q = 0; q < 8; ++q) ss = fmaf(h[q], h[q], ss);
     }
   }
   if (!tail.next_w) return;
-  r = 1.0f / sqrtf(row_reduce(ss, false) / (float)H + tail.next_eps);
+  const float rn = 1.0f / sqrtf(row_reduce(ss, false) / (float)H + tail.next_eps);
   float amax = 0.f;
   auto next8 = [&](int v, float (&f)[8]) {
     float w[8];
-    load_f(v * 8, f);
+    load8(kept(v), true, 0, f);
     load8(tail.next_w, false, v * 8, w);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f[q] = (f[q] * r) * w[q];
+    for (int q = 0; q < 8; ++q) f[q] = (f[q] * rn) * w[q];
   };
+#pragma unroll 2
   for (int v0 = 0; v0 < nv; v0 += ntr) {
     const int v = v0 + sub;
     float f[8], m = 0.f;
@@ -849,7 +954,7 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
   const int rows = (a.H / 8 + kLayerChunks - 1) / kLayerChunks * 8;
   cudaError_t e =
       launch_kernel(layer_route_kernel, dim3(kLayerChunks, a.router_w ? (a.E + 31) / 32 : 1),
-                    dim3(kThreadsL), a.router_w ? (size_t)rows * kLayerMaxT * 4 : 0, st, p);
+                    dim3(32 * kRouteWarps), a.router_w ? (size_t)rows * kLayerMaxT * 4 : 0, st, p);
   if (e != cudaSuccess) return e;
   auto kern = a.fp8 ? layer_experts_kernel<true> : layer_experts_kernel<false>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
