@@ -193,7 +193,9 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_row_kernel(
 #pragma unroll
       for (int q = 0; q < 8; ++q) b[q] = 0.f;
     }
-    tail_h8(p, H, v * 8, f[i], r, grow, factor, b, h);
+    float w[8] = {};
+    if (p.post_w) load8(p.post_w, false, v * 8, w);
+    tail_h8(p, H, v * 8, f[i], w, r, grow, factor, b, h);
     store8(p.out, p.out_f32 != 0, (size_t)t * H + v * 8, h);
 #pragma unroll
     for (int q = 0; q < 8; ++q) f[i][q] = h[q];

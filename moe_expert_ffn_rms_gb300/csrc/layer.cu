@@ -49,9 +49,22 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreadsL = 32 * kWarps;
-constexpr int kMaxStages = 6;                   // steps in flight per warp, at most
-constexpr int kStepA = 4096;                    // weights: 2 tiles x 2 row halves x 2 K blocks x 512 B
-constexpr int kRingBytes = 200 << 10;           // shared memory of the CTA's copies
+
+// Per-warp stage of the copy ring: weights [2 tiles][2 row halves][2 K blocks]
+// [32 lanes] of 16 bytes; activations [2 K blocks][hi, lo][pieces][8 tokens]
+// [4 lanes] of 16 bytes; FP8: the scales of the 32 rows.  Three steps of eight
+// warps keep 96 KB per SM in flight, which already streams at the copy
+// bandwidth (measured alone: 6.64 TB/s with 3 steps, 6.64 with 6).
+constexpr int kStepA = 4096;
+constexpr int kPieceB = 512;
+template <bool FP8>
+struct Ring {
+  static constexpr int kScaleAt = kStepA + 4 * (FP8 ? 2 : 1) * kPieceB;
+  static constexpr int kStage = kScaleAt + (FP8 ? 128 : 0);
+  static constexpr int kDepth = FP8 ? 3 : 4;
+  static constexpr int kWarp = kDepth * kStage;
+  static constexpr int kBytes = kWarps * kWarp;  // 192 KB, 195 KB
+};
 constexpr int kRedFloats = kWarps * 2 * 16 * 8; // partial sums of two row tiles
 constexpr int kMaxPairs = kLayerMaxT * kMaxTopK;
 
@@ -181,21 +194,9 @@ MOE_DEV void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 MOE_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits for the oldest of n groups in flight.
-MOE_DEV void cp_wait_oldest(int n) {
-  switch (n) {
-    case 6: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-  }
-}
-
 MOE_DEV void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                        uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -233,22 +234,35 @@ struct LayerSmem {
 // the arg-max is two warp reductions of integers: the logits' bits in an
 // order-preserving form, then the lowest expert that has the maximum.
 template <int PER>
-MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float r, LayerSmem* sm) {
+MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float ss, LayerSmem* sm) {
+  float zs[PER], bias[PER];  // every load is issued before the first use
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 32 * i;
+    zs[i] = bias[i] = 0.f;
+    if (e < p.E) {
+      if (p.bias) bias[i] = p.bias[e];
+      if (p.logits) {
+        zs[i] = p.logits[(size_t)t * p.E + e];
+      } else {
+        float part[kLayerChunks];
+#pragma unroll
+        for (int c = 0; c < kLayerChunks; ++c) part[c] = __ldcg(&p.part[((size_t)c * p.T + t) * p.E + e]);
+#pragma unroll
+        for (int c = 0; c < kLayerChunks; ++c) zs[i] += part[c];
+      }
+    }
+  }
+  const float r = 1.0f / sqrtf(warp_sum(ss) / (float)p.H + p.eps);
+  if (lane == 0) sm->r[t] = r;
   unsigned key[PER];  // 0: taken or beyond E
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 32 * i;
     key[i] = 0;
     if (e < p.E) {
-      float z = 0.f;
-      if (p.logits) {
-        z = p.logits[(size_t)t * p.E + e];
-      } else {
-#pragma unroll
-        for (int c = 0; c < kLayerChunks; ++c) z += __ldcg(&p.part[((size_t)c * p.T + t) * p.E + e]);
-        z *= r;
-      }
-      if (p.bias) z += p.bias[e];
+      float z = p.logits ? zs[i] : zs[i] * r;
+      if (p.bias) z += bias[i];
       z = (z != z) ? -INFINITY : z + 0.0f;  // (-0 counts as 0)
       const unsigned u = __float_as_uint(z);
       key[i] = (u & 0x80000000u) ? ~u : u | 0x80000000u;  // -inf: 0x007fffff
@@ -287,20 +301,6 @@ MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float r, LayerSmem* sm
   }
 }
 
-// Per-warp stage: weights [2 tiles][2 row halves][2 K blocks][32 lanes] of 16
-// bytes; activations [2 K blocks][hi, lo][pieces][T tokens][4 lanes] of 16 bytes;
-// FP8: the scales of the 32 rows.
-struct LayerRing {
-  int stage, depth;  // bytes, steps
-};
-__host__ __device__ inline LayerRing layer_ring(int T, bool fp8) {
-  LayerRing r;
-  r.stage = kStepA + T * (fp8 ? 512 : 256) + (fp8 ? 128 : 0);
-  r.depth = kRingBytes / (kWarps * r.stage);
-  if (r.depth > kMaxStages) r.depth = kMaxStages;
-  return r;
-}
-
 // FP8: E4M3 weights, one scale per (row >> rs) and K step * ks.
 template <bool FP8>
 __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
@@ -322,10 +322,8 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   pdl_wait();
 
   // ---- routing (every CTA by itself; warp t: token t)
-  if (tid == 0) {
-    sm.claim[0] = atomicAdd(&p.ctr[0], 1);
-    sm.claim[1] = atomicAdd(&p.ctr[0], 1);
-  }
+  int first_claim = 0;
+  if (tid == kThreadsL - 1) first_claim = atomicAdd(&p.ctr[0], 2);
   if (has_tail) {  // what the tail will read is brought to L2 meanwhile
     const int64_t line = (int64_t)blockIdx.x * kThreadsL + tid;
     auto warm = [&](const void* q, int64_t bytes) {
@@ -339,21 +337,21 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   }
   if (warp < T) {
     const float ss = lane < kLayerChunks ? __ldcg(&p.ssq[lane * kLayerMaxT + warp]) : 0.f;
-    const float r = 1.0f / sqrtf(warp_sum(ss) / (float)H + p.eps);
-    if (lane == 0) sm.r[warp] = r;
     if (p.ids_in) {
       if (lane < k) {
         sm.ids[warp][lane] = p.ids_in[warp * k + lane];
         sm.w[warp][lane] = p.tw_in[warp * k + lane];
       }
+      const float r = 1.0f / sqrtf(warp_sum(ss) / (float)H + p.eps);
+      if (lane == 0) sm.r[warp] = r;
     } else if (E <= 32) {
-      layer_topk<1>(p, warp, lane, r, &sm);
+      layer_topk<1>(p, warp, lane, ss, &sm);
     } else if (E <= 64) {
-      layer_topk<2>(p, warp, lane, r, &sm);
+      layer_topk<2>(p, warp, lane, ss, &sm);
     } else if (E <= 128) {
-      layer_topk<4>(p, warp, lane, r, &sm);
+      layer_topk<4>(p, warp, lane, ss, &sm);
     } else {
-      layer_topk<8>(p, warp, lane, r, &sm);
+      layer_topk<8>(p, warp, lane, ss, &sm);
     }
     // the token's experts: lane j, its j-th
     __syncwarp();
@@ -364,6 +362,10 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       if (p.tw_out) p.tw_out[warp * k + lane] = sm.w[warp][lane];
       if (id < 0 || id >= E) flag_status(p.status, MOE_ERR_INVALID_ARG);
     }
+  }
+  if (tid == kThreadsL - 1) {
+    sm.claim[0] = first_claim;
+    sm.claim[1] = first_claim + 1;
   }
   __syncthreads();
   // active experts in ascending order (thread e: expert e; E <= 256)
@@ -419,14 +421,10 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   const int kb1 = (int)(rb1 >> 6), kb2 = (int)(rb2 >> 6);                // 64-byte K blocks
   auto claim_tile = [&](int c) { return c < pairs ? 2 * c : c + pairs; };
 
-  const LayerRing rg = layer_ring(T, FP8);
-  unsigned char* ring = ring_all + warp * (rg.depth * rg.stage);
+  using R = Ring<FP8>;
+  unsigned char* ring = ring_all + warp * R::kWarp;
   const uint32_t ring_u = ptx::smem_u32(ring);
-  const uint32_t ring_end = (uint32_t)rg.depth * rg.stage;
-  const bool col = g < T;                       // this lane's column is a token
-  const uint32_t b_lane = kStepA + (g * 4 + tq) * 16;
-  const uint32_t b_piece = T * 64;              // bytes of one piece of all tokens
-  const uint32_t s_at = kStepA + 4 * Q * b_piece;
+  const bool col = g < T;  // this lane's column is a token
   // block scales: one row of the scale matrix per 128 weight rows, one column
   // per K step; channel scales: one per row
   const int rs = p.block_scales ? 7 : 0;
@@ -524,32 +522,43 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const bf16* src = b + kb * KE + q * 8;
-        const uint32_t dst = ring_u + at + b_lane + (kb * 2 * Q + q) * b_piece;
+        const uint32_t dst = ring_u + at + kStepA + lane * 16 + (kb * 2 * Q + q) * kPieceB;
         cp_async16(dst, src);
-        cp_async16(dst + Q * b_piece, src + lo);
+        cp_async16(dst + Q * kPieceB, src + lo);
       }
     }
   };
   // Keeps the ring full as far as the steps are known.
   auto top_up = [&]() {
-    while (flying < rg.depth) {
+    while (flying < R::kDepth) {
       if (p_step >= p_end && !next_segment()) break;
       const uint32_t dst = ring_u + p_at + lane * 16;
       const bool two = !FP8 || 2 * p_step + 1 < p_kb;
+      const unsigned char *s0 = p_src, *s1 = s0 + p_hs, *s2 = s0 + p_ts, *s3 = s2 + p_hs;
+      if (p_ok == 15u && two) {
+        cp_async16(dst, s0);
+        cp_async16(dst + 512, s0 + 64);
+        cp_async16(dst + 1024, s1);
+        cp_async16(dst + 1536, s1 + 64);
+        cp_async16(dst + 2048, s2);
+        cp_async16(dst + 2560, s2 + 64);
+        cp_async16(dst + 3072, s3);
+        cp_async16(dst + 3584, s3 + 64);
+      } else {
+        const unsigned char* src[4] = {s0, s1, s2, s3};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if ((p_ok >> i) & 1u) {
-          const unsigned char* src = p_src + (i >> 1) * p_ts + (i & 1) * p_hs;
-          cp_async16(dst + (2 * i) * 512, src);
-          if (two) cp_async16(dst + (2 * i + 1) * 512, src + 64);
+        for (int i = 0; i < 4; ++i) {
+          if ((p_ok >> i) & 1u) {
+            cp_async16(dst + 1024 * i, src[i]);
+            if (two) cp_async16(dst + 1024 * i + 512, src[i] + 64);
+          }
         }
       }
       if (p_on) copy_b(p_at, p_b, p_lo, two);
-      if (FP8 && p_sok) cp_async4(ring_u + p_at + s_at + lane * 4, p_sc);
+      if (FP8 && p_sok) cp_async4(ring_u + p_at + R::kScaleAt + lane * 4, p_sc);
       cp_commit();
       ++flying;
-      p_at += rg.stage;
-      if (p_at == ring_end) p_at = 0;
+      p_at = p_at == (R::kDepth - 1) * R::kStage ? 0 : p_at + R::kStage;
       p_src += kWarps * 128;
       p_b += kWarps * 2 * KE;
       p_sc += kWarps * ks;
@@ -571,19 +580,18 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   };
   auto multiply = [&](Acc& acc, float (&sc)[4], bool second_tile, bool two) {
     if (ready > 0) --ready;
-    else cp_wait_oldest(flying);
-    const unsigned char* st = ring + c_at;
-    const uint4* sp = reinterpret_cast<const uint4*>(st) + lane;
-    // (columns beyond the last token read a token's piece again; they are not used)
-    const unsigned char* bp = st + (col ? b_lane : (uint32_t)kStepA + tq * 16);
+    else if (flying == R::kDepth) asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
+    else asm volatile("cp.async.wait_all;" ::: "memory");
+    const unsigned char* st = ring + c_at + lane * 16;
+    const uint4* sp = reinterpret_cast<const uint4*>(st);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       if (FP8 && kb && !two) break;
       uint4 h[Q], l[Q];
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        h[q] = *reinterpret_cast<const uint4*>(bp + (kb * 2 * Q + q) * b_piece);
-        l[q] = *reinterpret_cast<const uint4*>(bp + (kb * 2 * Q + Q + q) * b_piece);
+        h[q] = *reinterpret_cast<const uint4*>(st + kStepA + (kb * 2 * Q + q) * kPieceB);
+        l[q] = *reinterpret_cast<const uint4*>(st + kStepA + (kb * 2 * Q + Q + q) * kPieceB);
       }
 #pragma unroll
       for (int tl = 0; tl < 2; ++tl) {
@@ -611,12 +619,11 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     if constexpr (FP8) {
       __syncwarp();  // the scales were copied by other lanes of the warp
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i] = *reinterpret_cast<const float*>(st + s_at + (g + 8 * i) * 4);
+      for (int i = 0; i < 4; ++i) sc[i] = *reinterpret_cast<const float*>(ring + c_at + R::kScaleAt + (g + 8 * i) * 4);
       __syncwarp();  // and are overwritten by them once all have read
     }
     --flying;
-    c_at += rg.stage;
-    if (c_at == ring_end) c_at = 0;
+    c_at = c_at == (R::kDepth - 1) * R::kStage ? 0 : c_at + R::kStage;
   };
   auto store_red = [&](float* rd, const float (&tot)[2][4]) {
 #pragma unroll
@@ -736,8 +743,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       if (pr >= 0)
         copy_b(at, p.act_hi + (size_t)pr * I + step * 2 * KE + tq * EPC, p.act_lo - p.act_hi,
                2 * step + 1 < kb2);
-      at += rg.stage;
-      if (at == ring_end) at = 0;
+      at = at == (R::kDepth - 1) * R::kStage ? 0 : at + R::kStage;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     ready = flying;
@@ -782,7 +788,29 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!has_tail) return;
 
-  // ---- tail: the CTA that finishes last takes all rows
+  // ---- tail: the CTA that finishes last takes all rows; 256 / Tp threads per
+  // row (Tp: T rounded up to a power of two), eight columns a thread at a time.
+  const int tp = T <= 1 ? 1 : (T <= 2 ? 2 : (T <= 4 ? 4 : 8));
+  const int ntr = kThreadsL / tp, wpr = kWarps / tp;
+  const int t = tid / ntr, sub = tid - t * ntr;
+  const bool on = t < T;
+  const int nv = H >> 3;
+  // What a thread's first kPre pieces need besides f is loaded before the CTA
+  // knows whether it is the last.
+  constexpr int kPre = 2;
+  float pre_res[kPre][8] = {};
+  uint4 pre_pw[kPre] = {}, pre_nw[kPre] = {};
+#pragma unroll
+  for (int i = 0; i < kPre; ++i) {
+    const int v = sub + i * ntr;
+    if (on && v < nv) {
+      if (tail.residual) load8(tail.residual, tail.res_f32 != 0, (size_t)t * H + v * 8, pre_res[i]);
+      if (tail.post_w) pre_pw[i] = reinterpret_cast<const uint4*>(tail.post_w)[v];
+      if (tail.next_w) pre_nw[i] = reinterpret_cast<const uint4*>(tail.next_w)[v];
+    }
+  }
+  const int grow = on ? tail_gate_row(tail, t, nullptr) : 0;
+  const float factor = on ? tail_row_factor(tail, grow) : 0.f;
   __syncthreads();
   if (tid == 0) {
     __threadfence();
@@ -791,14 +819,11 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   }
   __syncthreads();
   if (!sm.flag) return;
-  // 256 / Tp threads per row (Tp: T rounded up to a power of two).  The rows are
-  // kept in the weights' shared memory between the passes where they fit.
-  const int tp = T <= 1 ? 1 : (T <= 2 ? 2 : (T <= 4 ? 4 : 8));
-  const int ntr = kThreadsL / tp, wpr = kWarps / tp;
-  const int t = tid / ntr, sub = tid - t * ntr;
-  const bool on = t < T;
-  const int nv = H >> 3;
-  float* keep = (size_t)T * H * 4 <= (size_t)kRingBytes ? reinterpret_cast<float*>(ring_all) : p.f;
+  if (grow < 0 && sub == 0) flag_status(p.status, MOE_ERR_INVALID_ARG);
+  // The rows are kept in the ring's shared memory between the passes where they
+  // fit (a thread reads back only what it wrote).
+  float* keep = (size_t)T * H * 4 <= (size_t)R::kBytes ? reinterpret_cast<float*>(ring_all) : p.f;
+  auto kept = [&](int v) { return reinterpret_cast<float4*>(keep + (size_t)t * H + v * 8); };
   auto row_reduce = [&](float v, bool mx) {
     v = mx ? warp_max(v) : warp_sum(v);
     if (lane == 0) sm.sum[warp] = v;
@@ -808,10 +833,6 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     __syncthreads();
     return v;
   };
-  // (a thread reads back only what it wrote)
-  auto kept = [&](int v) { return reinterpret_cast<float4*>(keep + (size_t)t * H + v * 8); };
-  const int grow = on ? tail_gate_row(tail, t, sub == 0 ? p.status : nullptr) : 0;
-  const float factor = on ? tail_row_factor(tail, grow) : 0.f;
   float ss = 0.f;
   if (on) {
 #pragma unroll 4
@@ -825,36 +846,44 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   }
   const float r = tail.post_w ? 1.0f / sqrtf(row_reduce(ss, false) / (float)H + tail.post_eps) : 1.f;
   ss = 0.f;
-  if (on) {
-#pragma unroll 2
-    for (int v = sub; v < nv; v += ntr) {
-      float f[8], h[8], res[8] = {};
-      load8(kept(v), true, 0, f);
-      if (tail.residual) load8(tail.residual, tail.res_f32 != 0, (size_t)t * H + v * 8, res);
-      tail_h8(tail, H, v * 8, f, r, grow, factor, res, h);
-      store8(tail.out, tail.out_f32 != 0, (size_t)t * H + v * 8, h);
-      kept(v)[0] = make_float4(h[0], h[1], h[2], h[3]);
-      kept(v)[1] = make_float4(h[4], h[5], h[6], h[7]);
+  auto residual8 = [&](int v, const float (&res)[8], const uint4& pw) {
+    float f[8], w[8], h[8];
+    load8(kept(v), true, 0, f);
+    unpack8_bf16(pw, w);
+    tail_h8(tail, H, v * 8, f, w, r, grow, factor, res, h);
+    store8(tail.out, tail.out_f32 != 0, (size_t)t * H + v * 8, h);
+    kept(v)[0] = make_float4(h[0], h[1], h[2], h[3]);
+    kept(v)[1] = make_float4(h[4], h[5], h[6], h[7]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) ss = fmaf(h[q], h[q], ss);
+    for (int q = 0; q < 8; ++q) ss = fmaf(h[q], h[q], ss);
+  };
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < kPre; ++i)
+      if (sub + i * ntr < nv) residual8(sub + i * ntr, pre_res[i], pre_pw[i]);
+#pragma unroll 2
+    for (int v = sub + kPre * ntr; v < nv; v += ntr) {
+      float res[8] = {};
+      uint4 pw = make_uint4(0u, 0u, 0u, 0u);
+      if (tail.residual) load8(tail.residual, tail.res_f32 != 0, (size_t)t * H + v * 8, res);
+      if (tail.post_w) pw = reinterpret_cast<const uint4*>(tail.post_w)[v];
+      residual8(v, res, pw);
     }
   }
   if (!tail.next_w) return;
   const float rn = 1.0f / sqrtf(row_reduce(ss, false) / (float)H + tail.next_eps);
   float amax = 0.f;
-  auto next8 = [&](int v, float (&f)[8]) {
+  auto next8 = [&](int v, const uint4& nw, float (&f)[8]) {
     float w[8];
     load8(kept(v), true, 0, f);
-    load8(tail.next_w, false, v * 8, w);
+    unpack8_bf16(nw, w);
 #pragma unroll
     for (int q = 0; q < 8; ++q) f[q] = (f[q] * rn) * w[q];
   };
-#pragma unroll 2
-  for (int v0 = 0; v0 < nv; v0 += ntr) {
-    const int v = v0 + sub;
+  auto write8 = [&](int v, const uint4& nw) {  // (whole warps: a group's maximum is a shuffle)
     float f[8], m = 0.f;
     if (on && v < nv) {
-      next8(v, f);
+      next8(v, nw, f);
 #pragma unroll
       for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[q]));
       if (tail.xhat) store8_bf16(tail.xhat + (size_t)t * H + v * 8, f);
@@ -869,6 +898,14 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       }
     }
     amax = fmaxf(amax, m);
+  };
+#pragma unroll
+  for (int i = 0; i < kPre; ++i) write8(sub + i * ntr, pre_nw[i]);
+#pragma unroll 2
+  for (int v0 = kPre * ntr; v0 < nv; v0 += ntr) {
+    uint4 nw = make_uint4(0u, 0u, 0u, 0u);
+    if (v0 + sub < nv) nw = reinterpret_cast<const uint4*>(tail.next_w)[v0 + sub];
+    write8(v0 + sub, nw);
   }
   if (tail.xq && !tail.q_group) {
     amax = row_reduce(amax, true);
@@ -876,7 +913,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     if (on) {
       for (int v = sub; v < nv; v += ntr) {
         float f[8];
-        next8(v, f);
+        next8(v, reinterpret_cast<const uint4*>(tail.next_w)[v], f);
         *reinterpret_cast<uint2*>(tail.xq + (size_t)t * H + v * 8) = tail_e4m3x8(f, s);
       }
       if (sub == 0) tail.xscale[t] = s;
@@ -957,9 +994,10 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
                     dim3(32 * kRouteWarps), a.router_w ? (size_t)rows * kLayerMaxT * 4 : 0, st, p);
   if (e != cudaSuccess) return e;
   auto kern = a.fp8 ? layer_experts_kernel<true> : layer_experts_kernel<false>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  const int smem = a.fp8 ? Ring<true>::kBytes : Ring<false>::kBytes;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(sms), dim3(kThreadsL), kRingBytes, st, p, tail ? *tail : TailP{},
+  return launch_kernel(kern, dim3(sms), dim3(kThreadsL), smem, st, p, tail ? *tail : TailP{},
                        tail ? 1 : 0);
 }
 
