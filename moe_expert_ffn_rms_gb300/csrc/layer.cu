@@ -60,24 +60,22 @@ constexpr int kWarps = 8;
 constexpr int kThreadsL = 32 * kWarps;
 
 // Per-warp stage of the copy ring: weights [2 tiles][2 row halves][2 K blocks]
-// [32 lanes] of 16 bytes; activations [2 K blocks][hi, lo][pieces][8 tokens]
+// [32 lanes] of 16 bytes; activations [2 K blocks][hi, lo][pieces][TOK tokens]
 // [4 lanes] of 16 bytes; FP8: the scales of the 32 rows and [2 K blocks][8
-// tokens][8 groups] exponents.  Three steps of eight warps keep 96 KB per SM in
-// flight, which already streams at the copy bandwidth (measured alone: 6.64 TB/s
-// with 3 steps, 6.64 with 6).
+// tokens][8 groups] exponents.  TOK is 4 where T <= 4: the room goes to more
+// steps in flight.
 constexpr int kStepA = 4096;
-constexpr int kPieceB = 512;
-template <bool FP8>
+template <bool FP8, int TOK>
 struct Ring {
+  static constexpr int kPieceB = TOK * 64;
   static constexpr int kScaleAt = kStepA + 4 * (FP8 ? 2 : 1) * kPieceB;  // scales of the 32 rows
   static constexpr int kPowAt = kScaleAt + 128;  // exponents of the intermediate's 8-column groups
   static constexpr int kStage = kScaleAt + (FP8 ? 128 + 128 : 0);
-  static constexpr int kDepth = FP8 ? 3 : 4;
+  static constexpr int kDepth = (200 << 10) / (kWarps * kStage);  // 3 .. 5 steps
   static constexpr int kWarp = kDepth * kStage;
-  static constexpr int kBytes = kWarps * kWarp;  // 192 KB, 198 KB
-  // Groups of warps that take FC1 claims of their own.  E4M3 rows have half the
-  // steps, so two groups of four warps keep a claim as long for a warp.
-  static constexpr int kGroups = FP8 ? 2 : 1;
+  static constexpr int kBytes = kWarps * kWarp;
+  // Groups of warps that take FC1 claims of their own.
+  static constexpr int kGroups = 1;
 };
 constexpr int kGroupRed = 2 * 2 * 16 * 8;  // floats: two buffers of two row tiles, per warp of the group
 constexpr int kMaxPairs = kLayerMaxT * kMaxTopK;
@@ -505,14 +503,14 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
 }
 
 // FP8: E4M3 weights, one scale per (row >> rs) and K step * ks.
-template <bool FP8>
+template <bool FP8, int TOK>
 __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
                                                                      int has_tail) {
   constexpr int EB = FP8 ? 1 : 2;   // bytes per weight
   constexpr int EPC = 16 / EB;      // weights per 16-byte piece
   constexpr int KE = 64 / EB;       // K elements of a K block (64 bytes of a row)
   constexpr int Q = EPC / 8;        // 16-byte pieces of activations per K block and term
-  using R = Ring<FP8>;
+  using R = Ring<FP8, TOK>;
   constexpr int G = R::kGroups, GW = kWarps / G;  // groups, warps of a group
   extern __shared__ __align__(128) unsigned char ring_all[];
   __shared__ LayerSmem sm;
@@ -660,28 +658,30 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   int p_step = 0, p_end = 0, p_kb = kb1; // next step, end of its segment, K blocks of a row
   int p_inc = GW;                        // steps to the next (FC2: 1)
   int pn = -1, pu = 0, pa = a_first - 1; // claim; FC2 unit and active expert
-  int known = 1;                         // newest claim index published to this group
+  int n = 0;                             // claim being used; n + 1 is known too
   bool p_fc2 = false, fc1_done = false;
   int flying = 0;                        // steps issued and not yet used
   int ready = 0;                         // of these, steps known to have arrived
   uint32_t p_at = 0, c_at = 0;           // ring offsets of the next step to issue / to use
 
-  // Moves to the next segment that has a step for this warp.
+  auto start_fc2 = [&]() {
+    p_fc2 = true;
+    p_kb = kb2;
+    p_inc = 1;
+    p_ts = 16 * rb2;
+    p_hs = 8 * rb2;
+    p_lo = p.act_lo - p.act_hi;
+  };
+  // Moves to the next segment that has a step for this warp; false when there is
+  // none or it is not known yet.
   auto next_segment = [&]() -> bool {
-    while (!p_fc2) {
-      if (pn + 1 > known) return false;
-      const int c = sm.claim[grp][(pn + 1) & 3];
-      if (c >= claims) {
-        p_fc2 = true;
-        p_kb = kb2;
-        p_inc = 1;
-        p_ts = 16 * rb2;
-        p_hs = 8 * rb2;
-        p_lo = p.act_lo - p.act_hi;
-        break;
-      }
+    if (!p_fc2) {
+      if (pn > n || gw >= S1) return false;
+      if (sm.claim[grp][(pn + 1) & 3] >= claims) start_fc2();
+    }
+    if (!p_fc2) {
       ++pn;
-      if (gw >= S1) continue;
+      const int c = sm.claim[grp][pn & 3];
       int a, i0;
       claim_at(c, a, i0);
       const int e = sm.expert[a];
@@ -736,9 +736,9 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const uint16_t* src = b + kb * KE + q * 8;
-        const uint32_t dst = ring_u + at + kStepA + lane * 16 + (kb * 2 * Q + q) * kPieceB;
+        const uint32_t dst = ring_u + at + kStepA + lane * 16 + (kb * 2 * Q + q) * R::kPieceB;
         cp_async16(dst, src);
-        cp_async16(dst + Q * kPieceB, src + lo);
+        cp_async16(dst + Q * R::kPieceB, src + lo);
       }
     }
     // (lane tq of a token: the 8 exponents of K block tq)
@@ -806,14 +806,16 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     if (FP8) __syncwarp();  // scales and exponents were copied by other lanes of the warp
     const unsigned char* st = ring + c_at + lane * 16;
     const uint4* sp = reinterpret_cast<const uint4*>(st);
+    // (columns beyond TOK read another token's piece; they are not used)
+    const unsigned char* bp = ring + c_at + kStepA + ((g & (TOK - 1)) * 4 + tq) * 16;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       if (FP8 && kb && !two) break;
       uint4 h[Q], l[Q];
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        h[q] = *reinterpret_cast<const uint4*>(st + kStepA + (kb * 2 * Q + q) * kPieceB);
-        l[q] = *reinterpret_cast<const uint4*>(st + kStepA + (kb * 2 * Q + Q + q) * kPieceB);
+        h[q] = *reinterpret_cast<const uint4*>(bp + (kb * 2 * Q + q) * R::kPieceB);
+        l[q] = *reinterpret_cast<const uint4*>(bp + (kb * 2 * Q + Q + q) * R::kPieceB);
       }
       if (FP8 && top) {
         const unsigned ex = *reinterpret_cast<const uint16_t*>(ring + c_at + R::kPowAt + kb * 64 + g * 8 + tq * 2);
@@ -900,7 +902,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   // One loop over segments, so that the stream's code exists once: FC1 claims
   // (fc2 = false), then this warp's experts of each FC2 unit.
   bool fc2 = false;
-  int n = 0, u = 0, a = 0, i0 = 0;
+  int u = 0, a = 0, i0 = 0;
   while (true) {
     int step, end, inc, kbs, top = 0, next_claim = claims;
     unsigned mask = 0;
@@ -909,7 +911,10 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     const int c = fc2 ? 0 : sm.claim[grp][n & 3];
     if (!fc2) {
       if (c >= claims) {
-        // ---- all FC1 tiles done (each CTA's writes are visible before its count)
+        // ---- all FC1 tiles done (each CTA's writes are visible before its count).
+        // Meanwhile the first W2 steps are copied.
+        if (!p_fc2) start_fc2();
+        top_up();
         __syncthreads();
         if (tid == 0) {
           sm.flag = 0;
@@ -934,7 +939,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
         }
         // the activations of the W2 steps already in flight
         fc1_done = true;
-        if (p_fc2 && p_step < p_end) p_on = sm.pair[pa][g] >= 0;
+        if (p_step < p_end) p_on = sm.pair[pa][g] >= 0;
         int qa = a_first, qs = s_first, qq = q0;
         uint32_t at = c_at;
         for (int left = flying; left > 0; --left) {
@@ -961,7 +966,6 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
         a = a_first;
         continue;
       }
-      if (gw == 0 && lane == 0) next_claim = atomicAdd(&p.ctr[0], 1);  // used two claims from here
       claim_at(c, a, i0);
       mask = sm.mask[a];
       second = c < pairs;
@@ -969,6 +973,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       end = S1;
       inc = GW;
       kbs = kb1;
+      if (gw == 0 && lane == 0) next_claim = atomicAdd(&p.ctr[0], 1);  // used two claims from here
     } else {
       if (n0 + 32 * u >= n1) break;
       second = n0 + 32 * u + 16 < n1;
@@ -1029,7 +1034,6 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       zero(tot);
       if (gw == 0 && lane == 0) sm.claim[grp][(n + 2) & 3] = next_claim;
       group_sync();
-      known = n + 2;
       const int il = lane & 15;
       // G = 1: warp t, token t, each half warp half of the partial sums;
       // G = 2: two tokens a warp
@@ -1212,8 +1216,12 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
   e = launch_kernel(route, dim3(kLayerChunks, a.router_w ? (a.E + 31) / 32 : 1), dim3(32 * kRouteWarps),
                     (size_t)route_smem, st, p);
   if (e != cudaSuccess) return e;
-  auto kern = a.fp8 ? layer_experts_kernel<true> : layer_experts_kernel<false>;
-  const int smem = a.fp8 ? Ring<true>::kBytes : Ring<false>::kBytes;
+  auto kern = a.fp8 ? layer_experts_kernel<true, 8> : layer_experts_kernel<false, 8>;
+  int smem = a.fp8 ? Ring<true, 8>::kBytes : Ring<false, 8>::kBytes;
+  if (a.T <= 4) {
+    kern = a.fp8 ? layer_experts_kernel<true, 4> : layer_experts_kernel<false, 4>;
+    smem = a.fp8 ? Ring<true, 4>::kBytes : Ring<false, 4>::kBytes;
+  }
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(sms), dim3(kThreadsL), smem, st, p, tail ? *tail : TailP{},
