@@ -938,7 +938,8 @@ moe_status moe_combine(const void* y, int32_t y_bf16, int32_t y_pair_order,
 
 size_t moe_layer_workspace_size(const moe_shape* shape) {
   if (check_layer_shape(shape) != MOE_OK) return 0;
-  return moe::layer_workspace_bytes(shape->T, shape->H, shape->E, shape->I, shape->top_k);
+  return moe::layer_workspace_bytes(shape->T, shape->H, shape->E, shape->I, shape->top_k,
+                                    shape->wdtype != MOE_W_BF16);
 }
 
 moe_status moe_layer_forward(const moe_shape* shape, const void* x, const void* norm_w,

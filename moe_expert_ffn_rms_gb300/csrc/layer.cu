@@ -23,15 +23,17 @@
 // Claiming the FC1 tiles from a counter means the wait needs no co-residency:
 // a CTA that has not started holds no tile.
 //
-// Products: the weights are the 16 x 16 operand of m16n8k16 MMAs, the (at most
-// 8) tokens the 8 columns; fp32 accumulation.  Activations enter as two 16-bit
-// terms hi + lo, so neither x_hat nor the intermediate is rounded to 16 bits:
-// bf16 terms for bf16 weights (16 bits of mantissa); fp16 terms for E4M3 weights
-// (22 bits), because E4M3 -> fp16 is one instruction for two weights and
-// E4M3 -> bf16 four.  fp16 has little range, so its terms carry a power of two:
-// one per token and K chunk for x (the chunk's maximum), one per 8 columns for
-// the intermediate (a row tile's), brought to the pair's largest by an exact
-// fp16 product when they are used.
+// Products: the weights are the 16-row operand of MMAs with 8 columns and fp32
+// accumulation; the columns are the tokens' activations in several terms, so
+// that neither x_hat nor the intermediate is rounded to the weights' type:
+//   bf16 weights  m16n8k16, two bf16 terms hi + lo (16 bits of mantissa)
+//   E4M3 weights  m16n8k32, four E4M3 terms q0 + q1/16 + q2/256 + q3/4096 of
+//                 4 bits each.  The codes go to the tensor cores as they are
+//                 (measured: 4.5 cycles per m16n8k32 against 8 per m16n8k16, and
+//                 no conversion: 64 instructions of a warp's step otherwise).
+//                 E4M3 has little range, so each token and 128 columns share a
+//                 power of two, applied with the weight scale after a step.
+// With T <= 4 (E4M3: 2) tokens all terms of a token fit one MMA's columns.
 //
 // A warp reads its own operands: each lane copies exactly the 16-byte pieces it
 // will feed to its MMAs into its own part of shared memory (cp.async, a few
@@ -59,28 +61,31 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreadsL = 32 * kWarps;
 
+// TOK: tokens that the columns have room for (T <= TOK).  Column c of MMA j holds
+// term j * kTpg + c % kTpg of token c / kTpg.
+template <bool FP8, int TOK>
+struct Cols {
+  static constexpr int kTerms = FP8 ? 4 : 2;
+  static constexpr int kTpg = 8 / TOK;             // terms of a token per MMA
+  static constexpr int kMmas = kTerms / kTpg;      // MMAs per weight tile and K
+};
+
 // Per-warp stage of the copy ring: weights [2 tiles][2 row halves][2 K blocks]
-// [32 lanes] of 16 bytes; activations [2 K blocks][hi, lo][pieces][TOK tokens]
-// [4 lanes] of 16 bytes; FP8: the scales of the 32 rows and [2 K blocks][8
-// tokens][8 groups] exponents.  TOK is 4 where T <= 4: the room goes to more
-// steps in flight.
+// [32 lanes] of 16 bytes; activations [2 K blocks][MMAs][32 lanes] of 16 bytes;
+// FP8: the scales of the 32 rows and the powers of two of the tokens.
 constexpr int kStepA = 4096;
 template <bool FP8, int TOK>
 struct Ring {
-  static constexpr int kPieceB = TOK * 64;
-  static constexpr int kScaleAt = kStepA + 4 * (FP8 ? 2 : 1) * kPieceB;  // scales of the 32 rows
-  static constexpr int kPowAt = kScaleAt + 128;  // exponents of the intermediate's 8-column groups
-  static constexpr int kStage = kScaleAt + (FP8 ? 128 + 128 : 0);
+  static constexpr int kScaleAt = kStepA + 2 * Cols<FP8, TOK>::kMmas * 512;
+  static constexpr int kPowAt = kScaleAt + 128;
+  static constexpr int kStage = kScaleAt + (FP8 ? 128 + 64 : 0);
   static constexpr int kDepth = (200 << 10) / (kWarps * kStage);  // 3 .. 5 steps
   static constexpr int kWarp = kDepth * kStage;
   static constexpr int kBytes = kWarps * kWarp;
-  // Groups of warps that take FC1 claims of their own.
-  static constexpr int kGroups = 1;
 };
-constexpr int kGroupRed = 2 * 2 * 16 * 8;  // floats: two buffers of two row tiles, per warp of the group
+constexpr int kRed = kWarps * 2 * 16 * 8;  // floats: partial sums of all warps, two row tiles
 constexpr int kMaxPairs = kLayerMaxT * kMaxTopK;
-constexpr int kCtrPow = 8;  // ctr: largest exponent of each pair's intermediate
-constexpr int kCtrInts = kCtrPow + kMaxPairs;
+constexpr int kCtrInts = 8;
 
 struct LayerP {
   const bf16* x;
@@ -100,17 +105,20 @@ struct LayerP {
   int T, H, E, I, k, block_scales;
   float eps;
   // workspace
-  uint16_t *hi, *lo;          // x w [T, H] in two terms (bf16, or fp16 with FP8 weights)
-  uint16_t *act_hi, *act_lo;  // intermediate [T k, I], times the routing weight
-  uint8_t* act_pow;           // FP8: its exponents (pow_exponent) [T k, I / 8]
-  float *ssq, *xpow;          // sums of squares and factors of x w [chunks, 8]
-  float *part, *f;            // partial logits [chunks, T, E], f [T, H]
-  int* ctr;                   // [0] FC1 claims, [1] FC1 tiles done, [2] CTAs finished, [8..] kCtrPow
+  unsigned char* xt;   // terms of x w [terms][T, H], bf16 or E4M3
+  unsigned char* at;   // terms of the intermediate [terms][T k, I], times the routing weight
+  float* xpow;         // FP8: powers of two of x w [T, H / 128]
+  float* apow;         // FP8: of the intermediate [T k, I / 128]
+  float* act;          // FP8: the intermediate [T k, I]
+  float *ssq, *part;   // sums of squares [chunks, 8], partial logits [chunks, T, E]
+  float* f;            // [T, H]
+  int* ctr;            // [0] FC1 claims, [1] FC1 tiles done, [2] CTAs finished,
+                       // [3] claims and [4] units of the intermediate's terms
   int* status;
 };
 
 // K chunk c covers the units [c n / 16, (c + 1) n / 16) of 128 columns (the last
-// unit may be 64 wide), so that a 128-column step of the FP8 products lies in one.
+// unit may be 64 wide).
 struct Chunk {
   int k0, k1;
 };
@@ -123,29 +131,37 @@ __host__ __device__ inline Chunk layer_chunk(int H, int c) {
   return ch;
 }
 
-// v in two 16-bit terms.
-template <bool F16>
-MOE_DEV void split16(float v, uint16_t& hi, uint16_t& lo) {
-  if (F16) {
-    const __half h = __float2half_rn(v);
-    hi = __half_as_ushort(h);
-    lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
-  } else {
-    const bf16 h = __float2bfloat16_rn(v);
-    hi = __bfloat16_as_ushort(h);
-    lo = __bfloat16_as_ushort(__float2bfloat16_rn(v - __bfloat162float(h)));
-  }
+// bf16 terms of v.
+MOE_DEV void split_bf16(float v, bf16& hi, bf16& lo) {
+  hi = __float2bfloat16_rn(v);
+  lo = __float2bfloat16_rn(v - __bfloat162float(hi));
 }
 
-// fp16 terms: values of which the largest magnitude m has the biased exponent e
-// are scaled by 2^(141 - e), to below 2^15, and the products by 2^(e - 141).
-// Magnitudes below 2^-112 count as that; infinities and NaN stay what they are.
+// E4M3 terms.  Values of which the largest magnitude m has the biased exponent e
+// are scaled by 2^(134 - e), to below 256, and the products by 2^(e - 134).
+// Magnitudes below 2^-112 count as that.  Where a value is not finite the factor
+// is NaN: an E4M3 term cannot hold an infinity.
 MOE_DEV int pow_exponent(float m) {
   const int e = (int)((__float_as_uint(m) >> 23) & 255u);
   return e < 15 ? 15 : (e > 254 ? 254 : e);
 }
-MOE_DEV float pow_up(int e) { return __uint_as_float((uint32_t)(268 - e) << 23); }
-MOE_DEV float pow_down(int e) { return __uint_as_float((uint32_t)(e - 14) << 23); }
+MOE_DEV float pow_up(int e) { return __uint_as_float((uint32_t)(261 - e) << 23); }
+MOE_DEV float pow_down(int e) { return __uint_as_float((uint32_t)(e - 7) << 23); }
+
+// The next term of N scaled values: their E4M3 codes; v becomes 16 times what is
+// left.
+template <int N>
+MOE_DEV void take_term(float (&v)[N], uint32_t (&codes)[N / 4]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, __NV_E4M3);
+    const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+    v[i] = (v[i] - b.x) * 16.f;
+    v[i + 1] = (v[i + 1] - b.y) * 16.f;
+    if (i % 4 == 0) codes[i / 4] = c;
+    else codes[i / 4] |= (uint32_t)c << 16;
+  }
+}
 
 // ------------------------------------------------------------------ launch 1 --
 // Grid (kLayerChunks, groups of 32 experts): K chunk c, experts 32y .. 32y+31.
@@ -153,7 +169,7 @@ MOE_DEV float pow_down(int e) { return __uint_as_float((uint32_t)(e - 14) << 23)
 // their way before it waits for anything.
 constexpr int kRouteWarps = 16;
 
-template <bool F16>
+template <bool FP8>
 __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const LayerP p) {
   extern __shared__ __align__(16) float xw[];  // [rows of the chunk][8 tokens]
   __shared__ float red[kRouteWarps][kLayerMaxT][32];
@@ -177,47 +193,65 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
   }
   // warp t: token t (zeros beyond the last)
   if (warp < kLayerMaxT) {
-    const size_t row = (size_t)(warp < p.T ? warp : 0) * p.H + k0;
-    float ss = 0.f, up = 1.f;
-    if (F16 && warp < p.T) {  // the chunk's power of two
-      float m = 0.f;
-      for (int v = lane; v < rows >> 3; v += 32) {
-        float a[8], w[8];
-        load8(p.x, false, row + v * 8, a);
-        load8(p.norm_w, false, k0 + v * 8, w);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(a[q] * w[q]));
-      }
-      const int ex = pow_exponent(warp_max(m));
-      up = pow_up(ex);
-      if (blockIdx.y == 0 && lane == 0) p.xpow[c * kLayerMaxT + warp] = pow_down(ex);
-    }
-    for (int v = lane; v < rows >> 3; v += 32) {
+    const bool on = warp < p.T;
+    const size_t row = (size_t)(on ? warp : 0) * p.H + k0;
+    float ss = 0.f;
+#pragma unroll 1
+    for (int v0 = 0; v0 < rows >> 3; v0 += 32) {
+      const int v = v0 + lane;
       float a[8] = {};
-      if (warp < p.T) {
+      if (on && v < rows >> 3) {
         float w[8];
         load8(p.x, false, row + v * 8, a);
         load8(p.norm_w, false, k0 + v * 8, w);
-        __align__(16) uint16_t hi[8], lo[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           ss = fmaf(a[q], a[q], ss);
           a[q] *= w[q];
-          split16<F16>(F16 ? a[q] * up : a[q], hi[q], lo[q]);
-        }
-        if (blockIdx.y == 0) {
-          *reinterpret_cast<uint4*>(p.hi + row + v * 8) = *reinterpret_cast<uint4*>(hi);
-          *reinterpret_cast<uint4*>(p.lo + row + v * 8) = *reinterpret_cast<uint4*>(lo);
         }
       }
-      if (wr) {
+      if (wr && v < rows >> 3) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) xw[(v * 8 + q) * kLayerMaxT + warp] = a[q];
+      }
+      if (blockIdx.y == 0) {
+        const size_t at = row + v * 8, term = (size_t)p.T * p.H;
+        if (FP8) {  // 16 lanes share a power of two
+          float m = 0.f;
+          bool bad = false;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            m = fmaxf(m, fabsf(a[q]));
+            bad = bad || !(fabsf(a[q]) <= FLT_MAX);
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 16)) & 0xffffu;
+          const int ex = pow_exponent(m);
+          if (on && v < rows >> 3) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) a[q] *= pow_up(ex);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t c[2];
+              take_term(a, c);
+              *reinterpret_cast<uint2*>(p.xt + i * term + at) = make_uint2(c[0], c[1]);
+            }
+            if ((lane & 15) == 0)
+              p.xpow[warp * ((p.H + 127) >> 7) + ((k0 + v * 8) >> 7)] = bad ? NAN : pow_down(ex);
+          }
+        } else if (on && v < rows >> 3) {
+          __align__(16) bf16 hi[8], lo[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) split_bf16(a[q], hi[q], lo[q]);
+          *reinterpret_cast<uint4*>(p.xt + 2 * at) = *reinterpret_cast<uint4*>(hi);
+          *reinterpret_cast<uint4*>(p.xt + 2 * (term + at)) = *reinterpret_cast<uint4*>(lo);
+        }
       }
     }
     if (blockIdx.y == 0) {
       ss = warp_sum(ss);
-      if (lane == 0 && warp < p.T) p.ssq[c * kLayerMaxT + warp] = ss;
+      if (lane == 0 && on) p.ssq[c * kLayerMaxT + warp] = ss;
     }
   }
   if (!wr) return;
@@ -260,64 +294,44 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
 MOE_DEV void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-MOE_DEV void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 MOE_DEV void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 MOE_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 MOE_DEV void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <bool F16>
-MOE_DEV void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                       uint32_t b1) {
-  if (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four E4M3 codes as two fp16 pairs (exact).
-MOE_DEV void e4m3x4_f16(uint32_t q, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
-      " cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(q));
-}
-
-MOE_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-MOE_DEV uint4 hmul2x4(const uint4& a, uint32_t b) {
-  return make_uint4(hmul2(a.x, b), hmul2(a.y, b), hmul2(a.z, b), hmul2(a.w, b));
+// c += the 16 weight rows (pieces lo, hi: rows g and g + 8) times the 8 columns,
+// over the K elements of one 16-byte piece per lane.
+template <bool FP8>
+MOE_DEV void mma_piece(float (&c)[4], const uint4& lo, const uint4& hi, const uint4& b) {
+#define MOE_MMA(KIND, A0, A1, A2, A3, B0, B1)                                                   \
+  asm("mma.sync.aligned." KIND " {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};" \
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                          \
+      : "r"(A0), "r"(A1), "r"(A2), "r"(A3), "r"(B0), "r"(B1))
+  if (FP8) {
+    MOE_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32", lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+    MOE_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32", lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+  } else {
+    MOE_MMA("m16n8k16.row.col.f32.bf16.bf16.f32", lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+    MOE_MMA("m16n8k16.row.col.f32.bf16.bf16.f32", lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+  }
+#undef MOE_MMA
 }
 
 struct LayerSmem {
   int32_t ids[kLayerMaxT][kMaxTopK];
   float w[kLayerMaxT][kMaxTopK];
   float r[kLayerMaxT];
-  float xpow[kLayerChunks][kLayerMaxT];
-  uint8_t chunk[kLayerMaxH / 128];  // K chunk of a 128-column step
-  unsigned used[kMaxExperts];       // tokens of each expert, as a bit mask
-  int slot[kMaxExperts];            // its place among the active experts
+  unsigned used[kMaxExperts];  // tokens of each expert, as a bit mask
+  int slot[kMaxExperts];       // its place among the active experts
   int expert[kMaxPairs];
   unsigned mask[kMaxPairs];
   int pair[kMaxPairs][kLayerMaxT];
   float wt[kMaxPairs][kLayerMaxT];
   int warp_cnt[kWarps];
-  int claim[2][4];
+  int claim[4];
   int flag;
   float sum[kWarps];
-  int pow[kMaxPairs];  // FP8: largest exponent of the pair's intermediate
 };
 
 // Top-k of one token by one warp with the results of warp_topk (common.cuh):
@@ -506,19 +520,17 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
 template <bool FP8, int TOK>
 __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
                                                                      int has_tail) {
-  constexpr int EB = FP8 ? 1 : 2;   // bytes per weight
-  constexpr int EPC = 16 / EB;      // weights per 16-byte piece
-  constexpr int KE = 64 / EB;       // K elements of a K block (64 bytes of a row)
-  constexpr int Q = EPC / 8;        // 16-byte pieces of activations per K block and term
+  constexpr int EB = FP8 ? 1 : 2;   // bytes per weight, and per activation term
   using R = Ring<FP8, TOK>;
-  constexpr int G = R::kGroups, GW = kWarps / G;  // groups, warps of a group
+  using C = Cols<FP8, TOK>;
+  constexpr int NJ = C::kMmas, TPG = C::kTpg;
   extern __shared__ __align__(128) unsigned char ring_all[];
   __shared__ LayerSmem sm;
-  __shared__ __align__(16) float red_all[kWarps * kGroupRed];
+  __shared__ __align__(16) float red[2][kRed];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int grp = warp / GW, gw = warp % GW;  // group, warp of the group
-  const int g = lane >> 2, tq = lane & 3;     // MMA fragment row / column, K group
+  const int g = lane >> 2, tq = lane & 3;  // MMA fragment row / column, K group
+  const int tok = g / TPG;                 // token of this lane's column
   const int T = p.T, H = p.H, E = p.E, I = p.I, k = p.k;
   sm.used[tid] = 0;
   pdl_trigger();
@@ -527,10 +539,9 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
 
   // ---- routing (every CTA by itself; warp t: token t)
   int first_claim = 0;
-  if (tid == kThreadsL - 1) first_claim = atomicAdd(&p.ctr[0], 2 * G);
+  if (tid == kThreadsL - 1) first_claim = atomicAdd(&p.ctr[0], 2);
   if (warp < T) {
     const float ss = lane < kLayerChunks ? __ldcg(&p.ssq[lane * kLayerMaxT + warp]) : 0.f;
-    if (FP8 && lane < kLayerChunks) sm.xpow[lane][warp] = __ldcg(&p.xpow[lane * kLayerMaxT + warp]);
     if (p.ids_in) {
       if (lane < k) {
         sm.ids[warp][lane] = p.ids_in[warp * k + lane];
@@ -557,14 +568,9 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       if (id < 0 || id >= E) flag_status(p.status, MOE_ERR_INVALID_ARG);
     }
   }
-  if (FP8 && warp == kWarps - 1) {
-    if (lane < kLayerChunks) {
-      const Chunk ch = layer_chunk(H, lane);
-      for (int s = ch.k0 >> 7; s < (ch.k1 + 127) >> 7; ++s) sm.chunk[s] = (uint8_t)lane;
-    }
-  }
   if (tid == kThreadsL - 1) {
-    for (int i = 0; i < 2 * G; ++i) sm.claim[i % G][i / G] = first_claim + i;
+    sm.claim[0] = first_claim;
+    sm.claim[1] = first_claim + 1;
   }
   __syncthreads();
   // active experts in ascending order (thread e: expert e; E <= 256)
@@ -607,12 +613,12 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   for (int w = 0; w < kWarps; ++w) n_act += sm.warp_cnt[w];
 
   // ---- work.  FC1 row tiles (8 gate + 8 up rows) in claims of two, the last
-  // ones (about one per group) single, the K steps of a claim interleaved over
-  // the group's warps.  FC2: output rows [n0, n1) in units of 32, all experts' K
+  // ones (one per CTA) single, the K steps of a claim interleaved over the
+  // warps.  FC2: output rows [n0, n1) in units of 32, all experts' K
   // steps in one sequence of which warp w takes the w-th eighth.
   const int tiles_e = I >> 3;
   const int tiles = n_act * tiles_e;
-  const int singles = min(tiles, (int)(gridDim.x * G) & ~1);
+  const int singles = min(tiles, (int)gridDim.x & ~1);
   const int pairs = (tiles - singles) >> 1;  // tiles and singles are even
   const int claims = pairs + singles;
   const int n0 = (int)((int64_t)blockIdx.x * H / gridDim.x);
@@ -620,6 +626,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   const uint32_t rb1 = (uint32_t)H * EB, rb2 = (uint32_t)I * EB;  // bytes of a weight row
   const int S1 = (int)((rb1 + 127) >> 7), S2 = (int)((rb2 + 127) >> 7);  // 128-byte steps of a row
   const int kb1 = (int)(rb1 >> 6), kb2 = (int)(rb2 >> 6);                // 64-byte K blocks
+  const int P1 = (H + 127) >> 7, P2 = (I + 127) >> 7;                    // powers of two of a row
   const int q0 = n_act * S2 * warp / kWarps, q1 = n_act * S2 * (warp + 1) / kWarps;  // FC2 steps
   const int a_first = q0 / S2, s_first = q0 - a_first * S2;
   const unsigned magic = 0xffffffffu / (unsigned)tiles_e;
@@ -637,7 +644,6 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
 
   unsigned char* ring = ring_all + warp * R::kWarp;
   const uint32_t ring_u = ptx::smem_u32(ring);
-  const bool col = g < T;  // this lane's column is a token
   // block scales: one row of the scale matrix per 128 weight rows, one column
   // per K step; channel scales: one per row
   const int rs = p.block_scales ? 7 : 0;
@@ -649,14 +655,14 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   const unsigned char* p_src = nullptr;  // this lane's first row at the next step
   uint32_t p_ts = 0, p_hs = 0;           // to the second tile, to a tile's lower 8 rows (bytes)
   unsigned p_ok = 0;                     // bit 2 * tile + half: this lane's row is wanted
-  const uint16_t* p_b = nullptr;         // hi term of this lane's token at the next step
-  int64_t p_lo = p.lo - p.hi;            // to the lo term (elements)
-  bool p_on = false;                     // the lane's token uses the expert (and may be read)
+  const unsigned char* p_b = nullptr;    // this lane's column of the first MMA at the next step
+  size_t p_bj = 0;                       // to the next MMA's (bytes)
+  bool p_on = false;                     // the column's token uses the expert (and may be read)
   const float* p_sc = nullptr;           // FP8: scale of row `lane` of the step's 32 rows
-  const uint8_t* p_pow = nullptr;        // FP8: the token's exponents at the step (FC2)
+  const float* p_pow = nullptr;          // FP8: the token's power of two at the step
   bool p_sok = false;
   int p_step = 0, p_end = 0, p_kb = kb1; // next step, end of its segment, K blocks of a row
-  int p_inc = GW;                        // steps to the next (FC2: 1)
+  int p_inc = kWarps;                    // steps to the next (FC2: 1)
   int pn = -1, pu = 0, pa = a_first - 1; // claim; FC2 unit and active expert
   int n = 0;                             // claim being used; n + 1 is known too
   bool p_fc2 = false, fc1_done = false;
@@ -664,40 +670,43 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   int ready = 0;                         // of these, steps known to have arrived
   uint32_t p_at = 0, c_at = 0;           // ring offsets of the next step to issue / to use
 
+  const size_t x_term = (size_t)T * H * EB, a_term = (size_t)T * k * I * EB;  // bytes of a term
+  p_bj = TPG * x_term;
   auto start_fc2 = [&]() {
     p_fc2 = true;
     p_kb = kb2;
     p_inc = 1;
     p_ts = 16 * rb2;
     p_hs = 8 * rb2;
-    p_lo = p.act_lo - p.act_hi;
+    p_bj = TPG * a_term;
   };
   // Moves to the next segment that has a step for this warp; false when there is
   // none or it is not known yet.
   auto next_segment = [&]() -> bool {
     if (!p_fc2) {
-      if (pn > n || gw >= S1) return false;
-      if (sm.claim[grp][(pn + 1) & 3] >= claims) start_fc2();
+      if (pn > n || warp >= S1) return false;
+      if (sm.claim[(pn + 1) & 3] >= claims) start_fc2();
     }
     if (!p_fc2) {
       ++pn;
-      const int c = sm.claim[grp][pn & 3];
+      const int c = sm.claim[pn & 3];
       int a, i0;
       claim_at(c, a, i0);
       const int e = sm.expert[a];
-      p_step = gw;
+      p_step = warp;
       p_end = S1;
       p_src = static_cast<const unsigned char*>(p.w13) + ((size_t)e * 2 * I + i0 + g) * rb1 + p_step * 128 +
               tq * 16;
       p_ts = 8 * rb1;
       p_hs = (uint32_t)I * rb1;
       p_ok = c < pairs ? 15u : 3u;
-      p_on = col && ((sm.mask[a] >> g) & 1u);
-      p_b = p.hi + (size_t)(p_on ? g : 0) * H + p_step * 2 * KE + tq * EPC;
+      p_on = (sm.mask[a] >> tok) & 1u;
+      p_b = p.xt + (size_t)(g % TPG) * x_term + (size_t)(p_on ? tok : 0) * rb1 + p_step * 128 + tq * 16;
       if constexpr (FP8) {
         const int row = i0 + (lane & 7) + ((lane & 8) ? I : 0) + ((lane & 16) ? 8 : 0);
         p_sok = c < pairs || lane < 16;
         p_sc = p.s13 + ((size_t)e * (2 * I >> rs) + ((p_sok ? row : 0) >> rs)) * kg1 + p_step * ks;
+        p_pow = p.xpow + (p_on ? tok : 0) * P1 + p_step;
       }
       return true;
     }
@@ -718,31 +727,26 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     p_ok = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) p_ok |= (row0 + g + 8 * i < n1 ? 1u : 0u) << i;
-    const int pr = sm.pair[pa][g];
+    const int pr = sm.pair[pa][tok];
     p_on = pr >= 0 && fc1_done;
-    p_b = p.act_hi + (size_t)(pr >= 0 ? pr : 0) * I + p_step * 2 * KE + tq * EPC;
+    p_b = p.at + (size_t)(g % TPG) * a_term + (size_t)(pr >= 0 ? pr : 0) * rb2 + p_step * 128 + tq * 16;
     if constexpr (FP8) {
-      p_pow = p.act_pow + (size_t)(pr >= 0 ? pr : 0) * (I >> 3) + p_step * 16 + (tq & 1) * 8;
+      p_pow = p.apow + (pr >= 0 ? pr : 0) * P2 + p_step;
       p_sok = row0 + lane < n1;
       p_sc = p.s2 + ((size_t)e * (H >> rs) + ((p_sok ? row0 + lane : 0) >> rs)) * kg2 + p_step * ks;
     }
     return true;
   };
   // This lane's activations of a step into the stage at ring offset `at`.
-  auto copy_b = [&](uint32_t at, const uint16_t* b, int64_t lo, const uint8_t* pw, bool two) {
+  auto copy_b = [&](uint32_t at, const unsigned char* b, size_t bj, const float* pw, bool two) {
+    const uint32_t dst = ring_u + at + kStepA + lane * 16;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      if (FP8 && kb && !two) break;
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const uint16_t* src = b + kb * KE + q * 8;
-        const uint32_t dst = ring_u + at + kStepA + lane * 16 + (kb * 2 * Q + q) * R::kPieceB;
-        cp_async16(dst, src);
-        cp_async16(dst + Q * R::kPieceB, src + lo);
-      }
+    for (int j = 0; j < NJ; ++j) {
+      cp_async16(dst + j * 512, b + j * bj);
+      if (two) cp_async16(dst + (NJ + j) * 512, b + j * bj + 64);
     }
-    // (lane tq of a token: the 8 exponents of K block tq)
-    if (FP8 && pw && tq < (two ? 2 : 1)) cp_async8(ring_u + at + R::kPowAt + tq * 64 + g * 8, pw);
+    // (the token's first lane)
+    if (FP8 && lane % (4 * TPG) == 0) cp_async4(ring_u + at + R::kPowAt + tok * 4, pw);
   };
   // Keeps the ring full as far as the steps are known.
   auto top_up = [&]() {
@@ -770,145 +774,144 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
           }
         }
       }
-      if (p_on) copy_b(p_at, p_b, p_lo, FP8 && p_fc2 ? p_pow : nullptr, two);
+      if (p_on) copy_b(p_at, p_b, p_bj, p_pow, two);
       if (FP8 && p_sok) cp_async4(ring_u + p_at + R::kScaleAt + lane * 4, p_sc);
       cp_commit();
       ++flying;
       p_at = p_at == (R::kDepth - 1) * R::kStage ? 0 : p_at + R::kStage;
       p_src += p_inc * 128;
-      p_b += p_inc * 2 * KE;
+      p_b += p_inc * 128;
       if constexpr (FP8) {
         p_sc += p_inc * ks;
-        p_pow += p_inc * 16;
+        p_pow += p_inc;
       }
       p_step += p_inc;
     }
   };
 
-  // One step: h/l[tile] += weights of the step * the hi / lo activations.  What
-  // a lane did not copy (rows that are not wanted, tokens that do not use the
-  // expert) is whatever the ring held: it only reaches sums that are not used.
-  struct Acc {
-    float h[2][4], l[2][4];
-  };
-  auto clear = [](Acc& a) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) a.h[i][j] = a.l[i][j] = 0.f;
-  };
-  // top: FC2 with FP8, the exponent that the activations' groups are brought to
-  // (0 otherwise).
-  auto multiply = [&](Acc& acc, float (&sc)[4], int top, bool second_tile, bool two) {
+  // One step: acc[MMA][tile] += weights of the step * the columns.  What a lane
+  // did not copy (rows that are not wanted, tokens that do not use the expert) is
+  // whatever the ring held: it only reaches sums that are not used.  FP8: s, the
+  // scales of the lane's rows times the powers of two of its two columns.
+  using Sums = float[NJ][2][4];
+  constexpr int NC = TPG > 1 ? 1 : 2;  // tokens of the lane's two columns
+  auto multiply = [&](Sums& acc, float (&s)[4][NC], bool second_tile, bool two) {
     if (ready > 0) --ready;
     else if (flying == R::kDepth) asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
     else cp_wait_all();
-    if (FP8) __syncwarp();  // scales and exponents were copied by other lanes of the warp
-    const unsigned char* st = ring + c_at + lane * 16;
-    const uint4* sp = reinterpret_cast<const uint4*>(st);
-    // (columns beyond TOK read another token's piece; they are not used)
-    const unsigned char* bp = ring + c_at + kStepA + ((g & (TOK - 1)) * 4 + tq) * 16;
+    if (FP8) __syncwarp();  // scales and powers were copied by other lanes of the warp
+    const uint4* sp = reinterpret_cast<const uint4*>(ring + c_at) + lane;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       if (FP8 && kb && !two) break;
-      uint4 h[Q], l[Q];
+      uint4 b[NJ];
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        h[q] = *reinterpret_cast<const uint4*>(bp + (kb * 2 * Q + q) * R::kPieceB);
-        l[q] = *reinterpret_cast<const uint4*>(bp + (kb * 2 * Q + Q + q) * R::kPieceB);
-      }
-      if (FP8 && top) {
-        const unsigned ex = *reinterpret_cast<const uint16_t*>(ring + c_at + R::kPowAt + kb * 64 + g * 8 + tq * 2);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          const int d = (int)((ex >> (8 * q)) & 255u) - top;  // <= 0: an exact power of two (0 below 2^-24)
-          const __half2 f2 = __float2half2_rn(__uint_as_float((uint32_t)max(127 + d, 0) << 23));
-          const uint32_t f = *reinterpret_cast<const uint32_t*>(&f2);
-          h[q] = hmul2x4(h[q], f);
-          l[q] = hmul2x4(l[q], f);
-        }
-      }
+      for (int j = 0; j < NJ; ++j) b[j] = sp[kStepA / 16 + (kb * NJ + j) * 32];
 #pragma unroll
       for (int tl = 0; tl < 2; ++tl) {
         if (tl && !second_tile) break;
-        const uint4 u0 = sp[((tl * 2 + 0) * 2 + kb) * 32], u1 = sp[((tl * 2 + 1) * 2 + kb) * 32];
-        if constexpr (!FP8) {
-          mma_16816<false>(acc.h[tl], u0.x, u1.x, u0.y, u1.y, h[0].x, h[0].y);
-          mma_16816<false>(acc.l[tl], u0.x, u1.x, u0.y, u1.y, l[0].x, l[0].y);
-          mma_16816<false>(acc.h[tl], u0.z, u1.z, u0.w, u1.w, h[0].z, h[0].w);
-          mma_16816<false>(acc.l[tl], u0.z, u1.z, u0.w, u1.w, l[0].z, l[0].w);
-        } else {
-          const uint32_t c0[4] = {u0.x, u0.y, u0.z, u0.w}, c1[4] = {u1.x, u1.y, u1.z, u1.w};
+        const uint4 lo = sp[((tl * 2 + 0) * 2 + kb) * 32], hi = sp[((tl * 2 + 1) * 2 + kb) * 32];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_f16(c0[m], a0, a2);
-            e4m3x4_f16(c1[m], a1, a3);
-            const uint4 hm = h[(m >> 1) % Q], lm = l[(m >> 1) % Q];
-            mma_16816<true>(acc.h[tl], a0, a1, a2, a3, (m & 1) ? hm.z : hm.x, (m & 1) ? hm.w : hm.y);
-            mma_16816<true>(acc.l[tl], a0, a1, a2, a3, (m & 1) ? lm.z : lm.x, (m & 1) ? lm.w : lm.y);
-          }
-        }
+        for (int j = 0; j < NJ; ++j) mma_piece<FP8>(acc[j][tl], lo, hi, b[j]);
       }
     }
     if constexpr (FP8) {
+      const float* pw = reinterpret_cast<const float*>(ring + c_at + R::kPowAt) + 2 * tq / TPG;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i] = *reinterpret_cast<const float*>(ring + c_at + R::kScaleAt + (g + 8 * i) * 4);
+      for (int i = 0; i < 4; ++i) {
+        const float w = *reinterpret_cast<const float*>(ring + c_at + R::kScaleAt + (g + 8 * i) * 4);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) s[i][c] = w * pw[c];
+      }
       __syncwarp();  // and are overwritten by them once all have read
     }
     --flying;
     c_at = c_at == (R::kDepth - 1) * R::kStage ? 0 : c_at + R::kStage;
   };
-  // tot += s * acc, s per row and f per column (bit i of `mask`: token i counts).
-  // A token outside the mask gets nothing (not 0 times a weight that may not be
-  // finite).
-  auto fold = [&](float (&tot)[2][4], Acc& acc, const float (&s)[4], const float (&f)[2], unsigned mask) {
+  // tot += s * acc for the tokens in `mask` (bit i: token i); acc = 0.  A token
+  // outside the mask gets nothing (not 0 times a weight that may not be finite).
+  auto fold = [&](Sums& tot, Sums& acc, const float (&s)[4][NC], unsigned mask) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((mask >> ((2 * tq + (i & 1)) / TPG)) & 1u) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int tl = 0; tl < 2; ++tl)
+            tot[j][tl][i] = FP8 ? fmaf(s[tl * 2 + (i >> 1)][(i & 1) % NC], acc[j][tl][i], tot[j][tl][i])
+                                : tot[j][tl][i] + acc[j][tl][i];
+      }
+#pragma unroll
+    for (int i = 0; i < NJ * 8; ++i) acc[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
+  };
+  // This warp's partial sums, the terms of a token added, into rd [2 tiles][16
+  // rows][8 tokens]; tot = 0.
+  auto store_red = [&](float* rd, Sums& tot) {
+    constexpr float kTerm[4] = {1.f, 0x1p-4f, 0x1p-8f, 0x1p-12f};
+    auto term = [&](int j, int c) { return FP8 ? kTerm[(j * TPG + c) & 3] : 1.f; };
 #pragma unroll
     for (int tl = 0; tl < 2; ++tl)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((mask >> (2 * tq + (i & 1))) & 1u) {
-          const float v = acc.h[tl][i] + acc.l[tl][i];
-          tot[tl][i] = FP8 ? fmaf(s[tl * 2 + (i >> 1)] * f[i & 1], v, tot[tl][i]) : tot[tl][i] + v;
+      for (int h = 0; h < 2; ++h) {  // rows g and g + 8
+        float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+        for (int j = NJ - 1; j >= 0; --j) {  // (small terms first)
+          if (TPG == 4) {  // columns 2 tq, 2 tq + 1 are terms 2 (tq & 1), 2 (tq & 1) + 1
+            v1 += tot[j][tl][2 * h + 1] * ((tq & 1) ? kTerm[3] : kTerm[1]);
+            v0 += tot[j][tl][2 * h] * ((tq & 1) ? kTerm[2] : kTerm[0]);
+          } else if (TPG == 2) {
+            v0 += tot[j][tl][2 * h + 1] * term(j, 1);
+            v0 += tot[j][tl][2 * h] * term(j, 0);
+          } else {
+            v0 += tot[j][tl][2 * h] * term(j, 0);
+            v1 += tot[j][tl][2 * h + 1] * term(j, 0);
+          }
         }
-    clear(acc);
-  };
-  auto zero = [](float (&tot)[2][4]) {
+        float* d = rd + (tl * 16 + 8 * h + g) * 8;
+        if (TPG == 4) {
+          v0 += v1;
+          v0 += __shfl_xor_sync(0xffffffffu, v0, 1);
+          if (!(tq & 1)) d[tq >> 1] = v0;
+        } else if (TPG == 2) {
+          d[tq] = v0;
+        } else {
+          *reinterpret_cast<float2*>(d + 2 * tq) = make_float2(v0, v1);
+        }
+      }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tot[i >> 2][i & 3] = 0.f;
+    for (int i = 0; i < NJ * 8; ++i) tot[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
   };
-  auto store_red = [&](float* rd, const float (&tot)[2][4]) {
-#pragma unroll
-    for (int tl = 0; tl < 2; ++tl) {
-      float* d = rd + (tl * 16 + g) * 8 + 2 * tq;
-      *reinterpret_cast<float2*>(d) = make_float2(tot[tl][0], tot[tl][1]);
-      *reinterpret_cast<float2*>(d + 64) = make_float2(tot[tl][2], tot[tl][3]);
+  // Thread 0 waits until *ctr >= want; false (for all) when the wait runs out.
+  auto wait_for = [&](const int* ctr, int want) -> bool {
+    if (tid == 0) {
+      const long long t0 = clock64();
+      int seen;
+      do {
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(ctr) : "memory");
+      } while (seen < want && clock64() - t0 < ptx::kSpinLimitCycles);
+      sm.flag = seen < want;
+      if (seen < want) flag_status(p.status, MOE_ERR_TIMEOUT);
+      __threadfence();
     }
-  };
-  auto group_sync = [&]() {
-    if (G == 1) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(32 * GW) : "memory");
+    __syncthreads();
+    const bool ok = !sm.flag;
+    __syncthreads();
+    return ok;
   };
 
-  // Partial sums of a warp: buffer `buf` of its group, [warps of the group][2
-  // tiles][16 rows][8 tokens].
-  float* red = red_all + grp * GW * kGroupRed;
   int buf = 0, my_tiles = 0;
-  float sc[4] = {}, tot[2][4];
-  Acc acc;
-  clear(acc);
-  zero(tot);
+  float sc[4][NC] = {};
+  Sums acc = {}, tot = {};
 
   // One loop over segments, so that the stream's code exists once: FC1 claims
   // (fc2 = false), then this warp's experts of each FC2 unit.
   bool fc2 = false;
   int u = 0, a = 0, i0 = 0;
   while (true) {
-    int step, end, inc, kbs, top = 0, next_claim = claims;
+    int step, end, inc, kbs, next_claim = claims;
     unsigned mask = 0;
     bool second = true;
-    float down[2] = {1.f, 1.f};
-    const int c = fc2 ? 0 : sm.claim[grp][n & 3];
+    const int c = fc2 ? 0 : sm.claim[n & 3];
     if (!fc2) {
       if (c >= claims) {
         // ---- all FC1 tiles done (each CTA's writes are visible before its count).
@@ -916,38 +919,71 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
         if (!p_fc2) start_fc2();
         top_up();
         __syncthreads();
-        if (tid == 0) {
-          sm.flag = 0;
-          const long long t0 = clock64();
-          int seen;
-          do {
-            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(p.ctr + 1) : "memory");
-          } while (seen < tiles && clock64() - t0 < ptx::kSpinLimitCycles);
-          if (seen < tiles) {
-            flag_status(p.status, MOE_ERR_TIMEOUT);
-            sm.flag = 1;
-          }
-          __threadfence();
-        }
-        __syncthreads();
-        if (sm.flag) {
+        int conv = 0;
+        if (FP8 && tid == 0) conv = atomicAdd(&p.ctr[3], 1);
+        if (!wait_for(p.ctr + 1, tiles)) {
           cp_wait_all();
           return;
         }
         if constexpr (FP8) {
-          if (tid < T * k) sm.pow[tid] = max(15, __ldcg(&p.ctr[kCtrPow + tid]));
+          // ---- the intermediate's terms, 128 columns of a pair to a warp, eight
+          // such units to a claim
+          const int units = T * k * P2;
+          while (true) {
+            if (tid == 0) sm.flag = conv;
+            __syncthreads();
+            const int first = sm.flag * kWarps;
+            __syncthreads();
+            if (first >= units) break;
+            const int pr = (first + warp) / P2, blk = first + warp - pr * P2;
+            const int at = blk * 128 + lane * 4;
+            if (first + warp < units) {
+              float v[4] = {}, m = 0.f;
+              bool bad = false;
+              if (at < I) {
+                const float4 q = __ldcg(reinterpret_cast<const float4*>(p.act + (size_t)pr * I + at));
+                v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                m = fmaxf(m, fabsf(v[i]));
+                bad = bad || !(fabsf(v[i]) <= FLT_MAX);
+              }
+              m = warp_max(m);
+              bad = __any_sync(0xffffffffu, bad);
+              const int ex = pow_exponent(m);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] *= pow_up(ex);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t q[1];
+                take_term(v, q);
+                if (at < I) *reinterpret_cast<uint32_t*>(p.at + i * a_term + (size_t)pr * I + at) = q[0];
+              }
+              if (lane == 0) p.apow[pr * P2 + blk] = bad ? NAN : pow_down(ex);
+            }
+            __syncthreads();
+            if (tid == 0) {
+              __threadfence();
+              atomicAdd(&p.ctr[4], min(kWarps, units - first));
+              conv = atomicAdd(&p.ctr[3], 1);
+            }
+          }
+          if (!wait_for(p.ctr + 4, units)) {
+            cp_wait_all();
+            return;
+          }
         }
         // the activations of the W2 steps already in flight
         fc1_done = true;
-        if (p_step < p_end) p_on = sm.pair[pa][g] >= 0;
+        if (p_step < p_end) p_on = sm.pair[pa][tok] >= 0;
         int qa = a_first, qs = s_first, qq = q0;
         uint32_t at = c_at;
         for (int left = flying; left > 0; --left) {
-          const int pr = sm.pair[qa][g];
+          const int pr = sm.pair[qa][tok];
           if (pr >= 0)
-            copy_b(at, p.act_hi + (size_t)pr * I + qs * 2 * KE + tq * EPC, p.act_lo - p.act_hi,
-                   FP8 ? p.act_pow + (size_t)pr * (I >> 3) + qs * 16 + (tq & 1) * 8 : nullptr,
-                   2 * qs + 1 < kb2);
+            copy_b(at, p.at + (size_t)(g % TPG) * a_term + (size_t)pr * rb2 + qs * 128 + tq * 16, TPG * a_term,
+                   p.apow + pr * P2 + qs, 2 * qs + 1 < kb2);
           at = at == (R::kDepth - 1) * R::kStage ? 0 : at + R::kStage;
           if (++qq == q1) {  // (a short unit: the next one's steps follow)
             qa = a_first;
@@ -969,11 +1005,11 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       claim_at(c, a, i0);
       mask = sm.mask[a];
       second = c < pairs;
-      step = gw;
+      step = warp;
       end = S1;
-      inc = GW;
+      inc = kWarps;
       kbs = kb1;
-      if (gw == 0 && lane == 0) next_claim = atomicAdd(&p.ctr[0], 1);  // used two claims from here
+      if (tid == 0) next_claim = atomicAdd(&p.ctr[0], 1);  // used two claims from here
     } else {
       if (n0 + 32 * u >= n1) break;
       second = n0 + 32 * u + 16 < n1;
@@ -981,44 +1017,27 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       kbs = kb2;
       step = a == a_first ? s_first : 0;
       end = min(S2, q1 - a * S2);  // (nothing for a warp without steps)
-      if (step < end) {
-        mask = sm.mask[a];
-        if constexpr (FP8) {  // the pair's exponent of the lane's token, and its power for the two columns
-          const int pr = sm.pair[a][g], c0 = sm.pair[a][2 * tq], c1 = sm.pair[a][2 * tq + 1];
-          top = pr >= 0 ? sm.pow[pr] : 15;
-          if (c0 >= 0) down[0] = pow_down(sm.pow[c0]);
-          if (c1 >= 0) down[1] = pow_down(sm.pow[c1]);
-        }
-      }
+      if (step < end) mask = sm.mask[a];
     }
 #pragma unroll 1
     for (; step < end; step += inc) {
       top_up();
-      multiply(acc, sc, top, second, 2 * step + 1 < kbs);
-      if constexpr (FP8) {
-        if (!fc2) {
-          const float2 d = *reinterpret_cast<const float2*>(&sm.xpow[sm.chunk[step]][2 * tq]);
-          down[0] = d.x;
-          down[1] = d.y;
-        }
-        fold(tot, acc, sc, down, mask);
-      }
+      multiply(acc, sc, second, 2 * step + 1 < kbs);
+      if constexpr (FP8) fold(tot, acc, sc, mask);
     }
-    if constexpr (!FP8) fold(tot, acc, sc, down, mask);
+    if constexpr (!FP8) fold(tot, acc, sc, mask);
     if (fc2 && (a + 1) * S2 < q1) {  // the unit's next expert
       ++a;
       continue;
     }
-    float* rd = red + buf * (GW * kGroupRed / 2);
+    store_red(red[buf] + warp * 256, tot);
+    if (!fc2 && tid == 0) sm.claim[(n + 2) & 3] = next_claim;
+    __syncthreads();
     if (fc2) {
-      // ---- the unit's output rows: the partial sums of all warps
-      rd = red_all + buf * (kWarps * kGroupRed / 2);
-      store_red(rd + warp * 256, tot);
-      zero(tot);
-      __syncthreads();
+      // ---- the unit's output rows
       const int row = n0 + 32 * u + lane, t = warp;
       if (t < T && row < n1) {
-        const float* s = rd + lane * 8 + t;
+        const float* s = red[buf] + lane * 8 + t;
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += s[w * 256];
@@ -1029,54 +1048,38 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       ++u;
       a = a_first;
     } else {
-      // ---- the claim's intermediate columns: 16 lanes a token
-      store_red(rd + gw * 256, tot);
-      zero(tot);
-      if (gw == 0 && lane == 0) sm.claim[grp][(n + 2) & 3] = next_claim;
-      group_sync();
-      const int il = lane & 15;
-      // G = 1: warp t, token t, each half warp half of the partial sums;
-      // G = 2: two tokens a warp
-      const int t = G == 1 ? gw : 2 * gw + (lane >> 4);
-      if (G == 1 ? (mask >> t) & 1u : (mask >> (2 * gw)) & 3u) {
-        const float* s = rd + ((il >> 3) * 16 + (il & 7)) * 8 + t + (G == 1 ? (lane >> 4) * 1024 : 0);
+      // ---- the claim's 16 intermediate columns: warp t, token t; each half warp
+      // adds the partial sums of four warps
+      if ((mask >> warp) & 1u) {
+        const int il = lane & 15;
+        const float* s = red[buf] + ((il >> 3) * 16 + (il & 7)) * 8 + warp + (lane >> 4) * 1024;
         float gate = 0.f, up = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           gate += s[w * 256];
           up += s[w * 256 + 64];
         }
-        if (G == 1) {
-          gate += __shfl_xor_sync(0xffffffffu, gate, 16);
-          up += __shfl_xor_sync(0xffffffffu, up, 16);
-        }
-        const bool mine = ((mask >> t) & 1u) && il < (second ? 16 : 8) && (G == 2 || lane < 16);
-        const float r = sm.r[t];
-        // the routing weight goes into the intermediate, so FC2 adds the token's
-        // experts without a factor
-        float v = silu_f(gate * r) * (up * r) * sm.wt[a][t];
-        const int pr = max(sm.pair[a][t], 0);
-        if constexpr (FP8) {  // eight columns share a power of two
-          float m = fabsf(v);
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const int ex = pow_exponent(m);
-          if (mine && (il & 7) == 0) {
-            p.act_pow[(size_t)pr * (I >> 3) + (i0 + il) / 8] = (uint8_t)ex;
-            atomicMax(&p.ctr[kCtrPow + pr], ex);
+        gate += __shfl_xor_sync(0xffffffffu, gate, 16);
+        up += __shfl_xor_sync(0xffffffffu, up, 16);
+        if (lane < (second ? 16 : 8)) {
+          const float r = sm.r[warp];
+          // the routing weight goes into the intermediate, so FC2 adds the
+          // token's experts without a factor
+          const float v = silu_f(gate * r) * (up * r) * sm.wt[a][warp];
+          const size_t at = (size_t)sm.pair[a][warp] * I + i0 + il;
+          if constexpr (FP8) {
+            p.act[at] = v;
+          } else {
+            bf16* d = reinterpret_cast<bf16*>(p.at) + at;
+            split_bf16(v, d[0], d[(size_t)T * k * I]);
           }
-          v *= pow_up(ex);
-        }
-        if (mine) {
-          const size_t at = (size_t)pr * I + i0 + il;
-          split16<FP8>(v, p.act_hi[at], p.act_lo[at]);
         }
       }
       my_tiles += second ? 2 : 1;
-      // the group's last claim: its tiles are counted once its writes are there
-      if (sm.claim[grp][(n + 1) & 3] >= claims) {
-        group_sync();
-        if (gw == 0 && lane == 0) {
+      // the last claim: the tiles are counted once the writes are there
+      if (sm.claim[(n + 1) & 3] >= claims) {
+        __syncthreads();
+        if (tid == 0) {
           __threadfence();
           atomicAdd(&p.ctr[1], my_tiles);
         }
@@ -1134,10 +1137,10 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
 }
 
 struct LayerWs {
-  size_t hi, lo, ssq, xpow, part, ctr, act_hi, act_lo, act_pow, f, total;
+  size_t xt, at, xpow, apow, act, ssq, part, f, ctr, total;
 };
 
-LayerWs layer_layout(int T, int H, int E, int I, int k) {
+LayerWs layer_layout(int T, int H, int E, int I, int k, bool fp8) {
   LayerWs w{};
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -1146,28 +1149,27 @@ LayerWs layer_layout(int T, int H, int E, int I, int k) {
     return at;
   };
   const size_t t = T > 0 ? T : 1;
-  w.hi = take(t * H * 2);
-  w.lo = take(t * H * 2);
+  w.xt = take(t * H * 4);  // two terms of two bytes or four of one
+  w.at = take(t * k * I * 4);
+  w.xpow = take(fp8 ? t * ((H + 127) / 128) * 4 : 0);
+  w.apow = take(fp8 ? t * k * ((I + 127) / 128) * 4 : 0);
+  w.act = take(fp8 ? t * k * I * 4 : 0);
   w.ssq = take((size_t)kLayerChunks * kLayerMaxT * 4);
-  w.xpow = take((size_t)kLayerChunks * kLayerMaxT * 4);
   w.part = take((size_t)kLayerChunks * t * E * 4);
-  w.ctr = take(kCtrInts * 4);
-  w.act_hi = take(t * k * I * 2);
-  w.act_lo = take(t * k * I * 2);
-  w.act_pow = take(t * k * (I / 8));
   w.f = take(t * H * 4);
+  w.ctr = take(kCtrInts * 4);
   w.total = o;
   return w;
 }
 
 }  // namespace
 
-size_t layer_workspace_bytes(int T, int H, int E, int I, int k) {
-  return layer_layout(T, H, E, I, k).total;
+size_t layer_workspace_bytes(int T, int H, int E, int I, int k, bool fp8) {
+  return layer_layout(T, H, E, I, k, fp8).total;
 }
 
 cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* status, cudaStream_t st) {
-  const LayerWs w = layer_layout(a.T, a.H, a.E, a.I, a.k);
+  const LayerWs w = layer_layout(a.T, a.H, a.E, a.I, a.k, a.fp8);
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   LayerP p{};
   p.x = static_cast<const bf16*>(a.x);
@@ -1191,13 +1193,12 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
   p.k = a.k;
   p.block_scales = a.block_scales;
   p.eps = a.eps;
-  p.hi = reinterpret_cast<uint16_t*>(ws + w.hi);
-  p.lo = reinterpret_cast<uint16_t*>(ws + w.lo);
-  p.act_hi = reinterpret_cast<uint16_t*>(ws + w.act_hi);
-  p.act_lo = reinterpret_cast<uint16_t*>(ws + w.act_lo);
-  p.act_pow = ws + w.act_pow;
-  p.ssq = reinterpret_cast<float*>(ws + w.ssq);
+  p.xt = ws + w.xt;
+  p.at = ws + w.at;
   p.xpow = reinterpret_cast<float*>(ws + w.xpow);
+  p.apow = reinterpret_cast<float*>(ws + w.apow);
+  p.act = reinterpret_cast<float*>(ws + w.act);
+  p.ssq = reinterpret_cast<float*>(ws + w.ssq);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.f = reinterpret_cast<float*>(ws + w.f);
   p.ctr = reinterpret_cast<int*>(ws + w.ctr);
@@ -1216,12 +1217,21 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
   e = launch_kernel(route, dim3(kLayerChunks, a.router_w ? (a.E + 31) / 32 : 1), dim3(32 * kRouteWarps),
                     (size_t)route_smem, st, p);
   if (e != cudaSuccess) return e;
-  auto kern = a.fp8 ? layer_experts_kernel<true, 8> : layer_experts_kernel<false, 8>;
-  int smem = a.fp8 ? Ring<true, 8>::kBytes : Ring<false, 8>::kBytes;
-  if (a.T <= 4) {
-    kern = a.fp8 ? layer_experts_kernel<true, 4> : layer_experts_kernel<false, 4>;
-    smem = a.fp8 ? Ring<true, 4>::kBytes : Ring<false, 4>::kBytes;
+  auto kern = layer_experts_kernel<false, 8>;
+  int smem = Ring<false, 8>::kBytes;
+#define MOE_LAYER_KERNEL(F, TOK)          \
+  {                                       \
+    kern = layer_experts_kernel<F, TOK>;  \
+    smem = Ring<F, TOK>::kBytes;          \
   }
+  if (a.fp8) {
+    if (a.T <= 2) MOE_LAYER_KERNEL(true, 2)
+    else if (a.T <= 4) MOE_LAYER_KERNEL(true, 4)
+    else MOE_LAYER_KERNEL(true, 8)
+  } else if (a.T <= 4) {
+    MOE_LAYER_KERNEL(false, 4)
+  }
+#undef MOE_LAYER_KERNEL
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(sms), dim3(kThreadsL), smem, st, p, tail ? *tail : TailP{},

@@ -46,7 +46,7 @@ struct LayerArgs {
   float eps;
 };
 
-size_t layer_workspace_bytes(int T, int H, int E, int I, int k);
+size_t layer_workspace_bytes(int T, int H, int E, int I, int k, bool fp8);
 cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* status, cudaStream_t st);
 
 }  // namespace moe
