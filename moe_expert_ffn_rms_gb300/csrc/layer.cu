@@ -23,17 +23,17 @@
 // Claiming the FC1 tiles from a counter means the wait needs no co-residency:
 // a CTA that has not started holds no tile.
 //
-// Products: the weights are the 16-row operand of MMAs with 8 columns and fp32
-// accumulation; the columns are the tokens' activations in several terms, so
-// that neither x_hat nor the intermediate is rounded to the weights' type:
-//   bf16 weights  m16n8k16, two bf16 terms hi + lo (16 bits of mantissa)
-//   E4M3 weights  m16n8k32, four E4M3 terms q0 + q1/16 + q2/256 + q3/4096 of
-//                 4 bits each.  The codes go to the tensor cores as they are
-//                 (measured: 4.5 cycles per m16n8k32 against 8 per m16n8k16, and
-//                 no conversion: 64 instructions of a warp's step otherwise).
-//                 E4M3 has little range, so each token and 128 columns share a
-//                 power of two, applied with the weight scale after a step.
-// With T <= 4 (E4M3: 2) tokens all terms of a token fit one MMA's columns.
+// Products: the weights are the 16 x 16 operand of m16n8k16 MMAs with fp32
+// accumulation; the 8 columns are the tokens' activations in two 16-bit terms
+// hi + lo, so that neither x_hat nor the intermediate is rounded to 16 bits.  With
+// T <= 4 both terms of a token fit one MMA's columns.
+//   bf16 weights  bf16 terms (16 bits of mantissa)
+//   E4M3 weights  fp16 terms (22 bits): E4M3 -> fp16 is exact and one instruction
+//                 for two weights, E4M3 -> bf16 four.  fp16 has little range, so
+//                 a token's 128 columns share a power of two, applied with the
+//                 weight scale after a step.  (mma.sync on E4M3 itself is no way
+//                 around the conversion: it runs as one, 51 cycles per m16n8k32
+//                 against 22 per m16n8k16 with operands from shared memory.)
 //
 // A warp reads its own operands: each lane copies exactly the 16-byte pieces it
 // will feed to its MMAs into its own part of shared memory (cp.async, a few
@@ -63,20 +63,20 @@ constexpr int kThreadsL = 32 * kWarps;
 
 // TOK: tokens that the columns have room for (T <= TOK).  Column c of MMA j holds
 // term j * kTpg + c % kTpg of token c / kTpg.
-template <bool FP8, int TOK>
+template <int TOK>
 struct Cols {
-  static constexpr int kTerms = FP8 ? 4 : 2;
-  static constexpr int kTpg = 8 / TOK;             // terms of a token per MMA
-  static constexpr int kMmas = kTerms / kTpg;      // MMAs per weight tile and K
+  static constexpr int kTpg = 8 / TOK;     // terms of a token per MMA
+  static constexpr int kMmas = 2 / kTpg;   // MMAs per weight tile and K
 };
 
 // Per-warp stage of the copy ring: weights [2 tiles][2 row halves][2 K blocks]
-// [32 lanes] of 16 bytes; activations [2 K blocks][MMAs][32 lanes] of 16 bytes;
-// FP8: the scales of the 32 rows and the powers of two of the tokens.
+// [32 lanes] of 16 bytes; activations [2 K blocks][MMAs][pieces][32 lanes] of 16
+// bytes; FP8: the scales of the 32 rows and the powers of two of the tokens.
 constexpr int kStepA = 4096;
 template <bool FP8, int TOK>
 struct Ring {
-  static constexpr int kScaleAt = kStepA + 2 * Cols<FP8, TOK>::kMmas * 512;
+  static constexpr int kPieces = FP8 ? 2 : 1;  // of one term for 16 bytes of weights
+  static constexpr int kScaleAt = kStepA + 2 * Cols<TOK>::kMmas * kPieces * 512;
   static constexpr int kPowAt = kScaleAt + 128;
   static constexpr int kStage = kScaleAt + (FP8 ? 128 + 64 : 0);
   static constexpr int kDepth = (200 << 10) / (kWarps * kStage);  // 3 .. 5 steps
@@ -105,8 +105,8 @@ struct LayerP {
   int T, H, E, I, k, block_scales;
   float eps;
   // workspace
-  unsigned char* xt;   // terms of x w [terms][T, H], bf16 or E4M3
-  unsigned char* at;   // terms of the intermediate [terms][T k, I], times the routing weight
+  uint16_t* xt;        // terms of x w [2][T, H], bf16 or (FP8) fp16
+  uint16_t* at;        // terms of the intermediate [2][T k, I], times the routing weight
   float* xpow;         // FP8: powers of two of x w [T, H / 128]
   float* apow;         // FP8: of the intermediate [T k, I / 128]
   float* act;          // FP8: the intermediate [T k, I]
@@ -131,37 +131,29 @@ __host__ __device__ inline Chunk layer_chunk(int H, int c) {
   return ch;
 }
 
-// bf16 terms of v.
-MOE_DEV void split_bf16(float v, bf16& hi, bf16& lo) {
-  hi = __float2bfloat16_rn(v);
-  lo = __float2bfloat16_rn(v - __bfloat162float(hi));
+// v in two 16-bit terms.
+template <bool F16>
+MOE_DEV void split16(float v, uint16_t& hi, uint16_t& lo) {
+  if (F16) {
+    const __half h = __float2half_rn(v);
+    hi = __half_as_ushort(h);
+    lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
+  } else {
+    const bf16 h = __float2bfloat16_rn(v);
+    hi = __bfloat16_as_ushort(h);
+    lo = __bfloat16_as_ushort(__float2bfloat16_rn(v - __bfloat162float(h)));
+  }
 }
 
-// E4M3 terms.  Values of which the largest magnitude m has the biased exponent e
-// are scaled by 2^(134 - e), to below 256, and the products by 2^(e - 134).
-// Magnitudes below 2^-112 count as that.  Where a value is not finite the factor
-// is NaN: an E4M3 term cannot hold an infinity.
+// fp16 terms: values of which the largest magnitude m has the biased exponent e
+// are scaled by 2^(141 - e), to below 2^15, and the products by 2^(e - 141).
+// Magnitudes below 2^-112 count as that; infinities and NaN stay what they are.
 MOE_DEV int pow_exponent(float m) {
   const int e = (int)((__float_as_uint(m) >> 23) & 255u);
   return e < 15 ? 15 : (e > 254 ? 254 : e);
 }
-MOE_DEV float pow_up(int e) { return __uint_as_float((uint32_t)(261 - e) << 23); }
-MOE_DEV float pow_down(int e) { return __uint_as_float((uint32_t)(e - 7) << 23); }
-
-// The next term of N scaled values: their E4M3 codes; v becomes 16 times what is
-// left.
-template <int N>
-MOE_DEV void take_term(float (&v)[N], uint32_t (&codes)[N / 4]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, __NV_E4M3);
-    const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-    v[i] = (v[i] - b.x) * 16.f;
-    v[i + 1] = (v[i + 1] - b.y) * 16.f;
-    if (i % 4 == 0) codes[i / 4] = c;
-    else codes[i / 4] |= (uint32_t)c << 16;
-  }
-}
+MOE_DEV float pow_up(int e) { return __uint_as_float((uint32_t)(268 - e) << 23); }
+MOE_DEV float pow_down(int e) { return __uint_as_float((uint32_t)(e - 14) << 23); }
 
 // ------------------------------------------------------------------ launch 1 --
 // Grid (kLayerChunks, groups of 32 experts): K chunk c, experts 32y .. 32y+31.
@@ -216,36 +208,24 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
       }
       if (blockIdx.y == 0) {
         const size_t at = row + v * 8, term = (size_t)p.T * p.H;
+        float up = 1.f;
         if (FP8) {  // 16 lanes share a power of two
           float m = 0.f;
-          bool bad = false;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            m = fmaxf(m, fabsf(a[q]));
-            bad = bad || !(fabsf(a[q]) <= FLT_MAX);
-          }
+          for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(a[q]));
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 16)) & 0xffffu;
           const int ex = pow_exponent(m);
-          if (on && v < rows >> 3) {
+          up = pow_up(ex);
+          if (on && v < rows >> 3 && (lane & 15) == 0)
+            p.xpow[warp * ((p.H + 127) >> 7) + ((k0 + v * 8) >> 7)] = pow_down(ex);
+        }
+        if (on && v < rows >> 3) {
+          __align__(16) uint16_t hi[8], lo[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) a[q] *= pow_up(ex);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t c[2];
-              take_term(a, c);
-              *reinterpret_cast<uint2*>(p.xt + i * term + at) = make_uint2(c[0], c[1]);
-            }
-            if ((lane & 15) == 0)
-              p.xpow[warp * ((p.H + 127) >> 7) + ((k0 + v * 8) >> 7)] = bad ? NAN : pow_down(ex);
-          }
-        } else if (on && v < rows >> 3) {
-          __align__(16) bf16 hi[8], lo[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) split_bf16(a[q], hi[q], lo[q]);
-          *reinterpret_cast<uint4*>(p.xt + 2 * at) = *reinterpret_cast<uint4*>(hi);
-          *reinterpret_cast<uint4*>(p.xt + 2 * (term + at)) = *reinterpret_cast<uint4*>(lo);
+          for (int q = 0; q < 8; ++q) split16<FP8>(a[q] * up, hi[q], lo[q]);
+          *reinterpret_cast<uint4*>(p.xt + at) = *reinterpret_cast<uint4*>(hi);
+          *reinterpret_cast<uint4*>(p.xt + term + at) = *reinterpret_cast<uint4*>(lo);
         }
       }
     }
@@ -300,22 +280,27 @@ MOE_DEV void cp_async4(uint32_t dst, const void* src) {
 MOE_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 MOE_DEV void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// c += the 16 weight rows (pieces lo, hi: rows g and g + 8) times the 8 columns,
-// over the K elements of one 16-byte piece per lane.
-template <bool FP8>
-MOE_DEV void mma_piece(float (&c)[4], const uint4& lo, const uint4& hi, const uint4& b) {
-#define MOE_MMA(KIND, A0, A1, A2, A3, B0, B1)                                                   \
-  asm("mma.sync.aligned." KIND " {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};" \
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                          \
-      : "r"(A0), "r"(A1), "r"(A2), "r"(A3), "r"(B0), "r"(B1))
-  if (FP8) {
-    MOE_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32", lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-    MOE_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32", lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-  } else {
-    MOE_MMA("m16n8k16.row.col.f32.bf16.bf16.f32", lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-    MOE_MMA("m16n8k16.row.col.f32.bf16.bf16.f32", lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-  }
-#undef MOE_MMA
+template <bool F16>
+MOE_DEV void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                       uint32_t b1) {
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four E4M3 codes as two fp16 pairs (exact).
+MOE_DEV void e4m3x4_f16(uint32_t q, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(q));
 }
 
 struct LayerSmem {
@@ -520,10 +505,10 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
 template <bool FP8, int TOK>
 __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
                                                                      int has_tail) {
-  constexpr int EB = FP8 ? 1 : 2;   // bytes per weight, and per activation term
+  constexpr int EB = FP8 ? 1 : 2;  // bytes per weight
   using R = Ring<FP8, TOK>;
-  using C = Cols<FP8, TOK>;
-  constexpr int NJ = C::kMmas, TPG = C::kTpg;
+  constexpr int NJ = Cols<TOK>::kMmas, TPG = Cols<TOK>::kTpg;
+  constexpr int Q = R::kPieces, KE = 64 / EB;  // K elements of 64 bytes of weights
   extern __shared__ __align__(128) unsigned char ring_all[];
   __shared__ LayerSmem sm;
   __shared__ __align__(16) float red[2][kRed];
@@ -531,6 +516,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tq = lane & 3;  // MMA fragment row / column, K group
   const int tok = g / TPG;                 // token of this lane's column
+  const bool first_lane = lane % (4 * TPG) == 0;
   const int T = p.T, H = p.H, E = p.E, I = p.I, k = p.k;
   sm.used[tid] = 0;
   pdl_trigger();
@@ -655,8 +641,8 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   const unsigned char* p_src = nullptr;  // this lane's first row at the next step
   uint32_t p_ts = 0, p_hs = 0;           // to the second tile, to a tile's lower 8 rows (bytes)
   unsigned p_ok = 0;                     // bit 2 * tile + half: this lane's row is wanted
-  const unsigned char* p_b = nullptr;    // this lane's column of the first MMA at the next step
-  size_t p_bj = 0;                       // to the next MMA's (bytes)
+  const uint16_t* p_b = nullptr;         // this lane's column of the first MMA at the next step
+  size_t p_bj = 0;                       // to the next MMA's (elements)
   bool p_on = false;                     // the column's token uses the expert (and may be read)
   const float* p_sc = nullptr;           // FP8: scale of row `lane` of the step's 32 rows
   const float* p_pow = nullptr;          // FP8: the token's power of two at the step
@@ -667,10 +653,9 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   int n = 0;                             // claim being used; n + 1 is known too
   bool p_fc2 = false, fc1_done = false;
   int flying = 0;                        // steps issued and not yet used
-  int ready = 0;                         // of these, steps known to have arrived
   uint32_t p_at = 0, c_at = 0;           // ring offsets of the next step to issue / to use
 
-  const size_t x_term = (size_t)T * H * EB, a_term = (size_t)T * k * I * EB;  // bytes of a term
+  const size_t x_term = (size_t)T * H, a_term = (size_t)T * k * I;  // elements of a term
   p_bj = TPG * x_term;
   auto start_fc2 = [&]() {
     p_fc2 = true;
@@ -701,7 +686,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       p_hs = (uint32_t)I * rb1;
       p_ok = c < pairs ? 15u : 3u;
       p_on = (sm.mask[a] >> tok) & 1u;
-      p_b = p.xt + (size_t)(g % TPG) * x_term + (size_t)(p_on ? tok : 0) * rb1 + p_step * 128 + tq * 16;
+      p_b = p.xt + (size_t)(g % TPG) * x_term + (size_t)(p_on ? tok : 0) * H + p_step * 2 * KE + tq * 8 * Q;
       if constexpr (FP8) {
         const int row = i0 + (lane & 7) + ((lane & 8) ? I : 0) + ((lane & 16) ? 8 : 0);
         p_sok = c < pairs || lane < 16;
@@ -729,7 +714,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     for (int i = 0; i < 4; ++i) p_ok |= (row0 + g + 8 * i < n1 ? 1u : 0u) << i;
     const int pr = sm.pair[pa][tok];
     p_on = pr >= 0 && fc1_done;
-    p_b = p.at + (size_t)(g % TPG) * a_term + (size_t)(pr >= 0 ? pr : 0) * rb2 + p_step * 128 + tq * 16;
+    p_b = p.at + (size_t)(g % TPG) * a_term + (size_t)(pr >= 0 ? pr : 0) * I + p_step * 2 * KE + tq * 8 * Q;
     if constexpr (FP8) {
       p_pow = p.apow + (pr >= 0 ? pr : 0) * P2 + p_step;
       p_sok = row0 + lane < n1;
@@ -738,15 +723,18 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     return true;
   };
   // This lane's activations of a step into the stage at ring offset `at`.
-  auto copy_b = [&](uint32_t at, const unsigned char* b, size_t bj, const float* pw, bool two) {
+  auto copy_b = [&](uint32_t at, const uint16_t* b, size_t bj, const float* pw, bool two) {
     const uint32_t dst = ring_u + at + kStepA + lane * 16;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      cp_async16(dst + j * 512, b + j * bj);
-      if (two) cp_async16(dst + (NJ + j) * 512, b + j * bj + 64);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        cp_async16(dst + (j * Q + q) * 512, b + j * bj + q * 8);
+        if (two) cp_async16(dst + ((NJ + j) * Q + q) * 512, b + j * bj + KE + q * 8);
+      }
     }
     // (the token's first lane)
-    if (FP8 && lane % (4 * TPG) == 0) cp_async4(ring_u + at + R::kPowAt + tok * 4, pw);
+    if (FP8 && first_lane) cp_async4(ring_u + at + R::kPowAt + tok * 4, pw);
   };
   // Keeps the ring full as far as the steps are known.
   auto top_up = [&]() {
@@ -773,6 +761,14 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
             if (two) cp_async16(dst + 1024 * i + 512, src[i] + 64);
           }
         }
+        if (!two) {  // a row's odd last block: its partner counts as zeros on both sides
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+          uint4* st = reinterpret_cast<uint4*>(ring + p_at) + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st[(2 * i + 1) * 32] = z;
+#pragma unroll
+          for (int j = 0; j < NJ * Q; ++j) st[kStepA / 16 + (NJ * Q + j) * 32] = z;
+        }
       }
       if (p_on) copy_b(p_at, p_b, p_bj, p_pow, two);
       if (FP8 && p_sok) cp_async4(ring_u + p_at + R::kScaleAt + lane * 4, p_sc);
@@ -780,7 +776,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       ++flying;
       p_at = p_at == (R::kDepth - 1) * R::kStage ? 0 : p_at + R::kStage;
       p_src += p_inc * 128;
-      p_b += p_inc * 128;
+      p_b += p_inc * 2 * KE;
       if constexpr (FP8) {
         p_sc += p_inc * ks;
         p_pow += p_inc;
@@ -795,24 +791,40 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   // scales of the lane's rows times the powers of two of its two columns.
   using Sums = float[NJ][2][4];
   constexpr int NC = TPG > 1 ? 1 : 2;  // tokens of the lane's two columns
-  auto multiply = [&](Sums& acc, float (&s)[4][NC], bool second_tile, bool two) {
-    if (ready > 0) --ready;
-    else if (flying == R::kDepth) asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
+  auto multiply = [&](Sums& acc, float (&s)[4][NC]) {
+    if (flying == R::kDepth) asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
     else cp_wait_all();
     if (FP8) __syncwarp();  // scales and powers were copied by other lanes of the warp
     const uint4* sp = reinterpret_cast<const uint4*>(ring + c_at) + lane;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      if (FP8 && kb && !two) break;
-      uint4 b[NJ];
+      uint4 b[NJ][Q];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) b[j] = sp[kStepA / 16 + (kb * NJ + j) * 32];
+      for (int j = 0; j < NJ * Q; ++j) b[j / Q][j % Q] = sp[kStepA / 16 + (kb * NJ * Q + j) * 32];
 #pragma unroll
       for (int tl = 0; tl < 2; ++tl) {
-        if (tl && !second_tile) break;
-        const uint4 lo = sp[((tl * 2 + 0) * 2 + kb) * 32], hi = sp[((tl * 2 + 1) * 2 + kb) * 32];
+        const uint4 lo = sp[((tl * 2 + 0) * 2 + kb) * 32], hi = sp[((tl * 2 + 1) * 2 + kb) * 32];  // rows g, g + 8
+        if constexpr (FP8) {
+          const uint32_t c0[4] = {lo.x, lo.y, lo.z, lo.w}, c1[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) mma_piece<FP8>(acc[j][tl], lo, hi, b[j]);
+          for (int m = 0; m < 4; ++m) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_f16(c0[m], a0, a2);
+            e4m3x4_f16(c1[m], a1, a3);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const uint4 v = b[j][(m >> 1) % Q];
+              mma_16816<true>(acc[j][tl], a0, a1, a2, a3, (m & 1) ? v.z : v.x, (m & 1) ? v.w : v.y);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            mma_16816<false>(acc[j][tl], lo.x, hi.x, lo.y, hi.y, b[j][0].x, b[j][0].y);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            mma_16816<false>(acc[j][tl], lo.z, hi.z, lo.w, hi.w, b[j][0].z, b[j][0].w);
+        }
       }
     }
     if constexpr (FP8) {
@@ -832,14 +844,18 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   // outside the mask gets nothing (not 0 times a weight that may not be finite).
   auto fold = [&](Sums& tot, Sums& acc, const float (&s)[4][NC], unsigned mask) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if ((mask >> ((2 * tq + (i & 1)) / TPG)) & 1u) {
+    for (int c = 0; c < NC; ++c)
+      if ((mask >> (2 * tq / TPG + c)) & 1u) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int i = 0; i < 4; ++i) {
+          if (NC == 2 && (i & 1) != c) continue;
 #pragma unroll
-          for (int tl = 0; tl < 2; ++tl)
-            tot[j][tl][i] = FP8 ? fmaf(s[tl * 2 + (i >> 1)][(i & 1) % NC], acc[j][tl][i], tot[j][tl][i])
-                                : tot[j][tl][i] + acc[j][tl][i];
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int tl = 0; tl < 2; ++tl)
+              tot[j][tl][i] = FP8 ? fmaf(s[tl * 2 + (i >> 1)][c], acc[j][tl][i], tot[j][tl][i])
+                                  : tot[j][tl][i] + acc[j][tl][i];
+        }
       }
 #pragma unroll
     for (int i = 0; i < NJ * 8; ++i) acc[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
@@ -847,36 +863,15 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   // This warp's partial sums, the terms of a token added, into rd [2 tiles][16
   // rows][8 tokens]; tot = 0.
   auto store_red = [&](float* rd, Sums& tot) {
-    constexpr float kTerm[4] = {1.f, 0x1p-4f, 0x1p-8f, 0x1p-12f};
-    auto term = [&](int j, int c) { return FP8 ? kTerm[(j * TPG + c) & 3] : 1.f; };
 #pragma unroll
     for (int tl = 0; tl < 2; ++tl)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // rows g and g + 8
-        float v0 = 0.f, v1 = 0.f;
-#pragma unroll
-        for (int j = NJ - 1; j >= 0; --j) {  // (small terms first)
-          if (TPG == 4) {  // columns 2 tq, 2 tq + 1 are terms 2 (tq & 1), 2 (tq & 1) + 1
-            v1 += tot[j][tl][2 * h + 1] * ((tq & 1) ? kTerm[3] : kTerm[1]);
-            v0 += tot[j][tl][2 * h] * ((tq & 1) ? kTerm[2] : kTerm[0]);
-          } else if (TPG == 2) {
-            v0 += tot[j][tl][2 * h + 1] * term(j, 1);
-            v0 += tot[j][tl][2 * h] * term(j, 0);
-          } else {
-            v0 += tot[j][tl][2 * h] * term(j, 0);
-            v1 += tot[j][tl][2 * h + 1] * term(j, 0);
-          }
-        }
         float* d = rd + (tl * 16 + 8 * h + g) * 8;
-        if (TPG == 4) {
-          v0 += v1;
-          v0 += __shfl_xor_sync(0xffffffffu, v0, 1);
-          if (!(tq & 1)) d[tq >> 1] = v0;
-        } else if (TPG == 2) {
-          d[tq] = v0;
-        } else {
-          *reinterpret_cast<float2*>(d + 2 * tq) = make_float2(v0, v1);
-        }
+        if (TPG == 2) d[tq] = tot[0][tl][2 * h] + tot[0][tl][2 * h + 1];
+        else
+          *reinterpret_cast<float2*>(d + 2 * tq) =
+              make_float2(tot[0][tl][2 * h] + tot[NJ - 1][tl][2 * h], tot[0][tl][2 * h + 1] + tot[NJ - 1][tl][2 * h + 1]);
       }
 #pragma unroll
     for (int i = 0; i < NJ * 8; ++i) tot[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
@@ -908,7 +903,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   bool fc2 = false;
   int u = 0, a = 0, i0 = 0;
   while (true) {
-    int step, end, inc, kbs, next_claim = claims;
+    int step, end, inc, next_claim = claims;
     unsigned mask = 0;
     bool second = true;
     const int c = fc2 ? 0 : sm.claim[n & 3];
@@ -938,29 +933,21 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
             const int pr = (first + warp) / P2, blk = first + warp - pr * P2;
             const int at = blk * 128 + lane * 4;
             if (first + warp < units) {
-              float v[4] = {}, m = 0.f;
-              bool bad = false;
-              if (at < I) {
-                const float4 q = __ldcg(reinterpret_cast<const float4*>(p.act + (size_t)pr * I + at));
-                v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                m = fmaxf(m, fabsf(v[i]));
-                bad = bad || !(fabsf(v[i]) <= FLT_MAX);
-              }
-              m = warp_max(m);
-              bad = __any_sync(0xffffffffu, bad);
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (at < I) v = __ldcg(reinterpret_cast<const float4*>(p.act + (size_t)pr * I + at));
+              const float m = warp_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
               const int ex = pow_exponent(m);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] *= pow_up(ex);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t q[1];
-                take_term(v, q);
-                if (at < I) *reinterpret_cast<uint32_t*>(p.at + i * a_term + (size_t)pr * I + at) = q[0];
+              const float up = pow_up(ex);
+              ushort4 hi, lo;
+              split16<true>(v.x * up, hi.x, lo.x);
+              split16<true>(v.y * up, hi.y, lo.y);
+              split16<true>(v.z * up, hi.z, lo.z);
+              split16<true>(v.w * up, hi.w, lo.w);
+              if (at < I) {
+                *reinterpret_cast<ushort4*>(p.at + (size_t)pr * I + at) = hi;
+                *reinterpret_cast<ushort4*>(p.at + a_term + (size_t)pr * I + at) = lo;
               }
-              if (lane == 0) p.apow[pr * P2 + blk] = bad ? NAN : pow_down(ex);
+              if (lane == 0) p.apow[pr * P2 + blk] = pow_down(ex);
             }
             __syncthreads();
             if (tid == 0) {
@@ -982,7 +969,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
         for (int left = flying; left > 0; --left) {
           const int pr = sm.pair[qa][tok];
           if (pr >= 0)
-            copy_b(at, p.at + (size_t)(g % TPG) * a_term + (size_t)pr * rb2 + qs * 128 + tq * 16, TPG * a_term,
+            copy_b(at, p.at + (size_t)(g % TPG) * a_term + (size_t)pr * I + qs * 2 * KE + tq * 8 * Q, TPG * a_term,
                    p.apow + pr * P2 + qs, 2 * qs + 1 < kb2);
           at = at == (R::kDepth - 1) * R::kStage ? 0 : at + R::kStage;
           if (++qq == q1) {  // (a short unit: the next one's steps follow)
@@ -995,7 +982,6 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
           }
         }
         cp_wait_all();
-        ready = flying;
         __syncthreads();
         fc2 = true;
         buf = 0;
@@ -1008,13 +994,10 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       step = warp;
       end = S1;
       inc = kWarps;
-      kbs = kb1;
       if (tid == 0) next_claim = atomicAdd(&p.ctr[0], 1);  // used two claims from here
     } else {
       if (n0 + 32 * u >= n1) break;
-      second = n0 + 32 * u + 16 < n1;
       inc = 1;
-      kbs = kb2;
       step = a == a_first ? s_first : 0;
       end = min(S2, q1 - a * S2);  // (nothing for a warp without steps)
       if (step < end) mask = sm.mask[a];
@@ -1022,7 +1005,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
 #pragma unroll 1
     for (; step < end; step += inc) {
       top_up();
-      multiply(acc, sc, second, 2 * step + 1 < kbs);
+      multiply(acc, sc);
       if constexpr (FP8) fold(tot, acc, sc, mask);
     }
     if constexpr (!FP8) fold(tot, acc, sc, mask);
@@ -1067,12 +1050,8 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
           // token's experts without a factor
           const float v = silu_f(gate * r) * (up * r) * sm.wt[a][warp];
           const size_t at = (size_t)sm.pair[a][warp] * I + i0 + il;
-          if constexpr (FP8) {
-            p.act[at] = v;
-          } else {
-            bf16* d = reinterpret_cast<bf16*>(p.at) + at;
-            split_bf16(v, d[0], d[(size_t)T * k * I]);
-          }
+          if constexpr (FP8) p.act[at] = v;
+          else split16<false>(v, p.at[at], p.at[at + a_term]);
         }
       }
       my_tiles += second ? 2 : 1;
@@ -1149,7 +1128,7 @@ LayerWs layer_layout(int T, int H, int E, int I, int k, bool fp8) {
     return at;
   };
   const size_t t = T > 0 ? T : 1;
-  w.xt = take(t * H * 4);  // two terms of two bytes or four of one
+  w.xt = take(t * H * 4);
   w.at = take(t * k * I * 4);
   w.xpow = take(fp8 ? t * ((H + 127) / 128) * 4 : 0);
   w.apow = take(fp8 ? t * k * ((I + 127) / 128) * 4 : 0);
@@ -1193,8 +1172,8 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
   p.k = a.k;
   p.block_scales = a.block_scales;
   p.eps = a.eps;
-  p.xt = ws + w.xt;
-  p.at = ws + w.at;
+  p.xt = reinterpret_cast<uint16_t*>(ws + w.xt);
+  p.at = reinterpret_cast<uint16_t*>(ws + w.at);
   p.xpow = reinterpret_cast<float*>(ws + w.xpow);
   p.apow = reinterpret_cast<float*>(ws + w.apow);
   p.act = reinterpret_cast<float*>(ws + w.act);
@@ -1225,8 +1204,7 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
     smem = Ring<F, TOK>::kBytes;          \
   }
   if (a.fp8) {
-    if (a.T <= 2) MOE_LAYER_KERNEL(true, 2)
-    else if (a.T <= 4) MOE_LAYER_KERNEL(true, 4)
+    if (a.T <= 4) MOE_LAYER_KERNEL(true, 4)
     else MOE_LAYER_KERNEL(true, 8)
   } else if (a.T <= 4) {
     MOE_LAYER_KERNEL(false, 4)
