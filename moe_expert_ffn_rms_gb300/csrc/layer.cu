@@ -35,14 +35,16 @@
 //                 around the conversion: it runs as one, 51 cycles per m16n8k32
 //                 against 22 per m16n8k16 with operands from shared memory.)
 //
-// A warp reads its own operands: each lane copies exactly the 16-byte pieces it
-// will feed to its MMAs into its own part of shared memory (cp.async, a few
-// steps ahead) and reads them back, so the stream needs no barrier, and the
-// first W2 pieces are already on their way while the CTA waits for the other
-// CTAs' FC1 tiles.  The order of the K elements inside a piece is the same for
-// both operands and therefore free.  The activations go the same way as the
-// weights: a plain load of them would wait behind the copies in flight (4 us of
-// them with 160 KB per SM).
+// Sixteen warps: eight consumers, each with a producer warp of its own that fills
+// the consumer's part of shared memory a few steps ahead (cp.async; a pair of
+// mbarriers per step).  The pieces lie as the consumer's lanes feed them to the
+// MMAs, so a step is 16-byte shared loads, conversions and MMAs and nothing else
+// (with the copies in the same warp the issue of their addresses set the rate).
+// The order of the K elements inside a piece is the same for both operands and
+// therefore free.  The activations go the same way as the weights: a plain load
+// of them would wait behind the copies in flight (4 us of them with 160 KB per
+// SM).  The first W2 pieces are on their way while the CTA waits for the other
+// CTAs' FC1 tiles.
 //
 // mma.sync and not tcgen05: at 8 columns the tensor work is 1/16 of what the
 // legacy instruction sustains at this memory rate, a fragment load straight from
@@ -59,7 +61,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kThreadsL = 32 * kWarps;
+constexpr int kThreadsL = 32 * kWarps;  // consumers; as many producers follow them
 
 // TOK: tokens that the columns have room for (T <= TOK).  Column c of MMA j holds
 // term j * kTpg + c % kTpg of token c / kTpg.
@@ -277,7 +279,15 @@ MOE_DEV void cp_async16(uint32_t dst, const void* src) {
 MOE_DEV void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-MOE_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// The same with `bytes` of 16 from src, the rest zeros.
+MOE_DEV void cp_async16z(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Arrives on the barrier once this thread's copies so far have landed.
+MOE_DEV void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
+MOE_DEV void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreadsL) : "memory"); }
 MOE_DEV void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <bool F16>
@@ -303,6 +313,8 @@ MOE_DEV void e4m3x4_f16(uint32_t q, uint32_t& lo, uint32_t& hi) {
       : "r"(q));
 }
 
+constexpr int kMaxDepth = 5;
+
 struct LayerSmem {
   int32_t ids[kLayerMaxT][kMaxTopK];
   float w[kLayerMaxT][kMaxTopK];
@@ -315,8 +327,13 @@ struct LayerSmem {
   float wt[kMaxPairs][kLayerMaxT];
   int warp_cnt[kWarps];
   int claim[4];
+  int published;  // newest claim index in claim[]
+  int fc1_done;
   int flag;
+  int abort;
+  int in_time;  // result of a wait, for all consumers
   float sum[kWarps];
+  uint64_t full[kWarps][kMaxDepth], empty[kWarps][kMaxDepth];
 };
 
 // Top-k of one token by one warp with the results of warp_topk (common.cuh):
@@ -409,14 +426,14 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
   const unsigned char* s_pw = s_gate + (size_t)H * 4;
   const unsigned char* s_nw = s_pw + (size_t)H * 2;
   if (staged) cp_wait_all();
-  __syncthreads();
+  consumer_sync();
   auto reduce = [&](float v, bool mx) {
     v = mx ? warp_max(v) : warp_sum(v);
     if (lane == 0) red[tid >> 5] = v;
-    __syncthreads();
+    consumer_sync();
     v = red[0];
     for (int w = 1; w < kWarps; ++w) v = mx ? fmaxf(v, red[w]) : v + red[w];
-    __syncthreads();
+    consumer_sync();
     return v;
   };
   float r = 1.f;
@@ -503,7 +520,7 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
 
 // FP8: E4M3 weights, one scale per (row >> rs) and K step * ks.
 template <bool FP8, int TOK>
-__global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
+__global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
                                                                      int has_tail) {
   constexpr int EB = FP8 ? 1 : 2;  // bytes per weight
   using R = Ring<FP8, TOK>;
@@ -518,14 +535,26 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   const int tok = g / TPG;                 // token of this lane's column
   const bool first_lane = lane % (4 * TPG) == 0;
   const int T = p.T, H = p.H, E = p.E, I = p.I, k = p.k;
-  sm.used[tid] = 0;
+  if (tid < kMaxExperts) sm.used[tid] = 0;
   pdl_trigger();
+  static_assert(R::kDepth <= kMaxDepth && kMaxExperts <= kThreadsL, "shared tables");
+  if (tid < kWarps) {
+    for (int i = 0; i < R::kDepth; ++i) {
+      ptx::mbar_init(&sm.full[tid][i], 32);
+      ptx::mbar_init(&sm.empty[tid][i], 1);
+    }
+    ptx::fence_mbar_init();
+  }
+  if (tid == 0) {
+    sm.published = 1;
+    sm.fc1_done = sm.abort = 0;
+  }
   __syncthreads();
   pdl_wait();
 
   // ---- routing (every CTA by itself; warp t: token t)
   int first_claim = 0;
-  if (tid == kThreadsL - 1) first_claim = atomicAdd(&p.ctr[0], 2);
+  if (tid == 2 * kThreadsL - 1) first_claim = atomicAdd(&p.ctr[0], 2);
   if (warp < T) {
     const float ss = lane < kLayerChunks ? __ldcg(&p.ssq[lane * kLayerMaxT + warp]) : 0.f;
     if (p.ids_in) {
@@ -554,16 +583,16 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       if (id < 0 || id >= E) flag_status(p.status, MOE_ERR_INVALID_ARG);
     }
   }
-  if (tid == kThreadsL - 1) {
+  if (tid == 2 * kThreadsL - 1) {
     sm.claim[0] = first_claim;
     sm.claim[1] = first_claim + 1;
   }
   __syncthreads();
   // active experts in ascending order (thread e: expert e; E <= 256)
   {
-    const unsigned mask = sm.used[tid];
+    const unsigned mask = tid < kMaxExperts ? sm.used[tid] : 0u;
     const unsigned act = __ballot_sync(0xffffffffu, mask != 0);
-    if (lane == 0) sm.warp_cnt[warp] = __popc(act);
+    if (lane == 0 && warp < kWarps) sm.warp_cnt[warp] = __popc(act);
     __syncthreads();
     if (mask) {
       int at = __popc(act & ((1u << lane) - 1));
@@ -613,8 +642,6 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
   const int S1 = (int)((rb1 + 127) >> 7), S2 = (int)((rb2 + 127) >> 7);  // 128-byte steps of a row
   const int kb1 = (int)(rb1 >> 6), kb2 = (int)(rb2 >> 6);                // 64-byte K blocks
   const int P1 = (H + 127) >> 7, P2 = (I + 127) >> 7;                    // powers of two of a row
-  const int q0 = n_act * S2 * warp / kWarps, q1 = n_act * S2 * (warp + 1) / kWarps;  // FC2 steps
-  const int a_first = q0 / S2, s_first = q0 - a_first * S2;
   const unsigned magic = 0xffffffffu / (unsigned)tiles_e;
   // expert slot and first intermediate column of a claim
   auto claim_at = [&](int c, int& a, int& i0) {
@@ -628,124 +655,31 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     i0 = rest * 8;
   };
 
-  unsigned char* ring = ring_all + warp * R::kWarp;
-  const uint32_t ring_u = ptx::smem_u32(ring);
-  // block scales: one row of the scale matrix per 128 weight rows, one column
-  // per K step; channel scales: one per row
-  const int rs = p.block_scales ? 7 : 0;
-  const int kg1 = p.block_scales ? H >> 7 : 1, kg2 = p.block_scales ? I >> 7 : 1;
-  const int ks = p.block_scales ? 1 : 0;
-
-  // ---- producer: the warp's steps in the order it will use them.  A segment is
-  // the warp's steps of one FC1 claim, or of one expert for one FC2 unit.
-  const unsigned char* p_src = nullptr;  // this lane's first row at the next step
-  uint32_t p_ts = 0, p_hs = 0;           // to the second tile, to a tile's lower 8 rows (bytes)
-  unsigned p_ok = 0;                     // bit 2 * tile + half: this lane's row is wanted
-  const uint16_t* p_b = nullptr;         // this lane's column of the first MMA at the next step
-  size_t p_bj = 0;                       // to the next MMA's (elements)
-  bool p_on = false;                     // the column's token uses the expert (and may be read)
-  const float* p_sc = nullptr;           // FP8: scale of row `lane` of the step's 32 rows
-  const float* p_pow = nullptr;          // FP8: the token's power of two at the step
-  bool p_sok = false;
-  int p_step = 0, p_end = 0, p_kb = kb1; // next step, end of its segment, K blocks of a row
-  int p_inc = kWarps;                    // steps to the next (FC2: 1)
-  int pn = -1, pu = 0, pa = a_first - 1; // claim; FC2 unit and active expert
-  int n = 0;                             // claim being used; n + 1 is known too
-  bool p_fc2 = false, fc1_done = false;
-  int flying = 0;                        // steps issued and not yet used
-  uint32_t p_at = 0, c_at = 0;           // ring offsets of the next step to issue / to use
-
+  const int wk = warp % kWarps;  // consumer whose steps these are
+  const int q0 = n_act * S2 * wk / kWarps, q1 = n_act * S2 * (wk + 1) / kWarps;  // FC2 steps of a unit
+  const int a_first = q0 / S2, s_first = q0 - a_first * S2;
+  const int units = (n1 - n0 + 31) / 32;
+  unsigned char* ring = ring_all + wk * R::kWarp;
   const size_t x_term = (size_t)T * H, a_term = (size_t)T * k * I;  // elements of a term
-  p_bj = TPG * x_term;
-  auto start_fc2 = [&]() {
-    p_fc2 = true;
-    p_kb = kb2;
-    p_inc = 1;
-    p_ts = 16 * rb2;
-    p_hs = 8 * rb2;
-    p_bj = TPG * a_term;
-  };
-  // Moves to the next segment that has a step for this warp; false when there is
-  // none or it is not known yet.
-  auto next_segment = [&]() -> bool {
-    if (!p_fc2) {
-      if (pn > n || warp >= S1) return false;
-      if (sm.claim[(pn + 1) & 3] >= claims) start_fc2();
-    }
-    if (!p_fc2) {
-      ++pn;
-      const int c = sm.claim[pn & 3];
-      int a, i0;
-      claim_at(c, a, i0);
-      const int e = sm.expert[a];
-      p_step = warp;
-      p_end = S1;
-      p_src = static_cast<const unsigned char*>(p.w13) + ((size_t)e * 2 * I + i0 + g) * rb1 + p_step * 128 +
-              tq * 16;
-      p_ts = 8 * rb1;
-      p_hs = (uint32_t)I * rb1;
-      p_ok = c < pairs ? 15u : 3u;
-      p_on = (sm.mask[a] >> tok) & 1u;
-      p_b = p.xt + (size_t)(g % TPG) * x_term + (size_t)(p_on ? tok : 0) * H + p_step * 2 * KE + tq * 8 * Q;
-      if constexpr (FP8) {
-        const int row = i0 + (lane & 7) + ((lane & 8) ? I : 0) + ((lane & 16) ? 8 : 0);
-        p_sok = c < pairs || lane < 16;
-        p_sc = p.s13 + ((size_t)e * (2 * I >> rs) + ((p_sok ? row : 0) >> rs)) * kg1 + p_step * ks;
-        p_pow = p.xpow + (p_on ? tok : 0) * P1 + p_step;
-      }
-      return true;
-    }
-    if (q0 == q1 || n0 + 32 * pu >= n1) return false;
-    ++pa;
-    if (pa * S2 >= q1) {  // the next unit of output rows
-      if (n0 + 32 * (pu + 1) >= n1) {
-        --pa;
-        return false;
-      }
-      ++pu;
-      pa = a_first;
-    }
-    const int row0 = n0 + 32 * pu, e = sm.expert[pa];
-    p_step = pa == a_first ? s_first : 0;
-    p_end = min(S2, q1 - pa * S2);
-    p_src = static_cast<const unsigned char*>(p.w2) + ((size_t)e * H + row0 + g) * rb2 + p_step * 128 + tq * 16;
-    p_ok = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p_ok |= (row0 + g + 8 * i < n1 ? 1u : 0u) << i;
-    const int pr = sm.pair[pa][tok];
-    p_on = pr >= 0 && fc1_done;
-    p_b = p.at + (size_t)(g % TPG) * a_term + (size_t)(pr >= 0 ? pr : 0) * I + p_step * 2 * KE + tq * 8 * Q;
-    if constexpr (FP8) {
-      p_pow = p.apow + (pr >= 0 ? pr : 0) * P2 + p_step;
-      p_sok = row0 + lane < n1;
-      p_sc = p.s2 + ((size_t)e * (H >> rs) + ((p_sok ? row0 + lane : 0) >> rs)) * kg2 + p_step * ks;
-    }
-    return true;
-  };
-  // This lane's activations of a step into the stage at ring offset `at`.
-  auto copy_b = [&](uint32_t at, const uint16_t* b, size_t bj, const float* pw, bool two) {
-    const uint32_t dst = ring_u + at + kStepA + lane * 16;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        cp_async16(dst + (j * Q + q) * 512, b + j * bj + q * 8);
-        if (two) cp_async16(dst + ((NJ + j) * Q + q) * 512, b + j * bj + KE + q * 8);
-      }
-    }
-    // (the token's first lane)
-    if (FP8 && first_lane) cp_async4(ring_u + at + R::kPowAt + tok * 4, pw);
-  };
-  // Keeps the ring full as far as the steps are known.
-  auto top_up = [&]() {
-    while (flying < R::kDepth) {
-      if (p_step >= p_end && !next_segment()) break;
-      const uint32_t dst = ring_u + p_at + lane * 16;
-      const bool two = !FP8 || 2 * p_step + 1 < p_kb;
-      const unsigned char *s0 = p_src, *s1 = s0 + p_hs, *s2 = s0 + p_ts, *s3 = s2 + p_hs;
-      if (p_ok == 15u && two) {
-        cp_async16(dst, s0);
-        cp_async16(dst + 512, s0 + 64);
+
+  if (warp >= kWarps) {
+    // -------------------------------------------------------------- producer --
+    const uint32_t ring_u = ptx::smem_u32(ring);
+    // block scales: one row of the scale matrix per 128 weight rows, one column
+    // per K step; channel scales: one per row
+    const int rs = p.block_scales ? 7 : 0, ks = p.block_scales ? 1 : 0;
+    const int kg1 = p.block_scales ? H >> 7 : 1, kg2 = p.block_scales ? I >> 7 : 1;
+    int slot = 0;
+    uint32_t ph = 1;  // the ring starts empty
+    // Weights of a step: this lane's first row at the step, to the second tile and
+    // to a tile's lower 8 rows (bytes), bit 2 * tile + half of `ok` where the lane's
+    // row is wanted.  `two`: the step's second K block exists (else zeros).
+    auto copy_a = [&](int sl, const unsigned char* src, uint32_t ts, uint32_t hs, unsigned ok, bool two) {
+      const uint32_t dst = ring_u + sl * R::kStage + lane * 16;
+      const unsigned char *s1 = src + hs, *s2 = src + ts, *s3 = s2 + hs;
+      if (ok == 15u && two) {
+        cp_async16(dst, src);
+        cp_async16(dst + 512, src + 64);
         cp_async16(dst + 1024, s1);
         cp_async16(dst + 1536, s1 + 64);
         cp_async16(dst + 2048, s2);
@@ -753,49 +687,167 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
         cp_async16(dst + 3072, s3);
         cp_async16(dst + 3584, s3 + 64);
       } else {
-        const unsigned char* src[4] = {s0, s1, s2, s3};
+        const unsigned char* r[4] = {src, s1, s2, s3};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if ((p_ok >> i) & 1u) {
-            cp_async16(dst + 1024 * i, src[i]);
-            if (two) cp_async16(dst + 1024 * i + 512, src[i] + 64);
+          if ((ok >> i) & 1u) {
+            cp_async16(dst + 1024 * i, r[i]);
+            cp_async16z(dst + 1024 * i + 512, two ? r[i] + 64 : r[i], two ? 16 : 0);
           }
         }
-        if (!two) {  // a row's odd last block: its partner counts as zeros on both sides
-          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-          uint4* st = reinterpret_cast<uint4*>(ring + p_at) + lane;
+      }
+    };
+    // This lane's column of the activations at the step, to the next MMA's column.
+    auto copy_b = [&](int sl, const uint16_t* b, size_t bj, const float* pw, bool two) {
+      const uint32_t dst = ring_u + sl * R::kStage + kStepA + lane * 16;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) st[(2 * i + 1) * 32] = z;
+      for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-          for (int j = 0; j < NJ * Q; ++j) st[kStepA / 16 + (NJ * Q + j) * 32] = z;
+        for (int q = 0; q < Q; ++q) {
+          cp_async16(dst + (j * Q + q) * 512, b + j * bj + q * 8);
+          if (!FP8) cp_async16(dst + ((NJ + j) * Q + q) * 512, b + j * bj + KE + q * 8);
+          else cp_async16z(dst + ((NJ + j) * Q + q) * 512, b + j * bj + (two ? KE : 0) + q * 8, two ? 16 : 0);
         }
       }
-      if (p_on) copy_b(p_at, p_b, p_bj, p_pow, two);
-      if (FP8 && p_sok) cp_async4(ring_u + p_at + R::kScaleAt + lane * 4, p_sc);
-      cp_commit();
-      ++flying;
-      p_at = p_at == (R::kDepth - 1) * R::kStage ? 0 : p_at + R::kStage;
-      p_src += p_inc * 128;
-      p_b += p_inc * 2 * KE;
-      if constexpr (FP8) {
-        p_sc += p_inc * ks;
-        p_pow += p_inc;
+      if (FP8 && first_lane) cp_async4(ring_u + sl * R::kStage + R::kPowAt + tok * 4, pw);
+    };
+    auto wait_empty = [&]() -> bool { return ptx::mbar_wait(&sm.empty[wk][slot], ph, &sm.abort); };
+    auto next_slot = [&]() {
+      if (++slot == R::kDepth) {
+        slot = 0;
+        ph ^= 1;
       }
-      p_step += p_inc;
+    };
+    // Waits until *flag >= want (a word of shared memory that a consumer writes).
+    auto wait_flag = [&](int* flag, int want) -> bool {
+      const long long t0 = clock64();
+      while (*(volatile int*)flag < want) {
+        if (*(volatile int*)&sm.abort) return false;
+        if (clock64() - t0 > ptx::kSpinLimitCycles) {
+          *(volatile int*)&sm.abort = 1;
+          return false;
+        }
+        __nanosleep(64);
+      }
+      __threadfence_block();
+      return true;
+    };
+    bool ok = true;
+    // FC1 (a warp beyond the steps of a row has none)
+    for (int n = 0; ok && wk < S1; ++n) {
+      if (!(ok = wait_flag(&sm.published, n))) break;
+      const int c = *(volatile int*)&sm.claim[n & 3];
+      if (c >= claims) break;
+      int a, i0;
+      claim_at(c, a, i0);
+      const int e = sm.expert[a];
+      const unsigned char* src =
+          static_cast<const unsigned char*>(p.w13) + ((size_t)e * 2 * I + i0 + g) * rb1 + wk * 128 + tq * 16;
+      const bool on = (sm.mask[a] >> tok) & 1u;
+      const uint16_t* b =
+          p.xt + (size_t)(g % TPG) * x_term + (size_t)(on ? tok : 0) * H + wk * 2 * KE + tq * 8 * Q;
+      const float *sc = nullptr, *pw = nullptr;
+      bool sok = false;
+      if constexpr (FP8) {
+        const int row = i0 + (lane & 7) + ((lane & 8) ? I : 0) + ((lane & 16) ? 8 : 0);
+        sok = c < pairs || lane < 16;
+        sc = p.s13 + ((size_t)e * (2 * I >> rs) + ((sok ? row : 0) >> rs)) * kg1 + wk * ks;
+        pw = p.xpow + (on ? tok : 0) * P1 + wk;
+      }
+#pragma unroll 1
+      for (int step = wk; step < S1; step += kWarps) {
+        if (!(ok = wait_empty())) break;
+        const bool two = !FP8 || 2 * step + 1 < kb1;
+        copy_a(slot, src, 8 * rb1, (uint32_t)I * rb1, c < pairs ? 15u : 3u, two);
+        if (on) copy_b(slot, b, TPG * x_term, pw, two);
+        if (FP8 && sok) cp_async4(ring_u + slot * R::kStage + R::kScaleAt + lane * 4, sc);
+        cp_arrive(&sm.full[wk][slot]);
+        next_slot();
+        src += kWarps * 128;
+        b += kWarps * 2 * KE;
+        if constexpr (FP8) {
+          sc += kWarps * ks;
+          pw += kWarps;
+        }
+      }
     }
-  };
+    // FC2: (unit, expert, step) in order; the first steps' weights are copied
+    // before the intermediate is there
+    struct At {
+      int u, a, s;
+    };
+    const int total = (q1 - q0) * units;
+    auto advance = [&](At& t) {
+      if (t.a * S2 + ++t.s == q1) {
+        ++t.u;
+        t.a = a_first;
+        t.s = s_first;
+      } else if (t.s == S2) {
+        ++t.a;
+        t.s = 0;
+      }
+    };
+    auto step_a = [&](int sl, const At& t) {
+      const int row0 = n0 + 32 * t.u, e = sm.expert[t.a];
+      unsigned want = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) want |= (row0 + g + 8 * i < n1 ? 1u : 0u) << i;
+      copy_a(sl, static_cast<const unsigned char*>(p.w2) + ((size_t)e * H + row0 + g) * rb2 + t.s * 128 + tq * 16,
+             16 * rb2, 8 * rb2, want, !FP8 || 2 * t.s + 1 < kb2);
+      if (FP8 && row0 + lane < n1)
+        cp_async4(ring_u + sl * R::kStage + R::kScaleAt + lane * 4,
+                  p.s2 + ((size_t)e * (H >> rs) + ((row0 + lane) >> rs)) * kg2 + t.s * ks);
+    };
+    auto step_b = [&](int sl, const At& t) {
+      const int pr = sm.pair[t.a][tok];
+      if (pr >= 0)
+        copy_b(sl, p.at + (size_t)(g % TPG) * a_term + (size_t)pr * I + t.s * 2 * KE + tq * 8 * Q, TPG * a_term,
+               p.apow + pr * P2 + t.s, !FP8 || 2 * t.s + 1 < kb2);
+    };
+    if (ok && total > 0) {
+      const int early = min(R::kDepth, total);
+      const int slot0 = slot;
+      const uint32_t ph0 = ph;
+      At ta{0, a_first, s_first}, tb = ta;
+      for (int i = 0; ok && i < early; ++i) {
+        if (!(ok = wait_empty())) break;
+        step_a(slot, ta);
+        next_slot();
+        advance(ta);
+      }
+      if (ok) ok = wait_flag(&sm.fc1_done, 1);
+      slot = slot0;
+      ph = ph0;
+#pragma unroll 1
+      for (int i = 0; ok && i < total; ++i) {
+        if (i >= early) {
+          if (!(ok = wait_empty())) break;
+          step_a(slot, tb);
+        }
+        step_b(slot, tb);
+        cp_arrive(&sm.full[wk][slot]);
+        next_slot();
+        advance(tb);
+      }
+    }
+    cp_wait_all();
+    return;
+  }
 
-  // One step: acc[MMA][tile] += weights of the step * the columns.  What a lane
-  // did not copy (rows that are not wanted, tokens that do not use the expert) is
+  // ---------------------------------------------------------------- consumers --
+  // One step: acc[MMA][tile] += weights of the step * the columns.  What was not
+  // copied (rows that are not wanted, tokens that do not use the expert) is
   // whatever the ring held: it only reaches sums that are not used.  FP8: s, the
   // scales of the lane's rows times the powers of two of its two columns.
   using Sums = float[NJ][2][4];
   constexpr int NC = TPG > 1 ? 1 : 2;  // tokens of the lane's two columns
+  int slot = 0;
+  uint32_t ph = 0;
+  bool arrived = true;
   auto multiply = [&](Sums& acc, float (&s)[4][NC]) {
-    if (flying == R::kDepth) asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
-    else cp_wait_all();
-    if (FP8) __syncwarp();  // scales and powers were copied by other lanes of the warp
-    const uint4* sp = reinterpret_cast<const uint4*>(ring + c_at) + lane;
+    arrived = ptx::mbar_wait(&sm.full[warp][slot], ph, &sm.abort) && arrived;
+    const unsigned char* st = ring + slot * R::kStage;
+    const uint4* sp = reinterpret_cast<const uint4*>(st) + lane;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       uint4 b[NJ][Q];
@@ -828,17 +880,20 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       }
     }
     if constexpr (FP8) {
-      const float* pw = reinterpret_cast<const float*>(ring + c_at + R::kPowAt) + 2 * tq / TPG;
+      const float* pw = reinterpret_cast<const float*>(st + R::kPowAt) + 2 * tq / TPG;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float w = *reinterpret_cast<const float*>(ring + c_at + R::kScaleAt + (g + 8 * i) * 4);
+        const float w = *reinterpret_cast<const float*>(st + R::kScaleAt + (g + 8 * i) * 4);
 #pragma unroll
         for (int c = 0; c < NC; ++c) s[i][c] = w * pw[c];
       }
-      __syncwarp();  // and are overwritten by them once all have read
     }
-    --flying;
-    c_at = c_at == (R::kDepth - 1) * R::kStage ? 0 : c_at + R::kStage;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&sm.empty[warp][slot]);
+    if (++slot == R::kDepth) {
+      slot = 0;
+      ph ^= 1;
+    }
   };
   // tot += s * acc for the tokens in `mask` (bit i: token i); acc = 0.  A token
   // outside the mask gets nothing (not 0 times a weight that may not be finite).
@@ -884,201 +939,164 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
       do {
         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(ctr) : "memory");
       } while (seen < want && clock64() - t0 < ptx::kSpinLimitCycles);
-      sm.flag = seen < want;
-      if (seen < want) flag_status(p.status, MOE_ERR_TIMEOUT);
+      sm.in_time = seen >= want;
+      if (seen < want) *(volatile int*)&sm.abort = 1;
       __threadfence();
     }
-    __syncthreads();
-    const bool ok = !sm.flag;
-    __syncthreads();
-    return ok;
+    consumer_sync();
+    return sm.in_time != 0;
   };
 
   int buf = 0, my_tiles = 0;
   float sc[4][NC] = {};
   Sums acc = {}, tot = {};
 
-  // One loop over segments, so that the stream's code exists once: FC1 claims
-  // (fc2 = false), then this warp's experts of each FC2 unit.
-  bool fc2 = false;
-  int u = 0, a = 0, i0 = 0;
-  while (true) {
-    int step, end, inc, next_claim = claims;
-    unsigned mask = 0;
-    bool second = true;
-    const int c = fc2 ? 0 : sm.claim[n & 3];
-    if (!fc2) {
-      if (c >= claims) {
-        // ---- all FC1 tiles done (each CTA's writes are visible before its count).
-        // Meanwhile the first W2 steps are copied.
-        if (!p_fc2) start_fc2();
-        top_up();
-        __syncthreads();
-        int conv = 0;
-        if (FP8 && tid == 0) conv = atomicAdd(&p.ctr[3], 1);
-        if (!wait_for(p.ctr + 1, tiles)) {
-          cp_wait_all();
-          return;
-        }
-        if constexpr (FP8) {
-          // ---- the intermediate's terms, 128 columns of a pair to a warp, eight
-          // such units to a claim
-          const int units = T * k * P2;
-          while (true) {
-            if (tid == 0) sm.flag = conv;
-            __syncthreads();
-            const int first = sm.flag * kWarps;
-            __syncthreads();
-            if (first >= units) break;
-            const int pr = (first + warp) / P2, blk = first + warp - pr * P2;
-            const int at = blk * 128 + lane * 4;
-            if (first + warp < units) {
-              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (at < I) v = __ldcg(reinterpret_cast<const float4*>(p.act + (size_t)pr * I + at));
-              const float m = warp_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-              const int ex = pow_exponent(m);
-              const float up = pow_up(ex);
-              ushort4 hi, lo;
-              split16<true>(v.x * up, hi.x, lo.x);
-              split16<true>(v.y * up, hi.y, lo.y);
-              split16<true>(v.z * up, hi.z, lo.z);
-              split16<true>(v.w * up, hi.w, lo.w);
-              if (at < I) {
-                *reinterpret_cast<ushort4*>(p.at + (size_t)pr * I + at) = hi;
-                *reinterpret_cast<ushort4*>(p.at + a_term + (size_t)pr * I + at) = lo;
-              }
-              if (lane == 0) p.apow[pr * P2 + blk] = pow_down(ex);
-            }
-            __syncthreads();
-            if (tid == 0) {
-              __threadfence();
-              atomicAdd(&p.ctr[4], min(kWarps, units - first));
-              conv = atomicAdd(&p.ctr[3], 1);
-            }
-          }
-          if (!wait_for(p.ctr + 4, units)) {
-            cp_wait_all();
-            return;
-          }
-        }
-        // the activations of the W2 steps already in flight
-        fc1_done = true;
-        if (p_step < p_end) p_on = sm.pair[pa][tok] >= 0;
-        int qa = a_first, qs = s_first, qq = q0;
-        uint32_t at = c_at;
-        for (int left = flying; left > 0; --left) {
-          const int pr = sm.pair[qa][tok];
-          if (pr >= 0)
-            copy_b(at, p.at + (size_t)(g % TPG) * a_term + (size_t)pr * I + qs * 2 * KE + tq * 8 * Q, TPG * a_term,
-                   p.apow + pr * P2 + qs, 2 * qs + 1 < kb2);
-          at = at == (R::kDepth - 1) * R::kStage ? 0 : at + R::kStage;
-          if (++qq == q1) {  // (a short unit: the next one's steps follow)
-            qa = a_first;
-            qs = s_first;
-            qq = q0;
-          } else if (++qs == S2) {
-            ++qa;
-            qs = 0;
-          }
-        }
-        cp_wait_all();
-        __syncthreads();
-        fc2 = true;
-        buf = 0;
-        a = a_first;
-        continue;
-      }
-      claim_at(c, a, i0);
-      mask = sm.mask[a];
-      second = c < pairs;
-      step = warp;
-      end = S1;
-      inc = kWarps;
-      if (tid == 0) next_claim = atomicAdd(&p.ctr[0], 1);  // used two claims from here
-    } else {
-      if (n0 + 32 * u >= n1) break;
-      inc = 1;
-      step = a == a_first ? s_first : 0;
-      end = min(S2, q1 - a * S2);  // (nothing for a warp without steps)
-      if (step < end) mask = sm.mask[a];
-    }
+  // ---- FC1
+  for (int n = 0;; ++n) {
+    const int c = sm.claim[n & 3];
+    if (c >= claims) break;
+    int next_claim = claims;
+    if (tid == 0) next_claim = atomicAdd(&p.ctr[0], 1);  // used two claims from here
+    int a, i0;
+    claim_at(c, a, i0);
+    const unsigned mask = sm.mask[a];
+    const bool second = c < pairs;
 #pragma unroll 1
-    for (; step < end; step += inc) {
-      top_up();
+    for (int step = warp; step < S1; step += kWarps) {
       multiply(acc, sc);
       if constexpr (FP8) fold(tot, acc, sc, mask);
     }
     if constexpr (!FP8) fold(tot, acc, sc, mask);
-    if (fc2 && (a + 1) * S2 < q1) {  // the unit's next expert
+    store_red(red[buf] + warp * 256, tot);
+    if (tid == 0) {
+      sm.claim[(n + 2) & 3] = next_claim;
+      __threadfence_block();
+      *(volatile int*)&sm.published = n + 2;
+    }
+    consumer_sync();
+    // the claim's 16 intermediate columns: warp t, token t; each half warp adds the
+    // partial sums of four warps
+    if ((mask >> warp) & 1u) {
+      const int il = lane & 15;
+      const float* s = red[buf] + ((il >> 3) * 16 + (il & 7)) * 8 + warp + (lane >> 4) * 1024;
+      float gate = 0.f, up = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        gate += s[w * 256];
+        up += s[w * 256 + 64];
+      }
+      gate += __shfl_xor_sync(0xffffffffu, gate, 16);
+      up += __shfl_xor_sync(0xffffffffu, up, 16);
+      if (lane < (second ? 16 : 8)) {
+        const float r = sm.r[warp];
+        // the routing weight goes into the intermediate, so FC2 adds the token's
+        // experts without a factor
+        const float v = silu_f(gate * r) * (up * r) * sm.wt[a][warp];
+        const size_t at = (size_t)sm.pair[a][warp] * I + i0 + il;
+        if constexpr (FP8) p.act[at] = v;
+        else split16<false>(v, p.at[at], p.at[at + a_term]);
+      }
+    }
+    my_tiles += second ? 2 : 1;
+    buf ^= 1;
+  }
+  // ---- all FC1 tiles done (this CTA's are counted once its writes are there)
+  consumer_sync();
+  int conv = 0;
+  if (tid == 0) {
+    __threadfence();
+    if (my_tiles) atomicAdd(&p.ctr[1], my_tiles);
+    if (FP8) conv = atomicAdd(&p.ctr[3], 1);
+  }
+  bool ok = wait_for(p.ctr + 1, tiles);
+  if constexpr (FP8) {
+    // ---- the intermediate's terms, 128 columns of a pair to a warp, eight such
+    // units to a claim
+    const int parts = T * k * P2;
+    while (ok) {
+      if (tid == 0) sm.flag = conv;
+      consumer_sync();
+      const int first = sm.flag * kWarps;
+      consumer_sync();
+      if (first >= parts) break;
+      const int pr = (first + warp) / P2, blk = first + warp - pr * P2;
+      const int at = blk * 128 + lane * 4;
+      if (first + warp < parts) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at < I) v = __ldcg(reinterpret_cast<const float4*>(p.act + (size_t)pr * I + at));
+        const float m = warp_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        const int ex = pow_exponent(m);
+        const float up = pow_up(ex);
+        ushort4 hi, lo;
+        split16<true>(v.x * up, hi.x, lo.x);
+        split16<true>(v.y * up, hi.y, lo.y);
+        split16<true>(v.z * up, hi.z, lo.z);
+        split16<true>(v.w * up, hi.w, lo.w);
+        if (at < I) {
+          *reinterpret_cast<ushort4*>(p.at + (size_t)pr * I + at) = hi;
+          *reinterpret_cast<ushort4*>(p.at + a_term + (size_t)pr * I + at) = lo;
+        }
+        if (lane == 0) p.apow[pr * P2 + blk] = pow_down(ex);
+      }
+      consumer_sync();
+      if (tid == 0) {
+        __threadfence();
+        atomicAdd(&p.ctr[4], min(kWarps, parts - first));
+        conv = atomicAdd(&p.ctr[3], 1);
+      }
+    }
+    if (ok) ok = wait_for(p.ctr + 4, parts);
+  }
+  if (!ok) {
+    if (tid == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
+    return;
+  }
+  if (tid == 0) {
+    __threadfence_block();
+    *(volatile int*)&sm.fc1_done = 1;
+  }
+
+  // ---- FC2: this CTA's output rows over all active experts
+  for (int u = 0; u < units; ++u) {
+    int a = a_first, s_at = s_first;
+    for (int q = q0; q < q1;) {
+      const unsigned mask = sm.mask[a];
+      const int end = min(q1, q + S2 - s_at);
+#pragma unroll 1
+      for (; q < end; ++q) {
+        multiply(acc, sc);
+        if constexpr (FP8) fold(tot, acc, sc, mask);
+      }
+      if constexpr (!FP8) fold(tot, acc, sc, mask);
       ++a;
-      continue;
+      s_at = 0;
     }
     store_red(red[buf] + warp * 256, tot);
-    if (!fc2 && tid == 0) sm.claim[(n + 2) & 3] = next_claim;
-    __syncthreads();
-    if (fc2) {
-      // ---- the unit's output rows
-      const int row = n0 + 32 * u + lane, t = warp;
-      if (t < T && row < n1) {
-        const float* s = red[buf] + lane * 8 + t;
-        float v = 0.f;
+    consumer_sync();
+    const int row = n0 + 32 * u + lane, t = warp;
+    if (t < T && row < n1) {
+      const float* s = red[buf] + lane * 8 + t;
+      float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += s[w * 256];
-        const size_t at = (size_t)t * H + row;
-        if (has_tail) p.f[at] = v;
-        else static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(v);
-      }
-      ++u;
-      a = a_first;
-    } else {
-      // ---- the claim's 16 intermediate columns: warp t, token t; each half warp
-      // adds the partial sums of four warps
-      if ((mask >> warp) & 1u) {
-        const int il = lane & 15;
-        const float* s = red[buf] + ((il >> 3) * 16 + (il & 7)) * 8 + warp + (lane >> 4) * 1024;
-        float gate = 0.f, up = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          gate += s[w * 256];
-          up += s[w * 256 + 64];
-        }
-        gate += __shfl_xor_sync(0xffffffffu, gate, 16);
-        up += __shfl_xor_sync(0xffffffffu, up, 16);
-        if (lane < (second ? 16 : 8)) {
-          const float r = sm.r[warp];
-          // the routing weight goes into the intermediate, so FC2 adds the
-          // token's experts without a factor
-          const float v = silu_f(gate * r) * (up * r) * sm.wt[a][warp];
-          const size_t at = (size_t)sm.pair[a][warp] * I + i0 + il;
-          if constexpr (FP8) p.act[at] = v;
-          else split16<false>(v, p.at[at], p.at[at + a_term]);
-        }
-      }
-      my_tiles += second ? 2 : 1;
-      // the last claim: the tiles are counted once the writes are there
-      if (sm.claim[(n + 1) & 3] >= claims) {
-        __syncthreads();
-        if (tid == 0) {
-          __threadfence();
-          atomicAdd(&p.ctr[1], my_tiles);
-        }
-      }
-      ++n;
+      for (int w = 0; w < kWarps; ++w) v += s[w * 256];
+      const size_t at = (size_t)t * H + row;
+      if (has_tail) p.f[at] = v;
+      else static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(v);
     }
     buf ^= 1;
   }
-  cp_wait_all();
+  if (!arrived) flag_status(p.status, MOE_ERR_TIMEOUT);
   if (!has_tail) return;
 
   // ---- tail: the last T CTAs to finish take a row each.  (When they wait for
   // one another, fewer than T CTAs are unfinished, and the others have left their
   // SMs to them.)
-  __syncthreads();
+  consumer_sync();
   if (tid == 0) {
     __threadfence();
     sm.flag = atomicAdd(&p.ctr[2], 1) - ((int)gridDim.x - T);
   }
-  __syncthreads();
+  consumer_sync();
   const int t = sm.flag;
   if (t < 0) return;
   const int grow = tail_gate_row(tail, t, tid == 0 ? p.status : nullptr);
@@ -1109,7 +1127,7 @@ __global__ void __launch_bounds__(kThreadsL, 1) layer_experts_kernel(const Layer
     if (seen < (int)gridDim.x) flag_status(p.status, MOE_ERR_TIMEOUT);
     __threadfence();
   }
-  __syncthreads();
+  consumer_sync();
   stage(0, p.f + (size_t)t * H, (size_t)H * 4);
   cp_wait_all();
   layer_tail_row(p, tail, t, grow, ring_all, staged, sm.sum);
@@ -1212,7 +1230,7 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
 #undef MOE_LAYER_KERNEL
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(sms), dim3(kThreadsL), smem, st, p, tail ? *tail : TailP{},
+  return launch_kernel(kern, dim3(sms), dim3(2 * kThreadsL), smem, st, p, tail ? *tail : TailP{},
                        tail ? 1 : 0);
 }
 
