@@ -158,24 +158,33 @@ MOE_DEV float pow_up(int e) { return __uint_as_float((uint32_t)(268 - e) << 23);
 MOE_DEV float pow_down(int e) { return __uint_as_float((uint32_t)(e - 14) << 23); }
 
 // ------------------------------------------------------------------ launch 1 --
-// Grid (kLayerChunks, groups of 32 experts): K chunk c, experts 32y .. 32y+31.
-// Latency is all there is: each warp has its rows of W_r (16 at H = 4096) on
-// their way before it waits for anything.
+// Grid (kLayerChunks, groups of 32 experts): K chunk c, experts 32y .. 32y+31; TT:
+// tokens that the dot products have room for (T <= TT).  Latency is all there is:
+// the chunk of x and each warp's rows of W_r (16 at H = 4096) are on their way
+// before anything is waited for.
 constexpr int kRouteWarps = 16;
 
-template <bool FP8>
+template <bool FP8, int TT>
 __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const LayerP p) {
-  extern __shared__ __align__(16) float xw[];  // [rows of the chunk][8 tokens]
-  __shared__ float red[kRouteWarps][kLayerMaxT][32];
+  extern __shared__ __align__(16) float xw[];  // [rows of the chunk][TT tokens]
+  __shared__ float red[kRouteWarps][TT][32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = blockIdx.x;
   const Chunk ch = layer_chunk(p.H, c);
-  const int k0 = ch.k0, rows = ch.k1 - ch.k0;
+  const int k0 = ch.k0, rows = ch.k1 - ch.k0, nv = rows >> 3;
   if (c == 0 && blockIdx.y == 0 && tid < kCtrInts) p.ctr[tid] = 0;
   const int e = blockIdx.y * 32 + lane;
   const float* wr = p.router_w ? p.router_w + (size_t)k0 * p.E + e : nullptr;
+  const bool on = warp < p.T;  // warp t: token t (zeros beyond the last)
+  const size_t row = (size_t)(on ? warp : 0) * p.H + k0;
+  // the first 256 columns of x and the norm's weights
+  uint4 x0 = make_uint4(0u, 0u, 0u, 0u), w0 = x0;
+  if (on && lane < nv) {
+    x0 = *reinterpret_cast<const uint4*>(p.x + row + lane * 8);
+    w0 = *reinterpret_cast<const uint4*>(p.norm_w + k0 + lane * 8);
+  }
   constexpr int U = 16;
   float wv[U];
   if (wr) {
@@ -185,28 +194,29 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
       wv[u] = (r < rows && e < p.E) ? wr[(size_t)r * p.E] : 0.f;
     }
   }
-  // warp t: token t (zeros beyond the last)
-  if (warp < kLayerMaxT) {
-    const bool on = warp < p.T;
-    const size_t row = (size_t)(on ? warp : 0) * p.H + k0;
+  if (warp < TT) {
     float ss = 0.f;
 #pragma unroll 1
-    for (int v0 = 0; v0 < rows >> 3; v0 += 32) {
+    for (int v0 = 0; v0 < nv; v0 += 32) {
       const int v = v0 + lane;
+      if (v0 && on && v < nv) {
+        x0 = *reinterpret_cast<const uint4*>(p.x + row + v * 8);
+        w0 = *reinterpret_cast<const uint4*>(p.norm_w + k0 + v * 8);
+      }
       float a[8] = {};
-      if (on && v < rows >> 3) {
+      if (on && v < nv) {
         float w[8];
-        load8(p.x, false, row + v * 8, a);
-        load8(p.norm_w, false, k0 + v * 8, w);
+        unpack8_bf16(x0, a);
+        unpack8_bf16(w0, w);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           ss = fmaf(a[q], a[q], ss);
           a[q] *= w[q];
         }
       }
-      if (wr && v < rows >> 3) {
+      if (wr && v < nv) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) xw[(v * 8 + q) * kLayerMaxT + warp] = a[q];
+        for (int q = 0; q < 8; ++q) xw[(v * 8 + q) * TT + warp] = a[q];
       }
       if (blockIdx.y == 0) {
         const size_t at = row + v * 8, term = (size_t)p.T * p.H;
@@ -219,10 +229,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
           for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           const int ex = pow_exponent(m);
           up = pow_up(ex);
-          if (on && v < rows >> 3 && (lane & 15) == 0)
+          if (on && v < nv && (lane & 15) == 0)
             p.xpow[warp * ((p.H + 127) >> 7) + ((k0 + v * 8) >> 7)] = pow_down(ex);
         }
-        if (on && v < rows >> 3) {
+        if (on && v < nv) {
           __align__(16) uint16_t hi[8], lo[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) split16<FP8>(a[q] * up, hi[q], lo[q]);
@@ -238,31 +248,34 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
   }
   if (!wr) return;
   __syncthreads();
-  float acc[kLayerMaxT];
+  float acc[TT];
 #pragma unroll
-  for (int t = 0; t < kLayerMaxT; ++t) acc[t] = 0.f;
+  for (int t = 0; t < TT; ++t) acc[t] = 0.f;
   for (int r0 = warp; r0 < rows; r0 += kRouteWarps * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 + kRouteWarps * u;
       if (r < rows) {
-        const float4 a = *reinterpret_cast<const float4*>(&xw[r * kLayerMaxT]);
-        const float4 b = *reinterpret_cast<const float4*>(&xw[r * kLayerMaxT + 4]);
-        acc[0] = fmaf(a.x, wv[u], acc[0]);
-        acc[1] = fmaf(a.y, wv[u], acc[1]);
-        acc[2] = fmaf(a.z, wv[u], acc[2]);
-        acc[3] = fmaf(a.w, wv[u], acc[3]);
-        acc[4] = fmaf(b.x, wv[u], acc[4]);
-        acc[5] = fmaf(b.y, wv[u], acc[5]);
-        acc[6] = fmaf(b.z, wv[u], acc[6]);
-        acc[7] = fmaf(b.w, wv[u], acc[7]);
+        float a[TT];
+        if constexpr (TT % 4 == 0) {
+#pragma unroll
+          for (int t = 0; t < TT; t += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(&xw[r * TT + t]);
+            a[t] = q.x; a[t + 1] = q.y; a[t + 2] = q.z; a[t + 3] = q.w;
+          }
+        } else {
+          const float2 q = *reinterpret_cast<const float2*>(&xw[r * TT]);
+          a[0] = q.x; a[1] = q.y;
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[t] = fmaf(a[t], wv[u], acc[t]);
       }
       const int rn = r + kRouteWarps * U;
       wv[u] = (rn < rows && e < p.E) ? wr[(size_t)rn * p.E] : 0.f;
     }
   }
 #pragma unroll
-  for (int t = 0; t < kLayerMaxT; ++t) red[warp][t][lane] = acc[t];
+  for (int t = 0; t < TT; ++t) red[warp][t][lane] = acc[t];
   __syncthreads();
   if (warp < p.T && e < p.E) {
     float s = 0.f;
@@ -1205,8 +1218,11 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
     const Chunk ch = layer_chunk(a.H, c);
     if (ch.k1 - ch.k0 > rows) rows = ch.k1 - ch.k0;
   }
-  const int route_smem = a.router_w ? rows * kLayerMaxT * 4 : 0;  // up to 32 KB beside the static part
-  auto route = a.fp8 ? layer_route_kernel<true> : layer_route_kernel<false>;
+  const int tt = a.T <= 2 ? 2 : (a.T <= 4 ? 4 : kLayerMaxT);
+  const int route_smem = a.router_w ? rows * tt * 4 : 0;  // up to 32 KB beside the static part
+  auto route = a.fp8 ? layer_route_kernel<true, kLayerMaxT> : layer_route_kernel<false, kLayerMaxT>;
+  if (tt == 2) route = a.fp8 ? layer_route_kernel<true, 2> : layer_route_kernel<false, 2>;
+  if (tt == 4) route = a.fp8 ? layer_route_kernel<true, 4> : layer_route_kernel<false, 4>;
   cudaError_t e = cudaSuccess;
   if (route_smem > (24 << 10))
     e = cudaFuncSetAttribute(route, cudaFuncAttributeMaxDynamicSharedMemorySize, route_smem);
