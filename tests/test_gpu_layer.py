@@ -2,14 +2,18 @@
 
 The tolerances count roundings (u = 2^-24, half a step of fp32):
   products   activations enter as hi + lo bf16 terms: hi is half a bf16 step
-             (2^-8) off, lo half a step of that (2^-16 of the value); a product of
-             bf16 values is exact in fp32
+             (2^-8) off, lo half a step of that (2^-16 of the value); the fp16
+             terms beside E4M3 weights are nearer.  A product of two 16-bit terms
+             is exact in fp32
   sums       one MMA adds 16 products to the accumulator; its internal sums are
              taken to be good to 2^-22 of the magnitudes; each of 8 warps adds
-             2 K / (16 * 8) MMAs, then the 8 warps are added
+             at most 2 K / (16 * 8) MMAs one after the other, then the 8 warps
+             are added
   r          28 u (as in test_gpu_block_tail)
   silu(g) u  |silu'| <= 1.1; exp, divide and products within 8 u
-  logits     fp32 sums over 16 chunks of 8 warps of K / 128 rows
+  logits     a warp adds at most 8 ceil(H / 2048) rows (a chunk is at most
+             ceil(H / 2048) units of 128 rows over 16 warps), then the 16 warps
+             and the 16 chunks are added
   weights    the relative error of exp(z - z_max) is twice the logits' error
 and the tail adds what test_gpu_block_tail counts."""
 import pytest
@@ -153,7 +157,7 @@ def routing64(d):
     else:
         z = logits64(d, d["x"])
         mag = xhat64(d, d["x"]).abs() @ d["router_w"].double().abs()
-        dz = mag * (d["H"] / 128 + 8 + 16 + RNORM + 4) * U + 2 * U * z.abs()
+        dz = mag * (8 * -(-d["H"] // 2048) + 16 + 16 + RNORM + 4) * U + 2 * U * z.abs()
     zs, ids = z.sort(dim=1, descending=True, stable=True)
     w = torch.softmax(zs[:, :k], 1)
     return ids[:, :k].tolist(), w, 2 * dz.amax(1, keepdim=True) + 2 * U * zs[:, :k].abs().amax(1, keepdim=True) + 16 * U
@@ -242,6 +246,36 @@ def test_tail_outputs(M, nxt, gate, res):
         check(d, call(M, d))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,H", [(2, 16384), (8, 12352), (3, 12288), (5, 64)])
+def test_tail_of_long_and_short_rows(M, fmt, T, H):
+    """Rows that the tail keeps in shared memory with all their inputs, and longer ones."""
+    for gate, nxt in (("channel", "both"), ("rows", "bf16")):
+        d = make(T, H, 4, 2, 64, fmt=fmt, tail="full", gate=gate, nxt=nxt, res=torch.float32, seed=H)
+        check(d, call(M, d))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "block"])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8])
+def test_every_batch(M, fmt, T):
+    """Each kernel instance (tokens per MMA column set, routing width), rows that do not fill the
+    CTAs' slices evenly, experts from one to many."""
+    for H, E, k, I in ((1280, 40, 6, 640), (256, 2, 1, 128), (2304, 16, 4, 256)):
+        d = make(T, H, E, k, I, fmt=fmt, tail="full", seed=T)
+        check(d, call(M, d))
+    assert M.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_magnitudes(M, fmt):
+    """Columns and tokens of very different size share MMAs; tiny and huge weights of the norm."""
+    d = make(4, 512, 6, 2, 256, fmt=fmt, routing="ids", seed=12)
+    d["x"] *= torch.logspace(-6, 6, 4, device=DEV)[:, None].to(torch.bfloat16)
+    d["norm_w"] *= torch.logspace(-3, 3, 512, device=DEV).to(torch.bfloat16)
+    d["tw"] *= torch.logspace(-4, 0, 4, device=DEV)[:, None]
+    check(d, call(M, d))
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "block"])
 @pytest.mark.parametrize("T", [1, 8])
 def test_model_sized(M, fmt, T):
@@ -277,19 +311,24 @@ def test_ids_out_of_range_given_twice_and_empty(M):
     assert M.device_status(clear=True) == 0
 
 
-def test_non_finite_values_stay_in_their_token(M):
-    d = make(4, 256, 12, 2, 128, routing="ids", tail="full", nxt="both", seed=4)
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_non_finite_values_stay_in_their_token(M, fmt):
+    d = make(4, 256, 12, 2, 128, fmt=fmt, routing="ids", tail="full", nxt="both", seed=4)
     d["ids"].copy_(torch.tensor([[0, 1], [2, 3], [0, 4], [5, 1]], dtype=torch.int32))
     d["x"][1, 3] = float("nan")
     o = call(M, d)
     assert torch.isnan(o[0]["out"][1]).all()
     check(d, o, skip=(1,))
+    d["x"][1, 3] = float("inf")
+    o = call(M, d)
+    assert torch.isnan(o[0]["out"][1]).any() and not torch.isfinite(o[0]["out"][1]).all()
+    check(d, o, skip=(1,))
     # weights that are not finite, in an expert of token 0 and of an expert nobody uses
-    d = make(4, 256, 12, 2, 128, routing="ids", seed=4)
+    d = make(4, 256, 12, 2, 128, fmt=fmt, routing="ids", seed=4)
     d["ids"].copy_(torch.tensor([[0, 1], [2, 3], [6, 4], [5, 1]], dtype=torch.int32))
     for e in (0, 9):
-        d["w13"][e, 5] = float("inf")
-        d["w2"][e, 7] = float("nan")
+        d["w13"][e, 5] = float("inf") if fmt == "bf16" else 0x7f  # (E4M3 has NaN only)
+        d["w2"][e, 7] = float("nan") if fmt == "bf16" else 0xff
     o = call(M, d)
     assert torch.isnan(o[0]["out"][0, 7])
     check(d, o, skip=(0,))
@@ -314,8 +353,9 @@ def test_ties_take_the_lower_expert(M):
     assert (tw[0] == 0.25).all()
 
 
-def test_repeats_bit_for_bit(M):
-    d = make(8, 1024, 32, 8, 512, tail="full", nxt="both", seed=7)
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "block"])
+def test_repeats_bit_for_bit(M, fmt):
+    d = make(8, 1024, 32, 8, 512, fmt=fmt, tail="full", nxt="both", seed=7)
     p = plan(M, d)
     first = call(M, d, p)
     for _ in range(20):
@@ -356,8 +396,9 @@ def test_launches(M):
     assert M.lib.moe_launch_count() == n + 2
 
 
-def test_two_streams_at_once(M):
-    ds = [make(4, 1024, 16, 4, 512, tail="full", nxt="both", seed=30 + i) for i in range(3)]
+@pytest.mark.parametrize("n,fmt", [(2, "bf16"), (3, "fp8"), (8, "bf16")])
+def test_streams_at_once(M, n, fmt):
+    ds = [make(8 - i % 3, 1024, 16, 4, 512, fmt=fmt, tail="full", nxt="both", seed=30 + i) for i in range(n)]
     ps = [plan(M, d) for d in ds]
     want = [call(M, d, p) for d, p in zip(ds, ps)]
     torch.cuda.synchronize()
@@ -374,8 +415,23 @@ def test_two_streams_at_once(M):
     assert M.device_status() == 0
 
 
-def test_graphs_sharing_a_workspace(M):
-    d = make(2, 512, 16, 4, 256, tail="full", seed=40)
+def test_without_dependent_launch(M, monkeypatch):
+    # (the switch is read once per process: a process of its own)
+    import os
+    import subprocess
+    import sys
+    code = ("import tests.test_gpu_layer as t, moe_expert_ffn_rms_gb300 as M\n"
+            "d = t.make(4, 512, 16, 4, 256, tail='full', nxt='both', seed=1)\n"
+            "t.check(d, t.call(M, d))\nprint('fine')")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, MOE_PDL="0"),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_graphs_sharing_a_workspace(M, fmt):
+    d = make(2, 512, 16, 4, 256, fmt=fmt, tail="full", seed=40)
     d2 = dict(d, x=d["x"].flip(0).contiguous())
     d2["residual"] = d2["x"]
     p = plan(M, d)
