@@ -395,8 +395,10 @@ MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float ss, LayerSmem* s
       key[i] = (u & 0x80000000u) ? ~u : u | 0x80000000u;  // -inf: 0x007fffff
     }
   }
-  float sel = -INFINITY;
+  float mine = 0.f, top = 0.f, s = 0.f;
   int sel_e = 0;
+  bool some = false;
+#pragma unroll 1
   for (int j = 0; j < p.k; ++j) {
     unsigned m = key[0];
 #pragma unroll
@@ -412,19 +414,21 @@ MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float ss, LayerSmem* s
       for (int i = 0; i < PER; ++i)
         if ((int)(at >> 5) == i) key[i] = 0;
     }
+    const float z = __uint_as_float((m & 0x80000000u) ? m & 0x7fffffffu : ~m);  // (every lane)
+    if (j == 0) {
+      top = z;
+      some = z > -INFINITY;
+    }
+    const float e = some ? expf(z - top) : 0.f;
+    s += e;
     if (lane == j) {
-      sel = __uint_as_float((m & 0x80000000u) ? m & 0x7fffffffu : ~m);
+      mine = e;
       sel_e = (int)at;
     }
   }
-  const float top = __shfl_sync(0xffffffffu, sel, 0);
-  const bool some = top > -INFINITY;
-  const float e = (some && lane < p.k) ? expf(sel - top) : 0.f;
-  float s = 0.f;
-  for (int j = 0; j < p.k; ++j) s += __shfl_sync(0xffffffffu, e, j);
   if (lane < p.k) {
     sm->ids[t][lane] = sel_e;
-    sm->w[t][lane] = some ? e / s : 0.f;
+    sm->w[t][lane] = some ? mine / s : 0.f;
   }
 }
 
@@ -556,6 +560,15 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
   const int T = p.T, H = p.H, E = p.E, I = p.I, k = p.k;
   if (tid < kMaxExperts) sm.used[tid] = 0;
   pdl_trigger();
+  // what does not depend on the routing is worked out before the wait
+  const int n0 = (int)((int64_t)blockIdx.x * H / gridDim.x);
+  const int n1 = (int)((int64_t)(blockIdx.x + 1) * H / gridDim.x);
+  const uint32_t rb1 = (uint32_t)H * EB, rb2 = (uint32_t)I * EB;  // bytes of a weight row
+  const int S1 = (int)((rb1 + 127) >> 7), S2 = (int)((rb2 + 127) >> 7);  // 128-byte steps of a row
+  const int kb1 = (int)(rb1 >> 6), kb2 = (int)(rb2 >> 6);                // 64-byte K blocks
+  const int P1 = (H + 127) >> 7, P2 = (I + 127) >> 7;                    // powers of two of a row
+  const int tiles_e = I >> 3;                                            // FC1 row tiles of an expert
+  const unsigned magic = 0xffffffffu / (unsigned)tiles_e;
   static_assert(R::kDepth <= kMaxDepth && kMaxExperts <= kThreadsL, "shared tables");
   if (tid < kWarps) {
     for (int i = 0; i < R::kDepth; ++i) {
@@ -650,18 +663,10 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
   // ones (one per CTA) single, the K steps of a claim interleaved over the
   // warps.  FC2: output rows [n0, n1) in units of 32, all experts' K
   // steps in one sequence of which warp w takes the w-th eighth.
-  const int tiles_e = I >> 3;
   const int tiles = n_act * tiles_e;
   const int singles = min(tiles, (int)gridDim.x & ~1);
   const int pairs = (tiles - singles) >> 1;  // tiles and singles are even
   const int claims = pairs + singles;
-  const int n0 = (int)((int64_t)blockIdx.x * H / gridDim.x);
-  const int n1 = (int)((int64_t)(blockIdx.x + 1) * H / gridDim.x);
-  const uint32_t rb1 = (uint32_t)H * EB, rb2 = (uint32_t)I * EB;  // bytes of a weight row
-  const int S1 = (int)((rb1 + 127) >> 7), S2 = (int)((rb2 + 127) >> 7);  // 128-byte steps of a row
-  const int kb1 = (int)(rb1 >> 6), kb2 = (int)(rb2 >> 6);                // 64-byte K blocks
-  const int P1 = (H + 127) >> 7, P2 = (I + 127) >> 7;                    // powers of two of a row
-  const unsigned magic = 0xffffffffu / (unsigned)tiles_e;
   // expert slot and first intermediate column of a claim
   auto claim_at = [&](int c, int& a, int& i0) {
     const int tile = c < pairs ? 2 * c : c + pairs;
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
 
   const int wk = warp % kWarps;  // consumer whose steps these are
   const int q0 = n_act * S2 * wk / kWarps, q1 = n_act * S2 * (wk + 1) / kWarps;  // FC2 steps of a unit
-  const int a_first = q0 / S2, s_first = q0 - a_first * S2;
+  const int a_first = n_act * wk / kWarps, s_first = q0 - a_first * S2;  // (q0 / S2)
   const int units = (n1 - n0 + 31) / 32;
   unsigned char* ring = ring_all + wk * R::kWarp;
   const size_t x_term = (size_t)T * H, a_term = (size_t)T * k * I;  // elements of a term
