@@ -30,8 +30,11 @@
 //   bf16 weights  bf16 terms (16 bits of mantissa)
 //   E4M3 weights  fp16 terms (22 bits): E4M3 -> fp16 is exact and one instruction
 //                 for two weights, E4M3 -> bf16 four.  fp16 has little range, so
-//                 a token's 128 columns share a power of two, applied with the
-//                 weight scale after a step.  (mma.sync on E4M3 itself is no way
+//                 the terms carry powers of two: a token's 128 columns of x share
+//                 one, applied with the weight scale after a step; eight columns
+//                 of the intermediate do (a row tile, all that a claim is sure to
+//                 hold of them), brought to the pair's largest by an exact fp16
+//                 product when they are used.  (mma.sync on E4M3 itself is no way
 //                 around the conversion: it runs as one, 51 cycles per m16n8k32
 //                 against 22 per m16n8k16 with operands from shared memory.)
 //
@@ -39,17 +42,25 @@
 // the consumer's part of shared memory a few steps ahead (cp.async; a pair of
 // mbarriers per step).  The pieces lie as the consumer's lanes feed them to the
 // MMAs, so a step is 16-byte shared loads, conversions and MMAs and nothing else
-// (with the copies in the same warp the issue of their addresses set the rate).
-// The order of the K elements inside a piece is the same for both operands and
-// therefore free.  The activations go the same way as the weights: a plain load
-// of them would wait behind the copies in flight (4 us of them with 160 KB per
-// SM).  The first W2 pieces are on their way while the CTA waits for the other
-// CTAs' FC1 tiles.
+// (with the copies issued by the same warps: 119 us against 113 for four tokens
+// with block-wise FP8).  The order of the K elements inside a piece is the same for
+// both operands and therefore free.  The activations go the same way as the
+// weights: a plain load of them would wait behind the copies in flight (8 tokens
+// 375 us against 256).  The first W2 pieces are on their way while the CTA waits
+// for the other CTAs' FC1 tiles.
 //
-// mma.sync and not tcgen05: at 8 columns the tensor work is 1/16 of what the
-// legacy instruction sustains at this memory rate, a fragment load straight from
-// the copied bytes needs no descriptor layout, and accumulators in registers
-// spare the TMEM round trip between short row tiles.
+// mma.sync and not tcgen05: with 8 columns the tensor pipe is 13 to 20% busy and
+// HBM is what binds; a fragment read straight from the copied bytes needs no
+// descriptor layout, row tiles of 16 let every CTA have an equal share of the
+// output rows (27 of 4096), and accumulators in registers spare the TMEM round
+// trip between tiles that short.
+//
+// Measured (H = 4096, I = 1536, E = 64, top_k = 8, cold weights): one token 63.5 us
+// (302 MB; 7 us of it the routing launch and 4 the tail), eight tokens 250 us
+// (1.775 GB read, 7.1 TB/s), E4M3 one token 34 us, block-wise FP8 four tokens 96 us
+// (4.9 TB/s).  The separate launches of moe_ffn_forward, without a tail: 95, 251, 53
+// and 122 us.  What is left at one token is latency around the stream: routing 8 us,
+// the wait between FC1 and FC2 2 us, the tail 4 us.
 #include "block_tail.cuh"
 #include "kernels.h"
 #include "tail.h"
@@ -80,14 +91,15 @@ struct Ring {
   static constexpr int kPieces = FP8 ? 2 : 1;  // of one term for 16 bytes of weights
   static constexpr int kScaleAt = kStepA + 2 * Cols<TOK>::kMmas * kPieces * 512;
   static constexpr int kPowAt = kScaleAt + 128;
-  static constexpr int kStage = kScaleAt + (FP8 ? 128 + 64 : 0);
+  static constexpr int kStage = kScaleAt + (FP8 ? 128 + 2 * TOK * 8 : 0);
   static constexpr int kDepth = (200 << 10) / (kWarps * kStage);  // 3 .. 5 steps
   static constexpr int kWarp = kDepth * kStage;
   static constexpr int kBytes = kWarps * kWarp;
 };
 constexpr int kRed = kWarps * 2 * 16 * 8;  // floats: partial sums of all warps, two row tiles
 constexpr int kMaxPairs = kLayerMaxT * kMaxTopK;
-constexpr int kCtrInts = 8;
+constexpr int kCtrPow = 8;  // ctr: largest exponent of each pair's intermediate
+constexpr int kCtrInts = kCtrPow + kMaxPairs;
 
 struct LayerP {
   const bf16* x;
@@ -110,12 +122,11 @@ struct LayerP {
   uint16_t* xt;        // terms of x w [2][T, H], bf16 or (FP8) fp16
   uint16_t* at;        // terms of the intermediate [2][T k, I], times the routing weight
   float* xpow;         // FP8: powers of two of x w [T, H / 128]
-  float* apow;         // FP8: of the intermediate [T k, I / 128]
-  float* act;          // FP8: the intermediate [T k, I]
+  uint8_t* apow;       // FP8: exponents (pow_exponent) of the intermediate's 8-column groups [T k, I / 8]
   float *ssq, *part;   // sums of squares [chunks, 8], partial logits [chunks, T, E]
   float* f;            // [T, H]
   int* ctr;            // [0] FC1 claims, [1] FC1 tiles done, [2] CTAs finished,
-                       // [3] claims and [4] units of the intermediate's terms
+                       // [8..] kCtrPow
   int* status;
 };
 
@@ -306,6 +317,17 @@ MOE_DEV void cp_async16z(uint32_t dst, const void* src, int bytes) {
 MOE_DEV void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
+MOE_DEV void cp_async8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+MOE_DEV uint4 hmul2x4(const uint4& a, uint32_t b) {
+  uint4 d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d.x) : "r"(a.x), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d.y) : "r"(a.y), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d.z) : "r"(a.z), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d.w) : "r"(a.w), "r"(b));
+  return d;
+}
 MOE_DEV void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreadsL) : "memory"); }
 MOE_DEV void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -351,6 +373,7 @@ struct LayerSmem {
   int flag;
   int abort;
   int in_time;  // result of a wait, for all consumers
+  int pow[kMaxPairs];  // FP8: largest exponent of the pair's intermediate
   float sum[kWarps];
   uint64_t full[kWarps][kMaxDepth], empty[kWarps][kMaxDepth];
 };
@@ -566,7 +589,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
   const uint32_t rb1 = (uint32_t)H * EB, rb2 = (uint32_t)I * EB;  // bytes of a weight row
   const int S1 = (int)((rb1 + 127) >> 7), S2 = (int)((rb2 + 127) >> 7);  // 128-byte steps of a row
   const int kb1 = (int)(rb1 >> 6), kb2 = (int)(rb2 >> 6);                // 64-byte K blocks
-  const int P1 = (H + 127) >> 7, P2 = (I + 127) >> 7;                    // powers of two of a row
+  const int P1 = (H + 127) >> 7;                                         // powers of two of a row of x
   const int tiles_e = I >> 3;                                            // FC1 row tiles of an expert
   const unsigned magic = 0xffffffffu / (unsigned)tiles_e;
   static_assert(R::kDepth <= kMaxDepth && kMaxExperts <= kThreadsL, "shared tables");
@@ -722,7 +745,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
       }
     };
     // This lane's column of the activations at the step, to the next MMA's column.
-    auto copy_b = [&](int sl, const uint16_t* b, size_t bj, const float* pw, bool two) {
+    auto copy_b = [&](int sl, const uint16_t* b, size_t bj, bool two) {
       const uint32_t dst = ring_u + sl * R::kStage + kStepA + lane * 16;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
@@ -732,7 +755,6 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
           cp_async16_l1(dst + ((NJ + j) * Q + q) * 512, b + j * bj + (two ? KE : 0) + q * 8, two ? 16 : 0);
         }
       }
-      if (FP8 && first_lane) cp_async4(ring_u + sl * R::kStage + R::kPowAt + tok * 4, pw);
     };
     auto wait_empty = [&]() -> bool { return ptx::mbar_wait(&sm.empty[wk][slot], ph, &sm.abort); };
     auto next_slot = [&]() {
@@ -782,7 +804,10 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
         if (!(ok = wait_empty())) break;
         const bool two = !FP8 || 2 * step + 1 < kb1;
         copy_a(slot, src, 8 * rb1, (uint32_t)I * rb1, c < pairs ? 15u : 3u, two);
-        if (on) copy_b(slot, b, TPG * x_term, pw, two);
+        if (on) {
+          copy_b(slot, b, TPG * x_term, two);
+          if (FP8 && first_lane) cp_async4(ring_u + slot * R::kStage + R::kPowAt + tok * 4, pw);
+        }
         if (FP8 && sok) cp_async4(ring_u + slot * R::kStage + R::kScaleAt + lane * 4, sc);
         cp_arrive(&sm.full[wk][slot]);
         next_slot();
@@ -823,9 +848,17 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
     };
     auto step_b = [&](int sl, const At& t) {
       const int pr = sm.pair[t.a][tok];
-      if (pr >= 0)
-        copy_b(sl, p.at + (size_t)(g % TPG) * a_term + (size_t)pr * I + t.s * 2 * KE + tq * 8 * Q, TPG * a_term,
-               p.apow + pr * P2 + t.s, !FP8 || 2 * t.s + 1 < kb2);
+      if (pr >= 0) {
+        const bool two = !FP8 || 2 * t.s + 1 < kb2;
+        copy_b(sl, p.at + (size_t)(g % TPG) * a_term + (size_t)pr * I + t.s * 2 * KE + tq * 8 * Q, TPG * a_term, two);
+        // lane tq of the token's first column: the eight groups of K block tq (an
+        // absent block's exponents are 0, its factors too)
+        if (FP8 && g % TPG == 0 && tq < 2) {
+          const bool there = two || tq == 0;
+          cp_async8(ring_u + sl * R::kStage + R::kPowAt + (tq * TOK + tok) * 8,
+                    p.apow + (size_t)pr * (I >> 3) + t.s * 16 + (there ? tq * 8 : 0), there ? 8 : 0);
+        }
+      }
     };
     if (ok && total > 0) {
       const int early = min(R::kDepth, total);
@@ -867,7 +900,9 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
   int slot = 0;
   uint32_t ph = 0;
   bool arrived = true;
-  auto multiply = [&](Sums& acc, float (&s)[4][NC]) {
+  // FC2 with FP8: the groups of the lane's column are brought to the exponent
+  // `top`, and `down` holds the powers of two of the lane's columns.
+  auto multiply = [&](bool fc2, Sums& acc, float (&s)[4][NC], int top, const float (&down)[NC]) {
     arrived = ptx::mbar_wait(&sm.full[warp][slot], ph, &sm.abort) && arrived;
     const unsigned char* st = ring + slot * R::kStage;
     const uint4* sp = reinterpret_cast<const uint4*>(st) + lane;
@@ -876,6 +911,16 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
       uint4 b[NJ][Q];
 #pragma unroll
       for (int j = 0; j < NJ * Q; ++j) b[j / Q][j % Q] = sp[kStepA / 16 + (kb * NJ * Q + j) * 32];
+      if (FP8 && fc2) {
+        const unsigned ex = *reinterpret_cast<const uint16_t*>(st + R::kPowAt + (kb * TOK + tok) * 8 + tq * 2);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int d = (int)((ex >> (8 * q)) & 255u) - top;  // <= 0: an exact power of two (0 below 2^-24)
+          const __half2 f = __float2half2_rn(__uint_as_float((uint32_t)max(127 + d, 0) << 23));
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) b[j][q] = hmul2x4(b[j][q], *reinterpret_cast<const uint32_t*>(&f));
+        }
+      }
 #pragma unroll
       for (int tl = 0; tl < 2; ++tl) {
         const uint4 lo = sp[((tl * 2 + 0) * 2 + kb) * 32], hi = sp[((tl * 2 + 1) * 2 + kb) * 32];  // rows g, g + 8
@@ -908,7 +953,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
       for (int i = 0; i < 4; ++i) {
         const float w = *reinterpret_cast<const float*>(st + R::kScaleAt + (g + 8 * i) * 4);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) s[i][c] = w * pw[c];
+        for (int c = 0; c < NC; ++c) s[i][c] = w * (fc2 ? down[c] : pw[c]);
       }
     }
     __syncwarp();
@@ -971,7 +1016,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
   };
 
   int buf = 0, my_tiles = 0;
-  float sc[4][NC] = {};
+  float sc[4][NC] = {}, down[NC] = {};
   Sums acc = {}, tot = {};
 
   // ---- FC1
@@ -986,7 +1031,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
     const bool second = c < pairs;
 #pragma unroll 1
     for (int step = warp; step < S1; step += kWarps) {
-      multiply(acc, sc);
+      multiply(false, acc, sc, 0, down);
       if constexpr (FP8) fold(tot, acc, sc, mask);
     }
     if constexpr (!FP8) fold(tot, acc, sc, mask);
@@ -1010,14 +1055,26 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
       }
       gate += __shfl_xor_sync(0xffffffffu, gate, 16);
       up += __shfl_xor_sync(0xffffffffu, up, 16);
-      if (lane < (second ? 16 : 8)) {
-        const float r = sm.r[warp];
-        // the routing weight goes into the intermediate, so FC2 adds the token's
-        // experts without a factor
-        const float v = silu_f(gate * r) * (up * r) * sm.wt[a][warp];
-        const size_t at = (size_t)sm.pair[a][warp] * I + i0 + il;
-        if constexpr (FP8) p.act[at] = v;
-        else split16<false>(v, p.at[at], p.at[at + a_term]);
+      const float r = sm.r[warp];
+      // the routing weight goes into the intermediate, so FC2 adds the token's
+      // experts without a factor
+      float v = silu_f(gate * r) * (up * r) * sm.wt[a][warp];
+      const bool mine = lane < (second ? 16 : 8);
+      const int pr = sm.pair[a][warp];
+      if constexpr (FP8) {  // eight columns share a power of two
+        float m = fabsf(v);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int ex = pow_exponent(m);
+        v *= pow_up(ex);
+        if (mine && (il & 7) == 0) {
+          p.apow[(size_t)pr * (I >> 3) + (i0 + il) / 8] = (uint8_t)ex;
+          atomicMax(&p.ctr[kCtrPow + pr], ex);
+        }
+      }
+      if (mine) {
+        const size_t at = (size_t)pr * I + i0 + il;
+        split16<FP8>(v, p.at[at], p.at[at + a_term]);
       }
     }
     my_tiles += second ? 2 : 1;
@@ -1025,58 +1082,21 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
   }
   // ---- all FC1 tiles done (this CTA's are counted once its writes are there)
   consumer_sync();
-  int conv = 0;
-  if (tid == 0) {
+  if (tid == 0 && my_tiles) {
     __threadfence();
-    if (my_tiles) atomicAdd(&p.ctr[1], my_tiles);
-    if (FP8) conv = atomicAdd(&p.ctr[3], 1);
+    atomicAdd(&p.ctr[1], my_tiles);
   }
-  bool ok = wait_for(p.ctr + 1, tiles);
-  if constexpr (FP8) {
-    // ---- the intermediate's terms, 128 columns of a pair to a warp, eight such
-    // units to a claim
-    const int parts = T * k * P2;
-    while (ok) {
-      if (tid == 0) sm.flag = conv;
-      consumer_sync();
-      const int first = sm.flag * kWarps;
-      consumer_sync();
-      if (first >= parts) break;
-      const int pr = (first + warp) / P2, blk = first + warp - pr * P2;
-      const int at = blk * 128 + lane * 4;
-      if (first + warp < parts) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (at < I) v = __ldcg(reinterpret_cast<const float4*>(p.act + (size_t)pr * I + at));
-        const float m = warp_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-        const int ex = pow_exponent(m);
-        const float up = pow_up(ex);
-        ushort4 hi, lo;
-        split16<true>(v.x * up, hi.x, lo.x);
-        split16<true>(v.y * up, hi.y, lo.y);
-        split16<true>(v.z * up, hi.z, lo.z);
-        split16<true>(v.w * up, hi.w, lo.w);
-        if (at < I) {
-          *reinterpret_cast<ushort4*>(p.at + (size_t)pr * I + at) = hi;
-          *reinterpret_cast<ushort4*>(p.at + a_term + (size_t)pr * I + at) = lo;
-        }
-        if (lane == 0) p.apow[pr * P2 + blk] = pow_down(ex);
-      }
-      consumer_sync();
-      if (tid == 0) {
-        __threadfence();
-        atomicAdd(&p.ctr[4], min(kWarps, parts - first));
-        conv = atomicAdd(&p.ctr[3], 1);
-      }
-    }
-    if (ok) ok = wait_for(p.ctr + 4, parts);
-  }
-  if (!ok) {
+  if (!wait_for(p.ctr + 1, tiles)) {
     if (tid == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
     return;
   }
   if (tid == 0) {
     __threadfence_block();
     *(volatile int*)&sm.fc1_done = 1;
+  }
+  if constexpr (FP8) {
+    if (tid < T * k) sm.pow[tid] = max(15, __ldcg(&p.ctr[kCtrPow + tid]));
+    consumer_sync();
   }
 
   // ---- FC2: this CTA's output rows over all active experts
@@ -1085,9 +1105,19 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
     for (int q = q0; q < q1;) {
       const unsigned mask = sm.mask[a];
       const int end = min(q1, q + S2 - s_at);
+      int top = 15;
+      if constexpr (FP8) {
+        const int pr = sm.pair[a][tok];
+        if (pr >= 0) top = sm.pow[pr];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int pc = sm.pair[a][2 * tq / TPG + c];
+          down[c] = pc >= 0 ? pow_down(sm.pow[pc]) : 1.f;
+        }
+      }
 #pragma unroll 1
       for (; q < end; ++q) {
-        multiply(acc, sc);
+        multiply(true, acc, sc, top, down);
         if constexpr (FP8) fold(tot, acc, sc, mask);
       }
       if constexpr (!FP8) fold(tot, acc, sc, mask);
@@ -1157,7 +1187,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
 }
 
 struct LayerWs {
-  size_t xt, at, xpow, apow, act, ssq, part, f, ctr, total;
+  size_t xt, at, xpow, apow, ssq, part, f, ctr, total;
 };
 
 LayerWs layer_layout(int T, int H, int E, int I, int k, bool fp8) {
@@ -1172,8 +1202,7 @@ LayerWs layer_layout(int T, int H, int E, int I, int k, bool fp8) {
   w.xt = take(t * H * 4);
   w.at = take(t * k * I * 4);
   w.xpow = take(fp8 ? t * ((H + 127) / 128) * 4 : 0);
-  w.apow = take(fp8 ? t * k * ((I + 127) / 128) * 4 : 0);
-  w.act = take(fp8 ? t * k * I * 4 : 0);
+  w.apow = take(fp8 ? t * k * (I / 8) : 0);
   w.ssq = take((size_t)kLayerChunks * kLayerMaxT * 4);
   w.part = take((size_t)kLayerChunks * t * E * 4);
   w.f = take(t * H * 4);
@@ -1216,8 +1245,7 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
   p.xt = reinterpret_cast<uint16_t*>(ws + w.xt);
   p.at = reinterpret_cast<uint16_t*>(ws + w.at);
   p.xpow = reinterpret_cast<float*>(ws + w.xpow);
-  p.apow = reinterpret_cast<float*>(ws + w.apow);
-  p.act = reinterpret_cast<float*>(ws + w.act);
+  p.apow = ws + w.apow;
   p.ssq = reinterpret_cast<float*>(ws + w.ssq);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.f = reinterpret_cast<float*>(ws + w.f);
