@@ -1,5 +1,17 @@
 // moe_combine_norm: the sum of a token's expert rows and what follows the
 // block (block_tail.cuh) in one pass over the data.
+//
+// Each byte of the expert rows, the residual and the outputs moves once, so the
+// bound is the copy bandwidth (6770 GB/s measured); sums, norms and scales are
+// fp32 and only the stored outputs are rounded.  Device time per call, inputs
+// not in L2 (k rows of H per token; "from" are the types of rows and residual):
+//   T    H    k                                    us    of the copy bandwidth
+//   4096 4096 8  bf16, bf16 -> bf16, x_hat         57    95%
+//   2047 5120 1  bf16, fp32 -> fp32, E4M3          24.3  70%
+//   333  2944 4  fp32, bf16 -> bf16, E4M3 groups    8.0  38%
+//   64   7168 8  bf16, fp32 -> fp32, x_hat          5.5  33%
+//   1    4096 8  bf16, bf16 -> bf16, x_hat          3.3  (latency)
+// The short calls are a launch, one round of loads and two row reductions.
 #include "block_tail.cuh"
 #include "kernels.h"
 #include "tail.h"
@@ -45,12 +57,14 @@ MOE_DEV float row_rnorm(const float (&f)[VPT][8], int nt, int H, float eps, floa
   return 1.0f / sqrtf(rows_reduce<false>(ss, nt, red) / (float)H + eps);
 }
 
-// x_hat (and its quantisation) of the row h held in f; chunks beyond the row
-// hold zeros.  KEPT: next_w holds this thread's (one) chunk of the weights.
+// x_hat (and its quantisation) of the row h held in f; chunks beyond the row hold
+// zeros.  KEPT: next_w holds this thread's (one) chunk of the weights.  red: two
+// arrays of rows_reduce.
 template <int VPT, bool KEPT = false>
-MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], float r, int nt,
-                        const uint4& next_w, float* red) {
+MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], int nt, const uint4& next_w,
+                        float (*red)[16]) {
   const int tid = threadIdx.x, nv = H >> 3;
+  const float r = row_rnorm(f, nt, H, p.next_eps, red[0]);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -67,28 +81,26 @@ MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], float 
       }
       if (p.xhat) store8_bf16(p.xhat + (size_t)t * H + v * 8, f[i]);
     }
+    amax = fmaxf(amax, m);
     if (p.xq && p.q_group) {
       // a group of 128 columns is 16 consecutive lanes (nt is a multiple of 32,
       // H of 128)
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float s = m > 0.f ? __fdiv_rn(m, 448.0f) : 1.0f;
-      if (v < nv) {
-        *reinterpret_cast<uint2*>(p.xq + (size_t)t * H + v * 8) = tail_e4m3x8(f[i], s);
-        if ((v & 15) == 0) p.xscale[(size_t)t * (H >> 7) + (v >> 4)] = s;
-      }
+      if (v < nv && (v & 15) == 0) p.xscale[(size_t)t * (H >> 7) + (v >> 4)] = s;
+      if (v < nv) *reinterpret_cast<uint2*>(p.xq + (size_t)t * H + v * 8) = tail_e4m3x8(f[i], s);
     }
-    amax = fmaxf(amax, m);
   }
   if (p.xq && !p.q_group) {
-    amax = rows_reduce<true>(amax, nt, red);
+    amax = rows_reduce<true>(amax, nt, red[1]);
     const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    if (tid == 0) p.xscale[t] = s;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = tid + i * nt;
       if (v < nv) *reinterpret_cast<uint2*>(p.xq + (size_t)t * H + v * 8) = tail_e4m3x8(f[i], s);
     }
-    if (tid == 0) p.xscale[t] = s;
   }
 }
 
@@ -96,6 +108,7 @@ MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], float 
 // Few tokens (latency) and rows too long for the streaming form: every load of
 // a chunk (its k expert rows, residual, weights) is issued before the first
 // use, so the chain is one round of loads, two row reductions, the stores.
+// BJ and EARLY keep the chunks in flight within 128 registers per thread.
 struct Raw8 {
   uint4 a, b;  // 8 columns: bf16 in a, or fp32 in a and b
 };
@@ -201,7 +214,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_row_kernel(
     for (int q = 0; q < 8; ++q) f[i][q] = h[q];
   }
   if (!p.next_w) return;
-  write_next(p, t, H, f, row_rnorm(f, nt, H, p.next_eps, red[1]), nt, make_uint4(0u, 0u, 0u, 0u), red[2]);
+  write_next(p, t, H, f, nt, make_uint4(0u, 0u, 0u, 0u), red + 1);
 }
 
 // ----------------------------------------------------------- streaming form --
@@ -211,7 +224,9 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_row_kernel(
 // through its row reductions.  A stage holds R of the token's k expert rows
 // (one copy when they are consecutive); the token's last stage also holds its
 // residual and its gate row.  The producer reads the token's indices and
-// leaves them beside the rows.
+// leaves them beside the rows.  Without the stages the loads of a token wait for
+// the reductions of the one before it: 66.7 us instead of 57 at T = 4096, H = 4096,
+// k = 8, and 36.7 instead of 24.3 at T = 2047, H = 5120, k = 1.
 struct StreamMeta {
   unsigned use;   // slots whose row is present
   float factor;   // tail_row_factor
@@ -424,8 +439,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, VPT <= 2 ? 2 : 1)
     __syncwarp();
     if ((tid & 31) == 0) ptx::mbar_arrive(&empty[s]);
     if (p.next_w)
-      write_next<VPT, KEEP>(p, t, H, f, row_rnorm(f, nt, H, p.next_eps, red[n & 1][1]), nt, nw,
-                            red[n & 1][2]);
+      write_next<VPT, KEEP>(p, t, H, f, nt, nw, red[n & 1] + 1);
     if (++s == S) {
       s = 0;
       ph ^= 1;
@@ -462,11 +476,13 @@ cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_
   auto by_smem = [&](int64_t b) { return (int)(kStreamSmem / (b + kStreamStatic)); };
   int R = k, S, per_sm = by_smem(bytes(k)) < by_regs ? by_smem(bytes(k)) : by_regs;
   if (per_sm > 0 && T <= sms * per_sm) {
-    // every token gets a CTA of its own at once: one stage each
+    // every token gets a CTA of its own at once: one stage each (T = 333, H = 2944,
+    // k = 4: 8.0 us, against 9.9 with two stages and half the CTAs)
     S = 1;
   } else {
-    // two or more stages, each as much of a token as fits; then as many CTAs as
-    // fit, then the memory that is left goes to more stages
+    // two or more stages, each as much of a token as fits (a whole token wherever two
+    // fit: copies stay long, and a token waits once); then as many CTAs as fit, then
+    // the memory that is left goes to more stages
     while (R > 1 && by_smem(2 * bytes(R)) < 1) R = (R + 1) / 2;
     per_sm = by_smem(2 * bytes(R));
     if (per_sm < 1) return cudaErrorNotSupported;
@@ -476,7 +492,8 @@ cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_
     if (R < k) kern = combine_norm_stream_kernel<VPT, YF32, true>;
   }
   const size_t smem = (size_t)S * bytes(R);
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the same limit in every call: another thread's launch may lie between this and ours
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem - kStreamStatic);
   if (e != cudaSuccess) return e;
   const int grid = T < sms * per_sm ? T : sms * per_sm;
   return launch_kernel(kern, dim3(grid), dim3(threads + 32), smem, st, y, (int)pair_order, row_of_pair, T,
@@ -490,6 +507,11 @@ cudaError_t launch_combine_norm(const void* y, bool y_f32, bool pair_order,
                                 int* status, int sms, cudaStream_t st) {
   if (T == 0) return cudaSuccess;
   const int nv = H / 8;
+  // A CTA per token while the SMs hold all tokens at once, the streaming form beyond:
+  // T = 64 (H = 7168, k = 8) 5.5 us against 6.0 streamed; T = 333 (H = 2944, k = 4)
+  // 10.2 against 8.0.  Rows above 16384 columns always take a CTA per token: a thread
+  // of the streaming form would hold more than four chunks.  MOE_CN_STREAM=0|1 sets the
+  // form for measurements.
   const char* env = getenv("MOE_CN_STREAM");
   if (nv <= 2048 && (env ? env[0] == '1' : T > sms)) {
     const int vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);

@@ -1262,8 +1262,9 @@ cudaError_t launch_layer(const LayerArgs& a, const TailP* tail, int sms, int* st
   if (tt == 2) route = a.fp8 ? layer_route_kernel<true, 2> : layer_route_kernel<false, 2>;
   if (tt == 4) route = a.fp8 ? layer_route_kernel<true, 4> : layer_route_kernel<false, 4>;
   cudaError_t e = cudaSuccess;
-  if (route_smem > (24 << 10))
-    e = cudaFuncSetAttribute(route, cudaFuncAttributeMaxDynamicSharedMemorySize, route_smem);
+  if (route_smem > (24 << 10))  // (one limit for all calls: other threads may launch between)
+    e = cudaFuncSetAttribute(route, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kLayerMaxH / kLayerChunks * kLayerMaxT * 4);
   if (e != cudaSuccess) return e;
   e = launch_kernel(route, dim3(kLayerChunks, a.router_w ? (a.E + 31) / 32 : 1), dim3(32 * kRouteWarps),
                     (size_t)route_smem, st, p);

@@ -359,3 +359,49 @@ def test_after_the_grouped_ffn(M):
              post_w=randn(g, H, std=0.1, mean=0.5), gate=None, gate_row=None, scale=1.0,
              post_eps=1e-6, next_eps=1e-6, next_w=inp["norm_w"], next="both")
     check(d, call(M, d))
+
+
+def test_host_threads_at_once(M):
+    """Calls of different sizes from several host threads, each on a stream of its own."""
+    import threading
+    cases = [make(T, H, k, nxt="bf16", res=None, seed=70 + i)
+             for i, (T, H, k) in enumerate([(400, 2048, 8), (600, 512, 2), (300, 4096, 8), (900, 256, 1)])]
+    want = [call(M, d) for d in cases]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(200):
+                    o = call(M, cases[i])
+                s.synchronize()
+            for n in want[i]:
+                assert torch.equal(want[i][n], o[n]), n
+        except Exception as e:  # noqa: BLE001 (reported below, from the main thread)
+            errors.append(e)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not errors, errors
+
+
+@pytest.mark.parametrize("H,T,k", [(4096, 70000, 8), (32768, 70000, 1)])
+def test_offsets_beyond_32_bits(M, H, T, k):
+    """More elements than 32 bits count; the rows that are checked lie at the ends and beside 2^31 elements."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    base = randn(g, 4096, H, std=0.3)
+    y = base.repeat(-(-T * k // 4096), 1)[:T * k]
+    assert y.numel() > 2 ** 31
+    d = dict(T=T, H=H, k=k, scale=0.7, post_eps=1e-5, next_eps=1e-6, y=y, pair_order=True, row_of_pair=None,
+             residual=None, post_w=randn(g, H, std=0.2, mean=0.6), gate=None, gate_row=None,
+             next_w=randn(g, H, std=0.2, mean=1.0), next="bf16")
+    o = call(M, d)
+    at = 2 ** 31 // (H * k)  # the token that holds element 2^31 of y
+    rows = torch.tensor([0, 1, at - 1, at, at + 1, T // 2, T - 2, T - 1], device=DEV)
+    part = dict(d, T=len(rows), y=y.view(T, k, H)[rows].reshape(-1, H))
+    check(part, {n: v[rows] for n, v in o.items()})

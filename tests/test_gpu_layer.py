@@ -484,3 +484,80 @@ def test_two_layers_in_a_row(M):
     check(a, oa)
     assert torch.equal(stream, (oa[0]["out"].float() + mid.float()).to(torch.bfloat16))
     check(b, ob)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "block"])
+def test_calls_after_one_another_on_one_workspace(M, fmt):
+    """Each call's input is the output of the one before it, all in one workspace and one pair of
+    buffers: eagerly with a synchronisation after each call, without any, and in a graph."""
+    d = make(3, 768, 16, 4, 256, fmt=fmt, tail="full", nxt="bf16", seed=60)
+    p = plan(M, d)
+    n = 24
+
+    def run(sync):
+        a, b, outs = d["x"].clone(), torch.empty_like(d["x"]), []
+        for _ in range(n):
+            call(M, dict(d, x=a, residual=a), p, out=b)
+            if sync:
+                torch.cuda.synchronize()
+            outs.append(b.clone())
+            a, b = b, a
+        return outs
+
+    want = run(True)
+    got = run(False)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        replayed = run(False)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    for w, o, r in zip(want, got, replayed):
+        assert torch.equal(w, o) and torch.equal(w, r)
+    assert M.device_status() == 0
+
+
+def test_output_over_the_input(M):
+    """out = x (= residual): the block's update in place; and without a tail."""
+    for tail in ("full", "none"):
+        d = make(5, 512, 8, 2, 256, tail=tail, seed=61)
+        want = call(M, d)[0]["out"]
+        x = d["x"].clone()
+        e = dict(d, x=x, residual=x if tail == "full" else None)
+        call(M, e, out=x)
+        assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("T,H,E", [(8, 16384, 256), (8, 14336, 96), (4, 16384, 40)])
+def test_router_of_the_longest_rows(M, T, H, E):
+    d = make(T, H, E, 4, 64, tail="none", seed=62)
+    check(d, call(M, d))
+
+
+def test_host_threads_at_once(M):
+    """Layers of different sizes from several host threads, each with a stream and a workspace of its own."""
+    import threading
+    cases = [make(T, H, 8, 2, 128, fmt=fmt, tail="residual", seed=80 + T)
+             for T, H, fmt in [(8, 16384, "bf16"), (8, 12800, "bf16"), (2, 512, "fp8"), (6, 1024, "fp8")]]
+    plans = [plan(M, d) for d in cases]
+    want = [call(M, d, p)[0]["out"] for d, p in zip(cases, plans)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(100):
+                    o = call(M, cases[i], plans[i])[0]["out"]
+                s.synchronize()
+            assert torch.equal(o, want[i])
+        except Exception as e:  # noqa: BLE001 (reported below, from the main thread)
+            errors.append(e)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not errors, errors
