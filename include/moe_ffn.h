@@ -310,13 +310,13 @@ size_t moe_layer_workspace_size(const moe_shape* shape);
  *   twice for a token counts with the sum of its weights).
  *   wdtype: MOE_W_BF16, MOE_W_FP8_E4M3 or MOE_W_FP8_BLOCK.  Only the weights
  *   are quantised here: x_hat and the intermediate are not rounded to E4M3 or
- *   bf16 but enter the products with 16 bits of mantissa, products accumulate
- *   in fp32, and the only other rounding is that of the outputs.  (So the
+ *   bf16 but enter the products with at least 16 bits of mantissa, products
+ *   accumulate in fp32, and the only other rounding is that of the outputs.  (So the
  *   result is nearer to the exact one than moe_ffn_forward's, and not
  *   bit-equal to it.)
  *   tail NULL: out bf16 [T, H] = f (out_f32 must be 0).  Otherwise out [T, H]
  *   (bf16, or fp32 when out_f32) = h, and the tail's other outputs.  The
- *   block's own residual connection is tail->residual = x.
+ *   block's own residual connection is tail->residual = x.  out may be x.
  *   workspace >= moe_layer_workspace_size(shape) bytes, 256-byte aligned, not
  *   used by other work while this call runs; nothing in it has to be
  *   initialised or kept between calls.

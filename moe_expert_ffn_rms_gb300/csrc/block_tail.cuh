@@ -91,8 +91,9 @@ MOE_DEV float tail_row_factor(const TailP& p, int grow) {
 }
 
 // h of eight columns from column c: f the block's output, r its norm factor and
-// w its norm weights (unused without post_w), res the residual (zeros without).  A row whose gate index is out of range
-// (grow < 0) is the residual alone, whatever f holds.
+// w its norm weights (unused without post_w), res the residual (zeros without).  A
+// row whose gate index is out of range (grow < 0) is the residual alone, whatever f
+// holds.
 MOE_DEV void tail_h8(const TailP& p, int H, int c, const float (&f)[8], const float (&w)[8], float r,
                      int grow, float factor, const float (&res)[8], float (&h)[8]) {
   float g[8];

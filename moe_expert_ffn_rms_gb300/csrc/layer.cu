@@ -55,12 +55,12 @@
 // output rows (27 of 4096), and accumulators in registers spare the TMEM round
 // trip between tiles that short.
 //
-// Measured (H = 4096, I = 1536, E = 64, top_k = 8, cold weights): one token 63.5 us
-// (302 MB; 7 us of it the routing launch and 4 the tail), eight tokens 250 us
-// (1.775 GB read, 7.1 TB/s), E4M3 one token 34 us, block-wise FP8 four tokens 96 us
-// (4.9 TB/s).  The separate launches of moe_ffn_forward, without a tail: 95, 251, 53
-// and 122 us.  What is left at one token is latency around the stream: routing 8 us,
-// the wait between FC1 and FC2 2 us, the tail 4 us.
+// Measured (H = 4096, I = 1536, E = 64, top_k = 8, cold weights): one token 63.6 us
+// (302 MB), eight tokens 250 us (1.775 GB read, 7.1 TB/s), E4M3 one token 34 us,
+// block-wise FP8 four tokens 96 us (4.9 TB/s).  The separate launches of
+// moe_ffn_forward, without a tail: 96, 251, 54 and 122 us.  What is left at one token
+// is latency around the stream: the routing launch 4 to 5 us, the hand-over 1, the
+// routing in each CTA 4, the wait between FC1 and FC2 2, the tail 4.
 #include "block_tail.cuh"
 #include "kernels.h"
 #include "tail.h"
