@@ -180,119 +180,136 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
   extern __shared__ __align__(16) float xw[];  // [rows of the chunk][TT tokens]
   __shared__ float red[kRouteWarps][TT][32];
   pdl_trigger();
-  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = blockIdx.x;
   const Chunk ch = layer_chunk(p.H, c);
-  const int k0 = ch.k0, rows = ch.k1 - ch.k0, nv = rows >> 3;
-  if (c == 0 && blockIdx.y == 0 && tid < kCtrInts) p.ctr[tid] = 0;
+  const int k0 = ch.k0, rows = ch.k1 - ch.k0;
   const int e = blockIdx.y * 32 + lane;
   const float* wr = p.router_w ? p.router_w + (size_t)k0 * p.E + e : nullptr;
-  const bool on = warp < p.T;  // warp t: token t (zeros beyond the last)
-  const size_t row = (size_t)(on ? warp : 0) * p.H + k0;
-  // the first 256 columns of x and the norm's weights
-  uint4 x0 = make_uint4(0u, 0u, 0u, 0u), w0 = x0;
-  if (on && lane < nv) {
-    x0 = *reinterpret_cast<const uint4*>(p.x + row + lane * 8);
-    w0 = *reinterpret_cast<const uint4*>(p.norm_w + k0 + lane * 8);
-  }
-  constexpr int U = 16;
-  float wv[U];
-  if (wr) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = warp + kRouteWarps * u;
-      wv[u] = (r < rows && e < p.E) ? wr[(size_t)r * p.E] : 0.f;
-    }
-  }
-  if (warp < TT) {
-    float ss = 0.f;
+  // One warp runs the code twice: first, while the others already wait for the work in
+  // front of this launch, without touching what they share, for the instructions to be
+  // at hand afterwards (on the SMs that get these CTAs they rarely are: one token 1 us
+  // of 62, two tokens at H = 7168 1.5 of 201).
+  int live = warp != kRouteWarps - 1;
+  asm volatile("" : "+r"(live));
 #pragma unroll 1
-    for (int v0 = 0; v0 < nv; v0 += 32) {
-      const int v = v0 + lane;
-      if (v0 && on && v < nv) {
-        x0 = *reinterpret_cast<const uint4*>(p.x + row + v * 8);
-        w0 = *reinterpret_cast<const uint4*>(p.norm_w + k0 + v * 8);
-      }
-      float a[8] = {};
-      if (on && v < nv) {
-        float w[8];
-        unpack8_bf16(x0, a);
-        unpack8_bf16(w0, w);
+  for (;; live = 1) {
+    if (live) pdl_wait();
+    const int t0 = live ? warp : 0;
+    const bool on = t0 < p.T;  // warp t: token t (zeros beyond the last)
+    const int nv = (live ? rows : min(rows, 256)) >> 3;
+    const size_t row = (size_t)(on ? t0 : 0) * p.H + k0;
+    if (live && c == 0 && blockIdx.y == 0 && tid < kCtrInts) p.ctr[tid] = 0;
+    // the first 256 columns of x and the norm's weights
+    uint4 x0 = make_uint4(0u, 0u, 0u, 0u), w0 = x0;
+    if (live && on && lane < nv) {
+      x0 = *reinterpret_cast<const uint4*>(p.x + row + lane * 8);
+      w0 = *reinterpret_cast<const uint4*>(p.norm_w + k0 + lane * 8);
+    }
+    constexpr int U = 16;
+    float wv[U];
+    if (wr) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          ss = fmaf(a[q], a[q], ss);
-          a[q] *= w[q];
+      for (int u = 0; u < U; ++u) {
+        const int r = warp + kRouteWarps * u;
+        wv[u] = (live && r < rows && e < p.E) ? wr[(size_t)r * p.E] : 0.f;
+      }
+    }
+    if (t0 < TT) {
+      float ss = 0.f;
+#pragma unroll 1
+      for (int v0 = 0; v0 < nv; v0 += 32) {
+        const int v = v0 + lane;
+        if (v0 && on && v < nv) {  // (live)
+          x0 = *reinterpret_cast<const uint4*>(p.x + row + v * 8);
+          w0 = *reinterpret_cast<const uint4*>(p.norm_w + k0 + v * 8);
         }
-      }
-      if (wr && v < nv) {
+        float a[8] = {};
+        if (on && v < nv) {
+          float w[8];
+          unpack8_bf16(x0, a);
+          unpack8_bf16(w0, w);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) xw[(v * 8 + q) * TT + warp] = a[q];
+          for (int q = 0; q < 8; ++q) {
+            ss = fmaf(a[q], a[q], ss);
+            a[q] *= w[q];
+          }
+        }
+        if (live && wr && v < nv) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) xw[(v * 8 + q) * TT + warp] = a[q];
+        }
+        if (blockIdx.y == 0) {
+          const size_t at = row + v * 8, term = (size_t)p.T * p.H;
+          float up = 1.f;
+          if (FP8) {  // 16 lanes share a power of two
+            float m = 0.f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(a[q]));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int ex = pow_exponent(m);
+            up = pow_up(ex);
+            if (live && on && v < nv && (lane & 15) == 0)
+              p.xpow[warp * ((p.H + 127) >> 7) + ((k0 + v * 8) >> 7)] = pow_down(ex);
+          }
+          if (on && v < nv) {
+            __align__(16) uint16_t hi[8], lo[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) split16<FP8>(a[q] * up, hi[q], lo[q]);
+            if (live) {
+              *reinterpret_cast<uint4*>(p.xt + at) = *reinterpret_cast<uint4*>(hi);
+              *reinterpret_cast<uint4*>(p.xt + term + at) = *reinterpret_cast<uint4*>(lo);
+            }
+          }
+        }
       }
       if (blockIdx.y == 0) {
-        const size_t at = row + v * 8, term = (size_t)p.T * p.H;
-        float up = 1.f;
-        if (FP8) {  // 16 lanes share a power of two
-          float m = 0.f;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(a[q]));
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const int ex = pow_exponent(m);
-          up = pow_up(ex);
-          if (on && v < nv && (lane & 15) == 0)
-            p.xpow[warp * ((p.H + 127) >> 7) + ((k0 + v * 8) >> 7)] = pow_down(ex);
-        }
-        if (on && v < nv) {
-          __align__(16) uint16_t hi[8], lo[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) split16<FP8>(a[q] * up, hi[q], lo[q]);
-          *reinterpret_cast<uint4*>(p.xt + at) = *reinterpret_cast<uint4*>(hi);
-          *reinterpret_cast<uint4*>(p.xt + term + at) = *reinterpret_cast<uint4*>(lo);
-        }
+        ss = warp_sum(ss);
+        if (live && on && lane == 0) p.ssq[c * kLayerMaxT + warp] = ss;
       }
     }
-    if (blockIdx.y == 0) {
-      ss = warp_sum(ss);
-      if (lane == 0 && on) p.ssq[c * kLayerMaxT + warp] = ss;
+    if (!wr) {
+      if (live) return;
+      continue;
     }
-  }
-  if (!wr) return;
-  __syncthreads();
-  float acc[TT];
+    if (live) __syncthreads();
+    float acc[TT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) acc[t] = 0.f;
-  for (int r0 = warp; r0 < rows; r0 += kRouteWarps * U) {
+    for (int t = 0; t < TT; ++t) acc[t] = 0.f;
+    for (int r0 = warp; r0 < nv * 8; r0 += kRouteWarps * U) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + kRouteWarps * u;
-      if (r < rows) {
-        float a[TT];
-        if constexpr (TT % 4 == 0) {
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + kRouteWarps * u;
+        if (r < rows) {
+          float a[TT];
+          if constexpr (TT % 4 == 0) {
 #pragma unroll
-          for (int t = 0; t < TT; t += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(&xw[r * TT + t]);
-            a[t] = q.x; a[t + 1] = q.y; a[t + 2] = q.z; a[t + 3] = q.w;
+            for (int t = 0; t < TT; t += 4) {
+              const float4 q = *reinterpret_cast<const float4*>(&xw[r * TT + t]);
+              a[t] = q.x; a[t + 1] = q.y; a[t + 2] = q.z; a[t + 3] = q.w;
+            }
+          } else {
+            const float2 q = *reinterpret_cast<const float2*>(&xw[r * TT]);
+            a[0] = q.x; a[1] = q.y;
           }
-        } else {
-          const float2 q = *reinterpret_cast<const float2*>(&xw[r * TT]);
-          a[0] = q.x; a[1] = q.y;
+#pragma unroll
+          for (int t = 0; t < TT; ++t) acc[t] = fmaf(a[t], wv[u], acc[t]);
         }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) acc[t] = fmaf(a[t], wv[u], acc[t]);
+        const int rn = r + kRouteWarps * U;
+        wv[u] = (live && rn < rows && e < p.E) ? wr[(size_t)rn * p.E] : 0.f;
       }
-      const int rn = r + kRouteWarps * U;
-      wv[u] = (rn < rows && e < p.E) ? wr[(size_t)rn * p.E] : 0.f;
     }
-  }
 #pragma unroll
-  for (int t = 0; t < TT; ++t) red[warp][t][lane] = acc[t];
-  __syncthreads();
-  if (warp < p.T && e < p.E) {
-    float s = 0.f;
+    for (int t = 0; t < TT; ++t) red[warp][t][lane] = acc[t];
+    if (live) __syncthreads();
+    if (on && e < p.E) {
+      float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRouteWarps; ++w) s += red[w][warp][lane];
-    p.part[((size_t)c * p.T + warp) * p.E + e] = s;
+      for (int w = 0; w < kRouteWarps; ++w) s += red[w][t0][lane];
+      if (live) p.part[((size_t)c * p.T + warp) * p.E + e] = s;
+    }
+    if (live) return;
   }
 }
 
@@ -459,12 +476,14 @@ MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float ss, LayerSmem* s
 // the row's inputs, brought there by asynchronous copies that all run at once
 // (what the tail reads was last touched before the weights went through L2), or
 // nothing, when they do not fit.  The loops are kept short on purpose: this code
-// runs once per launch, from a cold instruction cache.
-MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow, unsigned char* buf,
-                            bool staged, float* red) {
-  const int tid = threadIdx.x, lane = tid & 31, H = p.H, nv = H >> 3;
+// runs once per launch, on T of the SMs, and its instructions come from wherever
+// the weights' way through L2 has left them.  dry: one round of the loops on
+// whatever `buf` holds, without a store to global memory (see the kernel).
+MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow, float factor,
+                            unsigned char* buf, bool staged, float* red, bool dry) {
+  const int tid = threadIdx.x, lane = tid & 31, H = p.H;
+  const int nv = dry ? min(H >> 3, kThreadsL) : H >> 3;
   const size_t row = (size_t)t * H;
-  const float factor = tail_row_factor(tail, grow);
   const bool gate_row = tail.gate && tail.gate_cols != 1 && grow >= 0;
   float* f = reinterpret_cast<float*>(buf);  // [H], then h
   const unsigned char* s_res = buf + (size_t)H * 4;
@@ -472,14 +491,14 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
   const unsigned char* s_pw = s_gate + (size_t)H * 4;
   const unsigned char* s_nw = s_pw + (size_t)H * 2;
   if (staged) cp_wait_all();
-  consumer_sync();
+  if (!dry) consumer_sync();
   auto reduce = [&](float v, bool mx) {
     v = mx ? warp_max(v) : warp_sum(v);
     if (lane == 0) red[tid >> 5] = v;
-    consumer_sync();
+    if (!dry) consumer_sync();
     v = red[0];
     for (int w = 1; w < kWarps; ++w) v = mx ? fmaxf(v, red[w]) : v + red[w];
-    consumer_sync();
+    if (!dry) consumer_sync();
     return v;
   };
   float r = 1.f;
@@ -521,7 +540,7 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
       h[q] = grow >= 0 ? fmaf(factor, a[q], res[q]) : res[q];
       ss = fmaf(h[q], h[q], ss);
     }
-    store8(tail.out, tail.out_f32 != 0, row + v * 8, h);
+    if (!dry) store8(tail.out, tail.out_f32 != 0, row + v * 8, h);
     float4* keep = reinterpret_cast<float4*>(f + v * 8);  // read back by this thread
     keep[0] = make_float4(h[0], h[1], h[2], h[3]);
     keep[1] = make_float4(h[4], h[5], h[6], h[7]);
@@ -535,7 +554,7 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
     if (pass) {
       amax = reduce(amax, true);
       s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-      if (tid == 0) tail.xscale[t] = s;
+      if (tid == 0 && !dry) tail.xscale[t] = s;
     }
 #pragma unroll 1
     for (int v0 = 0; v0 < nv; v0 += kThreadsL) {  // (whole warps: a group's maximum is a shuffle)
@@ -549,40 +568,36 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
           a[q] = (a[q] * rn) * w[q];
           m = fmaxf(m, fabsf(a[q]));
         }
-        if (!pass && tail.xhat) store8_bf16(tail.xhat + row + v * 8, a);
+        if (!pass && tail.xhat && !dry) store8_bf16(tail.xhat + row + v * 8, a);
       }
       if (tail.q_group) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         s = m > 0.f ? __fdiv_rn(m, 448.0f) : 1.0f;
-        if (tail.xq && v < nv && (v & 15) == 0) tail.xscale[(size_t)t * (H >> 7) + (v >> 4)] = s;
+        if (tail.xq && v < nv && (v & 15) == 0 && !dry) tail.xscale[(size_t)t * (H >> 7) + (v >> 4)] = s;
       }
       amax = fmaxf(amax, m);
-      if (tail.xq && v < nv && (pass || tail.q_group))
+      if (tail.xq && v < nv && (pass || tail.q_group) && !dry)
         *reinterpret_cast<uint2*>(tail.xq + row + v * 8) = tail_e4m3x8(a, s);
     }
   }
 }
 
 // FP8: E4M3 weights, one scale per (row >> rs) and K step * ks.
+// Returns the row of the tail that the CTA's consumers are to do, or -1.
 template <bool FP8, int TOK>
-__global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
-                                                                     int has_tail) {
+MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all, LayerSmem& sm,
+                          float (&red)[2][kRed]) {
   constexpr int EB = FP8 ? 1 : 2;  // bytes per weight
   using R = Ring<FP8, TOK>;
   constexpr int NJ = Cols<TOK>::kMmas, TPG = Cols<TOK>::kTpg;
   constexpr int Q = R::kPieces, KE = 64 / EB;  // K elements of 64 bytes of weights
-  extern __shared__ __align__(128) unsigned char ring_all[];
-  __shared__ LayerSmem sm;
-  __shared__ __align__(16) float red[2][kRed];
-
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tq = lane & 3;  // MMA fragment row / column, K group
   const int tok = g / TPG;                 // token of this lane's column
   const bool first_lane = lane % (4 * TPG) == 0;
   const int T = p.T, H = p.H, E = p.E, I = p.I, k = p.k;
   if (tid < kMaxExperts) sm.used[tid] = 0;
-  pdl_trigger();
   // what does not depend on the routing is worked out before the wait
   const int n0 = (int)((int64_t)blockIdx.x * H / gridDim.x);
   const int n1 = (int)((int64_t)(blockIdx.x + 1) * H / gridDim.x);
@@ -887,7 +902,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
       }
     }
     cp_wait_all();
-    return;
+    return -1;
   }
 
   // ---------------------------------------------------------------- consumers --
@@ -1088,7 +1103,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
   }
   if (!wait_for(p.ctr + 1, tiles)) {
     if (tid == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
-    return;
+    return -1;
   }
   if (tid == 0) {
     __threadfence_block();
@@ -1139,7 +1154,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
     buf ^= 1;
   }
   if (!arrived) flag_status(p.status, MOE_ERR_TIMEOUT);
-  if (!has_tail) return;
+  if (!has_tail) return -1;
 
   // ---- tail: the last T CTAs to finish take a row each.  (When they wait for
   // one another, fewer than T CTAs are unfinished, and the others have left their
@@ -1150,40 +1165,67 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
     sm.flag = atomicAdd(&p.ctr[2], 1) - ((int)gridDim.x - T);
   }
   consumer_sync();
-  const int t = sm.flag;
-  if (t < 0) return;
-  const int grow = tail_gate_row(tail, t, tid == 0 ? p.status : nullptr);
-  // the row's inputs into the ring's shared memory: f [H] fp32, residual, gate
-  // row (room for fp32 each), the norms' weights
+  return sm.flag;
+}
+
+// An SM does a tail row only every 152 / T calls, and by then the code of the tail has
+// left its instruction cache, and L2 as well (weights went through it): fetching it
+// again cost 1 us of 62 (one token) and more.  So one warp of every CTA runs it once
+// without effect while the others already wait for the first launch.
+template <bool FP8, int TOK>
+__global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
+                                                                     int has_tail) {
+  using R = Ring<FP8, TOK>;
+  extern __shared__ __align__(128) unsigned char ring_all[];
+  __shared__ LayerSmem sm;
+  __shared__ __align__(16) float red[2][kRed];
+  const int tid = threadIdx.x, H = p.H;
+  pdl_trigger();
   const bool staged = (size_t)H * 16 <= (size_t)R::kBytes;
   static_assert(kLayerMaxH * 4 <= R::kBytes, "f fits in any case");
-  auto stage = [&](size_t at, const void* src, size_t bytes) {
-    if (src)
+  bool dry = has_tail && staged && tid / 32 == kWarps - 1;
+  int t = 0, grow = 0;
+  float factor = 0.f;
 #pragma unroll 1
-      for (size_t o = tid * 16; o < bytes; o += kThreadsL * 16)
-        cp_async16(ptx::smem_u32(ring_all + at + o), static_cast<const unsigned char*>(src) + o);
-  };
-  if (staged) {
-    const size_t res_b = (size_t)H * (tail.res_f32 ? 4 : 2), gate_b = (size_t)H * (tail.gate_f32 ? 4 : 2);
-    if (tail.residual) stage((size_t)H * 4, static_cast<const unsigned char*>(tail.residual) + t * res_b, res_b);
-    if (tail.gate && tail.gate_cols != 1 && grow >= 0)
-      stage((size_t)H * 8, static_cast<const unsigned char*>(tail.gate) + grow * gate_b, gate_b);
-    stage((size_t)H * 12, tail.post_w, (size_t)H * 2);
-    stage((size_t)H * 14, tail.next_w, (size_t)H * 2);
+  for (;;) {  // (one copy of the tail's code, run twice)
+    if (!dry) {
+      t = layer_experts<FP8, TOK>(p, has_tail, ring_all, sm, red);
+      if (t < 0) return;
+      grow = tail_gate_row(tail, t, tid == 0 ? p.status : nullptr);
+      factor = tail_row_factor(tail, grow);
+      // the row's inputs into the ring's shared memory: f [H] fp32, residual, gate
+      // row (room for fp32 each), the norms' weights
+      auto stage = [&](size_t at, const void* src, size_t bytes) {
+        if (src)
+#pragma unroll 1
+          for (size_t o = tid * 16; o < bytes; o += kThreadsL * 16)
+            cp_async16(ptx::smem_u32(ring_all + at + o), static_cast<const unsigned char*>(src) + o);
+      };
+      if (staged) {
+        const size_t res_b = (size_t)H * (tail.res_f32 ? 4 : 2), gate_b = (size_t)H * (tail.gate_f32 ? 4 : 2);
+        if (tail.residual) stage((size_t)H * 4, static_cast<const unsigned char*>(tail.residual) + t * res_b, res_b);
+        if (tail.gate && tail.gate_cols != 1 && grow >= 0)
+          stage((size_t)H * 8, static_cast<const unsigned char*>(tail.gate) + grow * gate_b, gate_b);
+        stage((size_t)H * 12, tail.post_w, (size_t)H * 2);
+        stage((size_t)H * 14, tail.next_w, (size_t)H * 2);
+      }
+      if (tid == 0) {
+        const long long t0 = clock64();
+        int seen;
+        do {
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(p.ctr + 2) : "memory");
+        } while (seen < (int)gridDim.x && clock64() - t0 < ptx::kSpinLimitCycles);
+        if (seen < (int)gridDim.x) flag_status(p.status, MOE_ERR_TIMEOUT);
+        __threadfence();
+      }
+      consumer_sync();
+      stage(0, p.f + (size_t)t * H, (size_t)H * 4);
+      cp_wait_all();
+    }
+    layer_tail_row(p, tail, t, grow, factor, ring_all, staged, sm.sum, dry);
+    if (!dry) return;
+    dry = false;
   }
-  if (tid == 0) {
-    const long long t0 = clock64();
-    int seen;
-    do {
-      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(p.ctr + 2) : "memory");
-    } while (seen < (int)gridDim.x && clock64() - t0 < ptx::kSpinLimitCycles);
-    if (seen < (int)gridDim.x) flag_status(p.status, MOE_ERR_TIMEOUT);
-    __threadfence();
-  }
-  consumer_sync();
-  stage(0, p.f + (size_t)t * H, (size_t)H * 4);
-  cp_wait_all();
-  layer_tail_row(p, tail, t, grow, ring_all, staged, sm.sum);
 }
 
 struct LayerWs {
