@@ -49,18 +49,18 @@
 // 375 us against 256).  The first W2 pieces are on their way while the CTA waits
 // for the other CTAs' FC1 tiles.
 //
-// mma.sync and not tcgen05: with 8 columns the tensor pipe is 13 to 20% busy and
+// mma.sync and not tcgen05: with 8 columns the tensor pipe is 8 to 20% busy and
 // HBM is what binds; a fragment read straight from the copied bytes needs no
 // descriptor layout, row tiles of 16 let every CTA have an equal share of the
 // output rows (27 of 4096), and accumulators in registers spare the TMEM round
 // trip between tiles that short.
 //
-// Measured (H = 4096, I = 1536, E = 64, top_k = 8, cold weights): one token 63.6 us
+// Measured (H = 4096, I = 1536, E = 64, top_k = 8, cold weights): one token 61.7 us
 // (302 MB), eight tokens 250 us (1.775 GB read, 7.1 TB/s), E4M3 one token 34 us,
-// block-wise FP8 four tokens 96 us (4.9 TB/s).  The separate launches of
+// block-wise FP8 four tokens 94 us (5.0 TB/s).  The separate launches of
 // moe_ffn_forward, without a tail: 96, 251, 54 and 122 us.  What is left at one token
-// is latency around the stream: the routing launch 4 to 5 us, the hand-over 1, the
-// routing in each CTA 4, the wait between FC1 and FC2 2, the tail 4.
+// is latency around the stream: the routing launch 3 to 4 us, the hand-over 1, the
+// routing in each CTA 3, the wait between FC1 and FC2 2 to 3, the tail 3 to 4.
 #include "block_tail.cuh"
 #include "kernels.h"
 #include "tail.h"

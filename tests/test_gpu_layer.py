@@ -561,3 +561,32 @@ def test_host_threads_at_once(M):
     for t in ts:
         t.join()
     assert not errors, errors
+
+
+@pytest.mark.parametrize("E", [5, 31, 32, 33, 64, 65, 100, 128, 129, 200, 256])
+def test_choice_among_equal_and_special_logits(M, E):
+    """Larger logits first, equal ones (-0 and 0 among them) by the lower expert, NaN as -inf."""
+    g = torch.Generator().manual_seed(E)
+    k, T = min(8, E), 8
+    d = make(T, 128, E, k, 64, routing="logits", seed=7)
+    z = torch.randint(-2, 3, (T, E), generator=g).float() * 0.5
+    z[z == 0] = torch.where(torch.rand((T, E), generator=g) < 0.5, 0.0, -0.0)[z == 0]
+    z[1, torch.rand((E,), generator=g) < 0.7] = float("nan")
+    z[2, torch.rand((E,), generator=g) < 0.7] = float("-inf")
+    z[3] = 1.0
+    z[4] = float("-inf")
+    z[5] = float("nan")
+    z[6] = torch.linspace(3e38, -3e38, E)  # (its step is beyond fp32: infinities, too)
+    z[7] = torch.randn((E,), generator=g) * 1e-40
+    d["logits"] = z.to(DEV)
+    _, ids, tw = call(M, d)
+    key = z.double().masked_fill(z.isnan(), float("-inf")) + 0.0
+    want = key.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert ids.tolist() == want.tolist()
+    top = key.gather(1, want)
+    w = torch.softmax(top, 1)
+    w[top[:, 0] == float("-inf")] = 0.0  # nothing but -inf (a weight beside +inf is NaN, as in any softmax)
+    # exp, the sum and the divide: within 16 u of the weight (differences of fp32 logits are exact to u)
+    tol = (16 + 2 * (top - top[:, :1]).abs().nan_to_num(0, 0, 0).clamp_max(100)) * U * w + 2.0 ** -126
+    tw = tw.cpu().double()
+    assert (((tw - w).abs() <= tol) | (tw.isnan() & w.isnan())).all()
