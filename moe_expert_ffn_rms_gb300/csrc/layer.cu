@@ -1171,7 +1171,9 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
 // An SM does a tail row only every 152 / T calls, and by then the code of the tail has
 // left its instruction cache, and L2 as well (weights went through it): fetching it
 // again cost 1 us of 62 (one token) and more.  So one warp of every CTA runs it once
-// without effect while the others already wait for the first launch.
+// without effect while the others already wait for the first launch.  (Not with E4M3
+// weights and eight token columns: that kernel has no register to spare, and with the
+// loop around it its steps spill: eight tokens 168 us against 153.)
 template <bool FP8, int TOK>
 __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
                                                                      int has_tail) {
@@ -1183,7 +1185,7 @@ __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const L
   pdl_trigger();
   const bool staged = (size_t)H * 16 <= (size_t)R::kBytes;
   static_assert(kLayerMaxH * 4 <= R::kBytes, "f fits in any case");
-  bool dry = has_tail && staged && tid / 32 == kWarps - 1;
+  bool dry = !(FP8 && TOK == 8) && has_tail && staged && tid / 32 == kWarps - 1;
   int t = 0, grow = 0;
   float factor = 0.f;
 #pragma unroll 1
