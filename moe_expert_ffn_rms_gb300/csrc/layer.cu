@@ -395,13 +395,18 @@ struct LayerSmem {
   uint64_t full[kWarps][kMaxDepth], empty[kWarps][kMaxDepth];
 };
 
-// Top-k of one token by one warp with the results of warp_topk (common.cuh):
-// larger logit first, ties to the lower expert, NaN as -inf, softmax over the
-// selected (summed in slot order), weights 0 when all of them are -inf.  Here
-// the arg-max is two warp reductions of integers: the logits' bits in an
-// order-preserving form, then the lowest expert that has the maximum.
+// A logit as a key of the top-k: its bits in an order-preserving form, NaN as -inf
+// (0x007fffff), -0 as 0.  Keys of logits are above 0.
+MOE_DEV unsigned order_key(float z) {
+  z = (z != z) ? -INFINITY : z + 0.0f;
+  const unsigned u = __float_as_uint(z);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// The keys of the experts lane + 32 i of token t, 0 beyond E.  ss: this lane's part of
+// the token's sum of squares.
 template <int PER>
-MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float ss, LayerSmem* sm) {
+MOE_DEV void layer_keys(const LayerP& p, int t, int lane, float ss, unsigned (&key)[PER], float& r) {
   float zs[PER], bias[PER];  // every load is issued before the first use
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -420,20 +425,58 @@ MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float ss, LayerSmem* s
       }
     }
   }
-  const float r = 1.0f / sqrtf(warp_sum(ss) / (float)p.H + p.eps);
-  if (lane == 0) sm->r[t] = r;
-  unsigned key[PER];  // 0: taken or beyond E
+  r = 1.0f / sqrtf(warp_sum(ss) / (float)p.H + p.eps);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = lane + 32 * i;
     key[i] = 0;
-    if (e < p.E) {
+    if (lane + 32 * i < p.E) {
       float z = p.logits ? zs[i] : zs[i] * r;
       if (p.bias) z += bias[i];
-      z = (z != z) ? -INFINITY : z + 0.0f;  // (-0 counts as 0)
-      const unsigned u = __float_as_uint(z);
-      key[i] = (u & 0x80000000u) ? ~u : u | 0x80000000u;  // -inf: 0x007fffff
+      key[i] = order_key(z);
     }
+  }
+}
+
+// layer_keys of 32 experts (part `at`) for all warps; part: of chunk 0, `step` apart.
+// (Not inlined: the steps' registers are all taken, and code beside them moves them.)
+__device__ __noinline__ void layer_part(const float* logits, const float* part, const float* bias,
+                                        const float* ssq, int step, int E, int H, float eps, int at,
+                                        unsigned* keys, float* r_out) {
+  const int lane = threadIdx.x & 31, e = at * 32 + lane;
+  const float ss = lane < kLayerChunks ? __ldcg(&ssq[lane * kLayerMaxT]) : 0.f;
+  float z = 0.f, b = 0.f;
+  if (e < E) {
+    if (bias) b = bias[e];
+    if (logits) {
+      z = logits[e];
+    } else {
+      float v[kLayerChunks];
+#pragma unroll
+      for (int c = 0; c < kLayerChunks; ++c) v[c] = __ldcg(&part[(size_t)c * step + e]);
+#pragma unroll
+      for (int c = 0; c < kLayerChunks; ++c) z += v[c];
+    }
+  }
+  const float r = 1.0f / sqrtf(warp_sum(ss) / (float)H + eps);
+  if (e < E) keys[e] = order_key((logits ? z : z * r) + b);
+  if (e == 0) *r_out = r;
+}
+
+// Top-k of one token by one warp with the results of warp_topk (common.cuh):
+// larger logit first, ties to the lower expert, NaN as -inf, softmax over the
+// selected (summed in slot order), weights 0 when all of them are -inf.  Here
+// the arg-max is two warp reductions of integers: the keys, then the lowest expert
+// that has the maximum.  keys: where other warps have left them (and r), or NULL.
+template <int PER>
+MOE_DEV void layer_topk(const LayerP& p, int t, int lane, float ss, const unsigned* keys, LayerSmem* sm) {
+  unsigned key[PER];  // 0: taken or beyond E
+  if (PER > 2 && keys) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = lane + 32 * i < p.E ? keys[lane + 32 * i] : 0u;
+  } else {
+    float r;
+    layer_keys<PER>(p, t, lane, ss, key, r);
+    if (lane == 0) sm->r[t] = r;
   }
   float mine = 0.f, top = 0.f, s = 0.f;
   int sel_e = 0;
@@ -625,6 +668,23 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
   // ---- routing (every CTA by itself; warp t: token t)
   int first_claim = 0;
   if (tid == 2 * kThreadsL - 1) first_claim = atomicAdd(&p.ctr[0], 2);
+  // More than 64 experts of few tokens: the logits by all warps, 32 experts at a time,
+  // if each warp has one such part at most (one token, 256 experts: 58.2 us against
+  // 60.6 by the token's warp alone; eight tokens, four parts a warp, 200.2 against
+  // 199.4, and with 64 experts 0.2 us more).
+  const unsigned* keys = nullptr;
+  const int parts = (E + 31) >> 5;
+  if (!p.ids_in && E > 64 && T * parts <= 2 * kWarps) {
+    unsigned* all = reinterpret_cast<unsigned*>(red);  // [T][E]
+    static_assert(sizeof(red) >= sizeof(unsigned) * kLayerMaxT * kMaxExperts, "keys");
+    if (warp < T * parts) {
+      const int t = warp / parts;
+      layer_part(p.logits ? p.logits + (size_t)t * E : nullptr, p.part + (size_t)t * E, p.bias, p.ssq + t, T * E, E, H,
+                 p.eps, warp - t * parts, all + t * E, &sm.r[t]);
+    }
+    __syncthreads();
+    keys = all + warp * E;
+  }
   if (warp < T) {
     const float ss = lane < kLayerChunks ? __ldcg(&p.ssq[lane * kLayerMaxT + warp]) : 0.f;
     if (p.ids_in) {
@@ -635,13 +695,13 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
       const float r = 1.0f / sqrtf(warp_sum(ss) / (float)H + p.eps);
       if (lane == 0) sm.r[warp] = r;
     } else if (E <= 32) {
-      layer_topk<1>(p, warp, lane, ss, &sm);
+      layer_topk<1>(p, warp, lane, ss, keys, &sm);
     } else if (E <= 64) {
-      layer_topk<2>(p, warp, lane, ss, &sm);
+      layer_topk<2>(p, warp, lane, ss, keys, &sm);
     } else if (E <= 128) {
-      layer_topk<4>(p, warp, lane, ss, &sm);
+      layer_topk<4>(p, warp, lane, ss, keys, &sm);
     } else {
-      layer_topk<8>(p, warp, lane, ss, &sm);
+      layer_topk<8>(p, warp, lane, ss, keys, &sm);
     }
     // the token's experts: lane j, its j-th
     __syncwarp();

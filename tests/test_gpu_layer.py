@@ -590,3 +590,24 @@ def test_choice_among_equal_and_special_logits(M, E):
     tol = (16 + 2 * (top - top[:, :1]).abs().nan_to_num(0, 0, 0).clamp_max(100)) * U * w + 2.0 ** -126
     tw = tw.cpu().double()
     assert (((tw - w).abs() <= tol) | (tw.isnan() & w.isnan())).all()
+
+
+@pytest.mark.parametrize("routing", ["router", "bias", "logits"])
+@pytest.mark.parametrize("T,E", [(1, 65), (5, 96), (4, 128), (3, 129), (2, 200), (2, 256), (1, 256)])
+def test_many_experts_of_few_tokens(M, T, E, routing):
+    """The logits are added by all warps there, and by the token's own warp in a call with more tokens:
+    both against the definition, and the same choice and weights."""
+    d = make(8, 320, E, 8, 64, routing=routing, seed=E + T)
+    whole = call(M, d)
+    check(d, whole)
+    few = dict(d, T=T, x=d["x"][:T].contiguous(), logits=None if d["logits"] is None else d["logits"][:T].contiguous())
+    got = call(M, few)
+    check(few, got)
+    assert torch.equal(got[1], whole[1][:T]) and torch.equal(got[2], whole[2][:T])
+    if routing == "logits":  # special ones, through this path as well
+        few["logits"][0, ::2] = float("nan")
+        few["logits"][0, 1] = float("-inf")
+        few["logits"][T - 1, 3:] = 0.25
+        whole = call(M, dict(d, logits=torch.cat([few["logits"], d["logits"][T:]])))
+        got = call(M, few)
+        assert torch.equal(got[1], whole[1][:T]) and torch.equal(got[2], whole[2][:T])
