@@ -6,8 +6,10 @@
 // fp32 and only the stored outputs are rounded.  Device time per call, inputs
 // not in L2 (k rows of H per token; "from" are the types of rows and residual):
 //   T    H    k                                    us    of the copy bandwidth
+//   4096 7168 8  bf16, bf16 -> bf16, x_hat         95    100%
 //   4096 4096 8  bf16, bf16 -> bf16, x_hat         57    95%
-//   2047 5120 1  bf16, fp32 -> fp32, E4M3          24.3  70%
+//   4096 8192 1  bf16, bf16 -> bf16, x_hat         65    61%
+//   2047 5120 1  bf16, fp32 -> fp32, E4M3          23.4  73%
 //   333  2944 4  fp32, bf16 -> bf16, E4M3 groups    8.0  38%
 //   64   7168 8  bf16, fp32 -> fp32, x_hat          5.5  33%
 //   1    4096 8  bf16, bf16 -> bf16, x_hat          3.3  (latency)
@@ -28,18 +30,18 @@ namespace {
 // (L1 / L2 resident); the callers supply the sum and the residual.
 
 // Sum (or maximum) over the first nt threads of the CTA (nt a multiple of 32,
-// at most 512) with one barrier among them.  `red` (16 floats) must not be
+// at most 32 NW) with one barrier among them.  `red` (NW floats) must not be
 // written again before another such barrier has passed.
-template <bool MAX>
-MOE_DEV float rows_reduce(float v, int nt, float* red) {
+template <bool MAX, int NW>
+MOE_DEV float rows_reduce(float v, int nt, float (&red)[NW]) {
   v = MAX ? warp_max(v) : warp_sum(v);
   if (nt == 32) return v;
   const int lane = threadIdx.x & 31, nw = nt >> 5;
   if (lane == 0) red[threadIdx.x >> 5] = v;
   asm volatile("bar.sync 1, %0;" ::"r"(nt) : "memory");
-  v = (lane & 15) < nw ? red[lane & 15] : 0.f;
+  v = (lane & (NW - 1)) < nw ? red[lane & (NW - 1)] : 0.f;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = NW / 2; o > 0; o >>= 1) {
     const float u = __shfl_xor_sync(0xffffffffu, v, o);
     v = MAX ? fmaxf(v, u) : v + u;
   }
@@ -47,22 +49,22 @@ MOE_DEV float rows_reduce(float v, int nt, float* red) {
 }
 
 // 1 / norm of the row held in f.
-template <int VPT>
-MOE_DEV float row_rnorm(const float (&f)[VPT][8], int nt, int H, float eps, float* red) {
+template <int VPT, int NW>
+MOE_DEV float row_rnorm(const float (&f)[VPT][8], int nt, int H, float eps, float (&red)[NW]) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int q = 0; q < 8; ++q) ss = fmaf(f[i][q], f[i][q], ss);
-  return 1.0f / sqrtf(rows_reduce<false>(ss, nt, red) / (float)H + eps);
+  return 1.0f / sqrtf(rows_reduce<false, NW>(ss, nt, red) / (float)H + eps);
 }
 
 // x_hat (and its quantisation) of the row h held in f; chunks beyond the row hold
-// zeros.  KEPT: next_w holds this thread's (one) chunk of the weights.  red: two
-// arrays of rows_reduce.
-template <int VPT, bool KEPT = false>
-MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], int nt, const uint4& next_w,
-                        float (*red)[16]) {
+// zeros.  The norm's weights: KEPT this thread's (one) chunk in `kept`, else the row
+// next_w.  red: two arrays of rows_reduce.
+template <int VPT, bool KEPT, int NW>
+MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], int nt, const uint4& kept,
+                        const bf16* next_w, float (*red)[NW]) {
   const int tid = threadIdx.x, nv = H >> 3;
   const float r = row_rnorm(f, nt, H, p.next_eps, red[0]);
   float amax = 0.f;
@@ -72,8 +74,8 @@ MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], int nt
     float m = 0.f;
     if (v < nv) {
       float w[8];
-      if (KEPT) unpack8_bf16(next_w, w);
-      else load8(p.next_w, false, v * 8, w);
+      if (KEPT) unpack8_bf16(kept, w);
+      else load8(next_w, false, v * 8, w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         f[i][q] = (f[i][q] * r) * w[q];
@@ -93,7 +95,7 @@ MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], int nt
     }
   }
   if (p.xq && !p.q_group) {
-    amax = rows_reduce<true>(amax, nt, red[1]);
+    amax = rows_reduce<true, NW>(amax, nt, red[1]);
     const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
     if (tid == 0) p.xscale[t] = s;
 #pragma unroll
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_row_kernel(
     for (int q = 0; q < 8; ++q) f[i][q] = h[q];
   }
   if (!p.next_w) return;
-  write_next(p, t, H, f, nt, make_uint4(0u, 0u, 0u, 0u), red + 1);
+  write_next<VPT, false>(p, t, H, f, nt, make_uint4(0u, 0u, 0u, 0u), p.next_w, red + 1);
 }
 
 // ----------------------------------------------------------- streaming form --
@@ -226,22 +228,25 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_row_kernel(
 // residual and its gate row.  The producer reads the token's indices and
 // leaves them beside the rows.  Without the stages the loads of a token wait for
 // the reductions of the one before it: 66.7 us instead of 57 at T = 4096, H = 4096,
-// k = 8, and 36.7 instead of 24.3 at T = 2047, H = 5120, k = 1.
+// k = 8, and 36.7 instead of 23.4 at T = 2047, H = 5120, k = 1.
 struct StreamMeta {
   unsigned use;   // slots whose row is present
   float factor;   // tail_row_factor
   int gate_ok;    // 0: gate index out of range
 };
 
-template <int VPT, bool YF32, bool SPLIT>
-__global__ void __launch_bounds__(kRowThreads + 32, VPT <= 2 ? 2 : 1)
+constexpr int kWideThreads = 992;  // WIDE: consumers up to this many, else kRowThreads
+
+template <int VPT, bool YF32, bool SPLIT, bool WIDE>
+__global__ void __launch_bounds__((WIDE ? kWideThreads : kRowThreads) + 32, VPT <= 2 && !WIDE ? 2 : 1)
     combine_norm_stream_kernel(const void* __restrict__ y, int pair_order,
                                const int32_t* __restrict__ row_of_pair, int T, int k, int H,
-                               const TailP p, int* status, int S, int stage_bytes, int R_) {
+                               const TailP p, int* status, int S, int stage_bytes, int R_,
+                               int weights_at) {
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ uint64_t full[kStreamStages], empty[kStreamStages];
   __shared__ StreamMeta meta[kStreamStages];
-  __shared__ float red[2][3][16];
+  __shared__ float red[2][3][WIDE ? 32 : 16];
   __shared__ int s_abort;
   const int R = SPLIT ? R_ : k;
   const int tid = threadIdx.x, nt = blockDim.x - 32, nv = H >> 3;
@@ -344,6 +349,17 @@ __global__ void __launch_bounds__(kRowThreads + 32, VPT <= 2 ? 2 : 1)
     if (p.post_w) pw = reinterpret_cast<const uint4*>(p.post_w)[tid];
     if (p.next_w) nw = reinterpret_cast<const uint4*>(p.next_w)[tid];
   }
+  // else in shared memory when the CTA has several tokens (the stages leave little
+  // of L1): each thread's own chunks
+  const bf16 *post_w = p.post_w, *next_w = p.next_w;
+  if (!KEEP && weights_at) {
+    uint4* d = reinterpret_cast<uint4*>(stages + weights_at);
+    for (int v = tid; p.post_w && v < nv; v += nt) d[v] = reinterpret_cast<const uint4*>(p.post_w)[v];
+    if (p.post_w) post_w = reinterpret_cast<const bf16*>(d);
+    if (p.post_w) d += nv;
+    for (int v = tid; p.next_w && v < nv; v += nt) d[v] = reinterpret_cast<const uint4*>(p.next_w)[v];
+    if (p.next_w) next_w = reinterpret_cast<const bf16*>(d);
+  }
   int s = 0, n = 0;
   uint32_t ph = 0;
   bool ok = true;
@@ -411,7 +427,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, VPT <= 2 ? 2 : 1)
       float a[8];
       if (p.post_w) {
         if (KEEP) unpack8_bf16(pw, a);
-        else load8(p.post_w, false, v * 8, a);
+        else load8(post_w, false, v * 8, a);
 #pragma unroll
         for (int q = 0; q < 8; ++q) f[i][q] = (f[i][q] * r) * a[q];
       }
@@ -439,7 +455,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, VPT <= 2 ? 2 : 1)
     __syncwarp();
     if ((tid & 31) == 0) ptx::mbar_arrive(&empty[s]);
     if (p.next_w)
-      write_next<VPT, KEEP>(p, t, H, f, nt, nw, red[n & 1] + 1);
+      write_next<VPT, KEEP>(p, t, H, f, nt, nw, next_w, red[n & 1] + 1);
     if (++s == S) {
       s = 0;
       ph ^= 1;
@@ -456,10 +472,10 @@ cudaError_t launch_row(const void* y, bool pair_order, const int32_t* row_of_pai
 }
 
 // cudaErrorNotSupported when even one expert row per stage does not fit twice.
-template <int VPT, bool YF32>
+template <int VPT, bool YF32, bool WIDE>
 cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_pair, int T, int k, int H,
                           const TailP& p, int* status, int sms, int threads, cudaStream_t st) {
-  auto kern = combine_norm_stream_kernel<VPT, YF32, false>;
+  auto kern = combine_norm_stream_kernel<VPT, YF32, false, WIDE>;
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
@@ -473,7 +489,8 @@ cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_
   if (by_regs > 2048 / (threads + 32)) by_regs = 2048 / (threads + 32);
   if (by_regs > kStreamCtas) by_regs = kStreamCtas;
   if (by_regs < 1) return cudaErrorNotSupported;
-  auto by_smem = [&](int64_t b) { return (int)(kStreamSmem / (b + kStreamStatic)); };
+  int64_t weights = 0;  // of the norms, in shared memory
+  auto by_smem = [&](int64_t b) { return (int)(kStreamSmem / (b + kStreamStatic + weights)); };
   int R = k, S, per_sm = by_smem(bytes(k)) < by_regs ? by_smem(bytes(k)) : by_regs;
   if (per_sm > 0 && T <= sms * per_sm) {
     // every token gets a CTA of its own at once: one stage each (T = 333, H = 2944,
@@ -483,21 +500,39 @@ cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_
     // two or more stages, each as much of a token as fits (a whole token wherever two
     // fit: copies stay long, and a token waits once); then as many CTAs as fit, then
     // the memory that is left goes to more stages
-    while (R > 1 && by_smem(2 * bytes(R)) < 1) R = (R + 1) / 2;
-    per_sm = by_smem(2 * bytes(R));
+    auto plan = [&](int& rows, int& ctas) {
+      rows = k;
+      while (rows > 1 && by_smem(2 * bytes(rows)) < 1) rows = (rows + 1) / 2;
+      ctas = by_smem(2 * bytes(rows)) < by_regs ? by_smem(2 * bytes(rows)) : by_regs;
+    };
+    plan(R, per_sm);
     if (per_sm < 1) return cudaErrorNotSupported;
-    if (per_sm > by_regs) per_sm = by_regs;
-    S = (int)((kStreamSmem / per_sm - kStreamStatic) / bytes(R));
+    if (VPT > 1) {
+      // the norms' weights beside the stages (H = 12288, k = 1: 40.1 us, 54.5 without;
+      // H = 8192, k = 6: 109, 121 without), unless that leaves stages of one row (H = 15872,
+      // k = 8: 185, 132 without) or, with more than one row per token, fewer CTAs
+      // (H = 5120: k = 2 47.2, 44.0 without; but k = 1 34.7, 37.9 without)
+      int rows, ctas;
+      weights = (int64_t)H * ((p.post_w ? 2 : 0) + (p.next_w ? 2 : 0));
+      plan(rows, ctas);
+      if (ctas < 1 || (rows == 1 && R > 1) || (k > 1 && ctas < per_sm)) {
+        weights = 0;
+      } else {
+        R = rows;
+        per_sm = ctas;
+      }
+    }
+    S = (int)((kStreamSmem / per_sm - kStreamStatic - weights) / bytes(R));
     if (S > kStreamStages) S = kStreamStages;
-    if (R < k) kern = combine_norm_stream_kernel<VPT, YF32, true>;
+    if (R < k) kern = combine_norm_stream_kernel<VPT, YF32, true, WIDE>;
   }
-  const size_t smem = (size_t)S * bytes(R);
+  const size_t smem = (size_t)S * bytes(R) + weights;
   // the same limit in every call: another thread's launch may lie between this and ours
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem - kStreamStatic);
   if (e != cudaSuccess) return e;
   const int grid = T < sms * per_sm ? T : sms * per_sm;
   return launch_kernel(kern, dim3(grid), dim3(threads + 32), smem, st, y, (int)pair_order, row_of_pair, T,
-                       k, H, p, status, S, (int)bytes(R), R);
+                       k, H, p, status, S, (int)bytes(R), R, weights ? (int)(S * bytes(R)) : 0);
 }
 
 }  // namespace
@@ -514,15 +549,26 @@ cudaError_t launch_combine_norm(const void* y, bool y_f32, bool pair_order,
   // form for measurements.
   const char* env = getenv("MOE_CN_STREAM");
   if (nv <= 2048 && (env ? env[0] == '1' : T > sms)) {
-    const int vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);
+    // Long rows of several experts are bound by the consumers' instructions and shared
+    // loads, which more warps overlap better: T = 4096, H = 7168, k = 8 95 us with 896
+    // threads, 135 with 448 of two chunks each; k = 4 62.8 against 101.  With few bytes of
+    // rows per column, two or three smaller CTAs on an SM overlap their reductions
+    // better (bf16, H = 5120, k = 2 43.8 us against 50.5; H = 7168, k = 1 51.9 against 54.2; fp32
+    // k = 2 is on the other side, 55.3 against 37.6).  Rows of four chunks per thread always
+    // gain (H = 12288, k = 1 69.6 against 54.6).
+    const bool wide = nv > kRowThreads && nv <= 2 * kWideThreads &&
+                      (nv <= kWideThreads ? k * (y_f32 ? 4 : 2) >= 6 : nv > 2 * kRowThreads);
+    const int vpt = wide ? (nv <= kWideThreads ? 1 : 2) : (nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4));
     const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
     cudaError_t e;
-#define MOE_CN(V)                                                                                     \
-  e = y_f32 ? launch_stream<V, true>(y, pair_order, row_of_pair, T, k, H, p, status, sms, threads, st) \
-            : launch_stream<V, false>(y, pair_order, row_of_pair, T, k, H, p, status, sms, threads, st)
-    if (vpt == 1) MOE_CN(1);
-    else if (vpt == 2) MOE_CN(2);
-    else MOE_CN(4);
+#define MOE_CN(V, W)                                                                                     \
+  e = y_f32 ? launch_stream<V, true, W>(y, pair_order, row_of_pair, T, k, H, p, status, sms, threads, st) \
+            : launch_stream<V, false, W>(y, pair_order, row_of_pair, T, k, H, p, status, sms, threads, st)
+    if (wide && vpt == 1) MOE_CN(1, true);
+    else if (wide) MOE_CN(2, true);
+    else if (vpt == 1) MOE_CN(1, false);
+    else if (vpt == 2) MOE_CN(2, false);
+    else MOE_CN(4, false);
 #undef MOE_CN
     if (e != cudaErrorNotSupported) return e;
   }

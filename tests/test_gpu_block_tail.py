@@ -405,3 +405,23 @@ def test_offsets_beyond_32_bits(M, H, T, k):
     rows = torch.tensor([0, 1, at - 1, at, at + 1, T // 2, T - 2, T - 1], device=DEV)
     part = dict(d, T=len(rows), y=y.view(T, k, H)[rows].reshape(-1, H))
     check(part, {n: v[rows] for n, v in o.items()})
+
+
+@pytest.mark.parametrize("T,H,k,y,res", [
+    (400, 12288, 1, torch.bfloat16, torch.bfloat16), (330, 12288, 3, torch.bfloat16, torch.float32),
+    (400, 9000, 8, torch.bfloat16, torch.bfloat16), (310, 15872, 8, torch.bfloat16, torch.bfloat16),
+    (700, 5000, 2, torch.bfloat16, torch.bfloat16), (700, 5000, 8, torch.bfloat16, torch.bfloat16),
+    (320, 7936, 8, torch.float32, torch.float32), (500, 7944, 4, torch.bfloat16, None),
+    (900, 5120, 2, torch.float32, torch.bfloat16), (640, 8192, 1, torch.bfloat16, torch.float32),
+    (330, 16384, 2, torch.bfloat16, torch.bfloat16), (320, 8200, 1, torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("gate,post,nxt", [("none", True, "both"), ("rows", True, "bf16"),
+                                           ("channel", False, "both"), ("token", True, "none")])
+def test_long_rows_of_many_tokens(M, T, H, k, y, res, gate, post, nxt):
+    """Several tokens per CTA in every width of the streaming form, with whole and split tokens."""
+    d = make(T, H, k, y=y, order="pair_idx", res=res, post=post, gate=gate, nxt=nxt, drop=0.2, seed=T + H + k)
+    o = call(M, d)
+    check(d, o)
+    again = call(M, d)
+    for n in o:
+        assert torch.equal(o[n], again[n]), n
+    assert M.device_status() == 0
