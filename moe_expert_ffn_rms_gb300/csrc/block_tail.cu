@@ -8,7 +8,8 @@
 //   T    H    k                                    us    of the copy bandwidth
 //   4096 7168 8  bf16, bf16 -> bf16, x_hat         95    100%
 //   4096 4096 8  bf16, bf16 -> bf16, x_hat         57    95%
-//   4096 8192 1  bf16, bf16 -> bf16, x_hat         65    61%
+//   2048 8192 1  bf16, bf16 -> bf16, x_hat         28    71%
+//   2048 4096 1  bf16, bf16 -> bf16, x_hat         19    52%
 //   2047 5120 1  bf16, fp32 -> fp32, E4M3          23.4  73%
 //   333  2944 4  fp32, bf16 -> bf16, E4M3 groups    8.0  38%
 //   64   7168 8  bf16, fp32 -> fp32, x_hat          5.5  33%
@@ -20,6 +21,8 @@
 #include "tc_ptx.cuh"
 
 #include <stdlib.h>
+
+#include <atomic>
 
 namespace moe {
 namespace {
@@ -236,9 +239,11 @@ struct StreamMeta {
 };
 
 constexpr int kWideThreads = 992;  // WIDE: consumers up to this many, else kRowThreads
+constexpr int kThreeThreads = 352;  // consumers with VPT = 3 (two CTAs' registers on an SM)
 
 template <int VPT, bool YF32, bool SPLIT, bool WIDE>
-__global__ void __launch_bounds__((WIDE ? kWideThreads : kRowThreads) + 32, VPT <= 2 && !WIDE ? 2 : 1)
+__global__ void __launch_bounds__((WIDE ? kWideThreads : (VPT == 3 ? kThreeThreads : kRowThreads)) + 32,
+                                  VPT <= 3 && !WIDE ? 2 : 1)
     combine_norm_stream_kernel(const void* __restrict__ y, int pair_order,
                                const int32_t* __restrict__ row_of_pair, int T, int k, int H,
                                const TailP p, int* status, int S, int stage_bytes, int R_,
@@ -471,21 +476,27 @@ cudaError_t launch_row(const void* y, bool pair_order, const int32_t* row_of_pai
                        (int)pair_order, row_of_pair, T, k, H, p, status);
 }
 
-// cudaErrorNotSupported when even one expert row per stage does not fit twice.
+// cudaErrorNotSupported when even one expert row per stage does not fit twice;
+// with `two` also unless two CTAs of two whole tokens each fit an SM (or every token
+// gets a CTA at once).
 template <int VPT, bool YF32, bool WIDE>
 cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_pair, int T, int k, int H,
-                          const TailP& p, int* status, int sms, int threads, cudaStream_t st) {
+                          const TailP& p, int* status, int sms, int threads, bool two, cudaStream_t st) {
   auto kern = combine_norm_stream_kernel<VPT, YF32, false, WIDE>;
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
+  static std::atomic<int> regs{0};  // of the kernel's threads
+  cudaError_t e = cudaSuccess;
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
   const int64_t yb = (int64_t)H * (YF32 ? 4 : 2);
   const int64_t extra = (p.residual ? (int64_t)H * (p.res_f32 ? 4 : 2) : 0) +
                         (p.gate && p.gate_cols != 1 ? (int64_t)H * (p.gate_f32 ? 4 : 2) : 0);
   auto bytes = [&](int rows) { return (rows * yb + extra + 127) / 128 * 128; };
   // CTAs an SM holds by registers (given out to four warps at a time) and threads
   const int warps = (threads / 32 + 1 + 3) / 4 * 4;
-  int by_regs = 65536 / ((fa.numRegs + 7) / 8 * 8 * 32 * warps);
+  int by_regs = 65536 / ((regs.load(std::memory_order_relaxed) + 7) / 8 * 8 * 32 * warps);
   if (by_regs > 2048 / (threads + 32)) by_regs = 2048 / (threads + 32);
   if (by_regs > kStreamCtas) by_regs = kStreamCtas;
   if (by_regs < 1) return cudaErrorNotSupported;
@@ -506,16 +517,17 @@ cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_
       ctas = by_smem(2 * bytes(rows)) < by_regs ? by_smem(2 * bytes(rows)) : by_regs;
     };
     plan(R, per_sm);
-    if (per_sm < 1) return cudaErrorNotSupported;
+    if (per_sm < 1 || (two && (R < k || per_sm < 2))) return cudaErrorNotSupported;
     if (VPT > 1) {
       // the norms' weights beside the stages (H = 12288, k = 1: 40.1 us, 54.5 without;
       // H = 8192, k = 6: 109, 121 without), unless that leaves stages of one row (H = 15872,
-      // k = 8: 185, 132 without) or, with more than one row per token, fewer CTAs
-      // (H = 5120: k = 2 47.2, 44.0 without; but k = 1 34.7, 37.9 without)
+      // k = 8: 185, 132 without) or fewer CTAs: one instead of two (H = 7168, k = 1, fp32
+      // residual, T = 2048: 43.5, 37.4 without), or with more than one row per token two
+      // instead of three (H = 5120: k = 2 47.2, 44.0 without; but k = 1 34.7, 37.9 without)
       int rows, ctas;
       weights = (int64_t)H * ((p.post_w ? 2 : 0) + (p.next_w ? 2 : 0));
       plan(rows, ctas);
-      if (ctas < 1 || (rows == 1 && R > 1) || (k > 1 && ctas < per_sm)) {
+      if (ctas < 1 || (rows == 1 && R > 1) || (ctas < per_sm && (k > 1 || ctas < 2))) {
         weights = 0;
       } else {
         R = rows;
@@ -549,26 +561,39 @@ cudaError_t launch_combine_norm(const void* y, bool y_f32, bool pair_order,
   // form for measurements.
   const char* env = getenv("MOE_CN_STREAM");
   if (nv <= 2048 && (env ? env[0] == '1' : T > sms)) {
-    // Long rows of several experts are bound by the consumers' instructions and shared
-    // loads, which more warps overlap better: T = 4096, H = 7168, k = 8 95 us with 896
-    // threads, 135 with 448 of two chunks each; k = 4 62.8 against 101.  With few bytes of
-    // rows per column, two or three smaller CTAs on an SM overlap their reductions
-    // better (bf16, H = 5120, k = 2 43.8 us against 50.5; H = 7168, k = 1 51.9 against 54.2; fp32
-    // k = 2 is on the other side, 55.3 against 37.6).  Rows of four chunks per thread always
-    // gain (H = 12288, k = 1 69.6 against 54.6).
-    const bool wide = nv > kRowThreads && nv <= 2 * kWideThreads &&
-                      (nv <= kWideThreads ? k * (y_f32 ? 4 : 2) >= 6 : nv > 2 * kRowThreads);
-    const int vpt = wide ? (nv <= kWideThreads ? 1 : 2) : (nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4));
-    const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
-    cudaError_t e;
-#define MOE_CN(V, W)                                                                                     \
-  e = y_f32 ? launch_stream<V, true, W>(y, pair_order, row_of_pair, T, k, H, p, status, sms, threads, st) \
-            : launch_stream<V, false, W>(y, pair_order, row_of_pair, T, k, H, p, status, sms, threads, st)
-    if (wide && vpt == 1) MOE_CN(1, true);
-    else if (wide) MOE_CN(2, true);
-    else if (vpt == 1) MOE_CN(1, false);
-    else if (vpt == 2) MOE_CN(2, false);
-    else MOE_CN(4, false);
+    // Consumers and chunks per consumer (T = 2048, bf16, in us).  Where a token has few bytes of
+    // expert rows, its two reductions are most of a CTA's time, and two or three CTAs
+    // on an SM overlap them: the fewest chunks with which two fit (k = 1: H = 4096 19.0 with
+    // two chunks, 23.3 with one and a single CTA; H = 5120 21.3, 24.6 by 640 threads; H = 8192
+    // 28.2 with three, 37.2 with two).  With more rows the instructions and shared
+    // loads of the sums count, and more warps overlap those: H = 7168, k = 4 35.4 with 896
+    // threads, 43.2 with 448 of two chunks; k = 8 51.1, 61.2; H = 4096, k = 8 31.3 with one
+    // chunk, 40.7 with two; H = 12288 103 with two, 123 with four.  The border is at 4
+    // bytes per column (fp32, H = 5120, k = 2: 29.5 against 35.5), and at 8 for rows of up to 512
+    // chunks, whose one CTA has only 512 threads (k = 4, H = 4096: 24.6 against 26.4; not for up
+    // to two tokens per SM: T = 200 5.8 against 4.8).
+    cudaError_t e = cudaErrorNotSupported;
+#define MOE_CN(V, W, TWO)                                                                             \
+  {                                                                                                   \
+    const int threads = ((nv + V - 1) / V + 31) / 32 * 32;                                            \
+    e = y_f32 ? launch_stream<V, true, W>(y, pair_order, row_of_pair, T, k, H, p, status, sms,        \
+                                          threads, TWO, st)                                           \
+              : launch_stream<V, false, W>(y, pair_order, row_of_pair, T, k, H, p, status, sms,       \
+                                           threads, TWO, st);                                         \
+  }
+    const int row_bytes = k * (y_f32 ? 4 : 2);  // per column
+    if (nv <= kRowThreads ? row_bytes <= 8 && T > 2 * sms : row_bytes <= 4) {
+      if (nv <= kRowThreads) MOE_CN(1, false, true)
+      if (e == cudaErrorNotSupported && nv <= 2 * kRowThreads) MOE_CN(2, false, true)
+      if (e == cudaErrorNotSupported && nv > kWideThreads && nv <= 3 * kThreeThreads) MOE_CN(3, false, true)
+    }
+    if (e == cudaErrorNotSupported) {
+      if (nv <= kRowThreads) MOE_CN(1, false, false)
+      else if (nv <= kWideThreads) MOE_CN(1, true, false)
+      else if (nv <= 2 * kRowThreads) MOE_CN(2, false, false)
+      else if (nv <= 2 * kWideThreads) MOE_CN(2, true, false)
+      else MOE_CN(4, false, false)
+    }
 #undef MOE_CN
     if (e != cudaErrorNotSupported) return e;
   }
