@@ -802,12 +802,12 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
       if (ok == 15u && two) {
         cp_async16(dst, src);
         cp_async16(dst + 512, src + 64);
-        cp_async16(dst + 1024, s1);
-        cp_async16(dst + 1536, s1 + 64);
-        cp_async16(dst + 2048, s2);
-        cp_async16(dst + 2560, s2 + 64);
-        cp_async16(dst + 3072, s3);
-        cp_async16(dst + 3584, s3 + 64);
+        cp_async16(dst + 2 * 512, s1);
+        cp_async16(dst + 3 * 512, s1 + 64);
+        cp_async16(dst + 4 * 512, s2);
+        cp_async16(dst + 5 * 512, s2 + 64);
+        cp_async16(dst + 6 * 512, s3);
+        cp_async16(dst + 7 * 512, s3 + 64);
       } else {
         const unsigned char* r[4] = {src, s1, s2, s3};
 #pragma unroll
