@@ -310,10 +310,13 @@ size_t moe_layer_workspace_size(const moe_shape* shape);
  *   twice for a token counts with the sum of its weights).
  *   wdtype: MOE_W_BF16, MOE_W_FP8_E4M3 or MOE_W_FP8_BLOCK.  Only the weights
  *   are quantised here: x_hat and the intermediate are not rounded to E4M3 or
- *   bf16 but enter the products with at least 16 bits of mantissa, products
- *   accumulate in fp32, and the only other rounding is that of the outputs.  (So the
- *   result is nearer to the exact one than moe_ffn_forward's, and not
- *   bit-equal to it.)
+ *   bf16 but enter the products as two 16-bit terms, products accumulate in
+ *   fp32, and the only other rounding is that of the outputs.  Beside bf16
+ *   weights a value is held to 16 bits of mantissa; beside E4M3 weights to 22, or
+ *   to 2^-38 of the largest magnitude among the 128 consecutive columns (of x_hat,
+ *   or of the token's intermediate at one expert) that it lies in, whichever is
+ *   coarser.  (So the result is nearer to the exact one than moe_ffn_forward's,
+ *   and not bit-equal to it.)
  *   tail NULL: out bf16 [T, H] = f (out_f32 must be 0).  Otherwise out [T, H]
  *   (bf16, or fp32 when out_f32) = h, and the tail's other outputs.  The
  *   block's own residual connection is tail->residual = x.  out may be x.

@@ -33,8 +33,12 @@
 //                 the terms carry powers of two: a token's 128 columns of x share
 //                 one, applied with the weight scale after a step; eight columns
 //                 of the intermediate do (a row tile, all that a claim is sure to
-//                 hold of them), brought to the pair's largest by an exact fp16
-//                 product when they are used.  (mma.sync on E4M3 itself is no way
+//                 hold of them), brought by an fp16 product to the largest among the
+//                 step's 128 columns when they are used.  So a value is held to
+//                 2^-22 of itself or 2^-38 of the largest of its 128 columns,
+//                 whichever is more (fp16 steps end at 2^-24, the largest is
+//                 above 2^14), and a large column takes nothing from those of other
+//                 steps.  (mma.sync on E4M3 itself is no way
 //                 around the conversion: it runs as one, 51 cycles per m16n8k32
 //                 against 22 per m16n8k16 with operands from shared memory.)
 //
@@ -98,8 +102,7 @@ struct Ring {
 };
 constexpr int kRed = kWarps * 2 * 16 * 8;  // floats: partial sums of all warps, two row tiles
 constexpr int kMaxPairs = kLayerMaxT * kMaxTopK;
-constexpr int kCtrPow = 8;  // ctr: largest exponent of each pair's intermediate
-constexpr int kCtrInts = kCtrPow + kMaxPairs;
+constexpr int kCtrInts = 3;
 
 struct LayerP {
   const bf16* x;
@@ -125,8 +128,7 @@ struct LayerP {
   uint8_t* apow;       // FP8: exponents (pow_exponent) of the intermediate's 8-column groups [T k, I / 8]
   float *ssq, *part;   // sums of squares [chunks, 8], partial logits [chunks, T, E]
   float* f;            // [T, H]
-  int* ctr;            // [0] FC1 claims, [1] FC1 tiles done, [2] CTAs finished,
-                       // [8..] kCtrPow
+  int* ctr;            // [0] FC1 claims, [1] FC1 tiles done, [2] CTAs finished
   int* status;
 };
 
@@ -390,7 +392,6 @@ struct LayerSmem {
   int flag;
   int abort;
   int in_time;  // result of a wait, for all consumers
-  int pow[kMaxPairs];  // FP8: largest exponent of the pair's intermediate
   float sum[kWarps];
   uint64_t full[kWarps][kMaxDepth], empty[kWarps][kMaxDepth];
 };
@@ -975,12 +976,22 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
   int slot = 0;
   uint32_t ph = 0;
   bool arrived = true;
-  // FC2 with FP8: the groups of the lane's column are brought to the exponent
-  // `top`, and `down` holds the powers of two of the lane's columns.
-  auto multiply = [&](bool fc2, Sums& acc, float (&s)[4][NC], int top, const float (&down)[NC]) {
+  // FC2 with FP8: the 8-column groups of the lane's column are brought to the
+  // largest exponent among the step's sixteen.
+  auto multiply = [&](bool fc2, Sums& acc, float (&s)[4][NC]) {
     arrived = ptx::mbar_wait(&sm.full[warp][slot], ph, &sm.abort) && arrived;
     const unsigned char* st = ring + slot * R::kStage;
     const uint4* sp = reinterpret_cast<const uint4*>(st) + lane;
+    int top = 0;
+    if (FP8 && fc2) {
+      const uint2 e0 = *reinterpret_cast<const uint2*>(st + R::kPowAt + tok * 8);
+      const uint2 e1 = *reinterpret_cast<const uint2*>(st + R::kPowAt + (TOK + tok) * 8);
+      constexpr unsigned kEven = 0x00ff00ffu;  // of the largest 16-bit word, the upper byte is the largest upper byte
+      const unsigned odd = __vmaxu2(__vmaxu2(e0.x, e0.y), __vmaxu2(e1.x, e1.y));
+      const unsigned even = __vmaxu2(__vmaxu2(e0.x & kEven, e0.y & kEven), __vmaxu2(e1.x & kEven, e1.y & kEven));
+      const unsigned m = __vmaxu2((odd >> 8) & kEven, even);
+      top = (int)max(m & 0xffffu, m >> 16);
+    }
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       uint4 b[NJ][Q];
@@ -990,7 +1001,7 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
         const unsigned ex = *reinterpret_cast<const uint16_t*>(st + R::kPowAt + (kb * TOK + tok) * 8 + tq * 2);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-          const int d = (int)((ex >> (8 * q)) & 255u) - top;  // <= 0: an exact power of two (0 below 2^-24)
+          const int d = (int)((ex >> (8 * q)) & 255u) - top;  // <= 0: a power of two (0 below 2^-24)
           const __half2 f = __float2half2_rn(__uint_as_float((uint32_t)max(127 + d, 0) << 23));
 #pragma unroll
           for (int j = 0; j < NJ; ++j) b[j][q] = hmul2x4(b[j][q], *reinterpret_cast<const uint32_t*>(&f));
@@ -1024,11 +1035,16 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
     }
     if constexpr (FP8) {
       const float* pw = reinterpret_cast<const float*>(st + R::kPowAt) + 2 * tq / TPG;
+      const float mine = pow_down(top);
+      float down[NC];  // powers of two of the lane's columns
+#pragma unroll
+      for (int c = 0; c < NC; ++c)  // (lane 4 TPG t holds that of token t)
+        down[c] = fc2 ? __shfl_sync(0xffffffffu, mine, (2 * tq / TPG + c) * 4 * TPG) : pw[c];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float w = *reinterpret_cast<const float*>(st + R::kScaleAt + (g + 8 * i) * 4);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) s[i][c] = w * (fc2 ? down[c] : pw[c]);
+        for (int c = 0; c < NC; ++c) s[i][c] = w * down[c];
       }
     }
     __syncwarp();
@@ -1091,7 +1107,7 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
   };
 
   int buf = 0, my_tiles = 0;
-  float sc[4][NC] = {}, down[NC] = {};
+  float sc[4][NC] = {};
   Sums acc = {}, tot = {};
 
   // ---- FC1
@@ -1106,7 +1122,7 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
     const bool second = c < pairs;
 #pragma unroll 1
     for (int step = warp; step < S1; step += kWarps) {
-      multiply(false, acc, sc, 0, down);
+      multiply(false, acc, sc);
       if constexpr (FP8) fold(tot, acc, sc, mask);
     }
     if constexpr (!FP8) fold(tot, acc, sc, mask);
@@ -1142,10 +1158,7 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
         for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const int ex = pow_exponent(m);
         v *= pow_up(ex);
-        if (mine && (il & 7) == 0) {
-          p.apow[(size_t)pr * (I >> 3) + (i0 + il) / 8] = (uint8_t)ex;
-          atomicMax(&p.ctr[kCtrPow + pr], ex);
-        }
+        if (mine && (il & 7) == 0) p.apow[(size_t)pr * (I >> 3) + (i0 + il) / 8] = (uint8_t)ex;
       }
       if (mine) {
         const size_t at = (size_t)pr * I + i0 + il;
@@ -1169,10 +1182,6 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
     __threadfence_block();
     *(volatile int*)&sm.fc1_done = 1;
   }
-  if constexpr (FP8) {
-    if (tid < T * k) sm.pow[tid] = max(15, __ldcg(&p.ctr[kCtrPow + tid]));
-    consumer_sync();
-  }
 
   // ---- FC2: this CTA's output rows over all active experts
   for (int u = 0; u < units; ++u) {
@@ -1180,19 +1189,9 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
     for (int q = q0; q < q1;) {
       const unsigned mask = sm.mask[a];
       const int end = min(q1, q + S2 - s_at);
-      int top = 15;
-      if constexpr (FP8) {
-        const int pr = sm.pair[a][tok];
-        if (pr >= 0) top = sm.pow[pr];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int pc = sm.pair[a][2 * tq / TPG + c];
-          down[c] = pc >= 0 ? pow_down(sm.pow[pc]) : 1.f;
-        }
-      }
 #pragma unroll 1
       for (; q < end; ++q) {
-        multiply(true, acc, sc, top, down);
+        multiply(true, acc, sc);
         if constexpr (FP8) fold(tot, acc, sc, mask);
       }
       if constexpr (!FP8) fold(tot, acc, sc, mask);

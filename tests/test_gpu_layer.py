@@ -611,3 +611,44 @@ def test_many_experts_of_few_tokens(M, T, E, routing):
         whole = call(M, dict(d, logits=torch.cat([few["logits"], d["logits"][T:]])))
         got = call(M, few)
         assert torch.equal(got[1], whole[1][:T]) and torch.equal(got[2], whole[2][:T])
+
+
+@pytest.mark.parametrize("spread", [20, 40])
+@pytest.mark.parametrize("fmt", ["fp8", "block"])
+@pytest.mark.parametrize("T", [1, 3, 4, 5, 8])
+def test_spread_of_the_intermediate(M, T, fmt, spread):
+    """Some of 128 intermediate columns 2^spread times the others: output rows whose W2 codes are 0 there
+    come from the others alone.  (Values are held to 2^-38 of the largest of their 128 columns; at 2^20 that
+    is below the 2^-16 that the tolerance counts, so there only the large column's own codes are 0 in some
+    rows, at 2^40 those of its 128 columns.)"""
+    I = 512
+    d = make(T, 512, 6, 2, I, fmt=fmt, routing="ids", tail="residual", res=torch.float32, seed=90 + T)
+    d["residual"].zero_()  # out = f in fp32
+    if fmt == "fp8":
+        large = slice(130, 131)
+        d["w13_scale"][:, I + 130] *= 2.0 ** spread
+    else:
+        large = slice(128, 256)
+        d["w13_scale"][:, (I + 128) // 128] *= 2.0 ** spread
+    d["w2"][:, :, large] = 0x38  # 1.0
+    d["w2"][:, ::3, 128:256] = 0
+    if spread == 20:
+        d["w2"][:, 1::3, large] = 0
+    check(d, call(M, d))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "block"])
+@pytest.mark.parametrize("T", [1, 4, 7])
+def test_spread_of_the_input(M, T, fmt):
+    """A column of x 2^30 times the others and weights of 0 beside it: intermediate columns of 2^-60 beside
+    some of 2^8, and output rows that only the small ones reach."""
+    H, I = 512, 384
+    d = make(T, H, 6, 2, I, fmt=fmt, routing="ids", tail="residual", res=torch.float32, seed=95 + T)
+    d["residual"].zero_()
+    d["x"][:, 200] *= 2.0 ** 30
+    for first in (0, I):  # gate and up rows of the first 128 intermediate columns
+        d["w13"][:, first:first + 128, 128:256] = 0
+    d["w2"][:, ::3, 128:] = 0
+    res = call(M, d)
+    check(d, res)
+    assert 0 < res[0]["out"][:, ::3].abs().max() < 2.0 ** -40
