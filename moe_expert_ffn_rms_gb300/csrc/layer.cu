@@ -72,6 +72,8 @@
 
 #include <cuda_fp16.h>
 
+#include <stddef.h>
+
 namespace moe {
 namespace {
 
@@ -375,7 +377,7 @@ MOE_DEV void e4m3x4_f16(uint32_t q, uint32_t& lo, uint32_t& hi) {
 
 constexpr int kMaxDepth = 5;
 
-struct LayerSmem {
+struct __align__(16) LayerSmem {
   int32_t ids[kLayerMaxT][kMaxTopK];
   float w[kLayerMaxT][kMaxTopK];
   float r[kLayerMaxT];
@@ -383,7 +385,7 @@ struct LayerSmem {
   int slot[kMaxExperts];       // its place among the active experts
   int expert[kMaxPairs];
   unsigned mask[kMaxPairs];
-  int pair[kMaxPairs][kLayerMaxT];
+  __align__(16) int pair[kMaxPairs][kLayerMaxT];  // (written in 16-byte stores)
   float wt[kMaxPairs][kLayerMaxT];
   int warp_cnt[kWarps];
   int claim[4];
@@ -395,6 +397,9 @@ struct LayerSmem {
   float sum[kWarps];
   uint64_t full[kWarps][kMaxDepth], empty[kWarps][kMaxDepth];
 };
+static_assert(alignof(LayerSmem) == 16 && offsetof(LayerSmem, pair) % 16 == 0 &&
+                  sizeof(LayerSmem::pair[0]) % 16 == 0,
+              "16-byte stores to pair");
 
 // A logit as a key of the top-k: its bits in an order-preserving form, NaN as -inf
 // (0x007fffff), -0 as 0.  Keys of logits are above 0.
