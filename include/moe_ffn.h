@@ -113,9 +113,9 @@ typedef void* moe_stream_t; /* cudaStream_t */
  *   out   = h, rounded once to out's type
  *   x_hat = h / sqrt(mean(h^2) + next_eps) * next_w   from the unrounded h: the
  *           next block's rms_norm ([V100] "rewrite on torch::stable::Tensor")
- *   xq    = e4m3_satfinite_rne(x_hat / xscale), xscale = max|x_hat| / 448 of the
- *           token (or of its 128-column group; 1 where that maximum is 0), from
- *           the unrounded x_hat
+ *   xq    = e4m3_satfinite_rne(x_hat / xscale) (IEEE fp32 divide), xscale =
+ *           max|x_hat| / 448 of the token (or of its 128-column group; 1 where
+ *           that quotient is 0), from the unrounded x_hat
  * in fp32.  The pages name rms_norm only; the norm after the block, the gate
  * and the residual scale are the plain reading of models that have them.
  * A host struct; its pointers are device pointers.  `residual` may be the

@@ -92,14 +92,14 @@ MOE_DEV void write_next(const TailP& p, int t, int H, float (&f)[VPT][8], int nt
       // H of 128)
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float s = m > 0.f ? __fdiv_rn(m, 448.0f) : 1.0f;
+      const float s = tail_scale(m);
       if (v < nv && (v & 15) == 0) p.xscale[(size_t)t * (H >> 7) + (v >> 4)] = s;
       if (v < nv) *reinterpret_cast<uint2*>(p.xq + (size_t)t * H + v * 8) = tail_e4m3x8(f[i], s);
     }
   }
   if (p.xq && !p.q_group) {
     amax = rows_reduce<true, NW>(amax, nt, red[1]);
-    const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    const float s = tail_scale(amax);
     if (tid == 0) p.xscale[t] = s;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {

@@ -114,24 +114,44 @@ MOE_DEV void tail_h8(const TailP& p, int H, int c, const float (&f)[8], const fl
   for (int i = 0; i < 8; ++i) h[i] = grow >= 0 ? fmaf(factor, g[i], res[i]) : res[i];
 }
 
-// E4M3 codes of v / s.  The quotient is taken as a product with 1 / s (one
-// division per row or group instead of eight per thread; within two roundings
-// of the quotient, which is of the size of x_hat's own), except for scales so
-// small that 1 / s could overflow.
+// Scale of a row or group whose largest magnitude is m: m / 448, or 1 where that is 0
+// (nothing but zeros, or magnitudes whose 448th part is below fp32).
+MOE_DEV float tail_scale(float m) {
+  const float s = __fdiv_rn(m, 448.0f);
+  return s > 0.f ? s : 1.0f;
+}
+
+// Both parts of v times s, each rounded by itself.
+MOE_DEV float2 mul2(float2 v, float s) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mul.rn.f32x2 c, a, b;\n"
+      " mov.b64 {%0, %1}, c;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(v.x), "f"(v.y), "f"(s));
+  return d;
+}
+
+// E4M3 codes of v / s, the IEEE quotient (as moe_quantize_fp8_rows rounds it).  Taken from
+// products with 2^-21 less and 2^-21 more than 1 / s, which lie on either side of the
+// quotient (three roundings of 2^-24 are between them and it): where both have the same
+// code, it is the quotient's.  Only chunks with a value that near to the middle between
+// two codes take the divisions (about one chunk in 10^4), and those with a scale so small that
+// 1 / s could overflow.  T = 2048, one row per token: H = 4096 17.7 us, 19.7 with divisions
+// throughout; H = 8192 28.7, 32.1.
 MOE_DEV uint2 tail_e4m3x8(const float (&v)[8], float s) {
-  float q[8];
-  if (s >= 1e-30f) {
-    const float inv = __fdiv_rn(1.0f, s);
+  const float inv = __fdiv_rn(1.0f, s), lo = inv * (1.0f - 0x1p-21f), hi = inv * (1.0f + 0x1p-21f);
+  uint32_t c[4], apart = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+  for (int i = 0; i < 4; ++i) {
+    c[i] = __nv_cvt_float2_to_fp8x2(mul2(make_float2(v[2 * i], v[2 * i + 1]), lo), __NV_SATFINITE, __NV_E4M3);
+    apart |= c[i] ^ __nv_cvt_float2_to_fp8x2(mul2(make_float2(v[2 * i], v[2 * i + 1]), hi), __NV_SATFINITE, __NV_E4M3);
   }
-  uint32_t c[4];
+  if (apart != 0 || s < 1e-30f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i)
+      c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s)), __NV_SATFINITE,
+                                      __NV_E4M3);
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 

@@ -602,7 +602,7 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
   for (int pass = 0; pass < (tail.xq && !tail.q_group ? 2 : 1); ++pass) {
     if (pass) {
       amax = reduce(amax, true);
-      s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+      s = tail_scale(amax);
       if (tid == 0 && !dry) tail.xscale[t] = s;
     }
 #pragma unroll 1
@@ -622,7 +622,7 @@ MOE_DEV void layer_tail_row(const LayerP& p, const TailP& tail, int t, int grow,
       if (tail.q_group) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        s = m > 0.f ? __fdiv_rn(m, 448.0f) : 1.0f;
+        s = tail_scale(m);
         if (tail.xq && v < nv && (v & 15) == 0 && !dry) tail.xscale[(size_t)t * (H >> 7) + (v >> 4)] = s;
       }
       amax = fmaxf(amax, m);

@@ -85,3 +85,31 @@ def test_binding_refusals(M):
     assert t.T == 6 and t.struct.gate_cols == 1
     with pytest.raises(ValueError):  # host tensors are refused before any launch
         M.moe_combine_norm(torch.zeros((8, 256), dtype=bf), x, 4, 2, t)
+
+
+def test_codes_from_products_on_both_sides_of_the_quotient():
+    """The rule of the E4M3 codes in block_tail.cuh, in fp32 on the CPU: where the products with 2^-21 less and
+    2^-21 more than the rounded reciprocal have one code, it is the code of the IEEE quotient; elsewhere the
+    kernel divides.  Values beside every middle between two codes, over scales of every mantissa and size."""
+    g = torch.Generator().manual_seed(1)
+    grid = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    mid = (grid[1:] + grid[:-1]) / 2
+
+    def codes(q):
+        return q.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+    divided = 0
+    for e in (-99, -60, -20, -9, 0, 40, 110):
+        s = (1 + torch.rand((20000, 1), generator=g)) * 2.0 ** e
+        v = mid * s
+        v = torch.stack([v, *(v.view(torch.int32).add(d).view(torch.float32) for d in (-3, -2, -1, 1, 2, 3, 40, -40))])
+        inv = 1 / s
+        lo, hi = codes(v * (inv * (1 - 2.0 ** -21))), codes(v * (inv * (1 + 2.0 ** -21)))
+        same = lo == hi
+        assert torch.equal(lo[same], codes(v / s)[same])
+        divided += int((~same).sum())
+    assert divided > 0
+    w = torch.randn((1000, 4096), generator=g)  # ordinary rows hardly ever divide
+    s = w.abs().amax(1, keepdim=True) / 448
+    lo, hi = (codes(w * (1 / s * f)) for f in (1 - 2.0 ** -21, 1 + 2.0 ** -21))
+    assert (lo != hi).float().mean() < 5e-5

@@ -425,3 +425,63 @@ def test_long_rows_of_many_tokens(M, T, H, k, y, res, gate, post, nxt):
     for n in o:
         assert torch.equal(o[n], again[n]), n
     assert M.device_status() == 0
+
+
+def exact_weights(H, form):
+    """Norm weights in bf16 whose quotients by max / 448 lie beside ties of E4M3: every mantissa under a
+    maximum of every mantissa (a group's, or the row's own)."""
+    mant = 1.0 + torch.arange(128) / 128.0
+    j = torch.arange(H)
+    w = mant[j % 128] * 2.0 ** -(1 + (j // 128 + j) % 20)  # (codes below the normals and 0 among them)
+    if form == "group":
+        w[::128] = mant[(torch.arange(H // 128)) % 128]
+        return [w.to(torch.bfloat16).to(DEV)]
+    rows = []
+    for i in (0, 10, 24, 38, 68, 76, 80, 120, 127):  # where a product by the reciprocal differs, and others
+        v = w.clone()
+        v[5] = mant[i]
+        rows.append(v.to(torch.bfloat16).to(DEV))
+    return rows
+
+
+def codes_by_definition(x, n):
+    """Codes and scales of x (fp32, on the CPU): IEEE divisions, one scale per n columns."""
+    t = x.float().cpu().view(x.shape[0], -1, n)
+    s = t.abs().amax(-1) / 448
+    s = torch.where(s > 0, s, torch.ones_like(s))
+    q = (t / s[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return q.view(x.shape), s
+
+
+@pytest.mark.parametrize("T", [3, 400])
+@pytest.mark.parametrize("nxt,H", [("e4m3", 1024), ("e4m3", 5120), ("e4m3g", 16384)])
+def test_codes_are_those_of_the_quotient(M, form, nxt, H, T):
+    """Rows of +-1 (their norm is 1 without eps), so x_hat is +-next_w exactly: codes bit for bit."""
+    for w in exact_weights(H, "group" if nxt == "e4m3g" else "row"):
+        d = make(T, H, 1, post=False, nxt=nxt, seed=3)
+        d["y"].zero_()
+        d["residual"] = torch.where(d["residual"] > 0, 1.0, -1.0).to(torch.bfloat16)
+        d["next_w"], d["next_eps"] = w, 0.0
+        o = call(M, d)
+        x = (d["residual"].float() * w.float()).to(torch.bfloat16)
+        q, s = codes_by_definition(x, 128 if nxt == "e4m3g" else H)
+        assert torch.equal(o["xscale"].cpu().view(s.shape), s)
+        assert torch.equal(o["xq"].cpu(), q)
+        if nxt == "e4m3":  # and those of the library's own quantisation
+            q2, s2 = torch.empty_like(o["xq"]), torch.empty_like(o["xscale"])
+            M.moe_quantize_fp8_rows(x, q2, s2)
+            assert torch.equal(o["xq"], q2) and torch.equal(o["xscale"], s2)
+
+
+@pytest.mark.parametrize("nxt", ["e4m3", "e4m3g"])
+@pytest.mark.parametrize("T", [3, 400])
+def test_scale_of_rows_that_vanish(M, form, nxt, T):
+    """x_hat of 2^-143 (64 steps of the smallest fp32): its 448th part is 0, the scale 1, the codes 0."""
+    d = make(T, 512, 1, post=False, nxt=nxt, res=torch.float32, seed=3)
+    d["y"].zero_()
+    d["residual"].zero_()
+    d["residual"][:, ::2] = 2.0 ** -10
+    d["next_w"] = torch.full((512,), 1, dtype=torch.int16, device=DEV).view(torch.bfloat16)  # 2^-133
+    d["next_eps"] = 1.0
+    o = call(M, d)
+    assert (o["xscale"] == 1).all() and (o["xq"] & 0x7f == 0).all()

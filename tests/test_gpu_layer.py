@@ -19,7 +19,8 @@ and the tail adds what test_gpu_block_tail counts."""
 import pytest
 import torch
 
-from tests.test_gpu_block_tail import RNORM, U, check_outputs, randn, tail_reference
+from tests.test_gpu_block_tail import (RNORM, U, check_outputs, codes_by_definition, exact_weights, randn,
+                                       tail_reference)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -652,3 +653,28 @@ def test_spread_of_the_input(M, T, fmt):
     res = call(M, d)
     check(d, res)
     assert 0 < res[0]["out"][:, ::3].abs().max() < 2.0 ** -40
+
+
+@pytest.mark.parametrize("nxt,H", [("e4m3", 1024), ("e4m3g", 12288), ("e4m3g", 16384)])
+def test_codes_are_those_of_the_quotient(M, nxt, H):
+    """W2 of 0 and rows of +-1: x_hat is +-next_w exactly (as in test_gpu_block_tail), codes bit for bit."""
+    for w in exact_weights(H, "group" if nxt == "e4m3g" else "row"):
+        d = make(3, H, 2, 1, 64, routing="logits", tail="full", nxt=nxt, seed=5)
+        d["w2"].zero_()
+        d["residual"] = torch.where(d["x"] > 0, 1.0, -1.0).to(torch.bfloat16)
+        d["next_w"], d["next_eps"] = w, 0.0
+        o = call(M, d)[0]
+        q, s = codes_by_definition(d["residual"].float() * w.float(), 128 if nxt == "e4m3g" else H)
+        assert torch.equal(o["xscale"].cpu().view(s.shape), s) and torch.equal(o["xq"].cpu(), q)
+
+
+@pytest.mark.parametrize("nxt", ["e4m3", "e4m3g"])
+def test_scale_of_rows_that_vanish(M, nxt):
+    d = make(3, 512, 2, 1, 64, routing="logits", tail="full", nxt=nxt, res=torch.float32, seed=5)
+    d["w2"].zero_()
+    d["residual"].zero_()
+    d["residual"][:, ::2] = 2.0 ** -10
+    d["next_w"] = torch.full((512,), 1, dtype=torch.int16, device=DEV).view(torch.bfloat16)  # 2^-133
+    d["next_eps"] = 1.0
+    o = call(M, d)[0]
+    assert (o["xscale"] == 1).all() and (o["xq"] & 0x7f == 0).all()
