@@ -323,10 +323,11 @@ size_t moe_layer_workspace_size(const moe_shape* shape);
  *   workspace >= moe_layer_workspace_size(shape) bytes, 256-byte aligned, not
  *   used by other work while this call runs; nothing in it has to be
  *   initialised or kept between calls.
- * Weights must be finite for the experts a token uses: an infinite weight
- * gives NaN in its output column of those tokens (other tokens are not
- * affected).  The result does not depend on what else runs: sums are taken in
- * a fixed order.
+ * Weights must be finite for the experts a token uses.  One in w13 that is not
+ * makes the whole output row of those tokens NaN; one in w2 makes its own
+ * output column of them infinite or NaN, and a norm of the tail carries that to
+ * the rest of the row.  Other tokens are not affected.  The result does not depend
+ * on what else runs: sums are taken in a fixed order.
  * T = 0 returns MOE_OK without looking at the tensor pointers.
  * Errors: as moe_ffn_forward and moe_combine_norm; UNSUPPORTED_SHAPE for
  * T > 8, H > 16384, 2 * I * H >= 2^31 or wdtype = MOE_W_NVFP4 (use

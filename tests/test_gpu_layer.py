@@ -678,3 +678,26 @@ def test_scale_of_rows_that_vanish(M, nxt):
     d["next_eps"] = 1.0
     o = call(M, d)[0]
     assert (o["xscale"] == 1).all() and (o["xq"] & 0x7f == 0).all()
+
+
+@pytest.mark.parametrize("fmt,value", [("bf16", float("inf")), ("bf16", float("-inf")), ("bf16", float("nan")),
+                                       ("fp8", 0x7f), ("fp8", 0xff), ("block", 0x7f)])
+def test_one_weight_that_is_not_finite(M, fmt, value):
+    """In W13 it takes the whole row of the tokens that use the expert, in W2 (without a tail) its own
+    output column of them; other tokens keep theirs."""
+    d = make(4, 256, 12, 2, 128, fmt=fmt, routing="ids", seed=4)
+    d["ids"].copy_(torch.tensor([[0, 1], [2, 3], [6, 4], [5, 1]], dtype=torch.int32))
+    f, df, *_ = block64(d)
+    tol = df + 2.0 ** -8 * (f.abs() + df)
+    for name, at in (("w13", (0, 5, 3)), ("w13", (0, 128 + 9, 200)), ("w2", (0, 7, 3))):
+        w = d[name].clone()
+        w[at] = value
+        out = call(M, dict(d, **{name: w}))[0]["out"].double()
+        good = torch.ones_like(out, dtype=torch.bool)
+        if name == "w13":
+            good[0] = False
+            assert torch.isnan(out[0]).all()
+        else:
+            good[0, 7] = False
+            assert not torch.isfinite(out[0, 7])
+        assert ((out - f).abs() <= tol)[good].all()
