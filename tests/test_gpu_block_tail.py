@@ -485,3 +485,23 @@ def test_scale_of_rows_that_vanish(M, form, nxt, T):
     d["next_eps"] = 1.0
     o = call(M, d)
     assert (o["xscale"] == 1).all() and (o["xq"] & 0x7f == 0).all()
+
+
+@pytest.mark.parametrize("T", [33, 700])
+@pytest.mark.parametrize("res", [torch.bfloat16, torch.float32])
+def test_equals_combine_residual_and_rmsnorm(M, form, T, res):
+    """Integers whose sums and squares are exact in every step: out is moe_combine + residual and x_hat the
+    stand-alone moe_rmsnorm of it, bit for bit."""
+    d = make(T, 1024, 8, order="pair_idx", post=False, res=res, nxt="bf16", scale=1.0, seed=8)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    d["y"] = torch.randint(-4, 5, d["y"].shape, generator=g, device=DEV).to(torch.bfloat16)
+    d["residual"] = torch.randint(-64, 65, (T, 1024), generator=g, device=DEV).to(res)
+    d["next_eps"] = 2.0 ** -20
+    o = call(M, d)
+    f = torch.empty((T, 1024), dtype=torch.bfloat16, device=DEV)
+    M.moe_combine(d["y"], d["row_of_pair"], T, 8, f, pair_order=True)
+    h = f.float() + d["residual"].float()
+    assert torch.equal(o["out"].float(), h)
+    x = torch.empty_like(f)
+    M.moe_rmsnorm(h.to(torch.bfloat16), d["next_w"], d["next_eps"], x)
+    assert torch.equal(o["xhat"], x)
