@@ -372,7 +372,8 @@ __global__ void __launch_bounds__((WIDE ? kWideThreads : (VPT == 3 ? kThreeThrea
     // a wait that runs out leaves garbage in the outputs and is reported
     ok = ptx::mbar_wait(&full[s], ph, &s_abort) && ok;
     const unsigned char* st = stages + (size_t)s * stage_bytes;
-    const unsigned use = meta[s].use;
+    // (a wait that ran out leaves anything here; slots beyond k lie beyond the stage)
+    const unsigned use = meta[s].use & ((1u << k) - 1);
     const float factor = meta[s].factor;
     const bool gate_ok = meta[s].gate_ok != 0;
     float f[VPT][8];
