@@ -537,7 +537,14 @@ cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_
     }
     S = (int)((kStreamSmem / per_sm - kStreamStatic - weights) / bytes(R));
     if (S > kStreamStages) S = kStreamStages;
-    if (R < k) kern = combine_norm_stream_kernel<VPT, YF32, true, WIDE>;
+    // (part of a token per stage: never with VPT = 3, which takes whole tokens only, and never
+    // with bf16 rows of up to 512 chunks, of which two whole tokens always fit: at most 96 KB
+    // each with eight rows, an fp32 residual and an fp32 gate row)
+    if constexpr (VPT == 2 || VPT == 4 || (VPT == 1 && (YF32 || WIDE))) {
+      if (R < k) kern = combine_norm_stream_kernel<VPT, YF32, true, WIDE>;
+    } else if (R < k) {
+      return cudaErrorNotSupported;
+    }
   }
   const size_t smem = (size_t)S * bytes(R) + weights;
   // the same limit in every call: another thread's launch may lie between this and ours
