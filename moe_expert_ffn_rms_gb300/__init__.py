@@ -188,7 +188,12 @@ def _ws_ptr(ws: torch.Tensor) -> int:
 
 
 def _ws_bytes(ws: torch.Tensor) -> int:
-    return ws.numel() - (_ws_ptr(ws) - ws.data_ptr())
+    """Bytes from the aligned start on that surely belong to ws: none of a view that ends before
+    it, and no more of an expanded one than its storage holds."""
+    n = ws.numel()
+    if not ws.is_contiguous():
+        n = min(n, 1 + sum((size - 1) * stride for size, stride in zip(ws.shape, ws.stride())))
+    return max(0, n - (_ws_ptr(ws) - ws.data_ptr()))
 
 
 def moe_ffn_forward(shape: MoeShape, x, norm_w, w13, w2, out, workspace, router_w=None,

@@ -86,3 +86,29 @@ def test_binding_refusals(M):
     x = torch.zeros((4, 256), dtype=torch.bfloat16)
     with pytest.raises(ValueError):  # host tensors are refused before any launch
         M.moe_layer_forward(s, x, x[0], x, x, x, torch.empty(1 << 20, dtype=torch.uint8))
+
+
+def test_workspace_bytes_never_exceed_the_tensor(M):
+    """Views that end before their first 256-byte boundary, expanded and strided ones."""
+    whole = torch.empty(4096, dtype=torch.uint8)
+    start = -whole.data_ptr() % 256
+    assert M._ws_bytes(whole) == 4096 - start
+    assert M._ws_bytes(whole[start + 1:start + 41]) == 0
+    assert M._ws_bytes(whole[start:start + 1].expand(1 << 20)) == 1
+    assert M._ws_bytes(whole[start:start + 2000:2]) == 1000
+    assert M._ws_bytes(whole[start:start]) == 0
+    # a call with such a view is refused, before any CUDA call
+    bf = torch.bfloat16
+    T, H, E, I, k = 2, 256, 4, 128, 2
+    x, w, out = torch.zeros((T, H), dtype=bf), torch.zeros(H, dtype=bf), torch.zeros((T, H), dtype=bf)
+    w13, w2 = torch.zeros((E, 2 * I, H), dtype=bf), torch.zeros((E, H, I), dtype=bf)
+    wr = torch.zeros((H, E))
+    s = M.make_shape(T, H, E, I, k)
+    for ws in (whole[start + 1:start + 41], whole[start:start + 1].expand(1 << 30)):
+        with pytest.raises(M.MoeError) as e:
+            M.moe_ffn_forward(s, x, w, w13, w2, out, ws, router_w=wr, stream=0)
+        assert e.value.name == "MOE_ERR_WORKSPACE_TOO_SMALL"
+        rc = M.lib.moe_layer_forward(ctypes.byref(s), 1 << 20, 1 << 20, 1 << 20, None, None, None, None, 1 << 20,
+                                     1 << 20, None, None, None, 1 << 20, 0, None, None, M._ws_ptr(ws),
+                                     M._ws_bytes(ws), None)
+        assert rc == 4
