@@ -323,6 +323,10 @@ size_t moe_layer_workspace_size(const moe_shape* shape);
  *   workspace >= moe_layer_workspace_size(shape) bytes, 256-byte aligned, not
  *   used by other work while this call runs; nothing in it has to be
  *   initialised or kept between calls.
+ *   With a tail, the last T CTAs of a call wait for its others.  Calls that run at
+ *   the same time (on other streams) should have fewer tokens together than the
+ *   device has SMs, or such a wait could run out (MOE_ERR_TIMEOUT in the
+ *   device status word).
  * Weights must be finite for the experts a token uses.  One in w13 that is not
  * makes the whole output row of those tokens NaN; one in w2 makes its own
  * output column of them infinite or NaN, and a norm of the tail carries that to

@@ -193,7 +193,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
   // One warp runs the code twice: first, while the others already wait for the work in
   // front of this launch, without touching what they share, for the instructions to be
   // at hand afterwards (on the SMs that get these CTAs they rarely are: one token 1 us
-  // of 62, two tokens at H = 7168 1.5 of 201).
+  // of 62, two tokens at H = 7168 1.5 of 201).  In that round it reads shared memory that
+  // nobody has written yet or that the others, further ahead, are writing: that race is
+  // there on purpose, what it reads and computes goes nowhere but into its own part of
+  // `red`, which its second round writes before anyone reads it.
   int live = warp != kRouteWarps - 1;
   asm volatile("" : "+r"(live));
 #pragma unroll 1
@@ -1237,7 +1240,9 @@ MOE_DEV int layer_experts(const LayerP& p, int has_tail, unsigned char* ring_all
 // again cost 1 us of 62 (one token) and more.  So one warp of every CTA runs it once
 // without effect while the others already wait for the first launch.  (Not with E4M3
 // weights and eight token columns: that kernel has no register to spare, and with the
-// loop around it its steps spill: eight tokens 168 us against 153.)
+// loop around it its steps spill: eight tokens 168 us against 153.)  It reads and writes
+// shared memory that holds nothing yet (its own columns of `f` and one word of sm.sum, before
+// the ring's first copies): no result depends on it.
 template <bool FP8, int TOK>
 __global__ void __launch_bounds__(2 * kThreadsL, 1) layer_experts_kernel(const LayerP p, const TailP tail,
                                                                      int has_tail) {
