@@ -10,8 +10,8 @@
 //   4096 4096 8  bf16, bf16 -> bf16, x_hat         57    95%
 //   2048 8192 1  bf16, bf16 -> bf16, x_hat         28    71%
 //   2048 4096 1  bf16, bf16 -> bf16, x_hat         19    52%
-//   2047 5120 1  bf16, fp32 -> fp32, E4M3          23.4  73%
-//   333  2944 4  fp32, bf16 -> bf16, E4M3 groups    8.0  38%
+//   2047 5120 1  bf16, fp32 -> fp32, E4M3          24.1  71%
+//   333  2944 4  fp32, bf16 -> bf16, E4M3 groups    8.3  37%
 //   64   7168 8  bf16, fp32 -> fp32, x_hat          5.5  33%
 //   1    4096 8  bf16, bf16 -> bf16, x_hat          3.3  (latency)
 // The short calls are a launch, one round of loads and two row reductions.
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_row_kernel(
 // (one copy when they are consecutive); the token's last stage also holds its
 // residual and its gate row.  The producer reads the token's indices and
 // leaves them beside the rows.  Without the stages the loads of a token wait for
-// the reductions of the one before it: 66.7 us instead of 57 at T = 4096, H = 4096,
-// k = 8, and 36.7 instead of 23.4 at T = 2047, H = 5120, k = 1.
+// the reductions of the one before it: 66.7 us instead of 58 at T = 4096, H = 4096,
+// k = 8, and 37.1 instead of 24.1 at T = 2047, H = 5120, k = 1.
 struct StreamMeta {
   unsigned use;   // slots whose row is present
   float factor;   // tail_row_factor
@@ -505,8 +505,10 @@ cudaError_t launch_stream(const void* y, bool pair_order, const int32_t* row_of_
   auto by_smem = [&](int64_t b) { return (int)(kStreamSmem / (b + kStreamStatic + weights)); };
   int R = k, S, per_sm = by_smem(bytes(k)) < by_regs ? by_smem(bytes(k)) : by_regs;
   if (per_sm > 0 && T <= sms * per_sm) {
-    // every token gets a CTA of its own at once: one stage each (T = 333, H = 2944,
-    // k = 4: 8.0 us, against 9.9 with two stages and half the CTAs)
+    // every token gets a CTA of its own at once: one stage each.  Against two stages and
+    // fewer CTAs: T = 450, H = 5120, k = 1 4.85 us, 5.19; T = 200, H = 4096, k = 8 5.46, 5.43;
+    // T = 333, H = 2944, k = 4 8.3 either way; with short rows it loses (T = 400, H = 1024,
+    // k = 8 4.17, 3.41)
     S = 1;
   } else {
     // two or more stages, each as much of a token as fits (a whole token wherever two
@@ -564,7 +566,7 @@ cudaError_t launch_combine_norm(const void* y, bool y_f32, bool pair_order,
   const int nv = H / 8;
   // A CTA per token while the SMs hold all tokens at once, the streaming form beyond:
   // T = 64 (H = 7168, k = 8) 5.5 us against 6.0 streamed; T = 333 (H = 2944, k = 4)
-  // 10.2 against 8.0.  Rows above 16384 columns always take a CTA per token: a thread
+  // 10.6 against 8.3.  Rows above 16384 columns always take a CTA per token: a thread
   // of the streaming form would hold more than four chunks.  MOE_CN_STREAM=0|1 sets the
   // form for measurements.
   const char* env = getenv("MOE_CN_STREAM");

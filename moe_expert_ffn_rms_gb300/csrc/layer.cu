@@ -60,7 +60,7 @@
 // trip between tiles that short.
 //
 // Measured (H = 4096, I = 1536, E = 64, top_k = 8, cold weights): one token 61.7 us
-// (302 MB), eight tokens 250 us (1.775 GB read, 7.1 TB/s), E4M3 one token 34 us,
+// (302 MB), eight tokens 250 us (1.775 GB read, 7.1 TB/s), E4M3 one token 33.5 us,
 // block-wise FP8 four tokens 94 us (5.0 TB/s).  The separate launches of
 // moe_ffn_forward, without a tail: 96, 251, 54 and 122 us.  What is left at one token
 // is latency around the stream: the routing launch 3 to 4 us, the hand-over 1, the
