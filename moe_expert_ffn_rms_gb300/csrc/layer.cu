@@ -193,10 +193,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) layer_route_kernel(const Lay
   // One warp runs the code twice: first, while the others already wait for the work in
   // front of this launch, without touching what they share, for the instructions to be
   // at hand afterwards (on the SMs that get these CTAs they rarely are: one token 1 us
-  // of 62, two tokens at H = 7168 1.5 of 201).  In that round it reads shared memory that
+  // of 62, two tokens at H = 7168 1.5 of 201).  The first time it reads shared memory that
   // nobody has written yet or that the others, further ahead, are writing: that race is
   // there on purpose, what it reads and computes goes nowhere but into its own part of
-  // `red`, which its second round writes before anyone reads it.
+  // `red`, which it writes again before anyone reads it.
   int live = warp != kRouteWarps - 1;
   asm volatile("" : "+r"(live));
 #pragma unroll 1
