@@ -535,6 +535,102 @@ moe_status moe_quantize_nvfp4(const void* w, int32_t M, int32_t N, int32_t K, ui
 moe_status moe_quantize_fp8_blocks(const void* x, int32_t N, int32_t K, int32_t block_rows,
                                    uint8_t* q, float* scale, moe_stream_t stream);
 
+/* --------------------------------------- around the experts, and training -- */
+/* The pages describe none of the entry points below; the plain reading of
+ * layers that have them is used, with their exact gradients.  Sums, statistics
+ * and norms are fp32, every output is rounded once, sums are taken in a fixed
+ * order (the same call gives the same bits).  Unless said otherwise no output may
+ * overlap another buffer of the call. */
+
+/* Expert rows back to their tokens with the routing weights applied:
+ *   out[t, :] = residual[t, :] + sum_{j=0..k-1} topk_w[t, j] * y[row_of_pair[t*k+j], :]
+ * in slot order (moe_combine sums rows whose weight is already in them).
+ *   y           [T*k, H] bf16 (y_bf16 = 1) or fp32, rows in expert order
+ *   row_of_pair int32 [T*k] as moe_permute writes it; a negative entry is a pair
+ *               without a row (dropped: nothing is read and nothing added); one
+ *               >= T*k counts as such and is flagged in the device status word
+ *   topk_w      fp32 [T, k], or NULL: all 1
+ *   residual    [T, H] bf16 or fp32 (residual_f32), or NULL; may be out
+ *   out         [T, H] bf16 or fp32 (out_f32)
+ * T = 0 returns MOE_OK without looking at the tensor pointers (this and the next
+ * two).  Errors of the three: INVALID_ARG (null or misaligned pointers);
+ * UNSUPPORTED_SHAPE unless H % 8 == 0, H <= 32768, 0 < k <= 8 and T*k <= 2^24. */
+moe_status moe_unpermute(const void* y, int32_t y_bf16, const int32_t* row_of_pair,
+                         const float* topk_w, int32_t T, int32_t k, int32_t H,
+                         const void* residual, int32_t residual_f32, void* out, int32_t out_f32,
+                         moe_stream_t stream);
+
+/* Gradient of moe_unpermute from dout = d loss / d out:
+ *   dy[row_of_pair[t*k+j], :] = topk_w[t, j] * dout[t, :]     (y's type)
+ *   dw[t, j]      = sum_h dout[t, h] * y[row_of_pair[t*k+j], h]    fp32; 0 for a
+ *                   dropped pair
+ *   dlogits[t, e] = sum over j with ids[t, j] = e of
+ *                   topk_w[t, j] * (dw[t, j] - sum_i topk_w[t, i] * dw[t, i])
+ *                   fp32 [T, E]: the gradient of moe_route_topk's logits (topk_w
+ *                   the softmax over the selected logits); 0 where e is not selected
+ * (the residual's gradient is dout itself).  dy, dw, dlogits: any may be NULL, but
+ * not all; y is needed with dw or dlogits, ids int32 [T, k] with dlogits (an id
+ * outside [0, E) adds to no logit and is flagged).  Rows of dy that no pair owns are left
+ * as they were; two pairs must not own one row.  dy may be y. */
+moe_status moe_unpermute_backward(const void* dout, int32_t dout_f32, const void* y, int32_t y_bf16,
+                                  const int32_t* row_of_pair, const float* topk_w,
+                                  const int32_t* ids, int32_t T, int32_t k, int32_t H, int32_t E,
+                                  void* dy, float* dw, float* dlogits, moe_stream_t stream);
+
+/* Gradient of moe_permute's gather xp[r] = x[row_src[r] / k]:
+ *   dx[t, :] = dres[t, :] + sum_{j=0..k-1} dxp[row_of_pair[t*k+j], :]
+ * dxp [T*k, H] bf16 (dxp_bf16 = 1) or fp32; dres [T, H] (dres_f32) the gradient
+ * that reaches x past the experts, or NULL, may be dx; dx [T, H] (dx_f32).
+ * row_of_pair as in moe_unpermute. */
+moe_status moe_permute_backward(const void* dxp, int32_t dxp_bf16, const int32_t* row_of_pair,
+                                int32_t T, int32_t k, int32_t H, const void* dres, int32_t dres_f32,
+                                void* dx, int32_t dx_f32, moe_stream_t stream);
+
+/* Layer norm:
+ *   mean[t] = sum_i x[t, i] / H,  rstd[t] = 1 / sqrt(sum_i (x[t, i] - mean[t])^2 / H + eps)
+ *   y[t, i] = (x[t, i] - mean[t]) * rstd[t] * w[i] + b[i]
+ *   x [T, H] bf16 or fp32 (x_f32); w [H] and b [H] (or NULL: 0) bf16 or fp32 (w_f32);
+ *   y [T, H] bf16 or fp32 (y_f32), may be x when both have one type;
+ *   mean, rstd fp32 [T] for the backward pass, or both NULL.
+ * T = 0 returns MOE_OK without looking at the tensor pointers.
+ * Errors: INVALID_ARG (null or misaligned pointers, eps < 0, one of mean and rstd);
+ * UNSUPPORTED_SHAPE unless H % 8 == 0 and H <= 16384. */
+moe_status moe_layernorm(const void* x, int32_t x_f32, const void* w, const void* b, int32_t w_f32,
+                         int32_t T, int32_t H, float eps, void* y, int32_t y_f32, float* mean,
+                         float* rstd, moe_stream_t stream);
+
+/* Device workspace bytes moe_layernorm_backward and moe_rmsnorm_backward need
+ * (0 and an error message when the shape is outside their limits). */
+size_t moe_norm_backward_workspace_size(int32_t T, int32_t H);
+
+/* Gradient of moe_layernorm.  With xh = (x - mean) * rstd and g = dy * w:
+ *   dx[t, i] = dres[t, i] + rstd[t] * (g[t, i] - sum_i g / H - xh[t, i] * sum_i (g xh) / H)
+ *   dw[i] = sum_t dy[t, i] * xh[t, i],  db[i] = sum_t dy[t, i]
+ *   dy [T, H] bf16 or fp32 (dy_f32); x, w, mean, rstd of the forward call; dres
+ *   [T, H] of x's type (the gradient of a residual stream that passes the norm) or
+ *   NULL; dx [T, H] of x's type, may be x, dres, or dy of the same type; dw fp32 [H];
+ *   db fp32 [H] or NULL.
+ *   workspace >= moe_norm_backward_workspace_size(T, H) bytes, 256-byte aligned,
+ *   not used by other work while this call runs.
+ * T = 0 writes zeros to dw and db (both sums are empty).
+ * Errors: as moe_layernorm, WORKSPACE_TOO_SMALL. */
+moe_status moe_layernorm_backward(const void* dy, int32_t dy_f32, const void* x, int32_t x_f32,
+                                  const void* w, int32_t w_f32, const float* mean, const float* rstd,
+                                  const void* dres, int32_t T, int32_t H, void* dx, float* dw,
+                                  float* db, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream);
+
+/* Gradient of moe_rmsnorm's y = x * r * w, r = 1 / sqrt(sum_i x^2 / H + eps)
+ * (its rounding of y is passed over).  With xh = x * r and g = dy * w:
+ *   dx[t, i] = dres[t, i] + r[t] * (g[t, i] - xh[t, i] * sum_i (g xh) / H)
+ *   dw[i] = sum_t dy[t, i] * xh[t, i]
+ * The rest as moe_layernorm_backward; x may be fp32 (a residual stream that
+ * moe_combine_norm normalised). */
+moe_status moe_rmsnorm_backward(const void* dy, int32_t dy_f32, const void* x, int32_t x_f32,
+                                const void* w, int32_t w_f32, float eps, const void* dres, int32_t T,
+                                int32_t H, void* dx, float* dw, void* workspace,
+                                size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

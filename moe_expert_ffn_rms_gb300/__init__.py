@@ -103,6 +103,17 @@ _SIGS = {
     "moe_grouped_ffn_nvfp4": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _P, _P, _P, _P,
                                              _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_quantize_fp8_blocks": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_unpermute": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _I32, _P]),
+    "moe_unpermute_backward": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _P,
+                                              _P, _P, _P]),
+    "moe_permute_backward": (ctypes.c_int, [_P, _I32, _P, _I32, _I32, _I32, _P, _I32, _P, _I32, _P]),
+    "moe_layernorm": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P, _I32, _P, _P,
+                                     _P]),
+    "moe_norm_backward_workspace_size": (_SZ, [_I32, _I32]),
+    "moe_layernorm_backward": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _P, _P,
+                                              _P, _P, _SZ, _P]),
+    "moe_rmsnorm_backward": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _I32, ctypes.c_float, _P, _I32, _I32,
+                                            _P, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -542,3 +553,132 @@ def moe_quantize_fp8_blocks(x, q, scale, block_rows, stream=None):
     _check(lib.moe_quantize_fp8_blocks(_ptr(x), N, K, block_rows, _ptr(q), _ptr(scale),
                                        _stream(stream)))
     return q, scale
+
+
+# --------------------------------------------- around the experts, and training --
+
+def _ws(workspace, device):
+    if workspace.device != device:
+        raise ValueError(f"workspace: on {workspace.device}, need {device}")
+    return _ws_ptr(workspace), _ws_bytes(workspace)
+
+
+def _pairs(row_of_pair, n, device):
+    if row_of_pair.numel() != n:
+        raise ValueError(f"row_of_pair: {row_of_pair.numel()} entries, need {n}")
+    _check_tensor(row_of_pair, "row_of_pair", row_of_pair.shape, _I32S, device)
+    return row_of_pair.data_ptr()
+
+
+def moe_unpermute(y, row_of_pair, out, T, k, topk_w=None, residual=None, stream=None):
+    """out = residual + each token's expert rows times their routing weights.  y bf16 / fp32
+    [T*k, H] in expert order, row_of_pair int32 [T*k] of moe_permute (negative: dropped), topk_w
+    fp32 [T, k] (None: all 1), residual and out bf16 / fp32 [T, H]; residual may be out."""
+    H, device = y.shape[-1], y.device
+    _check_current(device)
+    _check_tensor(y, "y", (T * k, H), _FLOATS, device)
+    _check_tensor(out, "out", (T, H), _FLOATS, device)
+    _check(lib.moe_unpermute(
+        y.data_ptr(), y.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, device),
+        _opt(topk_w, "topk_w", (T, k), _F32S, device), T, k, H,
+        _opt(residual, "residual", (T, H), _FLOATS, device),
+        residual is not None and residual.dtype == torch.float32, out.data_ptr(),
+        out.dtype == torch.float32, _stream(stream)))
+    return out
+
+
+def moe_unpermute_backward(dout, y, row_of_pair, topk_w, T, k, dy=None, dw=None, ids=None, dlogits=None,
+                           stream=None):
+    """Gradients of moe_unpermute from dout bf16 / fp32 [T, H]: dy [T*k, H] (y's type, bf16 without
+    y; rows that no pair owns are left as they were), dw fp32 [T, k], and with ids int32 [T, k] the
+    router's dlogits fp32 [T, E].  y is needed for dw and dlogits; dy may be y."""
+    H, device = dout.shape[-1], dout.device
+    _check_current(device)
+    _check_tensor(dout, "dout", (T, H), _FLOATS, device)
+    _check_tensor(topk_w, "topk_w", (T, k), _F32S, device)
+    yt = y if y is not None else dy
+    if dy is not None and y is not None and dy.dtype != y.dtype:
+        raise ValueError(f"dy: dtype {dy.dtype}, need {y.dtype}")
+    if dlogits is not None and dlogits.dim() != 2:
+        raise ValueError("dlogits: must be [T, E]")
+    E = 0 if dlogits is None else dlogits.shape[1]
+    _check(lib.moe_unpermute_backward(
+        dout.data_ptr(), dout.dtype == torch.float32, _opt(y, "y", (T * k, H), _FLOATS, device),
+        yt is None or yt.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, device), topk_w.data_ptr(),
+        _opt(ids, "ids", (T, k), _I32S, device), T, k, H, E, _opt(dy, "dy", (T * k, H), _FLOATS, device),
+        _opt(dw, "dw", (T, k), _F32S, device), _opt(dlogits, "dlogits", (T, E), _F32S, device),
+        _stream(stream)))
+
+
+def moe_permute_backward(dxp, row_of_pair, dx, T, k, dres=None, stream=None):
+    """Gradient of moe_permute's gather: dx = dres + the sum of each token's rows of dxp (bf16 / fp32
+    [T*k, H], expert order).  dres and dx bf16 / fp32 [T, H]; dres may be dx."""
+    H, device = dxp.shape[-1], dxp.device
+    _check_current(device)
+    _check_tensor(dxp, "dxp", (T * k, H), _FLOATS, device)
+    _check_tensor(dx, "dx", (T, H), _FLOATS, device)
+    _check(lib.moe_permute_backward(
+        dxp.data_ptr(), dxp.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, device), T, k, H,
+        _opt(dres, "dres", (T, H), _FLOATS, device), dres is not None and dres.dtype == torch.float32,
+        dx.data_ptr(), dx.dtype == torch.float32, _stream(stream)))
+    return dx
+
+
+def moe_layernorm(x, w, eps, y, b=None, mean=None, rstd=None, stream=None):
+    """y = (x - mean) * rstd * w + b over the rows of x bf16 / fp32 [T, H]; w, b bf16 / fp32 [H] of one
+    type; y bf16 / fp32 [T, H]; mean, rstd fp32 [T] for the backward pass."""
+    T, H = x.shape
+    device = x.device
+    _check_current(device)
+    _check_tensor(x, "x", (T, H), _FLOATS, device)
+    _check_tensor(w, "w", (H,), _FLOATS, device)
+    _check_tensor(y, "y", (T, H), _FLOATS, device)
+    _check(lib.moe_layernorm(
+        x.data_ptr(), x.dtype == torch.float32, w.data_ptr(), _opt(b, "b", (H,), (w.dtype,), device),
+        w.dtype == torch.float32, T, H, eps, y.data_ptr(), y.dtype == torch.float32,
+        _opt(mean, "mean", (T,), _F32S, device), _opt(rstd, "rstd", (T,), _F32S, device), _stream(stream)))
+    return y
+
+
+def moe_norm_backward_workspace_size(T, H) -> int:
+    n = lib.moe_norm_backward_workspace_size(T, H)
+    if n == 0:
+        raise MoeError(2, last_error())
+    return n
+
+
+def _norm_grad_args(dy, x, w, dx, dw, dres):
+    T, H = x.shape
+    device = x.device
+    _check_current(device)
+    _check_tensor(x, "x", (T, H), _FLOATS, device)
+    _check_tensor(dy, "dy", (T, H), _FLOATS, device)
+    _check_tensor(w, "w", (H,), _FLOATS, device)
+    _check_tensor(dx, "dx", (T, H), (x.dtype,), device)
+    _check_tensor(dw, "dw", (H,), _F32S, device)
+    return T, H, device, _opt(dres, "dres", (T, H), (x.dtype,), device)
+
+
+def moe_layernorm_backward(dy, x, w, mean, rstd, dx, dw, workspace, db=None, dres=None, stream=None):
+    """Gradients of moe_layernorm: dx [T, H] of x's type (plus dres, of the same type), dw and db fp32
+    [H]; mean and rstd of the forward call, workspace of moe_norm_backward_workspace_size(T, H) bytes.
+    dx may be x, dres, or dy of the same type."""
+    T, H, device, pres = _norm_grad_args(dy, x, w, dx, dw, dres)
+    _check_tensor(mean, "mean", (T,), _F32S, device)
+    _check_tensor(rstd, "rstd", (T,), _F32S, device)
+    _check(lib.moe_layernorm_backward(
+        dy.data_ptr(), dy.dtype == torch.float32, x.data_ptr(), x.dtype == torch.float32, w.data_ptr(),
+        w.dtype == torch.float32, mean.data_ptr(), rstd.data_ptr(), pres, T, H, dx.data_ptr(),
+        dw.data_ptr(), _opt(db, "db", (H,), _F32S, device), *_ws(workspace, device), _stream(stream)))
+    return dx
+
+
+def moe_rmsnorm_backward(dy, x, w, eps, dx, dw, workspace, dres=None, stream=None):
+    """Gradients of moe_rmsnorm: dx [T, H] of x's type (plus dres), dw fp32 [H]; the rest as
+    moe_layernorm_backward."""
+    T, H, device, pres = _norm_grad_args(dy, x, w, dx, dw, dres)
+    _check(lib.moe_rmsnorm_backward(
+        dy.data_ptr(), dy.dtype == torch.float32, x.data_ptr(), x.dtype == torch.float32, w.data_ptr(),
+        w.dtype == torch.float32, eps, pres, T, H, dx.data_ptr(), dw.data_ptr(), *_ws(workspace, device),
+        _stream(stream)))
+    return dx

@@ -575,6 +575,14 @@ moe_status check_layer_shape(const moe_shape* s) {
 namespace moe {
 moe_status api_fail(moe_status s, const char* msg) { return fail(s, "%s", msg); }
 moe_status api_check_shape(const moe_shape* shape) { return check_shape(shape); }
+moe_status api_device(int* sms, int** status) {
+  DevInfo* d = nullptr;
+  const moe_status rc = device_info(&d);
+  if (rc != MOE_OK) return rc;
+  *sms = d->sms;
+  *status = d->status;
+  return MOE_OK;
+}
 }  // namespace moe
 
 extern "C" {

@@ -11,4 +11,8 @@ moe_status api_fail(moe_status s, const char* msg);
 // Status of the shape checks moe_ffn_forward applies (MOE_OK if valid).
 moe_status api_check_shape(const moe_shape* shape);
 
+// SM count and device status word of the current device, or why it cannot run
+// the library (as moe_check_device).
+moe_status api_device(int* sms, int** status);
+
 }  // namespace moe

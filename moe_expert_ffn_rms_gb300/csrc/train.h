@@ -1,0 +1,75 @@
+// Host-side launch functions of the operators around the experts' products:
+// weighted return of expert rows, layer norm, dense product, and their
+// gradients (internal to libmoeffn).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+// ------------------------------------------------------------------ rows.cu --
+constexpr int kRowsMaxH = 32768;
+
+// out[t] = residual[t] + sum_j w[t, j] y[row_of_pair[t, j]]; w NULL: 1.
+struct UnpermuteArgs {
+  const void* y;
+  const int32_t* row_of_pair;
+  const float* w;
+  const void* residual;
+  void* out;
+  int T, k, H;
+  bool y_f32, res_f32, out_f32;
+};
+cudaError_t launch_unpermute(const UnpermuteArgs& a, int* status, cudaStream_t st);
+
+struct UnpermuteGradArgs {
+  const void* dout;
+  const void* y;
+  const int32_t* row_of_pair;
+  const float* w;
+  const int32_t* ids;
+  void* dy;        // or NULL
+  float* dw;       // or NULL
+  float* dlogits;  // or NULL
+  int T, k, H, E;
+  bool dout_f32, y_f32;
+};
+cudaError_t launch_unpermute_grad(const UnpermuteGradArgs& a, int* status, cudaStream_t st);
+
+// ------------------------------------------------------------------ norm.cu --
+constexpr int kNormMaxH = 16384;
+
+struct LayerNormArgs {
+  const void* x;
+  const void* w;
+  const void* b;  // or NULL
+  void* y;
+  float* mean;    // or NULL
+  float* rstd;    // or NULL
+  int T, H;
+  float eps;
+  bool x_f32, y_f32, w_f32;
+};
+cudaError_t launch_layernorm(const LayerNormArgs& a, cudaStream_t st);
+
+struct NormGradArgs {
+  const void* dy;
+  const void* x;
+  const void* w;
+  const float* mean;  // NULL: rms_norm, statistics from x
+  const float* rstd;
+  const void* dres;   // or NULL, x's type
+  void* dx;
+  float* dw;
+  float* db;          // or NULL
+  void* workspace;
+  int T, H;
+  float eps;
+  bool x_f32, dy_f32, w_f32;
+};
+size_t norm_grad_workspace_bytes(int T, int H);
+cudaError_t launch_norm_grad(const NormGradArgs& a, int sms, int* status, cudaStream_t st);
+
+}  // namespace moe
