@@ -631,6 +631,59 @@ moe_status moe_rmsnorm_backward(const void* dy, int32_t dy_f32, const void* x, i
                                 int32_t H, void* dx, float* dw, void* workspace,
                                 size_t workspace_bytes, moe_stream_t stream);
 
+/* Activation of moe_linear, z = the product plus the bias:
+ *   RELU max(z, 0); SILU z / (1 + exp(-z)); GELU z Phi(z), Phi the normal
+ *   distribution function; GELU_TANH z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4
+} moe_act;
+
+/* Dense product with its epilogue (the projections beside the experts: an
+ * attention block's, a shared expert's, a dense layer's):
+ *   z[m, n]   = sum_k x[m, k] * w[n, k] + bias[n]
+ *   out[m, n] = residual[m, n] + act(z[m, n])
+ *   x bf16 [M, K]; w bf16 [N, K]; bias [N] bf16 or fp32 (bias_f32), or NULL;
+ *   residual [M, N] bf16 or fp32 (residual_f32), or NULL; may be out when both have
+ *   one type; pre bf16 [M, N] or NULL: receives z for the backward pass; out [M, N]
+ *   bf16 or fp32 (out_f32).
+ * Products accumulate in the tensor cores' fp32, whose additions truncate: a sum of
+ * K terms is off by about 1.1e-9 K of its magnitude.  With fp32 outputs no more
+ * than 1024 terms are added that way, and those sums in fp32 rounded to nearest.
+ * The activation takes the unrounded z.  Nothing of the result depends on what else runs.
+ * M = 0 returns MOE_OK without looking at the tensor pointers.
+ * Errors: INVALID_ARG (null or misaligned pointers, act); UNSUPPORTED_SHAPE unless N and K
+ * are multiples of 8, 0 <= M <= 2^23 and 0 < N, K <= 2^20. */
+moe_status moe_linear(const void* x, const void* w, const void* bias, int32_t bias_f32,
+                      const void* residual, int32_t residual_f32, int32_t M, int32_t N, int32_t K,
+                      int32_t act, void* pre, void* out, int32_t out_f32, moe_stream_t stream);
+
+/* Device workspace bytes moe_linear_backward needs (0 and an error message when
+ * the shape is outside moe_linear's limits). */
+size_t moe_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K);
+
+/* Gradient of moe_linear (the residual's is dout itself):
+ *   dpre = dout * act'(pre), rounded to bf16 for the two products (dout itself without
+ *          an activation; the tensor cores take bf16)
+ *   dx[m, k] = sum_n dpre[m, n] * w[n, k]
+ *   dw[n, k] = sum_m dpre[m, n] * x[m, k]
+ *   db[n]    = sum_m dpre[m, n], of the unrounded dpre
+ *   dout [M, N] bf16 or fp32 (dout_f32); pre bf16 [M, N] of the forward call (NULL
+ *   without activation; relu' is 0 at 0); x, w of the forward call; dx bf16 [M, K];
+ *   dw [N, K] bf16 or fp32 (dw_f32, accumulated as moe_linear's fp32 outputs); db fp32
+ *   [N].  dx, dw, db: any may be NULL, but not all; x is needed with dw, w with dx.
+ *   workspace >= moe_linear_backward_workspace_size(M, N, K) bytes, 256-byte aligned,
+ *   not used by other work while this call runs; nothing in it has to be
+ *   initialised or kept between calls.
+ * M = 0 writes zeros to dw and db.  Errors: as moe_linear, WORKSPACE_TOO_SMALL. */
+moe_status moe_linear_backward(const void* dout, int32_t dout_f32, const void* pre, const void* x,
+                               const void* w, int32_t M, int32_t N, int32_t K, int32_t act, void* dx,
+                               void* dw, int32_t dw_f32, float* db, void* workspace,
+                               size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

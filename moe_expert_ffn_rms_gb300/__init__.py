@@ -29,6 +29,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_S
                 3: "MOE_ERR_UNSUPPORTED_DEVICE", 4: "MOE_ERR_WORKSPACE_TOO_SMALL",
                 5: "MOE_ERR_CUDA", 6: "MOE_ERR_TIMEOUT"}
 W_BF16, W_FP8_E4M3, W_NVFP4, W_FP8_BLOCK = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
 GEMM_FC1_RAW, GEMM_FC1_SILU, GEMM_FC2, GEMM_FC2_BF16 = 0, 1, 2, 3
 ENGINE_AUTO, ENGINE_DECODE, ENGINE_PREFILL = 0, 1, 2
 
@@ -114,6 +115,10 @@ _SIGS = {
                                               _P, _P, _SZ, _P]),
     "moe_rmsnorm_backward": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _I32, ctypes.c_float, _P, _I32, _I32,
                                             _P, _P, _P, _SZ, _P]),
+    "moe_linear": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _P]),
+    "moe_linear_backward_workspace_size": (_SZ, [_I32, _I32, _I32]),
+    "moe_linear_backward": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _P,
+                                           _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -682,3 +687,49 @@ def moe_rmsnorm_backward(dy, x, w, eps, dx, dw, workspace, dres=None, stream=Non
         w.dtype == torch.float32, eps, pres, T, H, dx.data_ptr(), dw.data_ptr(), *_ws(workspace, device),
         _stream(stream)))
     return dx
+
+
+def moe_linear(x, w, out, bias=None, residual=None, act=ACT_NONE, pre=None, stream=None):
+    """out = residual + act(x w^T + bias).  x bf16 [M, K], w bf16 [N, K], bias bf16 / fp32 [N], residual
+    and out bf16 / fp32 [M, N] (residual may be out), act one of the ACT_ constants; pre bf16 [M, N]
+    receives the values before the activation."""
+    device = x.device
+    _check_current(device)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w: must be [M, K] and [N, K]")
+    (m, k), n = x.shape, w.shape[0]
+    _check_tensor(x, "x", (m, k), _BF16, device)
+    _check_tensor(w, "w", (n, k), _BF16, device)
+    _check_tensor(out, "out", (m, n), _FLOATS, device)
+    _check(lib.moe_linear(
+        x.data_ptr(), w.data_ptr(), _opt(bias, "bias", (n,), _FLOATS, device),
+        bias is not None and bias.dtype == torch.float32, _opt(residual, "residual", (m, n), _FLOATS, device),
+        residual is not None and residual.dtype == torch.float32, m, n, k, act,
+        _opt(pre, "pre", (m, n), _BF16, device), out.data_ptr(), out.dtype == torch.float32, _stream(stream)))
+    return out
+
+
+def moe_linear_backward_workspace_size(M, N, K) -> int:
+    n = lib.moe_linear_backward_workspace_size(M, N, K)
+    if n == 0:
+        raise MoeError(2, last_error())
+    return n
+
+
+def moe_linear_backward(dout, x, w, workspace, dx=None, dw=None, db=None, pre=None, act=ACT_NONE, stream=None):
+    """Gradients of moe_linear from dout bf16 / fp32 [M, N]: dx bf16 [M, K], dw bf16 / fp32 [N, K], db fp32
+    [N], each where it is given; pre of the forward call with an activation; workspace of
+    moe_linear_backward_workspace_size(M, N, K) bytes."""
+    device = dout.device
+    _check_current(device)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w: must be [M, K] and [N, K]")
+    (m, k), n = x.shape, w.shape[0]
+    _check_tensor(dout, "dout", (m, n), _FLOATS, device)
+    _check_tensor(x, "x", (m, k), _BF16, device)
+    _check_tensor(w, "w", (n, k), _BF16, device)
+    _check(lib.moe_linear_backward(
+        dout.data_ptr(), dout.dtype == torch.float32, _opt(pre, "pre", (m, n), _BF16, device), x.data_ptr(),
+        w.data_ptr(), m, n, k, act, _opt(dx, "dx", (m, k), _BF16, device), _opt(dw, "dw", (n, k), _FLOATS, device),
+        dw is not None and dw.dtype == torch.float32, _opt(db, "db", (n,), _F32S, device),
+        *_ws(workspace, device), _stream(stream)))

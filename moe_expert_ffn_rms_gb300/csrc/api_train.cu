@@ -94,6 +94,18 @@ moe_status norm_grad(moe::NormGradArgs& a, size_t workspace_bytes, moe_stream_t 
   return MOE_OK;
 }
 
+constexpr int kLinearMaxM = 1 << 23, kLinearMaxNK = 1 << 20;
+
+moe_status check_linear(int M, int N, int K, int act) {
+  MOE_REQ(M >= 0 && M <= kLinearMaxM && N > 0 && N <= kLinearMaxNK && N % 8 == 0 && K > 0 &&
+              K <= kLinearMaxNK && K % 8 == 0,
+          MOE_ERR_UNSUPPORTED_SHAPE, "M=%d N=%d K=%d (M <= 2^23; N, K multiples of 8, <= 2^20)", M, N, K);
+  MOE_REQ(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, MOE_ERR_INVALID_ARG, "act=%d", act);
+  return MOE_OK;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
 }  // namespace
 
 extern "C" {
@@ -228,6 +240,111 @@ moe_status moe_rmsnorm_backward(const void* dy, int32_t dy_f32, const void* x, i
   a.dy_f32 = dy_f32 != 0;
   a.w_f32 = w_f32 != 0;
   return norm_grad(a, workspace_bytes, stream);
+}
+
+moe_status moe_linear(const void* x, const void* w, const void* bias, int32_t bias_f32,
+                      const void* residual, int32_t residual_f32, int32_t M, int32_t N, int32_t K,
+                      int32_t act, void* pre, void* out, int32_t out_f32, moe_stream_t stream) {
+  moe_status rc = check_linear(M, N, K, act);
+  if (rc != MOE_OK || M == 0) return rc;
+  MOE_REQ(x && w && out, MOE_ERR_INVALID_ARG, "x, w and out must be non-NULL");
+  MOE_REQ(aligned(x, 16) && aligned(w, 16) && aligned(bias, 16) && aligned(residual, 16) && aligned(pre, 16) &&
+              aligned(out, 16),
+          MOE_ERR_INVALID_ARG, "misaligned pointer");
+  MOE_REQ(residual != out || (residual_f32 != 0) == (out_f32 != 0), MOE_ERR_INVALID_ARG,
+          "residual may be out only when both have one type");
+  int sms = 0, *status = nullptr;
+  if ((rc = moe::api_device(&sms, &status)) != MOE_OK) return rc;
+  moe::ProductArgs a{};
+  a.a = w;
+  a.b = x;
+  a.P = N;
+  a.Q = M;
+  a.K = K;
+  a.bias = bias;
+  a.residual = residual;
+  a.pre = pre;
+  a.out = out;
+  a.act = act;
+  a.bias_f32 = bias_f32 != 0;
+  a.res_f32 = residual_f32 != 0;
+  a.out_f32 = out_f32 != 0;
+  MOE_CUDA(moe::launch_product(a, sms, status, (cudaStream_t)stream), "linear launch");
+  return MOE_OK;
+}
+
+size_t moe_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K) {
+  if (check_linear(M, N, K, MOE_ACT_NONE) != MOE_OK) return 0;
+  return up256((size_t)M * N * 2) + (size_t)moe::kActGradRows * N * sizeof(float);
+}
+
+moe_status moe_linear_backward(const void* dout, int32_t dout_f32, const void* pre, const void* x,
+                               const void* w, int32_t M, int32_t N, int32_t K, int32_t act, void* dx,
+                               void* dw, int32_t dw_f32, float* db, void* workspace,
+                               size_t workspace_bytes, moe_stream_t stream) {
+  moe_status rc = check_linear(M, N, K, act);
+  if (rc != MOE_OK) return rc;
+  MOE_REQ(dx || dw || db, MOE_ERR_INVALID_ARG, "no output: give dx, dw or db");
+  MOE_REQ(aligned(dx, 16) && aligned(dw, 16) && aligned(db, 4), MOE_ERR_INVALID_ARG, "misaligned pointer");
+  if (M > 0) {
+    MOE_REQ(dout && (x || !dw) && (w || !dx), MOE_ERR_INVALID_ARG,
+            "dout, x (with dw) and w (with dx) must be non-NULL");
+    MOE_REQ(pre || act == MOE_ACT_NONE, MOE_ERR_INVALID_ARG, "an activation needs pre");
+    MOE_REQ(aligned(dout, 16) && aligned(pre, 16) && aligned(x, 16) && aligned(w, 16), MOE_ERR_INVALID_ARG,
+            "misaligned pointer");
+    const size_t need = moe_linear_backward_workspace_size(M, N, K);
+    MOE_REQ(workspace_bytes >= need && workspace, MOE_ERR_WORKSPACE_TOO_SMALL,
+            "linear backward workspace %zu < %zu bytes", workspace_bytes, need);
+    MOE_REQ(aligned(workspace, 256), MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  }
+  int sms = 0, *status = nullptr;
+  if ((rc = moe::api_device(&sms, &status)) != MOE_OK) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (M == 0) {
+    if (dw) MOE_CUDA(cudaMemsetAsync(dw, 0, (size_t)N * K * (dw_f32 ? 4 : 2), st), "linear backward memset");
+    if (db) MOE_CUDA(cudaMemsetAsync(db, 0, (size_t)N * 4, st), "linear backward memset");
+    return MOE_OK;
+  }
+  const bool round = (act != MOE_ACT_NONE || dout_f32) && (dx || dw);
+  const void* d = round ? workspace : dout;
+  if (round || db) {
+    moe::ActGradArgs g{};
+    g.dout = dout;
+    g.pre = pre;
+    g.dpre = round ? workspace : nullptr;
+    g.db = db;
+    g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256((size_t)M * N * 2));
+    g.M = M;
+    g.N = N;
+    g.act = act;
+    g.dout_f32 = dout_f32 != 0;
+    MOE_CUDA(moe::launch_act_grad(g, sms, st), "linear backward launch (activation)");
+  }
+  if (dx) {
+    moe::ProductArgs a{};
+    a.a = w;
+    a.a_mn = true;
+    a.b = d;
+    a.P = K;
+    a.Q = M;
+    a.K = N;
+    a.out = dx;
+    MOE_CUDA(moe::launch_product(a, sms, status, st), "linear backward launch (dx)");
+  }
+  if (dw) {
+    moe::ProductArgs a{};
+    a.a = x;
+    a.a_mn = true;
+    a.b = d;
+    a.b_mn = true;
+    a.P = K;
+    a.Q = N;
+    a.K = M;
+    a.out = dw;
+    a.out_f32 = dw_f32 != 0;
+    MOE_CUDA(moe::launch_product(a, sms, status, st), "linear backward launch (dw)");
+  }
+  return MOE_OK;
 }
 
 }  // extern "C"

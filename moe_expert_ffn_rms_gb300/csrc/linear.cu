@@ -1,0 +1,513 @@
+// Dense product with bias, activation and residual in its epilogue
+// (moe_linear), and the products of its gradient (moe_linear_backward):
+//   out  = residual + act(x W^T + b)
+//   dpre = dout act'(pre),  dx = dpre W,  dW = dpre^T x,  db = sum_m dpre
+//
+// All three products are D[q, p] = sum_k a[p, k] b[q, k] with p the contiguous
+// index of the output and each operand K-major ([rows, K] in memory) or MN-major
+// ([K, rows]):
+//   forward  a = W  [N, K]         b = x [M, K]
+//   dx       a = W  stored [K, P]  b = dpre [M, N]
+//   dW       a = x  stored [K, P]  b = dpre stored [K, Q]
+// The tensor cores take both layouts from shared memory (tcgen05 descriptors), so
+// nothing is transposed.
+#include <cuda.h>
+
+#include "block_tail.cuh"
+#include "common.cuh"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
+#include "train.h"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+using namespace tc;
+
+constexpr int kTileP = 128;    // rows of a per CTA (MMA M)
+constexpr int kStepK = 64;     // K of a ring stage: 128 bytes
+constexpr int kMaxRing = 12;
+constexpr int kBoxBytes = 64 * 128;  // an MN-major box: 64 K rows of 64 elements
+constexpr int kLinThreads = 320;     // producer, MMA issuer, eight epilogue warps
+constexpr int kEpiWarps = 8;
+// fp32 results: the tensor cores' fp32 additions truncate, which over K terms leaves
+// about 1.1e-9 K of the sum's magnitude (measured: 9e-7 at K = 1024, 1.9e-5 at
+// 16384).  Sums longer than this many stages go through registers, rounded to
+// nearest, every kSegSteps stages.
+constexpr int kSegSteps = 16;
+
+// ------------------------------------------------------------- activations --
+// sigmoid(z); exp overflows to infinity for z < -88, which gives 0.
+MOE_DEV float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+// 0.5 z (1 + tanh(u)) = z sigmoid(2 u): no difference of near values.
+MOE_DEV float act_f(float z, int act) {
+  switch (act) {
+    case kActRelu: return z < 0.f ? 0.f : z;
+    case kActSilu: return z * sigmoid_f(z);
+    case kActGelu: return z * normcdff(z);
+    case kActGeluTanh: return z * sigmoid_f(2.0f * kGeluA * (z + kGeluB * z * z * z));
+    default: return z;
+  }
+}
+
+MOE_DEV float act_slope(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f ? 1.f : 0.f;
+    case kActSilu: {
+      const float p = sigmoid_f(z);
+      return p * fmaf(z, 1.0f - p, 1.0f);
+    }
+    case kActGelu: return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), normcdff(z));
+    case kActGeluTanh: {
+      const float s = sigmoid_f(2.0f * kGeluA * (z + kGeluB * z * z * z));
+      const float t = s * (1.0f - s);  // 0 where z^3 is past the exponent's range
+      return t == 0.f ? s : fmaf(z * t, 2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z), s);
+    }
+    default: return 1.f;
+  }
+}
+
+// ------------------------------------------------------------- the epilogue --
+struct Epi {
+  const void* bias;
+  const void* residual;
+  bf16* pre;
+  void* out;
+  int act;
+  int bias_f32, res_f32, out_f32;
+  int64_t P, Q;
+};
+
+// Four columns p .. p + 3 of row q.
+MOE_DEV void epilogue4(const Epi& e, int64_t q, int64_t p, float (&v)[4]) {
+  const int64_t at = q * e.P + p;
+  if (e.bias) {
+    if (e.bias_f32) {
+      const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + p);
+      v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
+    } else {
+      const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(e.bias) + p);
+      v[0] += bf16_lo(b.x); v[1] += bf16_hi(b.x); v[2] += bf16_lo(b.y); v[3] += bf16_hi(b.y);
+    }
+  }
+  if (e.pre)
+    *reinterpret_cast<uint2*>(e.pre + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+  if (e.act != kActNone) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_f(v[i], e.act);
+  }
+  if (e.residual) {
+    if (e.res_f32) {
+      const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + at);
+      v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
+    } else {
+      const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(e.residual) + at);
+      v[0] += bf16_lo(r.x); v[1] += bf16_hi(r.x); v[2] += bf16_lo(r.y); v[3] += bf16_hi(r.y);
+    }
+  }
+  if (e.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(e.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<bf16*>(e.out) + at) =
+        make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+}
+
+// ------------------------------------------------------- cluster split-K form --
+// A tile is 128 columns p x BN rows q; the CTAs of a cluster take consecutive parts
+// of K.  Each leaves its fp32 tile in its shared memory (over the ring), then
+// every CTA adds a share of the tile's elements over the cluster in rank order and
+// runs the epilogue on them: no workspace, no atomics, the same bits every time.
+struct SplitP {
+  Epi e;
+  int steps;        // stages of the whole K
+  int ring, stage_bytes;
+  int seg;          // stages added up in the tensor cores
+  int* status;
+};
+
+template <bool A_MN, bool B_MN, int BN>
+__global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
+    product_split_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                         const SplitP p) {
+  constexpr int HC = BN >= 32 ? BN / 2 : 16;           // columns of an epilogue warp
+  constexpr int ACC = BN < 32 ? 32 : BN;               // TMEM columns of a buffer
+  constexpr int TMEM = 2 * ACC < 32 ? 32 : 2 * ACC;
+  constexpr int kBBoxes = B_MN ? (BN + 63) / 64 : 1;
+  extern __shared__ unsigned char dyn[];
+  __shared__ uint64_t full[kMaxRing], empty[kMaxRing], tfull[2], tempty[2], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  unsigned char* ring = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x, S = gridDim.x;  // the cluster is the grid's x
+  const int64_t p0 = (int64_t)blockIdx.y * kTileP, q0 = (int64_t)blockIdx.z * BN;
+  const int k0 = (int)((int64_t)p.steps * rank / S), k1 = (int)((int64_t)p.steps * (rank + 1) / S);
+
+  if (warp == 0 && lane == 0) {
+    s_abort = 0;
+    for (int i = 0; i < p.ring; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], kEpiWarps);
+    }
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+    prefetch_tmap(&ta);
+    prefetch_tmap(&tb);
+  } else if (warp == 1) {
+    tmem_alloc(&s_tmem, TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();  // (not before the allocation: the next kernel's waits for this one's)
+  pdl_wait();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer --
+    int s = 0;
+    uint32_t ph = 0, armed = 0, armed_ph = 0;
+    bool ok = true;
+    for (int k = k0; k < k1; ++k) {
+      if (!(ok = mbar_wait(&empty[s], ph ^ 1, &s_abort))) break;
+      if (elect_one()) {
+        unsigned char* a = ring + (size_t)s * p.stage_bytes;
+        unsigned char* b = a + kTileP * 128;
+        mbar_arrive_expect_tx(&full[s], kTileP * 128 + (B_MN ? kBBoxes * kBoxBytes : BN * 128));
+        if (A_MN) {
+          for (int i = 0; i < 2; ++i) tma_load_2d_plain(a + i * kBoxBytes, &ta, &full[s], (int)p0 + 64 * i, k * kStepK);
+        } else {
+          tma_load_2d_plain(a, &ta, &full[s], k * kStepK, (int)p0);
+        }
+        if (B_MN) {
+          for (int i = 0; i < kBBoxes; ++i)
+            tma_load_2d_plain(b + i * kBoxBytes, &tb, &full[s], (int)q0 + 64 * i, k * kStepK);
+        } else {
+          tma_load_2d_plain(b, &tb, &full[s], k * kStepK, (int)q0);
+        }
+      }
+      __syncwarp();
+      armed |= 1u << s;
+      armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
+      if (++s == p.ring) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (ok) ok = producer_tail(empty, p.ring, s, ph, &s_abort);
+    if (!ok) {
+      if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
+      drain_armed(full, p.ring, armed, armed_ph);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer --
+    const uint32_t idesc = make_idesc_major(kTileP, BN, A_MN, B_MN);
+    int s = 0, buf = 0, n = 0;
+    uint32_t ph = 0, bph = 0;
+    bool ok = true, issued = false;
+    for (int k = k0; k < k1; ++k) {
+      if (n == 0) {
+        if (!(ok = mbar_wait(&tempty[buf], bph ^ 1, &s_abort))) break;
+        tc_fence_after();
+      }
+      if (!(ok = mbar_wait(&full[s], ph, &s_abort))) break;
+      tc_fence_after();
+      const uint32_t a = smem_u32(ring + (size_t)s * p.stage_bytes), b = a + kTileP * 128;
+      const bool last = k + 1 == k1 || n + 1 == p.seg;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t ad = A_MN ? sw128_mn_desc(a + kk * 2048, 64) : sw128_desc(a + kk * 32);
+          const uint64_t bd = B_MN ? sw128_mn_desc(b + kk * 2048, 64) : sw128_desc(b + kk * 32);
+          mma_bf16(tmem + buf * ACC, ad, bd, idesc, (n | kk) ? 1u : 0u);
+        }
+        mma_commit(&empty[s]);
+        if (last) mma_commit(&tfull[buf]);
+      }
+      __syncwarp();
+      issued = true;
+      if (++s == p.ring) {
+        s = 0;
+        ph ^= 1;
+      }
+      ++n;
+      if (last) {
+        n = 0;
+        if (++buf == 2) {
+          buf = 0;
+          bph ^= 1;
+        }
+      }
+    }
+    if (ok) ok = accumulator_tail(tempty, buf, bph, &s_abort);
+    if (!ok) {
+      if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
+      if (issued) {  // issued MMAs complete before TMEM is released
+        if (elect_one()) mma_commit(&drain);
+        __syncwarp();
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&drain, 0) && clock64() - t0 < kSpinLimitCycles) {
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue --
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const bool mine = BN >= 32 || half == 0;
+    float acc[HC];
+    int buf = 0;
+    uint32_t bph = 0;
+    bool ok = true;
+    for (int k = k0; k < k1; k += p.seg) {
+      if (!(ok = mbar_wait(&tfull[buf], bph, &s_abort))) break;
+      tc_fence_after();
+      if (mine) {
+        const uint32_t at = tmem + buf * ACC + half * HC + ((uint32_t)(quarter * 32) << 16);
+        if (k == k0) {
+          if constexpr (HC <= 16) tmem_ld16(at, acc);
+          else {
+#pragma unroll
+            for (int i = 0; i < HC; i += 32) tmem_ld32(at + i, acc + i);
+          }
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < HC; i += 16) {
+            float v[16];
+            tmem_ld16(at + i, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[i + j] += v[j];
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[buf]);
+      if (++buf == 2) {
+        buf = 0;
+        bph ^= 1;
+      }
+    }
+    if (!ok && lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
+    // (the last tfull says that every MMA has read its stage: the ring is free)
+    if (ok && mine) {
+      float* t = reinterpret_cast<float*>(ring) + (size_t)(half * HC) * kTileP + quarter * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < HC; ++i) t[i * kTileP] = acc[i];
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  {
+    const int rows = (int)(p.e.Q - q0 < BN ? p.e.Q - q0 : BN);
+    const int units = rows * (kTileP / 4);
+    const int u1 = (int)((int64_t)units * (rank + 1) / S);
+    const uint32_t base = smem_u32(ring);
+    for (int u = (int)((int64_t)units * rank / S) + threadIdx.x; u < u1; u += kLinThreads) {
+      const int64_t pc = p0 + (u & 31) * 4;
+      if (pc >= p.e.P) continue;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (uint32_t r = 0; r < S; ++r) {
+        const float4 w = cluster_ld4(cluster_addr(base + u * 16, r));
+        v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+      }
+      epilogue4(p.e, q0 + (u >> 5), pc, v);
+    }
+  }
+  cluster_sync();  // the others have read this CTA's tile
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, TMEM);
+}
+
+// --------------------------------------------------------- activation gradient --
+// A CTA takes 64 x 8 columns and a share of the rows: thread (x, y) of 64 x 4 the
+// columns 8 x .. 8 x + 7 of rows y, y + 4, ...; the column sums of the CTA go to
+// row blockIdx.y of the partial sums.
+__global__ void __launch_bounds__(256) act_grad_kernel(const ActGradArgs a, int rows_per) {
+  __shared__ float red[4][64][9];
+  pdl_trigger();
+  pdl_wait();
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  const int64_t c = ((int64_t)blockIdx.x * 64 + x) * 8;
+  const int64_t m0 = (int64_t)blockIdx.y * rows_per;
+  const int64_t m1 = m0 + rows_per < a.M ? m0 + rows_per : a.M;
+  float s[8] = {};
+  if (c < a.N) {
+#pragma unroll 4
+    for (int64_t m = m0 + y; m < m1; m += 4) {
+      float d[8];
+      load8(a.dout, a.dout_f32, (size_t)(m * a.N + c), d);
+      if (a.act != kActNone) {
+        float z[8];
+        load8(a.pre, false, (size_t)(m * a.N + c), z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] *= act_slope(z[i], a.act);
+      }
+      if (a.dpre) store8_bf16(static_cast<bf16*>(a.dpre) + m * a.N + c, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += d[i];
+    }
+  }
+  if (!a.db) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[y][x][i] = s[i];
+  __syncthreads();
+  if (y != 0 || c >= a.N) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = ((red[0][x][i] + red[1][x][i]) + red[2][x][i]) + red[3][x][i];
+  store8(a.part, true, (size_t)((int64_t)blockIdx.y * a.N + c), s);
+}
+
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part, int n, int64_t N,
+                                                         float* out) {
+  __shared__ float red[8][32];
+  pdl_trigger();
+  pdl_wait();
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + x;
+  float s = 0.f;
+  if (c < N)
+    for (int i = y; i < n; i += 8) s += part[i * N + c];
+  red[y][x] = s;
+  __syncthreads();
+  if (y != 0 || c >= N) return;
+  for (int i = 1; i < 8; ++i) s += red[i][x];
+  out[c] = s;
+}
+
+// ------------------------------------------------------------------ host --
+// Map of an operand: K-major [rows, K] in boxes of 64 K x box_rows, or MN-major
+// [K, rows] in boxes of 64 rows x 64 K.
+bool operand_map(CUtensorMap* m, const void* base, bool mn, int64_t rows, int64_t K, int box_rows) {
+  return mn ? encode_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, K, rows, 64, kStepK,
+                         CU_TENSOR_MAP_SWIZZLE_128B)
+            : encode_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, K, kStepK, box_rows,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, size_t smem, cudaStream_t st,
+                           Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+constexpr int kSmemMax = 226 * 1024 - 1024;  // dynamic; the static part and the reserve beside it
+
+template <bool A_MN, bool B_MN, int BN>
+cudaError_t launch_split(const ProductArgs& a, const Epi& e, int S, int steps, int seg, int* status,
+                         cudaStream_t st) {
+  CUtensorMap ta, tb;
+  if (!operand_map(&ta, a.a, A_MN, a.P, a.K, kTileP) || !operand_map(&tb, a.b, B_MN, a.Q, a.K, BN))
+    return cudaErrorInvalidValue;
+  SplitP p{};
+  p.e = e;
+  p.steps = steps;
+  p.seg = seg;
+  p.status = status;
+  p.stage_bytes = kTileP * 128 + (B_MN ? (BN + 63) / 64 * kBoxBytes : BN * 128);
+  const int room = (BN <= 64 ? kSmemMax / 2 - 2048 : kSmemMax) - 1024;
+  p.ring = room / p.stage_bytes < kMaxRing ? room / p.stage_bytes : kMaxRing;
+  auto kern = product_split_kernel<A_MN, B_MN, BN>;
+  cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  if (rc != cudaSuccess) return rc;
+  const dim3 grid(S, (unsigned)((a.P + kTileP - 1) / kTileP), (unsigned)((a.Q + BN - 1) / BN));
+  return launch_cluster(kern, grid, S, (size_t)p.ring * p.stage_bytes + 1024, st, ta, tb, p);
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t launch_split_bn(int bn, const ProductArgs& a, const Epi& e, int S, int steps, int seg, int* status,
+                            cudaStream_t st) {
+  if constexpr (!B_MN) {
+    if (bn == 16) return launch_split<A_MN, B_MN, 16>(a, e, S, steps, seg, status, st);
+    if (bn == 32) return launch_split<A_MN, B_MN, 32>(a, e, S, steps, seg, status, st);
+  }
+  if (bn <= 64) return launch_split<A_MN, B_MN, 64>(a, e, S, steps, seg, status, st);
+  if (bn == 128) return launch_split<A_MN, B_MN, 128>(a, e, S, steps, seg, status, st);
+  return launch_split<A_MN, B_MN, 256>(a, e, S, steps, seg, status, st);
+}
+
+}  // namespace
+
+cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStream_t st) {
+  Epi e{};
+  e.bias = a.bias;
+  e.residual = a.residual;
+  e.pre = static_cast<bf16*>(a.pre);
+  e.out = a.out;
+  e.act = a.act;
+  e.bias_f32 = a.bias_f32;
+  e.res_f32 = a.res_f32;
+  e.out_f32 = a.out_f32;
+  e.P = a.P;
+  e.Q = a.Q;
+  const int steps = (int)((a.K + kStepK - 1) / kStepK);
+  const int seg = a.out_f32 ? kSegSteps : 1 << 30;
+  int bn = 16;
+  while (bn < a.Q && bn < 256) bn *= 2;
+  // The split with the least time in units of stages: waves of CTAs times the
+  // stages of a part and about six more for its start and end.
+  const int64_t tiles = ((a.P + kTileP - 1) / kTileP) * ((a.Q + bn - 1) / bn);
+  const int slots = bn <= 64 ? 2 * sms : sms;
+  int S = 1;
+  int64_t best = 0;
+  for (int s = 1; s <= 8 && s <= steps; ++s) {
+    const int64_t cost = (tiles * s + slots - 1) / slots * ((steps + s - 1) / s + 6);
+    if (s == 1 || cost < best) {
+      best = cost;
+      S = s;
+    }
+  }
+  if (a.a_mn && a.b_mn) return launch_split_bn<true, true>(bn, a, e, S, steps, seg, status, st);
+  if (a.a_mn) return launch_split_bn<true, false>(bn, a, e, S, steps, seg, status, st);
+  return launch_split_bn<false, false>(bn, a, e, S, steps, seg, status, st);
+}
+
+cudaError_t launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t st) {
+  // row shares so that the grid fills the SMs a few times over
+  const int64_t strips = (a.N + 511) / 512;
+  int64_t shares = (8 * sms + strips - 1) / strips;
+  if (shares > (a.M + 15) / 16) shares = (a.M + 15) / 16;
+  if (shares > kActGradRows) shares = kActGradRows;
+  if (shares < 1) shares = 1;
+  const int rows_per = (int)((a.M + shares - 1) / shares);
+  if (a.M > 0) shares = (a.M + rows_per - 1) / rows_per;
+  else shares = 0;
+  if (shares > 0) {
+    cudaError_t e = launch_kernel(act_grad_kernel, dim3((unsigned)strips, (unsigned)shares), dim3(256), 0, st, a,
+                                  rows_per);
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.db) return cudaSuccess;
+  return launch_kernel(column_sum_kernel, dim3((unsigned)((a.N + 31) / 32)), dim3(256), 0, st,
+                       (const float*)a.part, (int)shares, a.N, a.db);
+}
+
+}  // namespace moe

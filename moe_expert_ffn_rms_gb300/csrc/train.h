@@ -72,4 +72,39 @@ struct NormGradArgs {
 size_t norm_grad_workspace_bytes(int T, int H);
 cudaError_t launch_norm_grad(const NormGradArgs& a, int sms, int* status, cudaStream_t st);
 
+// ---------------------------------------------------------------- linear.cu --
+enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+// One product D[q, p] = sum_k a[p, k] b[q, k] with p the contiguous index of the
+// output, and its epilogue out = residual + act(D + bias).  a_mn: a is stored [K, P]
+// instead of [P, K]; b_mn likewise.
+struct ProductArgs {
+  const void* a;
+  const void* b;
+  bool a_mn, b_mn;
+  int64_t P, Q, K;
+  const void* bias;      // [P] or NULL
+  const void* residual;  // [Q, P] or NULL
+  void* pre;             // bf16 [Q, P] or NULL: D + bias
+  void* out;             // [Q, P]
+  int act;
+  bool bias_f32, res_f32, out_f32;
+};
+cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStream_t st);
+
+// dpre = dout * act'(pre) in bf16 (or NULL: not stored) and db = its column sums, before the
+// rounding (or NULL).
+constexpr int kActGradRows = 256;  // partial sums per column at most
+struct ActGradArgs {
+  const void* dout;
+  const void* pre;  // bf16, NULL without activation
+  void* dpre;
+  float* db;
+  float* part;      // [kActGradRows, N]
+  int64_t M, N;
+  int act;
+  bool dout_f32;
+};
+cudaError_t launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t st);
+
 }  // namespace moe

@@ -100,3 +100,40 @@ def test_binding_refuses_host_tensors_and_wrong_types(M):
                  lambda: M.moe_rmsnorm_backward(x, x, w, 1e-6, x, f, y.view(torch.uint8))):
         with pytest.raises(ValueError):
             call()
+
+
+LINEAR = [(dict(M=-1), 2), (dict(M=(1 << 23) + 1), 2), (dict(N=0), 2), (dict(N=100), 2), (dict(K=0), 2),
+          (dict(K=60), 2), (dict(K=(1 << 20) + 8), 2), (dict(act=-1), 1), (dict(act=5), 1), (dict(x=None), 1),
+          (dict(w=None), 1), (dict(x=FAKE + 8), 1), (dict(w=FAKE + 8), 1), (dict(pre=FAKE + 8), 1)]
+
+
+@pytest.mark.parametrize("kw,code", LINEAR + [
+    (dict(out=None), 1), (dict(out=FAKE + 8), 1), (dict(bias=FAKE + 8), 1), (dict(res=FAKE + 8), 1),
+    (dict(res=FAKE, res_f32=1), 1)])
+def test_linear(M, kw, code):
+    args = dict(x=FAKE, w=FAKE, bias=FAKE, bias_f32=0, res=FAKE, res_f32=0, M=4, N=256, K=128, act=2, pre=FAKE + 4096,
+                out=FAKE, out_f32=0, st=None)
+    refused(M, "moe_linear", args, kw, code)
+
+
+@pytest.mark.parametrize("kw,code", LINEAR + [
+    (dict(dout=None), 1), (dict(pre=None), 1), (dict(dx=None, dw=None, db=None), 1), (dict(dx=FAKE + 8), 1),
+    (dict(dw=FAKE + 8), 1), (dict(db=FAKE + 2), 1), (dict(dout=FAKE + 8), 1), (dict(ws=None), 4),
+    (dict(ws=FAKE + 16), 1), (dict(wsb=1000), 4)])
+def test_linear_backward(M, kw, code):
+    args = dict(dout=FAKE, dout_f32=0, pre=FAKE, x=FAKE, w=FAKE, M=4, N=256, K=128, act=2, dx=FAKE, dw=FAKE, dw_f32=0,
+                db=FAKE, ws=FAKE, wsb=1 << 30, st=None)
+    refused(M, "moe_linear_backward", args, kw, code)
+
+
+def test_linear_workspace_size_and_binding(M):
+    assert M.moe_linear_backward_workspace_size(0, 8, 8) > 0
+    assert M.moe_linear_backward_workspace_size(100, 256, 8) >= 100 * 256 * 2
+    for m, n, k in ((-1, 8, 8), (1, 4, 8), (1, 8, 4)):
+        with pytest.raises(M.MoeError):
+            M.moe_linear_backward_workspace_size(m, n, k)
+    x, w = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((8, 64), dtype=torch.bfloat16)
+    for call in (lambda: M.moe_linear(x, w, torch.zeros((4, 8))),
+                 lambda: M.moe_linear_backward(torch.zeros((4, 8)), x, w, w.view(torch.uint8), dx=x)):
+        with pytest.raises(ValueError):
+            call()
