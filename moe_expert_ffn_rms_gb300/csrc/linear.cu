@@ -12,6 +12,7 @@
 // The tensor cores take both layouts from shared memory (tcgen05 descriptors), so
 // nothing is transposed.
 #include <cuda.h>
+#include <stdlib.h>
 
 #include "block_tail.cuh"
 #include "common.cuh"
@@ -330,6 +331,306 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
   if (warp == 1) tmem_dealloc(tmem, TMEM);
 }
 
+// -------------------------------------------------------------- CTA-pair form --
+// Persistent pairs of CTAs (cluster of two), a tile of 256 rows q x BN columns p
+// at a time: each CTA of a pair loads its 128 rows and half of the columns, and the
+// MMAs of the pair, issued by its first CTA, take both halves (tcgen05
+// cta_group::2): 32 KB per 128 x 256 x 64 products of a CTA instead of the 48 KB of
+// a single one.  Two accumulators in TMEM, so that the eight epilogue warps of a
+// tile run under the products of the next.
+struct PairP {
+  Epi e;
+  int steps, ring, stage_bytes;
+  int bn;           // columns of a tile: 128, 192 or 256
+  int tq, tp;       // tiles along q and p
+  int group;        // row tiles of a raster group
+  int seg;          // KEEP: stages added up in the tensor cores
+  int* status;
+};
+
+// Tiles in groups of `group` row tiles, rows fastest within a group: the tiles in
+// flight share their operands in L2.
+MOE_DEV void pair_tile(const PairP& p, int t, int& q, int& c) {
+  const int per = p.group * p.tp, g = t / per, r = t - g * per;
+  const int rows = min(p.group, p.tq - g * p.group);
+  c = r / rows;
+  q = g * p.group + (r - c * rows);
+}
+
+// Sixteen columns p .. p + 15 of row q from registers (the first of them below P,
+// P a multiple of 8).
+MOE_DEV void epilogue16(const Epi& e, int64_t q, int64_t p, float* v) {
+  const bool two = p + 8 < e.P;
+  const int64_t at = q * e.P + p;
+  if (e.bias) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 0 || two) {
+        float b[8];
+        load8(e.bias, e.bias_f32, p + 8 * h, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] += b[i];
+      }
+    }
+  }
+  auto store = [&](void* base, bool f32) {
+    if (f32) {
+      store8(base, true, at, reinterpret_cast<float(&)[8]>(v[0]));
+      if (two) store8(base, true, at + 8, reinterpret_cast<float(&)[8]>(v[8]));
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
+      bf16* d = static_cast<bf16*>(base) + at;
+      if (two && ((uintptr_t)d & 31u) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+      } else {
+        reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (two) reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  };
+  if (e.pre) store(e.pre, false);
+  if (e.act != kActNone) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_f(v[i], e.act);
+  }
+  if (e.residual) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 0 || two) {
+        float r[8];
+        load8(e.residual, e.res_f32, at + 8 * h, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] += r[i];
+      }
+    }
+  }
+  store(e.out, e.out_f32);
+}
+
+template <bool A_MN, bool B_MN, bool KEEP>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    product_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                        const PairP p) {
+  extern __shared__ unsigned char dyn[];
+  __shared__ uint64_t full[kMaxRing], empty[kMaxRing], tfull[2], tempty[2], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  unsigned char* ring = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int half_n = p.bn >> 1, tiles = p.tq * p.tp;
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+  if (warp == 0 && lane == 0) {
+    s_abort = 0;
+    for (int i = 0; i < p.ring; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * kEpiWarps);
+    }
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+    prefetch_tmap(&ta);
+    prefetch_tmap(&tb);
+  } else if (warp == 1) {
+    tmem_alloc_pair(&s_tmem, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer --
+    // Both CTAs' copies of a stage count on the first CTA's barrier.
+    const int b_boxes = B_MN ? (half_n + 63) >> 6 : 1;
+    const uint32_t bytes = 2 * (kTileP * 128 + (B_MN ? b_boxes * kBoxBytes : half_n * 128));
+    int s = 0;
+    uint32_t ph = 0, armed = 0, armed_ph = 0;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += stride) {
+      int tq, tp;
+      pair_tile(p, t, tq, tp);
+      const int a0 = tq * 256 + (int)rank * 128, b0 = tp * p.bn + (int)rank * half_n;
+      for (int k = 0; k < p.steps; ++k) {
+        if (!(ok = mbar_wait(&empty[s], ph ^ 1, &s_abort))) break;
+        if (elect_one()) {
+          unsigned char* a = ring + (size_t)s * p.stage_bytes;
+          unsigned char* b = a + kTileP * 128;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          const uint32_t bar = cluster_addr(smem_u32(&full[s]), 0);
+          if (A_MN) {
+            for (int i = 0; i < 2; ++i) tma_load_2d_pair(a + i * kBoxBytes, &ta, bar, a0 + 64 * i, k * kStepK);
+          } else {
+            tma_load_2d_pair(a, &ta, bar, k * kStepK, a0);
+          }
+          if (B_MN) {
+            for (int i = 0; i < b_boxes; ++i) tma_load_2d_pair(b + i * kBoxBytes, &tb, bar, b0 + 64 * i, k * kStepK);
+          } else {
+            tma_load_2d_pair(b, &tb, bar, k * kStepK, b0);
+          }
+        }
+        __syncwarp();
+        armed |= 1u << s;
+        armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
+        if (++s == p.ring) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (ok) ok = producer_tail(empty, p.ring, s, ph, &s_abort);
+    if (!ok) {
+      if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
+      if (rank == 0) drain_armed(full, p.ring, armed, armed_ph);
+      // copies of the pair's other CTA that no barrier of this one was armed for
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1 << 21)) {
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer --
+    if (rank == 0) {
+      const uint32_t idesc = make_idesc_major(256, p.bn, A_MN, B_MN);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, bph = 0;
+      bool ok = true, issued = false;
+      for (int t = first; ok && t < tiles; t += stride) {
+        int n = 0;
+        for (int k = 0; k < p.steps; ++k) {
+          if (n == 0) {
+            if (!(ok = mbar_wait(&tempty[buf], bph ^ 1, &s_abort))) break;
+            tc_fence_after();
+          }
+          if (!(ok = mbar_wait(&full[s], ph, &s_abort))) break;
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring + (size_t)s * p.stage_bytes), b = a + kTileP * 128;
+          const bool last = k + 1 == p.steps || (KEEP && n + 1 == p.seg);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ad = A_MN ? sw128_mn_desc(a + kk * 2048, 64) : sw128_desc(a + kk * 32);
+              const uint64_t bd = B_MN ? sw128_mn_desc(b + kk * 2048, 64) : sw128_desc(b + kk * 32);
+              mma_bf16_pair(tmem + buf * 256, ad, bd, idesc, (n | kk) ? 1u : 0u);
+            }
+            mma_commit_pair(&empty[s]);
+            if (last) mma_commit_pair(&tfull[buf]);
+          }
+          __syncwarp();
+          issued = true;
+          if (++s == p.ring) {
+            s = 0;
+            ph ^= 1;
+          }
+          ++n;
+          if (last) {
+            n = 0;
+            if (++buf == 2) {
+              buf = 0;
+              bph ^= 1;
+            }
+          }
+        }
+      }
+      if (ok) ok = accumulator_tail(tempty, buf, bph, &s_abort);
+      if (!ok) {
+        if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
+        if (issued) {
+          if (elect_one()) mma_commit_pair(&drain);
+          __syncwarp();
+          const long long t0 = clock64();
+          while (!mbar_try_wait(&drain, 0) && clock64() - t0 < kSpinLimitCycles) {
+          }
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue --
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lead0 = cluster_addr(smem_u32(&tempty[0]), 0), lead1 = cluster_addr(smem_u32(&tempty[1]), 0);
+    int buf = 0;
+    uint32_t bph = 0;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += stride) {
+      int tq, tp;
+      pair_tile(p, t, tq, tp);
+      const int64_t q = (int64_t)tq * 256 + rank * 128 + quarter * 32 + lane;
+      const int64_t c0 = (int64_t)tp * p.bn + half * half_n;
+      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+      if constexpr (KEEP) {
+        float acc[128];
+        for (int k = 0; k < p.steps; k += p.seg) {
+          if (!(ok = mbar_wait(&tfull[buf], bph, &s_abort))) break;
+          tc_fence_after();
+          const uint32_t at = tmem + buf * 256 + half * half_n + lanes;
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            if (c < half_n) {
+              float v[16];
+              tmem_ld16(at + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[c + i] = k == 0 ? v[i] : acc[c + i] + v[i];
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cluster_mbar_arrive(buf ? lead1 : lead0);
+          if (++buf == 2) {
+            buf = 0;
+            bph ^= 1;
+          }
+        }
+        if (ok && q < p.e.Q) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 16)
+            if (c < half_n && c0 + c < p.e.P) epilogue16(p.e, q, c0 + c, acc + c);
+        }
+      } else {
+        if (!(ok = mbar_wait(&tfull[buf], bph, &s_abort))) break;
+        tc_fence_after();
+        const uint32_t at = tmem + buf * 256 + half * half_n + lanes;
+        for (int c = 0; c < half_n; c += 32) {
+          float v[32];
+          tmem_ld32(at + c, v);
+          tmem_ld_wait();
+          if (c + 32 >= half_n) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) cluster_mbar_arrive(buf ? lead1 : lead0);
+          }
+          if (q < p.e.Q) {
+            if (c0 + c < p.e.P) epilogue16(p.e, q, c0 + c, v);
+            if (c0 + c + 16 < p.e.P) epilogue16(p.e, q, c0 + c + 16, v + 16);
+          }
+        }
+        if (++buf == 2) {
+          buf = 0;
+          bph ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no copy, product or arrival of the pair is left
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
 // --------------------------------------------------------- activation gradient --
 // A CTA takes 64 x 8 columns and a share of the rows: thread (x, y) of 64 x 4 the
 // columns 8 x .. 8 x + 7 of rows y, y + 4, ...; the column sums of the CTA go to
@@ -454,6 +755,32 @@ cudaError_t launch_split_bn(int bn, const ProductArgs& a, const Epi& e, int S, i
   return launch_split<A_MN, B_MN, 256>(a, e, S, steps, seg, status, st);
 }
 
+template <bool A_MN, bool B_MN, bool KEEP>
+cudaError_t launch_pair(const ProductArgs& a, const Epi& e, int bn, int steps, int sms, int* status,
+                        cudaStream_t st) {
+  CUtensorMap ta, tb;  // the pair's rows are q (b of the product), its columns p (a)
+  if (!operand_map(&ta, a.b, A_MN, a.Q, a.K, kTileP) || !operand_map(&tb, a.a, B_MN, a.P, a.K, bn / 2))
+    return cudaErrorInvalidValue;
+  PairP p{};
+  p.e = e;
+  p.steps = steps;
+  p.bn = bn;
+  p.tq = (int)((a.Q + 255) / 256);
+  p.tp = (int)((a.P + bn - 1) / bn);
+  p.group = 8;
+  p.seg = kSegSteps;
+  p.status = status;
+  p.stage_bytes = kTileP * 128 + (B_MN ? (bn / 2 + 63) / 64 * kBoxBytes : bn / 2 * 128);
+  const int room = kSmemMax - 1024;
+  p.ring = room / p.stage_bytes < kMaxRing ? room / p.stage_bytes : kMaxRing;
+  auto kern = product_pair_kernel<A_MN, B_MN, KEEP>;
+  cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  if (rc != cudaSuccess) return rc;
+  const int64_t tiles = (int64_t)p.tq * p.tp;
+  const int pairs = tiles < sms / 2 ? (int)tiles : sms / 2;
+  return launch_cluster(kern, dim3(2 * pairs), 2, (size_t)p.ring * p.stage_bytes + 1024, st, ta, tb, p);
+}
+
 }  // namespace
 
 cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStream_t st) {
@@ -484,6 +811,29 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
       best = cost;
       S = s;
     }
+  }
+  // Pairs: waves of 256 x bn tiles, in the same units (a stage of 128 x 256 per SM).
+  int pair_bn = 0;
+  double pair_best = 0;
+  for (int b = 256; b >= 128; b -= 64) {
+    const int64_t t = (a.Q + 255) / 256 * ((a.P + b - 1) / b);
+    const int pairs = sms / 2;
+    const double c = (double)((t + pairs - 1) / pairs) * steps * (b + 16) / 256;
+    if (!pair_bn || c < pair_best) {
+      pair_best = c;
+      pair_bn = b;
+    }
+  }
+  const char* env = getenv("MOE_LINEAR_FORM");
+  const bool pair = env && *env ? env[0] == 'p' : pair_best + 8 < (bn <= 64 ? 0.5 : bn == 128 ? 0.6 : 1.2) * best;
+  if (pair) {
+    const bool keep = a.out_f32 && steps > kSegSteps;
+    if (a.a_mn && a.b_mn)
+      return keep ? launch_pair<true, true, true>(a, e, pair_bn, steps, sms, status, st)
+                  : launch_pair<true, true, false>(a, e, pair_bn, steps, sms, status, st);
+    if (a.a_mn) return launch_pair<false, true, false>(a, e, pair_bn, steps, sms, status, st);
+    return keep ? launch_pair<false, false, true>(a, e, pair_bn, steps, sms, status, st)
+                : launch_pair<false, false, false>(a, e, pair_bn, steps, sms, status, st);
   }
   if (a.a_mn && a.b_mn) return launch_split_bn<true, true>(bn, a, e, S, steps, seg, status, st);
   if (a.a_mn) return launch_split_bn<true, false>(bn, a, e, S, steps, seg, status, st);

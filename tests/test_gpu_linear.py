@@ -32,6 +32,14 @@ def M():
     return M
 
 
+@pytest.fixture(params=["auto", "pair", "split"])
+def form(request, monkeypatch):
+    """The launcher's own choice, and both kernels everywhere."""
+    if request.param != "auto":
+        monkeypatch.setenv("MOE_LINEAR_FORM", request.param)
+    return request.param
+
+
 def step(t, v):
     return v * (torch.finfo(t).eps / 2)
 
@@ -101,7 +109,7 @@ SHAPES = [(1, 8, 8), (1, 128, 64), (1, 4096, 4096), (2, 136, 200), (3, 256, 1000
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
-def test_forward_shapes(M, m, n, k):
+def test_forward_shapes(M, m, n, k, form):
     forward(M, m, n, k)
     forward(M, m, n, k, act="SILU", bias=BF, res=F32, out=F32)
     forward(M, m, n, k, bias=F32, res=BF, out=BF, inplace=True)
@@ -109,7 +117,7 @@ def test_forward_shapes(M, m, n, k):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("m,n,k", [(5, 264, 136), (300, 1032, 520), (2100, 2312, 200)])
-def test_forward_epilogues(M, m, n, k, act):
+def test_forward_epilogues(M, m, n, k, act, form):
     for bias in (None, BF, F32):
         for res in (None, BF, F32):
             for out in (BF, F32):
@@ -118,7 +126,7 @@ def test_forward_epilogues(M, m, n, k, act):
 
 
 @pytest.mark.parametrize("m", [1, 300, 1100])
-def test_long_sums_keep_fp32(M, m):
+def test_long_sums_keep_fp32(M, m, form):
     """fp32 outputs of long sums: against 64 bits, relative to the whole output."""
     n, k = 512, 16384
     rn = gen(m)
@@ -173,7 +181,7 @@ def backward(M, m, n, k, act="NONE", dout=BF, dw=BF, which="dx dw db", seed=0):
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
-def test_backward_shapes(M, m, n, k):
+def test_backward_shapes(M, m, n, k, form):
     backward(M, m, n, k, dw=F32)
     backward(M, m, n, k, act="GELU_TANH")
     one = backward(M, m, n, k, dout=F32, dw=F32)
@@ -184,7 +192,7 @@ def test_backward_shapes(M, m, n, k):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("m,n,k", [(40, 264, 136), (700, 1032, 520), (4096, 256, 256)])
-def test_backward_activations(M, m, n, k, act):
+def test_backward_activations(M, m, n, k, act, form):
     for dout in (BF, F32):
         for dw in (BF, F32):
             backward(M, m, n, k, act=act, dout=dout, dw=dw)
@@ -218,7 +226,7 @@ def test_backward_against_differences(M, act):
     assert abs(num - sum(p.sum() for p in parts)) <= tol
 
 
-def test_special_values_stay_where_they_belong(M):
+def test_special_values_stay_where_they_belong(M, form):
     """A NaN or an infinity in a row of x (a column of the output's transpose) reaches that row alone, values outside
     the matrices never count, and each activation keeps its limits."""
     m, n, k = 70, 200, 72
@@ -258,7 +266,7 @@ def test_special_values_stay_where_they_belong(M):
         assert ok[z.abs() >= 20].all(), (act, db)
 
 
-def test_streams_graphs_shared_workspace_and_empty_batches(M):
+def test_streams_graphs_shared_workspace_and_empty_batches(M, form):
     m, n, k = 130, 1032, 520
     rn = gen(4)
     x, w, b, d = rn(m, k), rn(n, k, std=0.05), rn(n), rn(m, n)
