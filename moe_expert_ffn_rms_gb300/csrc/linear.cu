@@ -56,6 +56,23 @@ MOE_DEV float act_f(float z, int act) {
   }
 }
 
+// The choice once for N values.
+template <int N>
+MOE_DEV void act_all(float* v, int act) {
+#define MOE_ACT(A)                                       \
+  case A:                                                \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = act_f(v[i], A); \
+    break;
+  switch (act) {
+    MOE_ACT(kActRelu)
+    MOE_ACT(kActSilu)
+    MOE_ACT(kActGelu)
+    MOE_ACT(kActGeluTanh)
+    default: break;
+  }
+#undef MOE_ACT
+}
+
 MOE_DEV float act_slope(float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
@@ -98,10 +115,7 @@ MOE_DEV void epilogue4(const Epi& e, int64_t q, int64_t p, float (&v)[4]) {
   }
   if (e.pre)
     *reinterpret_cast<uint2*>(e.pre + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
-  if (e.act != kActNone) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_f(v[i], e.act);
-  }
+  act_all<4>(v, e.act);
   if (e.residual) {
     if (e.res_f32) {
       const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + at);
@@ -341,31 +355,68 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
 struct PairP {
   Epi e;
   int steps, ring, stage_bytes;
-  int bn;           // columns of a tile: 128, 192 or 256
-  int tq, tp;       // tiles along q and p
+  int tq, tp;       // tiles of 256 x 256 along q and p
+  int whole;        // tiles taken whole; those after them in two halves of 128 columns
   int group;        // row tiles of a raster group
   int seg;          // KEEP: stages added up in the tensor cores
   int* status;
 };
 
-// Tiles in groups of `group` row tiles, rows fastest within a group: the tiles in
-// flight share their operands in L2.
-MOE_DEV void pair_tile(const PairP& p, int t, int& q, int& c) {
+// Unit u: rows q .. q + 255, columns c .. c + 2 half - 1.  Tiles in groups of `group`
+// row tiles, rows fastest within a group: the tiles in flight share their operands in
+// L2.  A tile with no more than 128 columns left in the matrix has them alone; the
+// second half of such a tile is no work (half 0).
+MOE_DEV void pair_unit(const PairP& p, int u, int& q, int& c, int& half) {
+  const bool split = u >= p.whole;
+  const int t = split ? p.whole + ((u - p.whole) >> 1) : u;
   const int per = p.group * p.tp, g = t / per, r = t - g * per;
   const int rows = min(p.group, p.tq - g * p.group);
   c = r / rows;
-  q = g * p.group + (r - c * rows);
+  q = (g * p.group + (r - c * rows)) * 256;
+  c *= 256;
+  half = 128;
+  if (split || p.e.P - c <= 128) half = 64;
+  if (split && ((u - p.whole) & 1)) {
+    c += 128;
+    if (c >= p.e.P) half = 0;
+  }
 }
 
-// Sixteen columns p .. p + 15 of row q from registers (the first of them below P,
-// P a multiple of 8).
-MOE_DEV void epilogue16(const Epi& e, int64_t q, int64_t p, float* v) {
-  const bool two = p + 8 < e.P;
-  const int64_t at = q * e.P + p;
+// A warp's 32 rows x 128 bytes on their way out: each lane writes its row's words in
+// 16-byte chunks at the places of the 128-byte swizzle, and one lane hands them
+// to a TMA store, which writes whole lines and drops what lies outside the matrix.
+// (Straight from registers, 32 bytes of 32 rows at a time: 38.6 us instead of 29.7
+// at 4096 x 12288 x 64.)
+constexpr int kStoreBytes = 32 * 128;
+
+MOE_DEV void store_box(unsigned char* stage, int lane, const uint32_t (&w)[32], const CUtensorMap* map, int x,
+                       int y) {
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, stage, x, y);
+    bulk_commit();
+  }
+}
+
+// Columns p .. p + N - 1 (N = 64 for bf16 outputs, 32 for fp32) of the warp's 32 rows,
+// one row per lane (q: this lane's, q0: the first); the first column is below P, a
+// multiple of 8.  Rows from Q on hold values of no row and are dropped.
+template <bool F32>
+MOE_DEV void epilogue_box(const Epi& e, int64_t q, int64_t q0, int64_t p, float* v, unsigned char* stage, int lane,
+                          const CUtensorMap* tout, const CUtensorMap* tpre) {
+  constexpr int N = F32 ? 32 : 64;
+  const int groups = (int)min((int64_t)(N / 8), (e.P - p) >> 3);
   if (e.bias) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 0 || two) {
+    for (int h = 0; h < N / 8; ++h) {
+      if (h < groups) {
         float b[8];
         load8(e.bias, e.bias_f32, p + 8 * h, b);
 #pragma unroll
@@ -373,47 +424,41 @@ MOE_DEV void epilogue16(const Epi& e, int64_t q, int64_t p, float* v) {
       }
     }
   }
-  auto store = [&](void* base, bool f32) {
-    if (f32) {
-      store8(base, true, at, reinterpret_cast<float(&)[8]>(v[0]));
-      if (two) store8(base, true, at + 8, reinterpret_cast<float(&)[8]>(v[8]));
-    } else {
-      uint32_t w[8];
+  uint32_t w[32];
+  if (e.pre) {
+    if constexpr (F32) {  // half a box of bf16: straight out
+      if (q < e.Q) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
-      bf16* d = static_cast<bf16*>(base) + at;
-      if (two && ((uintptr_t)d & 31u) == 0) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(w[0]), "r"(w[1]),
-                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-      } else {
-        reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (two) reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int h = 0; h < N / 8; ++h)
+          if (h < groups) store8_bf16(e.pre + q * e.P + p + 8 * h, reinterpret_cast<float(&)[8]>(v[8 * h]));
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
+      store_box(stage, lane, w, tpre, (int)p, (int)q0);
     }
-  };
-  if (e.pre) store(e.pre, false);
-  if (e.act != kActNone) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = act_f(v[i], e.act);
   }
-  if (e.residual) {
+  act_all<N>(v, e.act);
+  if (e.residual && q < e.Q) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 0 || two) {
+    for (int h = 0; h < N / 8; ++h) {
+      if (h < groups) {
         float r[8];
-        load8(e.residual, e.res_f32, at + 8 * h, r);
+        load8(e.residual, e.res_f32, q * e.P + p + 8 * h, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[8 * h + i] += r[i];
       }
     }
   }
-  store(e.out, e.out_f32);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) w[i] = F32 ? __float_as_uint(v[i]) : pack2_bf16(v[2 * i], v[2 * i + 1]);
+  store_box(stage, lane, w, tout, (int)p, (int)q0);
 }
 
-template <bool A_MN, bool B_MN, bool KEEP>
+template <bool A_MN, bool B_MN, bool F32, bool KEEP>
 __global__ void __launch_bounds__(kLinThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                        const __grid_constant__ CUtensorMap tout, const __grid_constant__ CUtensorMap tpre,
                         const PairP p) {
   extern __shared__ unsigned char dyn[];
   __shared__ uint64_t full[kMaxRing], empty[kMaxRing], tfull[2], tempty[2], drain;
@@ -422,7 +467,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   unsigned char* ring = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int half_n = p.bn >> 1, tiles = p.tq * p.tp;
+  const int units = 2 * p.tq * p.tp - p.whole;
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
   if (warp == 0 && lane == 0) {
@@ -454,15 +499,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (warp == 0) {
     // -------------------------------------------------------------- producer --
     // Both CTAs' copies of a stage count on the first CTA's barrier.
-    const int b_boxes = B_MN ? (half_n + 63) >> 6 : 1;
-    const uint32_t bytes = 2 * (kTileP * 128 + (B_MN ? b_boxes * kBoxBytes : half_n * 128));
     int s = 0;
     uint32_t ph = 0, armed = 0, armed_ph = 0;
     bool ok = true;
-    for (int t = first; ok && t < tiles; t += stride) {
-      int tq, tp;
-      pair_tile(p, t, tq, tp);
-      const int a0 = tq * 256 + (int)rank * 128, b0 = tp * p.bn + (int)rank * half_n;
+    for (int u = first; ok && u < units; u += stride) {
+      int a0, b0, half;
+      pair_unit(p, u, a0, b0, half);
+      if (half == 0) continue;
+      a0 += (int)rank * 128;
+      b0 += (int)rank * half;
+      const uint32_t bytes = 2 * (kTileP * 128 + half * 128);
       for (int k = 0; k < p.steps; ++k) {
         if (!(ok = mbar_wait(&empty[s], ph ^ 1, &s_abort))) break;
         if (elect_one()) {
@@ -475,10 +521,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           } else {
             tma_load_2d_pair(a, &ta, bar, k * kStepK, a0);
           }
-          if (B_MN) {
-            for (int i = 0; i < b_boxes; ++i) tma_load_2d_pair(b + i * kBoxBytes, &tb, bar, b0 + 64 * i, k * kStepK);
-          } else {
-            tma_load_2d_pair(b, &tb, bar, k * kStepK, b0);
+          for (int i = 0; i < half; i += 64) {
+            if (B_MN) tma_load_2d_pair(b + i * 128, &tb, bar, b0 + i, k * kStepK);
+            else tma_load_2d_pair(b + i * 128, &tb, bar, k * kStepK, b0 + i);
           }
         }
         __syncwarp();
@@ -502,12 +547,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer --
     if (rank == 0) {
-      const uint32_t idesc = make_idesc_major(256, p.bn, A_MN, B_MN);
       int s = 0, buf = 0;
       uint32_t ph = 0, bph = 0;
       bool ok = true, issued = false;
-      for (int t = first; ok && t < tiles; t += stride) {
-        int n = 0;
+      for (int u = first; ok && u < units; u += stride) {
+        int q, c, half, n = 0;
+        pair_unit(p, u, q, c, half);
+        if (half == 0) continue;
+        const uint32_t idesc = make_idesc_major(256, 2 * half, A_MN, B_MN);
         for (int k = 0; k < p.steps; ++k) {
           if (n == 0) {
             if (!(ok = mbar_wait(&tempty[buf], bph ^ 1, &s_abort))) break;
@@ -557,31 +604,35 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue --
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    constexpr int N = F32 ? 32 : 64;  // columns of a store
+    const int quarter = warp & 3, side = (warp - 2) >> 2;
+    unsigned char* stage = ring + (size_t)p.ring * p.stage_bytes + (warp - 2) * kStoreBytes;
     const uint32_t lead0 = cluster_addr(smem_u32(&tempty[0]), 0), lead1 = cluster_addr(smem_u32(&tempty[1]), 0);
     int buf = 0;
     uint32_t bph = 0;
     bool ok = true;
-    for (int t = first; ok && t < tiles; t += stride) {
-      int tq, tp;
-      pair_tile(p, t, tq, tp);
-      const int64_t q = (int64_t)tq * 256 + rank * 128 + quarter * 32 + lane;
-      const int64_t c0 = (int64_t)tp * p.bn + half * half_n;
-      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    for (int u = first; ok && u < units; u += stride) {
+      int q, c, half;
+      pair_unit(p, u, q, c, half);
+      if (half == 0) continue;
+      const int64_t q0 = (int64_t)q + rank * 128 + quarter * 32;
+      const int64_t c0 = (int64_t)c + side * half;
+      const uint32_t col = side * half + ((uint32_t)(quarter * 32) << 16);
+      const bool rows = q0 < p.e.Q;
       if constexpr (KEEP) {
         float acc[128];
         for (int k = 0; k < p.steps; k += p.seg) {
           if (!(ok = mbar_wait(&tfull[buf], bph, &s_abort))) break;
           tc_fence_after();
-          const uint32_t at = tmem + buf * 256 + half * half_n + lanes;
+          const uint32_t at = tmem + buf * 256 + col;
 #pragma unroll
-          for (int c = 0; c < 128; c += 16) {
-            if (c < half_n) {
+          for (int i = 0; i < 128; i += 16) {
+            if (i < half) {
               float v[16];
-              tmem_ld16(at + c, v);
+              tmem_ld16(at + i, v);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) acc[c + i] = k == 0 ? v[i] : acc[c + i] + v[i];
+              for (int j = 0; j < 16; ++j) acc[i + j] = k == 0 ? v[j] : acc[i + j] + v[j];
             }
           }
           tc_fence_before();
@@ -592,28 +643,29 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             bph ^= 1;
           }
         }
-        if (ok && q < p.e.Q) {
+        if (ok && rows) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 16)
-            if (c < half_n && c0 + c < p.e.P) epilogue16(p.e, q, c0 + c, acc + c);
+          for (int i = 0; i < 128; i += N)
+            if (i < half && c0 + i < p.e.P)
+              epilogue_box<F32>(p.e, q0 + lane, q0, c0 + i, acc + i, stage, lane, &tout, &tpre);
         }
       } else {
         if (!(ok = mbar_wait(&tfull[buf], bph, &s_abort))) break;
         tc_fence_after();
-        const uint32_t at = tmem + buf * 256 + half * half_n + lanes;
-        for (int c = 0; c < half_n; c += 32) {
-          float v[32];
-          tmem_ld32(at + c, v);
+        const uint32_t at = tmem + buf * 256 + col;
+#pragma unroll 1
+        for (int i = 0; i < half; i += N) {
+          float v[N];
+#pragma unroll
+          for (int j = 0; j < N; j += 32) tmem_ld32(at + i + j, v + j);
           tmem_ld_wait();
-          if (c + 32 >= half_n) {
+          if (i + N >= half) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) cluster_mbar_arrive(buf ? lead1 : lead0);
           }
-          if (q < p.e.Q) {
-            if (c0 + c < p.e.P) epilogue16(p.e, q, c0 + c, v);
-            if (c0 + c + 16 < p.e.P) epilogue16(p.e, q, c0 + c + 16, v + 16);
-          }
+          if (rows && c0 + i < p.e.P)
+            epilogue_box<F32>(p.e, q0 + lane, q0, c0 + i, v, stage, lane, &tout, &tpre);
         }
         if (++buf == 2) {
           buf = 0;
@@ -621,6 +673,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
       }
     }
+    if (lane == 0) bulk_wait_all();
     if (!ok && lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
   }
   __syncwarp();
@@ -635,6 +688,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // A CTA takes 64 x 8 columns and a share of the rows: thread (x, y) of 64 x 4 the
 // columns 8 x .. 8 x + 7 of rows y, y + 4, ...; the column sums of the CTA go to
 // row blockIdx.y of the partial sums.
+template <int ACT, bool DF32>
 __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradArgs a, int rows_per) {
   __shared__ float red[4][64][9];
   pdl_trigger();
@@ -648,12 +702,12 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradArgs a, int 
 #pragma unroll 4
     for (int64_t m = m0 + y; m < m1; m += 4) {
       float d[8];
-      load8(a.dout, a.dout_f32, (size_t)(m * a.N + c), d);
-      if (a.act != kActNone) {
+      load8(a.dout, DF32, (size_t)(m * a.N + c), d);
+      if (ACT != kActNone) {
         float z[8];
         load8(a.pre, false, (size_t)(m * a.N + c), z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= act_slope(z[i], a.act);
+        for (int i = 0; i < 8; ++i) d[i] *= act_slope(z[i], ACT);
       }
       if (a.dpre) store8_bf16(static_cast<bf16*>(a.dpre) + m * a.N + c, d);
 #pragma unroll
@@ -755,30 +809,41 @@ cudaError_t launch_split_bn(int bn, const ProductArgs& a, const Epi& e, int S, i
   return launch_split<A_MN, B_MN, 256>(a, e, S, steps, seg, status, st);
 }
 
-template <bool A_MN, bool B_MN, bool KEEP>
-cudaError_t launch_pair(const ProductArgs& a, const Epi& e, int bn, int steps, int sms, int* status,
-                        cudaStream_t st) {
-  CUtensorMap ta, tb;  // the pair's rows are q (b of the product), its columns p (a)
-  if (!operand_map(&ta, a.b, A_MN, a.Q, a.K, kTileP) || !operand_map(&tb, a.a, B_MN, a.P, a.K, bn / 2))
+// Tiles of 256 x 256 that the pairs take whole: where half of the pairs or more would idle
+// in the last round, its tiles are split in two.
+int pair_whole(int64_t tiles, int pairs) {
+  const int64_t rest = tiles % pairs;
+  return (int)(2 * rest <= pairs ? tiles - rest : tiles);
+}
+
+template <bool A_MN, bool B_MN, bool F32, bool KEEP>
+cudaError_t launch_pair(const ProductArgs& a, const Epi& e, int steps, int sms, int* status, cudaStream_t st) {
+  CUtensorMap ta, tb, to, tp;  // the pair's rows are q (b of the product), its columns p (a)
+  const auto out_type = F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!operand_map(&ta, a.b, A_MN, a.Q, a.K, kTileP) || !operand_map(&tb, a.a, B_MN, a.P, a.K, 64) ||
+      !encode_map(&to, a.out, out_type, F32 ? 4 : 2, a.Q, a.P, F32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(&tp, a.pre ? a.pre : a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.Q, a.P, 64, 32,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  const int64_t tiles = (a.Q + 255) / 256 * ((a.P + 255) / 256);
   PairP p{};
   p.e = e;
   p.steps = steps;
-  p.bn = bn;
   p.tq = (int)((a.Q + 255) / 256);
-  p.tp = (int)((a.P + bn - 1) / bn);
+  p.tp = (int)((a.P + 255) / 256);
+  p.whole = pair_whole(tiles, sms / 2);
   p.group = 8;
   p.seg = kSegSteps;
   p.status = status;
-  p.stage_bytes = kTileP * 128 + (B_MN ? (bn / 2 + 63) / 64 * kBoxBytes : bn / 2 * 128);
-  const int room = kSmemMax - 1024;
-  p.ring = room / p.stage_bytes < kMaxRing ? room / p.stage_bytes : kMaxRing;
-  auto kern = product_pair_kernel<A_MN, B_MN, KEEP>;
+  p.stage_bytes = 2 * kTileP * 128;
+  p.ring = (kSmemMax - 1024 - kEpiWarps * kStoreBytes) / p.stage_bytes;
+  auto kern = product_pair_kernel<A_MN, B_MN, F32, KEEP>;
   cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (rc != cudaSuccess) return rc;
-  const int64_t tiles = (int64_t)p.tq * p.tp;
-  const int pairs = tiles < sms / 2 ? (int)tiles : sms / 2;
-  return launch_cluster(kern, dim3(2 * pairs), 2, (size_t)p.ring * p.stage_bytes + 1024, st, ta, tb, p);
+  const int64_t units = 2 * tiles - p.whole;
+  const int pairs = units < sms / 2 ? (int)units : sms / 2;
+  return launch_cluster(kern, dim3(2 * pairs), 2,
+                        (size_t)p.ring * p.stage_bytes + kEpiWarps * kStoreBytes + 1024, st, ta, tb, to, tp, p);
 }
 
 }  // namespace
@@ -812,28 +877,24 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
       S = s;
     }
   }
-  // Pairs: waves of 256 x bn tiles, in the same units (a stage of 128 x 256 per SM).
-  int pair_bn = 0;
-  double pair_best = 0;
-  for (int b = 256; b >= 128; b -= 64) {
-    const int64_t t = (a.Q + 255) / 256 * ((a.P + b - 1) / b);
-    const int pairs = sms / 2;
-    const double c = (double)((t + pairs - 1) / pairs) * steps * (b + 16) / 256;
-    if (!pair_bn || c < pair_best) {
-      pair_best = c;
-      pair_bn = b;
-    }
-  }
+  // Pairs: rounds of tiles (a half one takes a little more than half of the time), in the same
+  // units (a stage of 128 x 256 per SM).
+  const int64_t pt = (a.Q + 255) / 256 * ((a.P + 255) / 256);
+  const int pairs = sms / 2;
+  const int64_t whole = pair_whole(pt, pairs), halves = 2 * (pt - whole);
+  const double pair_cost = ((double)((whole + pairs - 1) / pairs) + 0.55 * ((halves + pairs - 1) / pairs)) * steps;
   const char* env = getenv("MOE_LINEAR_FORM");
-  const bool pair = env && *env ? env[0] == 'p' : pair_best + 8 < (bn <= 64 ? 0.5 : bn == 128 ? 0.6 : 1.2) * best;
+  const bool pair = env && *env ? env[0] == 'p' : pair_cost + 8 < (bn <= 64 ? 0.5 : bn == 128 ? 0.6 : 1.2) * best;
   if (pair) {
     const bool keep = a.out_f32 && steps > kSegSteps;
-    if (a.a_mn && a.b_mn)
-      return keep ? launch_pair<true, true, true>(a, e, pair_bn, steps, sms, status, st)
-                  : launch_pair<true, true, false>(a, e, pair_bn, steps, sms, status, st);
-    if (a.a_mn) return launch_pair<false, true, false>(a, e, pair_bn, steps, sms, status, st);
-    return keep ? launch_pair<false, false, true>(a, e, pair_bn, steps, sms, status, st)
-                : launch_pair<false, false, false>(a, e, pair_bn, steps, sms, status, st);
+#define MOE_PAIR(A, B)                                                                              \
+  return keep        ? launch_pair<A, B, true, true>(a, e, steps, sms, status, st)                  \
+         : a.out_f32 ? launch_pair<A, B, true, false>(a, e, steps, sms, status, st)                 \
+                     : launch_pair<A, B, false, false>(a, e, steps, sms, status, st)
+    if (a.a_mn && a.b_mn) MOE_PAIR(true, true);
+    if (a.a_mn) return launch_pair<false, true, false, false>(a, e, steps, sms, status, st);  // (dx is bf16)
+    MOE_PAIR(false, false);
+#undef MOE_PAIR
   }
   if (a.a_mn && a.b_mn) return launch_split_bn<true, true>(bn, a, e, S, steps, seg, status, st);
   if (a.a_mn) return launch_split_bn<true, false>(bn, a, e, S, steps, seg, status, st);
@@ -851,7 +912,16 @@ cudaError_t launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t st) {
   if (a.M > 0) shares = (a.M + rows_per - 1) / rows_per;
   else shares = 0;
   if (shares > 0) {
-    cudaError_t e = launch_kernel(act_grad_kernel, dim3((unsigned)strips, (unsigned)shares), dim3(256), 0, st, a,
+    auto kern = act_grad_kernel<kActNone, false>;
+#define MOE_ACT(A) \
+  if (a.act == A) kern = a.dout_f32 ? act_grad_kernel<A, true> : act_grad_kernel<A, false>
+    MOE_ACT(kActNone);
+    MOE_ACT(kActRelu);
+    MOE_ACT(kActSilu);
+    MOE_ACT(kActGelu);
+    MOE_ACT(kActGeluTanh);
+#undef MOE_ACT
+    cudaError_t e = launch_kernel(kern, dim3((unsigned)strips, (unsigned)shares), dim3(256), 0, st, a,
                                   rows_per);
     if (e != cudaSuccess) return e;
   }

@@ -402,6 +402,23 @@ MOE_DEV void tma_load_2d_plain(void* smem_dst, const void* tmap, uint64_t* bar, 
       : "memory");
 }
 
+// ------------------------------------------------------------ TMA stores --
+// Box at (x, y) from shared memory (16-byte aligned x, never negative); the part outside
+// the tensor is dropped.  One thread issues, commits and waits.
+MOE_DEV void tma_store_2d(const void* tmap, const void* smem_src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap),
+               "r"(smem_u32(smem_src)), "r"(x), "r"(y)
+               : "memory");
+}
+MOE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the N newest groups have read their shared memory / are complete.
+template <int N>
+MOE_DEV void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+MOE_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+MOE_DEV void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // ------------------------------------------------------------- CTA pairs --
 // The same load for a CTA of a pair: `bar` (a cluster address) may lie in either CTA.
 MOE_DEV void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar, int x, int y) {
