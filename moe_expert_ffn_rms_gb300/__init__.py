@@ -562,6 +562,29 @@ def moe_quantize_fp8_blocks(x, q, scale, block_rows, stream=None):
 
 # --------------------------------------------- around the experts, and training --
 
+# The checks of these calls cost as much host time as a small call's kernel takes, so each
+# tensor's are one expression that also ends in its pointer.
+
+_cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _arg(t, name, shape, dtypes, device):
+    """Pointer of a checked tensor."""
+    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    _check_tensor(t, name, shape, dtypes, device)
+    return t.data_ptr()
+
+
+def _queue(device, stream):
+    """The call's stream; ValueError unless the device is the current one."""
+    if device.type != "cuda" or device.index != _cur_device():
+        _check_current(device)
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream)
+
+
 def _ws(workspace, device):
     if workspace.device != device:
         raise ValueError(f"workspace: on {workspace.device}, need {device}")
@@ -571,8 +594,7 @@ def _ws(workspace, device):
 def _pairs(row_of_pair, n, device):
     if row_of_pair.numel() != n:
         raise ValueError(f"row_of_pair: {row_of_pair.numel()} entries, need {n}")
-    _check_tensor(row_of_pair, "row_of_pair", row_of_pair.shape, _I32S, device)
-    return row_of_pair.data_ptr()
+    return _arg(row_of_pair, "row_of_pair", row_of_pair.shape, _I32S, device)
 
 
 def moe_unpermute(y, row_of_pair, out, T, k, topk_w=None, residual=None, stream=None):
@@ -580,27 +602,23 @@ def moe_unpermute(y, row_of_pair, out, T, k, topk_w=None, residual=None, stream=
     [T*k, H] in expert order, row_of_pair int32 [T*k] of moe_permute (negative: dropped), topk_w
     fp32 [T, k] (None: all 1), residual and out bf16 / fp32 [T, H]; residual may be out."""
     H, device = y.shape[-1], y.device
-    _check_current(device)
-    _check_tensor(y, "y", (T * k, H), _FLOATS, device)
-    _check_tensor(out, "out", (T, H), _FLOATS, device)
+    st = _queue(device, stream)
     _check(lib.moe_unpermute(
-        y.data_ptr(), y.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, device),
-        _opt(topk_w, "topk_w", (T, k), _F32S, device), T, k, H,
-        _opt(residual, "residual", (T, H), _FLOATS, device),
-        residual is not None and residual.dtype == torch.float32, out.data_ptr(),
-        out.dtype == torch.float32, _stream(stream)))
+        _arg(y, "y", (T * k, H), _FLOATS, device), y.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, device),
+        None if topk_w is None else _arg(topk_w, "topk_w", (T, k), _F32S, device), T, k, H,
+        None if residual is None else _arg(residual, "residual", (T, H), _FLOATS, device),
+        residual is not None and residual.dtype == torch.float32, _arg(out, "out", (T, H), _FLOATS, device),
+        out.dtype == torch.float32, st))
     return out
 
 
 def moe_unpermute_backward(dout, y, row_of_pair, topk_w, T, k, dy=None, dw=None, ids=None, dlogits=None,
                            stream=None):
-    """Gradients of moe_unpermute from dout bf16 / fp32 [T, H]: dy [T*k, H] (y's type, bf16 without
-    y; rows that no pair owns are left as they were), dw fp32 [T, k], and with ids int32 [T, k] the
+    """Gradients of moe_unpermute from dout bf16 / fp32 [T, H]: dy [T*k, H] (y's type, bf16 or fp32
+    without y; rows that no pair owns are left as they were), dw fp32 [T, k], and with ids int32 [T, k] the
     router's dlogits fp32 [T, E].  y is needed for dw and dlogits; dy may be y."""
     H, device = dout.shape[-1], dout.device
-    _check_current(device)
-    _check_tensor(dout, "dout", (T, H), _FLOATS, device)
-    _check_tensor(topk_w, "topk_w", (T, k), _F32S, device)
+    st = _queue(device, stream)
     yt = y if y is not None else dy
     if dy is not None and y is not None and dy.dtype != y.dtype:
         raise ValueError(f"dy: dtype {dy.dtype}, need {y.dtype}")
@@ -608,40 +626,42 @@ def moe_unpermute_backward(dout, y, row_of_pair, topk_w, T, k, dy=None, dw=None,
         raise ValueError("dlogits: must be [T, E]")
     E = 0 if dlogits is None else dlogits.shape[1]
     _check(lib.moe_unpermute_backward(
-        dout.data_ptr(), dout.dtype == torch.float32, _opt(y, "y", (T * k, H), _FLOATS, device),
-        yt is None or yt.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, device), topk_w.data_ptr(),
-        _opt(ids, "ids", (T, k), _I32S, device), T, k, H, E, _opt(dy, "dy", (T * k, H), _FLOATS, device),
-        _opt(dw, "dw", (T, k), _F32S, device), _opt(dlogits, "dlogits", (T, E), _F32S, device),
-        _stream(stream)))
+        _arg(dout, "dout", (T, H), _FLOATS, device), dout.dtype == torch.float32,
+        None if y is None else _arg(y, "y", (T * k, H), _FLOATS, device), yt is None or yt.dtype == torch.bfloat16,
+        _pairs(row_of_pair, T * k, device), _arg(topk_w, "topk_w", (T, k), _F32S, device),
+        None if ids is None else _arg(ids, "ids", (T, k), _I32S, device), T, k, H, E,
+        None if dy is None else _arg(dy, "dy", (T * k, H), _FLOATS, device),
+        None if dw is None else _arg(dw, "dw", (T, k), _F32S, device),
+        None if dlogits is None else _arg(dlogits, "dlogits", (T, E), _F32S, device), st))
 
 
 def moe_permute_backward(dxp, row_of_pair, dx, T, k, dres=None, stream=None):
     """Gradient of moe_permute's gather: dx = dres + the sum of each token's rows of dxp (bf16 / fp32
     [T*k, H], expert order).  dres and dx bf16 / fp32 [T, H]; dres may be dx."""
     H, device = dxp.shape[-1], dxp.device
-    _check_current(device)
-    _check_tensor(dxp, "dxp", (T * k, H), _FLOATS, device)
-    _check_tensor(dx, "dx", (T, H), _FLOATS, device)
+    st = _queue(device, stream)
     _check(lib.moe_permute_backward(
-        dxp.data_ptr(), dxp.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, device), T, k, H,
-        _opt(dres, "dres", (T, H), _FLOATS, device), dres is not None and dres.dtype == torch.float32,
-        dx.data_ptr(), dx.dtype == torch.float32, _stream(stream)))
+        _arg(dxp, "dxp", (T * k, H), _FLOATS, device), dxp.dtype == torch.bfloat16,
+        _pairs(row_of_pair, T * k, device), T, k, H,
+        None if dres is None else _arg(dres, "dres", (T, H), _FLOATS, device),
+        dres is not None and dres.dtype == torch.float32, _arg(dx, "dx", (T, H), _FLOATS, device),
+        dx.dtype == torch.float32, st))
     return dx
 
 
 def moe_layernorm(x, w, eps, y, b=None, mean=None, rstd=None, stream=None):
     """y = (x - mean) * rstd * w + b over the rows of x bf16 / fp32 [T, H]; w, b bf16 / fp32 [H] of one
     type; y bf16 / fp32 [T, H]; mean, rstd fp32 [T] for the backward pass."""
-    T, H = x.shape
-    device = x.device
-    _check_current(device)
-    _check_tensor(x, "x", (T, H), _FLOATS, device)
-    _check_tensor(w, "w", (H,), _FLOATS, device)
-    _check_tensor(y, "y", (T, H), _FLOATS, device)
+    shape, device = x.shape, x.device
+    T, H = shape
+    st = _queue(device, stream)
+    wt = w.dtype
     _check(lib.moe_layernorm(
-        x.data_ptr(), x.dtype == torch.float32, w.data_ptr(), _opt(b, "b", (H,), (w.dtype,), device),
-        w.dtype == torch.float32, T, H, eps, y.data_ptr(), y.dtype == torch.float32,
-        _opt(mean, "mean", (T,), _F32S, device), _opt(rstd, "rstd", (T,), _F32S, device), _stream(stream)))
+        _arg(x, "x", shape, _FLOATS, device), x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, device),
+        None if b is None else _arg(b, "b", (H,), (wt,), device), wt == torch.float32, T, H, eps,
+        _arg(y, "y", shape, _FLOATS, device), y.dtype == torch.float32,
+        None if mean is None else _arg(mean, "mean", (T,), _F32S, device),
+        None if rstd is None else _arg(rstd, "rstd", (T,), _F32S, device), st))
     return y
 
 
@@ -652,40 +672,34 @@ def moe_norm_backward_workspace_size(T, H) -> int:
     return n
 
 
-def _norm_grad_args(dy, x, w, dx, dw, dres):
-    T, H = x.shape
-    device = x.device
-    _check_current(device)
-    _check_tensor(x, "x", (T, H), _FLOATS, device)
-    _check_tensor(dy, "dy", (T, H), _FLOATS, device)
-    _check_tensor(w, "w", (H,), _FLOATS, device)
-    _check_tensor(dx, "dx", (T, H), (x.dtype,), device)
-    _check_tensor(dw, "dw", (H,), _F32S, device)
-    return T, H, device, _opt(dres, "dres", (T, H), (x.dtype,), device)
-
-
 def moe_layernorm_backward(dy, x, w, mean, rstd, dx, dw, workspace, db=None, dres=None, stream=None):
     """Gradients of moe_layernorm: dx [T, H] of x's type (plus dres, of the same type), dw and db fp32
     [H]; mean and rstd of the forward call, workspace of moe_norm_backward_workspace_size(T, H) bytes.
     dx may be x, dres, or dy of the same type."""
-    T, H, device, pres = _norm_grad_args(dy, x, w, dx, dw, dres)
-    _check_tensor(mean, "mean", (T,), _F32S, device)
-    _check_tensor(rstd, "rstd", (T,), _F32S, device)
+    shape, device, xt = x.shape, x.device, (x.dtype,)
+    T, H = shape
+    st = _queue(device, stream)
     _check(lib.moe_layernorm_backward(
-        dy.data_ptr(), dy.dtype == torch.float32, x.data_ptr(), x.dtype == torch.float32, w.data_ptr(),
-        w.dtype == torch.float32, mean.data_ptr(), rstd.data_ptr(), pres, T, H, dx.data_ptr(),
-        dw.data_ptr(), _opt(db, "db", (H,), _F32S, device), *_ws(workspace, device), _stream(stream)))
+        _arg(dy, "dy", shape, _FLOATS, device), dy.dtype == torch.float32, _arg(x, "x", shape, _FLOATS, device),
+        x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, device), w.dtype == torch.float32,
+        _arg(mean, "mean", (T,), _F32S, device), _arg(rstd, "rstd", (T,), _F32S, device),
+        None if dres is None else _arg(dres, "dres", shape, xt, device), T, H, _arg(dx, "dx", shape, xt, device),
+        _arg(dw, "dw", (H,), _F32S, device), None if db is None else _arg(db, "db", (H,), _F32S, device),
+        *_ws(workspace, device), st))
     return dx
 
 
 def moe_rmsnorm_backward(dy, x, w, eps, dx, dw, workspace, dres=None, stream=None):
     """Gradients of moe_rmsnorm: dx [T, H] of x's type (plus dres), dw fp32 [H]; the rest as
     moe_layernorm_backward."""
-    T, H, device, pres = _norm_grad_args(dy, x, w, dx, dw, dres)
+    shape, device, xt = x.shape, x.device, (x.dtype,)
+    T, H = shape
+    st = _queue(device, stream)
     _check(lib.moe_rmsnorm_backward(
-        dy.data_ptr(), dy.dtype == torch.float32, x.data_ptr(), x.dtype == torch.float32, w.data_ptr(),
-        w.dtype == torch.float32, eps, pres, T, H, dx.data_ptr(), dw.data_ptr(), *_ws(workspace, device),
-        _stream(stream)))
+        _arg(dy, "dy", shape, _FLOATS, device), dy.dtype == torch.float32, _arg(x, "x", shape, _FLOATS, device),
+        x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, device), w.dtype == torch.float32, eps,
+        None if dres is None else _arg(dres, "dres", shape, xt, device), T, H, _arg(dx, "dx", shape, xt, device),
+        _arg(dw, "dw", (H,), _F32S, device), *_ws(workspace, device), st))
     return dx
 
 
@@ -694,18 +708,18 @@ def moe_linear(x, w, out, bias=None, residual=None, act=ACT_NONE, pre=None, stre
     and out bf16 / fp32 [M, N] (residual may be out), act one of the ACT_ constants; pre bf16 [M, N]
     receives the values before the activation."""
     device = x.device
-    _check_current(device)
+    st = _queue(device, stream)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: must be [M, K] and [N, K]")
     (m, k), n = x.shape, w.shape[0]
-    _check_tensor(x, "x", (m, k), _BF16, device)
-    _check_tensor(w, "w", (n, k), _BF16, device)
-    _check_tensor(out, "out", (m, n), _FLOATS, device)
     _check(lib.moe_linear(
-        x.data_ptr(), w.data_ptr(), _opt(bias, "bias", (n,), _FLOATS, device),
-        bias is not None and bias.dtype == torch.float32, _opt(residual, "residual", (m, n), _FLOATS, device),
+        _arg(x, "x", (m, k), _BF16, device), _arg(w, "w", (n, k), _BF16, device),
+        None if bias is None else _arg(bias, "bias", (n,), _FLOATS, device),
+        bias is not None and bias.dtype == torch.float32,
+        None if residual is None else _arg(residual, "residual", (m, n), _FLOATS, device),
         residual is not None and residual.dtype == torch.float32, m, n, k, act,
-        _opt(pre, "pre", (m, n), _BF16, device), out.data_ptr(), out.dtype == torch.float32, _stream(stream)))
+        None if pre is None else _arg(pre, "pre", (m, n), _BF16, device),
+        _arg(out, "out", (m, n), _FLOATS, device), out.dtype == torch.float32, st))
     return out
 
 
@@ -721,15 +735,15 @@ def moe_linear_backward(dout, x, w, workspace, dx=None, dw=None, db=None, pre=No
     [N], each where it is given; pre of the forward call with an activation; workspace of
     moe_linear_backward_workspace_size(M, N, K) bytes."""
     device = dout.device
-    _check_current(device)
+    st = _queue(device, stream)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: must be [M, K] and [N, K]")
     (m, k), n = x.shape, w.shape[0]
-    _check_tensor(dout, "dout", (m, n), _FLOATS, device)
-    _check_tensor(x, "x", (m, k), _BF16, device)
-    _check_tensor(w, "w", (n, k), _BF16, device)
     _check(lib.moe_linear_backward(
-        dout.data_ptr(), dout.dtype == torch.float32, _opt(pre, "pre", (m, n), _BF16, device), x.data_ptr(),
-        w.data_ptr(), m, n, k, act, _opt(dx, "dx", (m, k), _BF16, device), _opt(dw, "dw", (n, k), _FLOATS, device),
-        dw is not None and dw.dtype == torch.float32, _opt(db, "db", (n,), _F32S, device),
-        *_ws(workspace, device), _stream(stream)))
+        _arg(dout, "dout", (m, n), _FLOATS, device), dout.dtype == torch.float32,
+        None if pre is None else _arg(pre, "pre", (m, n), _BF16, device), _arg(x, "x", (m, k), _BF16, device),
+        _arg(w, "w", (n, k), _BF16, device), m, n, k, act,
+        None if dx is None else _arg(dx, "dx", (m, k), _BF16, device),
+        None if dw is None else _arg(dw, "dw", (n, k), _FLOATS, device),
+        dw is not None and dw.dtype == torch.float32, None if db is None else _arg(db, "db", (n,), _F32S, device),
+        *_ws(workspace, device), st))

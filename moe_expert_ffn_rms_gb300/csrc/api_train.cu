@@ -155,7 +155,7 @@ moe_status moe_unpermute_backward(const void* dout, int32_t dout_f32, const void
   a.E = E;
   a.dout_f32 = dout_f32 != 0;
   a.y_f32 = y_bf16 == 0;
-  MOE_CUDA(moe::launch_unpermute_grad(a, status, (cudaStream_t)stream), "unpermute backward launch");
+  MOE_CUDA(moe::launch_unpermute_grad(a, sms, status, (cudaStream_t)stream), "unpermute backward launch");
   return MOE_OK;
 }
 
@@ -186,7 +186,7 @@ moe_status moe_layernorm(const void* x, int32_t x_f32, const void* w, const void
   a.x_f32 = x_f32 != 0;
   a.y_f32 = y_f32 != 0;
   a.w_f32 = w_f32 != 0;
-  MOE_CUDA(moe::launch_layernorm(a, (cudaStream_t)stream), "layernorm launch");
+  MOE_CUDA(moe::launch_layernorm(a, sms, status, (cudaStream_t)stream), "layernorm launch");
   return MOE_OK;
 }
 

@@ -345,6 +345,84 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
   if (warp == 1) tmem_dealloc(tmem, TMEM);
 }
 
+// ---------------------------------------------------------------- few rows --
+// One to four rows of b (tokens), both operands K-major: no tensor cores, each warp
+// streams R rows of a (weights) once, 16 bytes per lane and load, kRowsUnroll loads of each in
+// flight, against b's rows from L1; W warps share a row's K where there are few
+// rows.  Products are exact in fp32 and added with fmaf.  The bound is the copy
+// bandwidth and a launch: no barriers, TMEM or clusters to set up.
+constexpr int kRowsWarps = 8;
+constexpr int kRowsUnroll = 4;
+
+template <int MT, int R>
+__global__ void __launch_bounds__(kRowsWarps * 32) product_rows_kernel(const bf16* __restrict__ a,
+                                                                       const bf16* __restrict__ b, int64_t K, int W,
+                                                                       const Epi e) {
+  __shared__ float red[kRowsWarps][R * MT];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = warp % W, group = warp / W;
+  const int64_t p0 = ((int64_t)blockIdx.x * (kRowsWarps / W) + group) * R;
+  const int Q = (int)e.Q, nk = (int)(K >> 3), step = 32 * W;
+  float acc[R][MT] = {};
+  for (int k0 = sub * 32 + lane; k0 < nk; k0 += step * kRowsUnroll) {
+    uint4 w[kRowsUnroll][R];
+#pragma unroll
+    for (int i = 0; i < kRowsUnroll; ++i)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        w[i][r] = make_uint4(0u, 0u, 0u, 0u);
+        if (k0 + i * step < nk && p0 + r < e.P)
+          w[i][r] = *reinterpret_cast<const uint4*>(a + (p0 + r) * K + (int64_t)(k0 + i * step) * 8);
+      }
+#pragma unroll
+    for (int i = 0; i < kRowsUnroll; ++i) {
+      if (k0 + i * step >= nk) break;
+      float x[MT][8];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (m < Q) unpack8_bf16(*reinterpret_cast<const uint4*>(b + m * K + (int64_t)(k0 + i * step) * 8), x[m]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float f[8];
+        unpack8_bf16(w[i][r], f);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m < Q) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[r][m] = fmaf(f[q], x[m][q], acc[r][m]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float v = warp_sum(acc[r][m]);
+      if (lane == 0) red[warp][r * MT + m] = v;
+    }
+  if (W > 1) __syncthreads();
+  else __syncwarp();
+  const int r = lane / MT, m = lane - r * MT;
+  if (sub != 0 || r >= R || m >= Q || p0 + r >= e.P) return;
+  float v = 0.f;
+  for (int i = 0; i < W; ++i) v += red[warp + i][lane];
+  const int64_t p = p0 + r, at = m * e.P + p;
+  auto get = [](const void* s, int f32, int64_t i) {
+    return f32 ? static_cast<const float*>(s)[i] : __bfloat162float(static_cast<const bf16*>(s)[i]);
+  };
+  if (e.bias) v += get(e.bias, e.bias_f32, p);
+  if (e.pre) e.pre[at] = __float2bfloat16_rn(v);
+  act_all<1>(&v, e.act);
+  if (e.residual) v += get(e.residual, e.res_f32, at);
+  if (e.out_f32) static_cast<float*>(e.out)[at] = v;
+  else static_cast<bf16*>(e.out)[at] = __float2bfloat16_rn(v);
+}
+
 // -------------------------------------------------------------- CTA-pair form --
 // Persistent pairs of CTAs (cluster of two), a tile of 256 rows q x BN columns p
 // at a time: each CTA of a pair loads its 128 rows and half of the columns, and the
@@ -860,6 +938,17 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
   e.out_f32 = a.out_f32;
   e.P = a.P;
   e.Q = a.Q;
+  const char* env = getenv("MOE_LINEAR_FORM");
+  const char form = env ? env[0] : 0;
+  if (!a.a_mn && !a.b_mn && a.Q <= 4 && (!form || form == 'r')) {
+    constexpr int R = 2;
+    int W = 1;  // warps per row: enough of them to fill the SMs, four loads for each at least
+    while (W < kRowsWarps && a.P / R * W < (int64_t)sms * 24 && a.K / 8 > 64 * W) W *= 2;
+    const int64_t per = kRowsWarps / W * R;
+    auto kern = a.Q == 1 ? product_rows_kernel<1, R> : (a.Q == 2 ? product_rows_kernel<2, R> : product_rows_kernel<4, R>);
+    return launch_kernel(kern, dim3((unsigned)((a.P + per - 1) / per)), dim3(kRowsWarps * 32), 0, st,
+                         static_cast<const bf16*>(a.a), static_cast<const bf16*>(a.b), a.K, W, e);
+  }
   const int steps = (int)((a.K + kStepK - 1) / kStepK);
   const int seg = a.out_f32 ? kSegSteps : 1 << 30;
   int bn = 16;
@@ -883,8 +972,7 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
   const int pairs = sms / 2;
   const int64_t whole = pair_whole(pt, pairs), halves = 2 * (pt - whole);
   const double pair_cost = ((double)((whole + pairs - 1) / pairs) + 0.55 * ((halves + pairs - 1) / pairs)) * steps;
-  const char* env = getenv("MOE_LINEAR_FORM");
-  const bool pair = env && *env ? env[0] == 'p' : pair_cost + 8 < (bn <= 64 ? 0.5 : bn == 128 ? 0.6 : 1.2) * best;
+  const bool pair = form ? form == 'p' : pair_cost + 8 < (bn <= 64 ? 0.5 : bn == 128 ? 0.6 : 1.2) * best;
   if (pair) {
     const bool keep = a.out_f32 && steps > kSegSteps;
 #define MOE_PAIR(A, B)                                                                              \

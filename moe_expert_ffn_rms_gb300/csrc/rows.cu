@@ -74,100 +74,114 @@ __global__ void __launch_bounds__(kRowsThreads) unpermute_kernel(const Unpermute
   store8(a.out, a.out_f32, (size_t)t * a.H + v * 8, f);
 }
 
-// blockDim = (threads of a token, a multiple of 32; tokens).
-template <int KB, bool YF32>
-__global__ void __launch_bounds__(kRowsThreads) unpermute_grad_kernel(const UnpermuteGradArgs a,
-                                                                      int* status) {
-  __shared__ float red[kRowsThreads / 32][KB];
-  pdl_trigger();
-  pdl_wait();
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int nv = a.H >> 3, tx = threadIdx.x, nt = blockDim.x;
-  const bool on = t < a.T;
-  int row[KB];
-  float w[KB], dot[KB];
+// 32 blockDim.x / 32 lanes take one (token, slot) pair, so each row's dot product stays
+// with its warps; the k pairs of a token lie in one CTA (blockDim.y = k x tokens) and
+// read its dout row from L1.  Four chunks (two of fp32) of both rows are in flight per lane.
+// (A CTA per token with all k rows in flight per thread, at T = 4096, H = 4096, k = 8:
+// 123 registers, 113 us.)
+constexpr int kGradThreads = 1024;
+
+// Eight columns as they are in memory.
+template <bool F32>
+struct Raw {
+  uint4 u[F32 ? 2 : 1];
+  MOE_DEV void load(const void* p, size_t at) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (F32 ? 4 : 2));
 #pragma unroll
-  for (int j = 0; j < KB; ++j) {
-    row[j] = -1;
-    w[j] = dot[j] = 0.f;
-    if (on && j < a.k) {
-      row[j] = pair_row(a.row_of_pair, t * a.k + j, a.T * a.k, tx == 0, status);
-      w[j] = a.w[t * a.k + j];
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) u[i] = s[i];
+  }
+  MOE_DEV void get(float (&f)[8]) const {
+    if constexpr (F32) {
+      f[0] = __uint_as_float(u[0].x); f[1] = __uint_as_float(u[0].y);
+      f[2] = __uint_as_float(u[0].z); f[3] = __uint_as_float(u[0].w);
+      f[4] = __uint_as_float(u[1].x); f[5] = __uint_as_float(u[1].y);
+      f[6] = __uint_as_float(u[1].z); f[7] = __uint_as_float(u[1].w);
+    } else {
+      unpack8_bf16(u[0], f);
     }
   }
+};
+
+template <bool YF32, bool DF32>
+__global__ void __launch_bounds__(kGradThreads) unpermute_grad_kernel(const UnpermuteGradArgs a, int* status) {
+  __shared__ float red[kGradThreads / 32];
+  __shared__ float s_dw[kGradThreads / 32], s_w[kGradThreads / 32];
+  __shared__ int s_id[kGradThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  const int nv = a.H >> 3, tx = threadIdx.x, ty = threadIdx.y, nt = blockDim.x;
+  const int64_t pair = (int64_t)blockIdx.x * blockDim.y + ty;
+  const bool on = pair < (int64_t)a.T * a.k;
+  const int64_t t = pair / a.k;
+  const int j = (int)(pair - t * a.k);
   const bool dots = a.dw || a.dlogits;
-  constexpr int W = YF32 ? 2 : 1;
-  for (int v = tx; on && v < nv; v += nt) {
-    float d[8];
-    uint4 q[KB][W];
-    if (dots) {
+  int row = -1;
+  float w = 0.f, dot = 0.f;
+  if (on) {
+    row = pair_row(a.row_of_pair, pair, a.T * a.k, tx == 0, status);
+    w = a.w[pair];
+  }
+  if (row >= 0) {
+    const size_t at_d = (size_t)t * a.H, at_y = (size_t)row * a.H;
+    constexpr int N = YF32 || DF32 ? 2 : 4;
+    for (int v0 = tx; v0 < nv; v0 += nt * N) {
+      Raw<YF32> y[N];
+      Raw<DF32> d[N];
 #pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        if (row[j] >= 0) {
-          const uint4* s = static_cast<const uint4*>(a.y) + ((int64_t)row[j] * nv + v) * W;
-#pragma unroll
-          for (int i = 0; i < W; ++i) q[j][i] = s[i];
+      for (int i = 0; i < N; ++i) {
+        const int v = v0 + i * nt;
+        if (v < nv) {
+          if (dots) y[i].load(a.y, at_y + v * 8);
+          d[i].load(a.dout, at_d + v * 8);
         }
       }
-    }
-    load8(a.dout, a.dout_f32, (size_t)t * a.H + v * 8, d);
 #pragma unroll
-    for (int j = 0; j < KB; ++j) {
-      if (row[j] < 0) continue;
-      if (dots) {
-        float b[8];
-        if (YF32) {
+      for (int i = 0; i < N; ++i) {
+        const int v = v0 + i * nt;
+        if (v >= nv) break;
+        float f[8], g[8];
+        d[i].get(f);
+        if (dots) {
+          y[i].get(g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] = __uint_as_float((&q[j][0].x)[i]);
-        } else {
-          unpack8_bf16(q[j][0], b);
+          for (int q = 0; q < 8; ++q) dot = fmaf(f[q], g[q], dot);
         }
+        if (a.dy) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], b[i], dot[j]);
-      }
-      if (a.dy) {
-        float g[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = w[j] * d[i];
-        store8(a.dy, YF32, (size_t)row[j] * a.H + v * 8, g);
+          for (int q = 0; q < 8; ++q) f[q] *= w;
+          store8(a.dy, YF32, at_y + v * 8, f);
+        }
       }
     }
   }
   if (!dots) return;
-  const int warp0 = threadIdx.y * (nt >> 5);
-#pragma unroll
-  for (int j = 0; j < KB; ++j) {
-    dot[j] = warp_sum(dot[j]);
-    if ((tx & 31) == 0) red[warp0 + (tx >> 5)][j] = dot[j];
+  dot = warp_sum(dot);
+  const int wp = nt >> 5;
+  if (wp > 1) {
+    if ((tx & 31) == 0) red[ty * wp + (tx >> 5)] = dot;
+    __syncthreads();
+    dot = 0.f;
+    for (int i = 0; i < wp; ++i) dot += red[ty * wp + i];
+  }
+  if (tx == 0 && on && a.dw) a.dw[pair] = dot;
+  if (!a.dlogits) return;
+  if (tx == 0 && on) {
+    const int id = a.ids[pair];
+    if (id < 0 || id >= a.E) flag_status(status, MOE_ERR_INVALID_ARG);
+    s_dw[ty] = dot;
+    s_w[ty] = w;
+    s_id[ty] = id;
   }
   __syncthreads();
   if (!on) return;
+  const int y0 = ty - j;  // the token's first pair
   float s = 0.f;
-#pragma unroll
-  for (int j = 0; j < KB; ++j) {
-    dot[j] = 0.f;
-    for (int i = 0; i < nt >> 5; ++i) dot[j] += red[warp0 + i][j];
-    s = fmaf(w[j], dot[j], s);
-  }
-  if (a.dw) {
-#pragma unroll
-    for (int j = 0; j < KB; ++j)
-      if (tx == j && j < a.k) a.dw[t * a.k + j] = dot[j];
-  }
-  if (a.dlogits) {
-    int id[KB];
-#pragma unroll
-    for (int j = 0; j < KB; ++j) {
-      id[j] = j < a.k ? a.ids[t * a.k + j] : -1;
-      if (tx == 0 && j < a.k && (id[j] < 0 || id[j] >= a.E)) flag_status(status, MOE_ERR_INVALID_ARG);
-    }
-    for (int e = tx; e < a.E; e += nt) {
-      float g = 0.f;
-#pragma unroll
-      for (int j = 0; j < KB; ++j)
-        if (id[j] == e) g += w[j] * (dot[j] - s);
-      a.dlogits[t * a.E + e] = g;
-    }
+  for (int i = 0; i < a.k; ++i) s = fmaf(s_w[y0 + i], s_dw[y0 + i], s);
+  for (int e = j * nt + tx; e < a.E; e += a.k * nt) {
+    float g = 0.f;
+    for (int i = 0; i < a.k; ++i)
+      if (s_id[y0 + i] == e) g += s_w[y0 + i] * (s_dw[y0 + i] - s);
+    a.dlogits[t * a.E + e] = g;
   }
 }
 
@@ -196,12 +210,20 @@ cudaError_t launch_unpermute(const UnpermuteArgs& a, int* status, cudaStream_t s
   return launch_kernel(kern, grid, block, 0, st, a, status);
 }
 
-cudaError_t launch_unpermute_grad(const UnpermuteGradArgs& a, int* status, cudaStream_t st) {
-  if (a.T == 0) return cudaSuccess;
-  MOE_ROWS(unpermute_grad_kernel);
-  const dim3 block = rows_block(a.H >> 3);
-  return launch_kernel(kern, dim3((a.T + block.y - 1) / block.y), block, 0, st, a, status);
-}
 #undef MOE_ROWS
+
+cudaError_t launch_unpermute_grad(const UnpermuteGradArgs& a, int sms, int* status, cudaStream_t st) {
+  if (a.T == 0) return cudaSuccess;
+  const int nv = a.H >> 3;
+  // warps per pair: more where few pairs would leave the SMs idle
+  const int64_t pairs = (int64_t)a.T * a.k;
+  int wp = 1;
+  while (wp < 4 && wp * 64 < nv && pairs * wp < (int64_t)sms * 16) wp *= 2;
+  int tokens = 8 / (a.k * wp);
+  if (tokens < 1) tokens = 1;
+  auto kern = a.y_f32 ? (a.dout_f32 ? unpermute_grad_kernel<true, true> : unpermute_grad_kernel<true, false>)
+                      : (a.dout_f32 ? unpermute_grad_kernel<false, true> : unpermute_grad_kernel<false, false>);
+  return launch_kernel(kern, dim3((a.T + tokens - 1) / tokens), dim3(32 * wp, a.k * tokens), 0, st, a, status);
+}
 
 }  // namespace moe

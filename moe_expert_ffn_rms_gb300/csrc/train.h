@@ -36,7 +36,7 @@ struct UnpermuteGradArgs {
   int T, k, H, E;
   bool dout_f32, y_f32;
 };
-cudaError_t launch_unpermute_grad(const UnpermuteGradArgs& a, int* status, cudaStream_t st);
+cudaError_t launch_unpermute_grad(const UnpermuteGradArgs& a, int sms, int* status, cudaStream_t st);
 
 // ------------------------------------------------------------------ norm.cu --
 constexpr int kNormMaxH = 16384;
@@ -52,7 +52,7 @@ struct LayerNormArgs {
   float eps;
   bool x_f32, y_f32, w_f32;
 };
-cudaError_t launch_layernorm(const LayerNormArgs& a, cudaStream_t st);
+cudaError_t launch_layernorm(const LayerNormArgs& a, int sms, int* status, cudaStream_t st);
 
 struct NormGradArgs {
   const void* dy;

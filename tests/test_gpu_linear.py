@@ -102,7 +102,7 @@ def forward(M, m, n, k, act="NONE", bias=None, res=None, out=BF, pre=False, seed
     return o
 
 
-SHAPES = [(1, 8, 8), (1, 128, 64), (1, 4096, 4096), (2, 136, 200), (3, 256, 1000), (16, 512, 256), (17, 1032, 72),
+SHAPES = [(1, 8, 8), (1, 128, 64), (1, 4096, 4096), (1, 1032, 12296), (2, 136, 200), (4, 5128, 520), (3, 256, 1000), (16, 512, 256), (17, 1032, 72),
           (33, 264, 4104), (61, 7168, 2048), (64, 128, 512), (65, 384, 320), (100, 1544, 2944), (128, 256, 128),
           (129, 2056, 136), (255, 520, 1032), (256, 4096, 512), (257, 776, 264), (333, 2944, 1000),
           (512, 512, 8192), (1000, 4104, 1536), (2047, 2048, 520), (4096, 1288, 264), (2500, 5128, 1024)]
