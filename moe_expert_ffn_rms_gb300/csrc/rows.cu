@@ -102,7 +102,7 @@ struct Raw {
   }
 };
 
-template <bool YF32, bool DF32>
+template <bool YF32, bool DF32, int N>
 __global__ void __launch_bounds__(kGradThreads) unpermute_grad_kernel(const UnpermuteGradArgs a, int* status) {
   __shared__ float red[kGradThreads / 32];
   __shared__ float s_dw[kGradThreads / 32], s_w[kGradThreads / 32];
@@ -115,26 +115,31 @@ __global__ void __launch_bounds__(kGradThreads) unpermute_grad_kernel(const Unpe
   const int64_t t = pair / a.k;
   const int j = (int)(pair - t * a.k);
   const bool dots = a.dw || a.dlogits;
-  int row = -1;
+  int row = -1, id = -1;
   float w = 0.f, dot = 0.f;
+  const size_t at_d = (size_t)t * a.H;
+  Raw<DF32> d[N];
+  auto load_dout = [&](int v0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (v0 + i * nt < nv) d[i].load(a.dout, at_d + (v0 + i * nt) * 8);
+  };
   if (on) {
+    load_dout(tx);  // (does not wait for the row's index)
     row = pair_row(a.row_of_pair, pair, a.T * a.k, tx == 0, status);
     w = a.w[pair];
+    if (a.dlogits && tx == 0) id = a.ids[pair];
   }
   if (row >= 0) {
-    const size_t at_d = (size_t)t * a.H, at_y = (size_t)row * a.H;
-    constexpr int N = YF32 || DF32 ? 2 : 4;
+    const size_t at_y = (size_t)row * a.H;
     for (int v0 = tx; v0 < nv; v0 += nt * N) {
       Raw<YF32> y[N];
-      Raw<DF32> d[N];
+      if (dots) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int v = v0 + i * nt;
-        if (v < nv) {
-          if (dots) y[i].load(a.y, at_y + v * 8);
-          d[i].load(a.dout, at_d + v * 8);
-        }
+        for (int i = 0; i < N; ++i)
+          if (v0 + i * nt < nv) y[i].load(a.y, at_y + (v0 + i * nt) * 8);
       }
+      if (v0 != tx) load_dout(v0);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int v = v0 + i * nt;
@@ -166,7 +171,6 @@ __global__ void __launch_bounds__(kGradThreads) unpermute_grad_kernel(const Unpe
   if (tx == 0 && on && a.dw) a.dw[pair] = dot;
   if (!a.dlogits) return;
   if (tx == 0 && on) {
-    const int id = a.ids[pair];
     if (id < 0 || id >= a.E) flag_status(status, MOE_ERR_INVALID_ARG);
     s_dw[ty] = dot;
     s_w[ty] = w;
@@ -221,8 +225,12 @@ cudaError_t launch_unpermute_grad(const UnpermuteGradArgs& a, int sms, int* stat
   while (wp < 4 && wp * 64 < nv && pairs * wp < (int64_t)sms * 16) wp *= 2;
   int tokens = 8 / (a.k * wp);
   if (tokens < 1) tokens = 1;
-  auto kern = a.y_f32 ? (a.dout_f32 ? unpermute_grad_kernel<true, true> : unpermute_grad_kernel<true, false>)
-                      : (a.dout_f32 ? unpermute_grad_kernel<false, true> : unpermute_grad_kernel<false, false>);
+  // chunks of a row in flight per lane: two of fp32 or of short rows (fewer registers, more warps)
+  const bool two = nv <= 64 * wp;
+  auto kern = a.y_f32        ? (a.dout_f32 ? unpermute_grad_kernel<true, true, 2> : unpermute_grad_kernel<true, false, 2>)
+              : a.dout_f32   ? unpermute_grad_kernel<false, true, 2>
+              : two          ? unpermute_grad_kernel<false, false, 2>
+                             : unpermute_grad_kernel<false, false, 4>;
   return launch_kernel(kern, dim3((a.T + tokens - 1) / tokens), dim3(32 * wp, a.k * tokens), 0, st, a, status);
 }
 
