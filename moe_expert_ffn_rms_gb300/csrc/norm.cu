@@ -73,49 +73,6 @@ MOE_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar
       : "memory");
 }
 
-// ------------------------------------------------------------------ forward --
-// What is left of a row once it is held in f (VPT chunks v0, v0 + step, ... per thread,
-// zeros beyond the row): mean, centred squares, output.  SUM adds one value over
-// the row's threads.
-template <int VPT, typename Sum>
-MOE_DEV void layernorm_row(const LayerNormArgs& a, int64_t t, int v0, int step, float inv, float (&f)[VPT][8],
-                           Sum sum) {
-  const int nv = a.H >> 3;
-  const size_t at = (size_t)t * a.H;
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s += f[i][q];
-  const float mean = sum(s, 0) * inv;
-  s = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-    if (v0 + i * step < nv) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        f[i][q] -= mean;
-        s = fmaf(f[i][q], f[i][q], s);
-      }
-    }
-  const float rstd = 1.0f / sqrtf(fmaf(sum(s, 1), inv, a.eps));
-  if (v0 == 0 && a.mean) {
-    a.mean[t] = mean;
-    a.rstd[t] = rstd;
-  }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = v0 + i * step;
-    if (v >= nv) continue;
-    float w[8], b[8] = {};
-    load8(a.w, a.w_f32, v * 8, w);
-    if (a.b) load8(a.b, a.w_f32, v * 8, b);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) f[i][q] = fmaf(f[i][q] * rstd, w[q], b[q]);
-    store8(a.y, a.y_f32, at + v * 8, f[i]);
-  }
-}
-
 // Eight columns as they are in memory.
 template <bool F32>
 struct Raw {
@@ -129,21 +86,114 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  MOE_DEV void get(float (&f)[8]) const {
+  MOE_DEV void get(float2 (&f)[4]) const {
     if constexpr (F32) {
-      f[0] = __uint_as_float(u[0].x); f[1] = __uint_as_float(u[0].y);
-      f[2] = __uint_as_float(u[0].z); f[3] = __uint_as_float(u[0].w);
-      f[4] = __uint_as_float(u[1].x); f[5] = __uint_as_float(u[1].y);
-      f[6] = __uint_as_float(u[1].z); f[7] = __uint_as_float(u[1].w);
+      f[0] = make_float2(__uint_as_float(u[0].x), __uint_as_float(u[0].y));
+      f[1] = make_float2(__uint_as_float(u[0].z), __uint_as_float(u[0].w));
+      f[2] = make_float2(__uint_as_float(u[1].x), __uint_as_float(u[1].y));
+      f[3] = make_float2(__uint_as_float(u[1].z), __uint_as_float(u[1].w));
     } else {
-      unpack8_bf16(u[0], f);
+      f[0] = make_float2(bf16_lo(u[0].x), bf16_hi(u[0].x));
+      f[1] = make_float2(bf16_lo(u[0].y), bf16_hi(u[0].y));
+      f[2] = make_float2(bf16_lo(u[0].z), bf16_hi(u[0].z));
+      f[3] = make_float2(bf16_lo(u[0].w), bf16_hi(u[0].w));
+    }
+  }
+};
+
+MOE_DEV void load_pairs(const void* p, bool f32, size_t at, float2 (&f)[4]) {
+  if (f32) {
+    Raw<true> r;
+    r.load(p, at);
+    r.get(f);
+  } else {
+    Raw<false> r;
+    r.load(p, at);
+    r.get(f);
+  }
+}
+
+MOE_DEV void store_pairs(void* p, bool f32, size_t at, const float2 (&f)[4]) {
+  const float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+  store8(p, f32, at, v);
+}
+
+MOE_DEV float2 both(float v) { return make_float2(v, v); }
+
+// ------------------------------------------------------------------ forward --
+// What is left of a row once it is held in f (VPT chunks v0, v0 + step, ... per thread,
+// zeros beyond the row): mean, centred squares, output.  sum adds one value over
+// the row's threads; weights(i, v, w, b) gives a chunk's weight and bias.
+template <int VPT, typename Sum, typename Weights>
+MOE_DEV void layernorm_row(const LayerNormArgs& a, int64_t t, int v0, int step, float inv, float2 (&f)[VPT][4],
+                           Sum sum, Weights weights) {
+  const int nv = a.H >> 3;
+  float2 s = both(0.f);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s = add_f2(s, f[i][q]);
+  const float mean = sum(s.x + s.y, 0) * inv;
+  s = both(0.f);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (v0 + i * step < nv) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f[i][q] = add_f2(f[i][q], both(-mean));
+        s = fma_f2(f[i][q], f[i][q], s);
+      }
+    }
+  const float rstd = 1.0f / sqrtf(fmaf(sum(s.x + s.y, 1), inv, a.eps));
+  if (v0 == 0 && a.mean) {
+    a.mean[t] = mean;
+    a.rstd[t] = rstd;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = v0 + i * step;
+    if (v >= nv) continue;
+    float2 w[4], b[4];
+    weights(i, v, w, b);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f[i][q] = fma_f2(mul_f2(f[i][q], both(rstd)), w[q], b[q]);
+    store_pairs(a.y, a.y_f32, (size_t)t * a.H + v * 8, f[i]);
+  }
+}
+
+// The weights and bias of a thread's chunks for all of its rows: bf16 ones stay in
+// registers, fp32 ones (and those of a thread with one row) are read where they are used.
+template <int VPT, bool KEPT>
+struct Weights {
+  Raw<false> w[KEPT ? VPT : 1], b[KEPT ? VPT : 1];
+  MOE_DEV void load(const LayerNormArgs& a, int v0, int step) {
+    if constexpr (KEPT) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        b[i].zero();
+        if (v0 + i * step < (a.H >> 3)) {
+          w[i].load(a.w, (v0 + i * step) * 8);
+          if (a.b) b[i].load(a.b, (v0 + i * step) * 8);
+        }
+      }
+    }
+  }
+  MOE_DEV void get(const LayerNormArgs& a, int i, int v, float2 (&fw)[4], float2 (&fb)[4]) const {
+    if constexpr (KEPT) {
+      w[i].get(fw);
+      b[i].get(fb);
+    } else {
+      load_pairs(a.w, a.w_f32, v * 8, fw);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) fb[q] = both(0.f);
+      if (a.b) load_pairs(a.b, a.w_f32, v * 8, fb);
     }
   }
 };
 
 // A warp takes the rows t, t + all warps, ...; the next one is on its way while it works
 // on one.
-template <int VPT, bool XF32>
+template <int VPT, bool XF32, bool KEPT>
 __global__ void __launch_bounds__(kNarrowWarps * 32) layernorm_narrow_kernel(const LayerNormArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -160,12 +210,16 @@ __global__ void __launch_bounds__(kNarrowWarps * 32) layernorm_narrow_kernel(con
     }
   };
   load(t);
+  Weights<VPT, KEPT> wb;
+  wb.load(a, lane, 32);
   for (; t < a.T; t += step) {
-    float f[VPT][8];
+    float2 f[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) next[i].get(f[i]);
     load(t + step);
-    layernorm_row<VPT>(a, t, lane, 32, inv, f, [](float v, int) { return warp_sum(v); });
+    layernorm_row<VPT>(
+        a, t, lane, 32, inv, f, [](float v, int) { return warp_sum(v); },
+        [&](int i, int v, float2 (&w)[4], float2 (&b)[4]) { wb.get(a, i, v, w, b); });
   }
 }
 
@@ -173,33 +227,39 @@ __global__ void __launch_bounds__(kNarrowWarps * 32) layernorm_narrow_kernel(con
 // warp repeats, are few beside the row's own (8192 x 7168 bf16 with two chunks: 69 us).
 constexpr int kRowVpt = 4;
 constexpr int kRowNw = 16;
+constexpr int kRowThreadsPerSm = 672;  // of the streaming form: 96 registers each
 
-template <bool XF32>
+template <bool XF32, bool KEPT>
 __global__ void __launch_bounds__(kRowNw * 32) layernorm_row_kernel(const LayerNormArgs a) {
   __shared__ float red[2][1][kRowNw];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, nt = blockDim.x, nv = a.H >> 3;
-  float f[kRowVpt][8];
+  float2 f[kRowVpt][4];
 #pragma unroll
   for (int i = 0; i < kRowVpt; ++i) {
     const int v = tid + i * nt;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
-    if (v < nv) load8(a.x, XF32, (size_t)blockIdx.x * a.H + v * 8, f[i]);
+    for (int q = 0; q < 4; ++q) f[i][q] = both(0.f);
+    if (v < nv) load_pairs(a.x, XF32, (size_t)blockIdx.x * a.H + v * 8, f[i]);
   }
-  layernorm_row<kRowVpt>(a, blockIdx.x, tid, nt, 1.0f / (float)a.H, f, [&](float v, int i) {
-    float s[1] = {v};
-    block_sums(s, red[i]);
-    return s[0];
-  });
+  Weights<kRowVpt, KEPT> wb;  // (on their way during the reductions)
+  wb.load(a, tid, nt);
+  layernorm_row<kRowVpt>(
+      a, blockIdx.x, tid, nt, 1.0f / (float)a.H, f,
+      [&](float v, int i) {
+        float s[1] = {v};
+        block_sums(s, red[i]);
+        return s[0];
+      },
+      [&](int i, int v, float2 (&w)[4], float2 (&b)[4]) { wb.get(a, i, v, w, b); });
 }
 
 // Stage n % S holds row blockIdx.x + n gridDim.x.  A stage is free once the row's
 // first reduction has passed (every thread holds its part), and thread 0 then sends for
 // the row S further on.
-template <bool XF32>
-__global__ void __launch_bounds__(kRowNw * 32, 2)
+template <bool XF32, bool KEPT>
+__global__ void __launch_bounds__(kRowThreadsPerSm)
     layernorm_stream_kernel(const LayerNormArgs a, int S, int* status) {
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ float red[2][1][kRowNw];
@@ -223,25 +283,30 @@ __global__ void __launch_bounds__(kRowNw * 32, 2)
   if (tid == 0)
     for (int s = 0; s < S; ++s)
       if (blockIdx.x + (int64_t)s * gridDim.x < a.T) send(blockIdx.x + (int64_t)s * gridDim.x, s);
+  Weights<kRowVpt, KEPT> wb;
+  wb.load(a, tid, nt);
   int s = 0;
   uint32_t ph = 0;
   bool ok = true;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     ok = ptx::mbar_wait(&full[s], ph, &s_abort) && ok;
-    float f[kRowVpt][8];
+    float2 f[kRowVpt][4];
 #pragma unroll
     for (int i = 0; i < kRowVpt; ++i) {
       const int v = tid + i * nt;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
-      if (v < nv) load8(stages + (size_t)s * bytes, XF32, v * 8, f[i]);
+      for (int q = 0; q < 4; ++q) f[i][q] = both(0.f);
+      if (v < nv) load_pairs(stages + (size_t)s * bytes, XF32, v * 8, f[i]);
     }
-    layernorm_row<kRowVpt>(a, t, tid, nt, inv, f, [&](float v, int i) {
-      float r[1] = {v};
-      block_sums(r, red[i]);
-      if (i == 0 && tid == 0 && ok && t + (int64_t)S * gridDim.x < a.T) send(t + (int64_t)S * gridDim.x, s);
-      return r[0];
-    });
+    layernorm_row<kRowVpt>(
+        a, t, tid, nt, inv, f,
+        [&](float v, int i) {
+          float r[1] = {v};
+          block_sums(r, red[i]);
+          if (i == 0 && tid == 0 && ok && t + (int64_t)S * gridDim.x < a.T) send(t + (int64_t)S * gridDim.x, s);
+          return r[0];
+        },
+        [&](int i, int v, float2 (&w)[4], float2 (&b)[4]) { wb.get(a, i, v, w, b); });
     if (++s == S) {
       s = 0;
       ph ^= 1;
@@ -251,33 +316,34 @@ __global__ void __launch_bounds__(kRowNw * 32, 2)
 }
 
 // ----------------------------------------------------------------- backward --
-// One row, x and g = dy (VPT chunks per thread, zeros beyond the row) and res(i, v, d)
-// to load dres's chunk.  sum adds two values over the row's threads.
-template <int VPT, bool RMS, typename Sum, typename Res>
-MOE_DEV void norm_grad_row(const NormGradArgs& a, int64_t t, int v0, int step, float (&x)[VPT][8],
-                           float (&g)[VPT][8], float (&dw)[VPT][8], float (&db)[VPT][8], float m, float r, Sum sum,
-                           Res res) {
+// One row, x and g = dy (VPT chunks per thread, zeros beyond the row); w(i, v, f) gives
+// the weights of a chunk and res(i, v, f) its part of dres.  sum adds two values over the
+// row's threads.
+template <int VPT, bool RMS, typename Sum, typename W, typename Res>
+MOE_DEV void norm_grad_row(const NormGradArgs& a, int64_t t, int v0, int step, float inv, float2 (&x)[VPT][4],
+                           float2 (&g)[VPT][4], float2 (&dw)[VPT][4], float2 (&db)[VPT][4], float m, float r, Sum sum,
+                           W weights, Res res) {
   const int nv = a.H >> 3;
-  const float inv = 1.0f / (float)a.H;
-  float s[2] = {0.f, 0.f};
+  float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = v0 + i * step;
     if (v >= nv) continue;
-    float w[8];
-    load8(a.w, a.w_f32, v * 8, w);
+    float2 w[4];
+    weights(i, v, w);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float gw = g[i][q] * w[q];
+    for (int q = 0; q < 4; ++q) {
+      const float2 gw = mul_f2(g[i][q], w[q]);
       if (RMS) {
-        s[0] = fmaf(x[i][q], x[i][q], s[0]);
+        s0 = fma_f2(x[i][q], x[i][q], s0);
       } else {
-        x[i][q] = (x[i][q] - m) * r;
-        s[0] += gw;
+        x[i][q] = mul_f2(add_f2(x[i][q], both(-m)), both(r));
+        s0 = add_f2(s0, gw);
       }
-      s[1] = fmaf(gw, x[i][q], s[1]);
+      s1 = fma_f2(gw, x[i][q], s1);
     }
   }
+  float s[2] = {s0.x + s0.y, s1.x + s1.y};
   sum(s);
   float c0 = 0.f, c1 = s[1] * inv;
   if (RMS) {
@@ -290,41 +356,43 @@ MOE_DEV void norm_grad_row(const NormGradArgs& a, int64_t t, int v0, int step, f
   for (int i = 0; i < VPT; ++i) {
     const int v = v0 + i * step;
     if (v >= nv) continue;
-    float w[8], d[8] = {};
-    load8(a.w, a.w_f32, v * 8, w);
+    float2 w[4], d[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d[q] = both(0.f);
+    weights(i, v, w);
     if (a.dres) res(i, v, d);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float xh = RMS ? x[i][q] * r : x[i][q];
-      dw[i][q] = fmaf(g[i][q], xh, dw[i][q]);
-      if (!RMS) db[i][q] += g[i][q];
-      d[q] = fmaf(r, fmaf(g[i][q], w[q], -c0) - xh * c1, d[q]);
+    for (int q = 0; q < 4; ++q) {
+      const float2 xh = RMS ? mul_f2(x[i][q], both(r)) : x[i][q];
+      dw[i][q] = fma_f2(g[i][q], xh, dw[i][q]);
+      if (!RMS) db[i][q] = add_f2(db[i][q], g[i][q]);
+      d[q] = fma_f2(both(r), fma_f2(xh, both(-c1), fma_f2(g[i][q], w[q], both(-c0))), d[q]);
     }
-    store8(a.dx, a.x_f32, (size_t)t * a.H + v * 8, d);
+    store_pairs(a.dx, a.x_f32, (size_t)t * a.H + v * 8, d);
   }
 }
 
 // A thread's sums to the CTA's row [2, H] of the workspace.
 template <int VPT>
-MOE_DEV void norm_grad_part(const NormGradArgs& a, int v0, int step, const float (&dw)[VPT][8],
-                            const float (&db)[VPT][8]) {
+MOE_DEV void norm_grad_part(const NormGradArgs& a, int v0, int step, const float2 (&dw)[VPT][4],
+                            const float2 (&db)[VPT][4]) {
   float* part = static_cast<float*>(a.workspace) + (size_t)blockIdx.x * 2 * a.H;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = v0 + i * step;
     if (v >= (a.H >> 3)) continue;
-    store8(part, true, v * 8, dw[i]);
-    if (a.db) store8(part, true, a.H + v * 8, db[i]);
+    store_pairs(part, true, v * 8, dw[i]);
+    if (a.db) store_pairs(part, true, a.H + v * 8, db[i]);
   }
 }
 
 template <int VPT, bool RMS, bool XF32, bool DF32>
 __global__ void __launch_bounds__(kNarrowWarps * 32, kNarrowCtas) norm_grad_narrow_kernel(const NormGradArgs a) {
-  __shared__ float sums[2][kNarrowMaxV * 8];
+  __shared__ __align__(16) float sums[2][kNarrowMaxV * 8];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nv = a.H >> 3;
-  float dw[VPT][8] = {}, db[VPT][8] = {};
+  float2 dw[VPT][4] = {}, db[VPT][4] = {};
   const int64_t step = (int64_t)gridDim.x * kNarrowWarps;
   int64_t t = (int64_t)blockIdx.x * kNarrowWarps + warp;
   Raw<XF32> nx[VPT], nd[VPT];
@@ -348,8 +416,13 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, kNarrowCtas) norm_grad_narr
     }
   };
   load(t);
+  const float inv = 1.0f / (float)a.H;
+  float2 w[VPT][4] = {};
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (lane + i * 32 < nv) load_pairs(a.w, a.w_f32, (lane + i * 32) * 8, w[i]);
   for (; t < a.T; t += step) {
-    float x[VPT][8], g[VPT][8];
+    float2 x[VPT][4], g[VPT][4];
     Raw<XF32> d[VPT];
     const float m = nm, r = nr;
 #pragma unroll
@@ -360,8 +433,12 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, kNarrowCtas) norm_grad_narr
     }
     load(t + step);
     norm_grad_row<VPT, RMS>(
-        a, t, lane, 32, x, g, dw, db, m, r, [](float (&s)[2]) { warp_sums(s); },
-        [&](int i, int, float (&e)[8]) { d[i].get(e); });
+        a, t, lane, 32, inv, x, g, dw, db, m, r, [](float (&s)[2]) { warp_sums(s); },
+        [&](int i, int, float2 (&e)[4]) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) e[q] = w[i][q];
+        },
+        [&](int i, int, float2 (&e)[4]) { d[i].get(e); });
   }
   // the warps' sums, one warp after the other
   for (int k = 0; k < kNarrowWarps; ++k) {
@@ -370,14 +447,16 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, kNarrowCtas) norm_grad_narr
       for (int i = 0; i < VPT; ++i) {
         const int v = lane + i * 32;
         if (v >= nv) continue;
+        float2* s0 = reinterpret_cast<float2*>(&sums[0][v * 8]);
+        float2* s1 = reinterpret_cast<float2*>(&sums[1][v * 8]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 4; ++q) {
           if (k > 0) {
-            dw[i][q] += sums[0][v * 8 + q];
-            db[i][q] += sums[1][v * 8 + q];
+            dw[i][q] = add_f2(s0[q], dw[i][q]);
+            db[i][q] = add_f2(s1[q], db[i][q]);
           }
-          sums[0][v * 8 + q] = dw[i][q];
-          sums[1][v * 8 + q] = db[i][q];
+          s0[q] = dw[i][q];
+          s1[q] = db[i][q];
         }
       }
     }
@@ -392,11 +471,12 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradA
   pdl_trigger();
   pdl_wait();
   const int nv = a.H >> 3, tid = threadIdx.x, nt = blockDim.x;
-  float dw[VPT][8] = {}, db[VPT][8] = {};
+  float2 dw[VPT][4] = {}, db[VPT][4] = {};
   int n = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, ++n) {
     const size_t at = (size_t)t * a.H;
-    float x[VPT][8], g[VPT][8], m = 0.f, r = 0.f;
+    float2 x[VPT][4], g[VPT][4];
+    float m = 0.f, r = 0.f;
     if (!RMS) {
       r = a.rstd[t];
       m = a.mean[t];
@@ -405,15 +485,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradA
     for (int i = 0; i < VPT; ++i) {
       const int v = tid + i * nt;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[i][q] = g[i][q] = 0.f;
+      for (int q = 0; q < 4; ++q) x[i][q] = g[i][q] = both(0.f);
       if (v < nv) {
-        load8(a.x, a.x_f32, at + v * 8, x[i]);
-        load8(a.dy, a.dy_f32, at + v * 8, g[i]);
+        load_pairs(a.x, a.x_f32, at + v * 8, x[i]);
+        load_pairs(a.dy, a.dy_f32, at + v * 8, g[i]);
       }
     }
     norm_grad_row<VPT, RMS>(
-        a, t, tid, nt, x, g, dw, db, m, r, [&](float (&s)[2]) { block_sums(s, red[n & 1]); },
-        [&](int, int v, float (&d)[8]) { load8(a.dres, a.x_f32, at + v * 8, d); });
+        a, t, tid, nt, 1.0f / (float)a.H, x, g, dw, db, m, r, [&](float (&s)[2]) { block_sums(s, red[n & 1]); },
+        [&](int, int v, float2 (&f)[4]) { load_pairs(a.w, a.w_f32, v * 8, f); },
+        [&](int, int v, float2 (&d)[4]) { load_pairs(a.dres, a.x_f32, at + v * 8, d); });
   }
   norm_grad_part<VPT>(a, tid, nt, dw, db);
 }
@@ -452,16 +533,26 @@ __global__ void __launch_bounds__(kGradNw * 32) norm_grad_stream_kernel(const No
   if (tid == 0)
     for (int s = 0; s < S; ++s)
       if (blockIdx.x + (int64_t)s * gridDim.x < a.T) send(blockIdx.x + (int64_t)s * gridDim.x, s);
-  float dw[V][8] = {}, db[V][8] = {};
+  float2 dw[V][4] = {}, db[V][4] = {}, w[V][4] = {};
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (tid + i * nt < nv) load_pairs(a.w, a.w_f32, (tid + i * nt) * 8, w[i]);
+  const float inv = 1.0f / (float)a.H;
+  float nm = 0.f, nr = 0.f;
+  if (!RMS) {  // (the grid has no more CTAs than rows)
+    nr = a.rstd[blockIdx.x];
+    nm = a.mean[blockIdx.x];
+  }
   int s = 0, n = 0;
   uint32_t ph = 0;
   bool ok = true;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, ++n) {
-    float x[V][8], g[V][8], m = 0.f, r = 0.f;
+    float2 x[V][4], g[V][4];
     Raw<XF32> d[V];
-    if (!RMS) {
-      r = a.rstd[t];
-      m = a.mean[t];
+    const float m = nm, r = nr;
+    if (!RMS && t + gridDim.x < a.T) {  // (a row ahead: their latency would be in every row)
+      nr = a.rstd[t + gridDim.x];
+      nm = a.mean[t + gridDim.x];
     }
     ok = ptx::mbar_wait(&full[s], ph, &s_abort) && ok;
     const unsigned char* from = stages + (size_t)s * stage;
@@ -469,20 +560,24 @@ __global__ void __launch_bounds__(kGradNw * 32) norm_grad_stream_kernel(const No
     for (int i = 0; i < V; ++i) {
       const int v = tid + i * nt;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[i][q] = g[i][q] = 0.f;
+      for (int q = 0; q < 4; ++q) x[i][q] = g[i][q] = both(0.f);
       if (v < nv) {
-        load8(from, XF32, v * 8, x[i]);
-        load8(from + xb, DF32, v * 8, g[i]);
+        load_pairs(from, XF32, v * 8, x[i]);
+        load_pairs(from + xb, DF32, v * 8, g[i]);
         if (rb) d[i].load(from + xb + gb, v * 8);
       }
     }
     norm_grad_row<V, RMS>(
-        a, t, tid, nt, x, g, dw, db, m, r,
+        a, t, tid, nt, inv, x, g, dw, db, m, r,
         [&](float (&v)[2]) {
           block_sums(v, red[n & 1]);
           if (tid == 0 && ok && t + (int64_t)S * gridDim.x < a.T) send(t + (int64_t)S * gridDim.x, s);
         },
-        [&](int i, int, float (&e)[8]) { d[i].get(e); });
+        [&](int i, int, float2 (&f)[4]) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) f[q] = w[i][q];
+        },
+        [&](int i, int, float2 (&f)[4]) { d[i].get(f); });
     if (++s == S) {
       s = 0;
       ph ^= 1;
@@ -516,10 +611,10 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_grad_sum_kernel(const flo
 
 int row_threads(int nv) { return (nv + 31) / 32 * 32; }
 
-// CTAs per SM: the forward kernels are held to 64 registers, the backward ones to 128.
+// CTAs per SM: the forward kernels have at most 96 registers, the backward ones 128.
 int row_ctas(int nv) {
-  const int n = 1024 / row_threads((nv + kRowVpt - 1) / kRowVpt);
-  return n < 16 ? n : 16;
+  const int n = kRowThreadsPerSm / row_threads((nv + kRowVpt - 1) / kRowVpt);
+  return n < 1 ? 1 : (n < 16 ? n : 16);
 }
 int grad_ctas(int nv) {
   const int n = 512 / row_threads((nv + kGradVpt - 1) / kGradVpt);
@@ -548,18 +643,25 @@ cudaError_t launch_layernorm(const LayerNormArgs& a, int sms, int* status, cudaS
   if (nv <= kNarrowMaxV) {
     const int64_t n = ((int64_t)a.T + kNarrowWarps - 1) / kNarrowWarps;
     const int grid = (int)(n < sms * 8 ? n : sms * 8);
-    auto kern = nv <= 32 ? (a.x_f32 ? layernorm_narrow_kernel<1, true> : layernorm_narrow_kernel<1, false>)
-                         : (a.x_f32 ? layernorm_narrow_kernel<2, true> : layernorm_narrow_kernel<2, false>);
+    auto pick = [&](auto k) {
+      constexpr bool K = decltype(k)::value;
+      return nv <= 32 ? (a.x_f32 ? layernorm_narrow_kernel<1, true, K> : layernorm_narrow_kernel<1, false, K>)
+                      : (a.x_f32 ? layernorm_narrow_kernel<2, true, K> : layernorm_narrow_kernel<2, false, K>);
+    };
+    auto kern = a.w_f32 ? pick(std::false_type{}) : pick(std::true_type{});
     return launch_kernel(kern, dim3(grid), dim3(kNarrowWarps * 32), 0, st, a);
   }
   const int threads = row_threads((nv + kRowVpt - 1) / kRowVpt), ctas = row_ctas(nv);
   const int64_t bytes = (int64_t)a.H * (a.x_f32 ? 4 : 2);
   if (a.T <= sms * ctas)
-    return launch_kernel(a.x_f32 ? layernorm_row_kernel<true> : layernorm_row_kernel<false>, dim3(a.T), dim3(threads),
-                         0, st, a);
+    return launch_kernel(
+        a.x_f32 ? (a.w_f32 ? layernorm_row_kernel<true, false> : layernorm_row_kernel<true, true>)
+                : (a.w_f32 ? layernorm_row_kernel<false, false> : layernorm_row_kernel<false, true>),
+        dim3(a.T), dim3(threads), 0, st, a);
   int S = (int)(kNormSmem / ctas / bytes);
   if (S > kNormStages) S = kNormStages;
-  auto kern = a.x_f32 ? layernorm_stream_kernel<true> : layernorm_stream_kernel<false>;
+  auto kern = a.x_f32 ? (a.w_f32 ? layernorm_stream_kernel<true, false> : layernorm_stream_kernel<true, true>)
+                      : (a.w_f32 ? layernorm_stream_kernel<false, false> : layernorm_stream_kernel<false, true>);
   // the same limit in every call: another thread's launch may lie between this and ours
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
   if (e != cudaSuccess) return e;
