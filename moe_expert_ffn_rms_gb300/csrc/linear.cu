@@ -15,6 +15,7 @@
 #include <stdlib.h>
 
 #include "block_tail.cuh"
+#include "column_sum.cuh"
 #include "common.cuh"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
@@ -802,23 +803,6 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradArgs a, int 
   store8(a.part, true, (size_t)((int64_t)blockIdx.y * a.N + c), s);
 }
 
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part, int n, int64_t N,
-                                                         float* out) {
-  __shared__ float red[8][32];
-  pdl_trigger();
-  pdl_wait();
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + x;
-  float s = 0.f;
-  if (c < N)
-    for (int i = y; i < n; i += 8) s += part[i * N + c];
-  red[y][x] = s;
-  __syncthreads();
-  if (y != 0 || c >= N) return;
-  for (int i = 1; i < 8; ++i) s += red[i][x];
-  out[c] = s;
-}
-
 // ------------------------------------------------------------------ host --
 // Map of an operand: K-major [rows, K] in boxes of 64 K x box_rows, or MN-major
 // [K, rows] in boxes of 64 rows x 64 K.
@@ -1014,8 +998,7 @@ cudaError_t launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   if (!a.db) return cudaSuccess;
-  return launch_kernel(column_sum_kernel, dim3((unsigned)((a.N + 31) / 32)), dim3(256), 0, st,
-                       (const float*)a.part, (int)shares, a.N, a.db);
+  return launch_column_sum(a.part, (int)shares, a.N, a.N, a.N, a.db, nullptr, sms, st);
 }
 
 }  // namespace moe

@@ -20,6 +20,7 @@
 // their part of dw and db in registers; each CTA leaves one row of partial sums,
 // and a second kernel adds those in their order.
 #include "block_tail.cuh"
+#include "column_sum.cuh"
 #include "common.cuh"
 #include "tc_ptx.cuh"
 #include "train.h"
@@ -59,10 +60,35 @@ MOE_DEV void block_sums(float (&v)[N], float (*red)[NW]) {
   }
 }
 
-template <int N>
-MOE_DEV void warp_sums(float (&v)[N]) {
+// The sums of two values over the warp: the half-warps take one each after the first
+// step.  Lanes 0 to 15 return v[0]'s, lanes 16 to 31 v[1]'s.
+MOE_DEV float warp_halves(const float (&v)[2]) {
+  const bool hi = (threadIdx.x & 16) != 0;
+  float u = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[1], 16);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+  for (int o = 8; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+  return u;
+}
+
+MOE_DEV void warp_sums2(float (&v)[2]) {
+  const float u = warp_halves(v);
+  v[0] = __shfl_sync(0xffffffffu, u, 0);
+  v[1] = __shfl_sync(0xffffffffu, u, 16);
+}
+
+// Both over a CTA of at most 16 warps (red as in block_sums).
+MOE_DEV void block_sums2(float (&v)[2], float (*red)[16]) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  float u = warp_halves(v);
+  if ((lane & 15) == 0) red[lane >> 4][wid] = u;
+  __syncthreads();
+  if (nw > 1) {
+    u = (lane & 15) < nw ? red[lane >> 4][lane & 15] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+  }
+  v[0] = __shfl_sync(0xffffffffu, u, 0);
+  v[1] = __shfl_sync(0xffffffffu, u, 16);
 }
 
 MOE_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -113,6 +139,18 @@ MOE_DEV void load_pairs(const void* p, bool f32, size_t at, float2 (&f)[4]) {
   }
 }
 
+// The same from shared memory.
+template <bool F32>
+MOE_DEV Raw<F32> load_shared(uint32_t saddr) {
+  Raw<F32> r;
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.u[i].x), "=r"(r.u[i].y), "=r"(r.u[i].z), "=r"(r.u[i].w)
+                 : "r"(saddr + 16 * i));
+  return r;
+}
+
 MOE_DEV void store_pairs(void* p, bool f32, size_t at, const float2 (&f)[4]) {
   const float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
   store8(p, f32, at, v);
@@ -144,7 +182,7 @@ MOE_DEV void layernorm_row(const LayerNormArgs& a, int64_t t, int v0, int step, 
         s = fma_f2(f[i][q], f[i][q], s);
       }
     }
-  const float rstd = 1.0f / sqrtf(fmaf(sum(s.x + s.y, 1), inv, a.eps));
+  const float rstd = rsqrtf(fmaf(sum(s.x + s.y, 1), inv, a.eps));  // (within two units in the last place)
   if (v0 == 0 && a.mean) {
     a.mean[t] = mean;
     a.rstd[t] = rstd;
@@ -225,9 +263,9 @@ __global__ void __launch_bounds__(kNarrowWarps * 32) layernorm_narrow_kernel(con
 
 // CTA-wide forms: kRowVpt chunks per thread, so that the reductions' instructions, which every
 // warp repeats, are few beside the row's own (8192 x 7168 bf16 with two chunks: 69 us).
-constexpr int kRowVpt = 4;
-constexpr int kRowNw = 16;
-constexpr int kRowThreadsPerSm = 672;  // of the streaming form: 96 registers each
+constexpr int kRowVpt = 2;
+constexpr int kRowNw = 32;
+constexpr int kRowThreadsPerSm = 1024;  // of the streaming form: 64 registers each
 
 template <bool XF32, bool KEPT>
 __global__ void __launch_bounds__(kRowNw * 32) layernorm_row_kernel(const LayerNormArgs a) {
@@ -296,7 +334,7 @@ __global__ void __launch_bounds__(kRowThreadsPerSm)
       const int v = tid + i * nt;
 #pragma unroll
       for (int q = 0; q < 4; ++q) f[i][q] = both(0.f);
-      if (v < nv) load_pairs(stages + (size_t)s * bytes, XF32, v * 8, f[i]);
+      if (v < nv) load_shared<XF32>(ptx::smem_u32(stages) + s * bytes + v * (XF32 ? 32 : 16)).get(f[i]);
     }
     layernorm_row<kRowVpt>(
         a, t, tid, nt, inv, f,
@@ -318,11 +356,11 @@ __global__ void __launch_bounds__(kRowThreadsPerSm)
 // ----------------------------------------------------------------- backward --
 // One row, x and g = dy (VPT chunks per thread, zeros beyond the row); w(i, v, f) gives
 // the weights of a chunk and res(i, v, f) its part of dres.  sum adds two values over the
-// row's threads.
-template <int VPT, bool RMS, typename Sum, typename W, typename Res>
+// row's threads; store(at, f) writes a chunk of dx.
+template <int VPT, bool RMS, typename Sum, typename W, typename Res, typename Store>
 MOE_DEV void norm_grad_row(const NormGradArgs& a, int64_t t, int v0, int step, float inv, float2 (&x)[VPT][4],
                            float2 (&g)[VPT][4], float2 (&dw)[VPT][4], float2 (&db)[VPT][4], float m, float r, Sum sum,
-                           W weights, Res res) {
+                           W weights, Res res, Store store) {
   const int nv = a.H >> 3;
   float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
@@ -347,7 +385,7 @@ MOE_DEV void norm_grad_row(const NormGradArgs& a, int64_t t, int v0, int step, f
   sum(s);
   float c0 = 0.f, c1 = s[1] * inv;
   if (RMS) {
-    r = 1.0f / sqrtf(fmaf(s[0], inv, a.eps));
+    r = rsqrtf(fmaf(s[0], inv, a.eps));
     c1 *= r;
   } else {
     c0 = s[0] * inv;
@@ -368,7 +406,7 @@ MOE_DEV void norm_grad_row(const NormGradArgs& a, int64_t t, int v0, int step, f
       if (!RMS) db[i][q] = add_f2(db[i][q], g[i][q]);
       d[q] = fma_f2(both(r), fma_f2(xh, both(-c1), fma_f2(g[i][q], w[q], both(-c0))), d[q]);
     }
-    store_pairs(a.dx, a.x_f32, (size_t)t * a.H + v * 8, d);
+    store((size_t)t * a.H + v * 8, d);
   }
 }
 
@@ -433,12 +471,13 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, kNarrowCtas) norm_grad_narr
     }
     load(t + step);
     norm_grad_row<VPT, RMS>(
-        a, t, lane, 32, inv, x, g, dw, db, m, r, [](float (&s)[2]) { warp_sums(s); },
+        a, t, lane, 32, inv, x, g, dw, db, m, r, [](float (&s)[2]) { warp_sums2(s); },
         [&](int i, int, float2 (&e)[4]) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) e[q] = w[i][q];
         },
-        [&](int i, int, float2 (&e)[4]) { d[i].get(e); });
+        [&](int i, int, float2 (&e)[4]) { d[i].get(e); },
+        [&](size_t to, const float2 (&e)[4]) { store_pairs(a.dx, XF32, to, e); });
   }
   // the warps' sums, one warp after the other
   for (int k = 0; k < kNarrowWarps; ++k) {
@@ -494,7 +533,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradA
     norm_grad_row<VPT, RMS>(
         a, t, tid, nt, 1.0f / (float)a.H, x, g, dw, db, m, r, [&](float (&s)[2]) { block_sums(s, red[n & 1]); },
         [&](int, int v, float2 (&f)[4]) { load_pairs(a.w, a.w_f32, v * 8, f); },
-        [&](int, int v, float2 (&d)[4]) { load_pairs(a.dres, a.x_f32, at + v * 8, d); });
+        [&](int, int v, float2 (&d)[4]) { load_pairs(a.dres, a.x_f32, at + v * 8, d); },
+        [&](size_t to, const float2 (&d)[4]) { store_pairs(a.dx, a.x_f32, to, d); });
   }
   norm_grad_part<VPT>(a, tid, nt, dw, db);
 }
@@ -555,29 +595,30 @@ __global__ void __launch_bounds__(kGradNw * 32) norm_grad_stream_kernel(const No
       nm = a.mean[t + gridDim.x];
     }
     ok = ptx::mbar_wait(&full[s], ph, &s_abort) && ok;
-    const unsigned char* from = stages + (size_t)s * stage;
+    const uint32_t from = ptx::smem_u32(stages) + s * stage;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = tid + i * nt;
 #pragma unroll
       for (int q = 0; q < 4; ++q) x[i][q] = g[i][q] = both(0.f);
       if (v < nv) {
-        load_pairs(from, XF32, v * 8, x[i]);
-        load_pairs(from + xb, DF32, v * 8, g[i]);
-        if (rb) d[i].load(from + xb + gb, v * 8);
+        load_shared<XF32>(from + v * (XF32 ? 32 : 16)).get(x[i]);
+        load_shared<DF32>(from + xb + v * (DF32 ? 32 : 16)).get(g[i]);
+        if (rb) d[i] = load_shared<XF32>(from + xb + gb + v * (XF32 ? 32 : 16));
       }
     }
     norm_grad_row<V, RMS>(
         a, t, tid, nt, inv, x, g, dw, db, m, r,
         [&](float (&v)[2]) {
-          block_sums(v, red[n & 1]);
+          block_sums2(v, red[n & 1]);
           if (tid == 0 && ok && t + (int64_t)S * gridDim.x < a.T) send(t + (int64_t)S * gridDim.x, s);
         },
         [&](int i, int, float2 (&f)[4]) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) f[q] = w[i][q];
         },
-        [&](int i, int, float2 (&f)[4]) { d[i].get(f); });
+        [&](int i, int, float2 (&f)[4]) { d[i].get(f); },
+        [&](size_t to, const float2 (&f)[4]) { store_pairs(a.dx, XF32, to, f); });
     if (++s == S) {
       s = 0;
       ph ^= 1;
@@ -587,37 +628,15 @@ __global__ void __launch_bounds__(kGradNw * 32) norm_grad_stream_kernel(const No
   if (!ok && tid == 0) flag_status(status, MOE_ERR_TIMEOUT);
 }
 
-// dw (and db) = the sum of the n partial rows, in their order.
-constexpr int kSumWarps = 16;
-__global__ void __launch_bounds__(kSumWarps * 32) norm_grad_sum_kernel(const float* __restrict__ part, int n, int H,
-                                                                       float* dw, float* db) {
-  __shared__ float red[kSumWarps][32];
-  pdl_trigger();
-  pdl_wait();
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, cols = db ? 2 * H : H;
-  const int c = blockIdx.x * 32 + x;
-  float s = 0.f;
-  if (c < cols) {
-#pragma unroll 8
-    for (int i = y; i < n; i += kSumWarps) s += part[(size_t)i * 2 * H + c];
-  }
-  red[y][x] = s;
-  __syncthreads();
-  if (y != 0 || c >= cols) return;
-  for (int i = 1; i < kSumWarps; ++i) s += red[i][x];
-  if (c < H) dw[c] = s;
-  else db[c - H] = s;
-}
-
 int row_threads(int nv) { return (nv + 31) / 32 * 32; }
 
-// CTAs per SM: the forward kernels have at most 96 registers, the backward ones 128.
+// CTAs per SM: the forward kernels have at most 64 registers, the backward ones 128.
 int row_ctas(int nv) {
   const int n = kRowThreadsPerSm / row_threads((nv + kRowVpt - 1) / kRowVpt);
   return n < 1 ? 1 : (n < 16 ? n : 16);
 }
 int grad_ctas(int nv) {
-  const int n = 512 / row_threads((nv + kGradVpt - 1) / kGradVpt);
+  const int n = kGradNw * 32 / row_threads((nv + kGradVpt - 1) / kGradVpt);
   return n < 8 ? n : 8;
 }
 
@@ -710,8 +729,7 @@ cudaError_t launch_norm_grad(const NormGradArgs& a, int sms, int* status, cudaSt
     if (e != cudaSuccess) return e;
   }
   const int cols = a.db ? 2 * a.H : a.H;
-  return launch_kernel(norm_grad_sum_kernel, dim3((cols + 31) / 32), dim3(kSumWarps * 32), 0, st,
-                       (const float*)a.workspace, grid, a.H, a.dw, a.db);
+  return launch_column_sum((const float*)a.workspace, grid, 2 * (int64_t)a.H, cols, a.H, a.dw, a.db, sms, st);
 }
 
 }  // namespace moe
