@@ -14,6 +14,8 @@
 #include <cuda.h>
 #include <stdlib.h>
 
+#include <atomic>
+
 #include "block_tail.cuh"
 #include "column_sum.cuh"
 #include "common.cuh"
@@ -138,6 +140,8 @@ MOE_DEV void epilogue4(const Epi& e, int64_t q, int64_t p, float (&v)[4]) {
 // of K.  Each leaves its fp32 tile in its shared memory (over the ring), then
 // every CTA adds a share of the tile's elements over the cluster in rank order and
 // runs the epilogue on them: no workspace, no atomics, the same bits every time.
+constexpr int kMaxSplit = 8;  // CTAs of a cluster
+
 struct SplitP {
   Epi e;
   int steps;        // stages of the whole K
@@ -333,10 +337,16 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
     for (int u = (int)((int64_t)units * rank / S) + threadIdx.x; u < u1; u += kLinThreads) {
       const int64_t pc = p0 + (u & 31) * 4;
       if (pc >= p.e.P) continue;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (uint32_t r = 0; r < S; ++r) {
-        const float4 w = cluster_ld4(cluster_addr(base + u * 16, r));
-        v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+      float4 w[kMaxSplit];
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxSplit; ++r)
+        if (r < S) w[r] = cluster_ld4(cluster_addr(base + u * 16, r));
+      float v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (uint32_t r = 1; r < kMaxSplit; ++r) {
+        if (r < S) {
+          v[0] += w[r].x; v[1] += w[r].y; v[2] += w[r].z; v[3] += w[r].w;
+        }
       }
       epilogue4(p.e, q0 + (u >> 5), pc, v);
     }
@@ -346,27 +356,47 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
   if (warp == 1) tmem_dealloc(tmem, TMEM);
 }
 
-// ---------------------------------------------------------------- few rows --
-// One to four rows of b (tokens), both operands K-major: no tensor cores, each warp
-// streams R rows of a (weights) once, 16 bytes per lane and load, kRowsUnroll loads of each in
-// flight, against b's rows from L1; W warps share a row's K where there are few
-// rows.  Products are exact in fp32 and added with fmaf.  The bound is the copy
-// bandwidth and a launch: no barriers, TMEM or clusters to set up.
-constexpr int kRowsWarps = 8;
-constexpr int kRowsUnroll = 4;
+// --------------------------------------------------------------- one token --
+// One row of b, both operands K-major: no tensor cores.  Each warp streams kRowsR rows
+// of a (weights) once, 16 bytes per lane and load, kRowsUnroll loads of each in flight,
+// against b's row from L1; W warps share a row's K where there are few rows.
+// Products are exact in fp32 and added with fma.  The bound is the copy bandwidth and
+// a launch: there are no barriers, TMEM or clusters to set up.  4096 x 4096 7.0 us (the
+// cluster form 9.4; two tokens 9.7 in the cluster form, 10.3 so), 12288 x 4096 17.7 (20.0);
+// 4 rows x 2 loads against 2 x 4: 7.0, 8.7; weights kept out of L1: 7.9, 8.4 before.
+constexpr int kRowsWarps = 4;
+constexpr int kRowsUnroll = 2;
+constexpr int kRowsR = 4;
 
-template <int MT, int R>
-__global__ void __launch_bounds__(kRowsWarps * 32) product_rows_kernel(const bf16* __restrict__ a,
-                                                                       const bf16* __restrict__ b, int64_t K, int W,
-                                                                       const Epi e) {
-  __shared__ float red[kRowsWarps][R * MT];
+MOE_DEV void unpack_pairs(const uint4& u, float2 (&f)[4]) {
+  f[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x));
+  f[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
+  f[2] = make_float2(bf16_lo(u.z), bf16_hi(u.z));
+  f[3] = make_float2(bf16_lo(u.w), bf16_hi(u.w));
+}
+
+// 16 bytes that are read once: not kept in L1, where b's rows are.
+MOE_DEV uint4 load_once(const bf16* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kRowsWarps * 32) product_token_kernel(const bf16* __restrict__ a,
+                                                                        const bf16* __restrict__ b, int64_t K, int W,
+                                                                        const Epi e) {
+  constexpr int R = kRowsR;
+  __shared__ float red[kRowsWarps][R];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = warp % W, group = warp / W;
   const int64_t p0 = ((int64_t)blockIdx.x * (kRowsWarps / W) + group) * R;
-  const int Q = (int)e.Q, nk = (int)(K >> 3), step = 32 * W;
-  float acc[R][MT] = {};
+  const int nk = (int)(K >> 3), step = 32 * W;
+  float2 acc[R] = {};
   for (int k0 = sub * 32 + lane; k0 < nk; k0 += step * kRowsUnroll) {
     uint4 w[kRowsUnroll][R];
 #pragma unroll
@@ -374,54 +404,42 @@ __global__ void __launch_bounds__(kRowsWarps * 32) product_rows_kernel(const bf1
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         w[i][r] = make_uint4(0u, 0u, 0u, 0u);
-        if (k0 + i * step < nk && p0 + r < e.P)
-          w[i][r] = *reinterpret_cast<const uint4*>(a + (p0 + r) * K + (int64_t)(k0 + i * step) * 8);
+        if (k0 + i * step < nk && p0 + r < e.P) w[i][r] = load_once(a + (p0 + r) * K + (int64_t)(k0 + i * step) * 8);
       }
 #pragma unroll
     for (int i = 0; i < kRowsUnroll; ++i) {
       if (k0 + i * step >= nk) break;
-      float x[MT][8];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if (m < Q) unpack8_bf16(*reinterpret_cast<const uint4*>(b + m * K + (int64_t)(k0 + i * step) * 8), x[m]);
-      }
+      float2 x[4];
+      unpack_pairs(*reinterpret_cast<const uint4*>(b + (int64_t)(k0 + i * step) * 8), x);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float f[8];
-        unpack8_bf16(w[i][r], f);
+        float2 f[4];
+        unpack_pairs(w[i][r], f);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (m < Q) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) acc[r][m] = fmaf(f[q], x[m][q], acc[r][m]);
-          }
-        }
+        for (int q = 0; q < 4; ++q) acc[r] = fma_f2(f[q], x[q], acc[r]);
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const float v = warp_sum(acc[r][m]);
-      if (lane == 0) red[warp][r * MT + m] = v;
-    }
+  for (int r = 0; r < R; ++r) {
+    const float v = warp_sum(acc[r].x + acc[r].y);
+    if (lane == 0) red[warp][r] = v;
+  }
   if (W > 1) __syncthreads();
   else __syncwarp();
-  const int r = lane / MT, m = lane - r * MT;
-  if (sub != 0 || r >= R || m >= Q || p0 + r >= e.P) return;
+  const int64_t p = p0 + lane;
+  if (sub != 0 || lane >= R || p >= e.P) return;
   float v = 0.f;
   for (int i = 0; i < W; ++i) v += red[warp + i][lane];
-  const int64_t p = p0 + r, at = m * e.P + p;
   auto get = [](const void* s, int f32, int64_t i) {
     return f32 ? static_cast<const float*>(s)[i] : __bfloat162float(static_cast<const bf16*>(s)[i]);
   };
   if (e.bias) v += get(e.bias, e.bias_f32, p);
-  if (e.pre) e.pre[at] = __float2bfloat16_rn(v);
+  if (e.pre) e.pre[p] = __float2bfloat16_rn(v);
   act_all<1>(&v, e.act);
-  if (e.residual) v += get(e.residual, e.res_f32, at);
-  if (e.out_f32) static_cast<float*>(e.out)[at] = v;
-  else static_cast<bf16*>(e.out)[at] = __float2bfloat16_rn(v);
+  if (e.residual) v += get(e.residual, e.res_f32, p);
+  if (e.out_f32) static_cast<float*>(e.out)[p] = v;
+  else static_cast<bf16*>(e.out)[p] = __float2bfloat16_rn(v);
 }
 
 // -------------------------------------------------------------- CTA-pair form --
@@ -650,8 +668,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               const uint64_t bd = B_MN ? sw128_mn_desc(b + kk * 2048, 64) : sw128_desc(b + kk * 32);
               mma_bf16_pair(tmem + buf * 256, ad, bd, idesc, (n | kk) ? 1u : 0u);
             }
-            mma_commit_pair(&empty[s]);
-            if (last) mma_commit_pair(&tfull[buf]);
+            mma_commit_pair(&empty[s], 3);
+            if (last) mma_commit_pair(&tfull[buf], 3);
           }
           __syncwarp();
           issued = true;
@@ -673,7 +691,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (!ok) {
         if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
         if (issued) {
-          if (elect_one()) mma_commit_pair(&drain);
+          if (elect_one()) mma_commit_pair(&drain, 3);
           __syncwarp();
           const long long t0 = clock64();
           while (!mbar_try_wait(&drain, 0) && clock64() - t0 < kSpinLimitCycles) {
@@ -838,37 +856,95 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, size_
 
 constexpr int kSmemMax = 226 * 1024 - 1024;  // dynamic; the static part and the reserve beside it
 
+// One instance of the split kernel: how many of its clusters of S CTAs run at once, and its
+// launch.
+struct SplitForm {
+  int (*clusters)(int S);
+  cudaError_t (*launch)(const ProductArgs& a, const Epi& e, int S, int steps, int seg, int* status, cudaStream_t st);
+};
+
 template <bool A_MN, bool B_MN, int BN>
-cudaError_t launch_split(const ProductArgs& a, const Epi& e, int S, int steps, int seg, int* status,
-                         cudaStream_t st) {
-  CUtensorMap ta, tb;
-  if (!operand_map(&ta, a.a, A_MN, a.P, a.K, kTileP) || !operand_map(&tb, a.b, B_MN, a.Q, a.K, BN))
-    return cudaErrorInvalidValue;
-  SplitP p{};
-  p.e = e;
-  p.steps = steps;
-  p.seg = seg;
-  p.status = status;
-  p.stage_bytes = kTileP * 128 + (B_MN ? (BN + 63) / 64 * kBoxBytes : BN * 128);
-  const int room = (BN <= 64 ? kSmemMax / 2 - 2048 : kSmemMax) - 1024;
-  p.ring = room / p.stage_bytes < kMaxRing ? room / p.stage_bytes : kMaxRing;
-  auto kern = product_split_kernel<A_MN, B_MN, BN>;
-  cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-  if (rc != cudaSuccess) return rc;
-  const dim3 grid(S, (unsigned)((a.P + kTileP - 1) / kTileP), (unsigned)((a.Q + BN - 1) / BN));
-  return launch_cluster(kern, grid, S, (size_t)p.ring * p.stage_bytes + 1024, st, ta, tb, p);
-}
+struct Split {
+  static constexpr int kPerSm = BN <= 64 ? 2 : 1;  // CTAs
+  static constexpr int kStage = kTileP * 128 + (B_MN ? (BN + 63) / 64 * kBoxBytes : BN * 128);
+  static constexpr int kRoom = (kPerSm == 2 ? kSmemMax / 2 - 2048 : kSmemMax) - 1024;
+  static constexpr int kRing = kRoom / kStage < kMaxRing ? kRoom / kStage : kMaxRing;
+  static constexpr size_t kSmem = (size_t)kRing * kStage + 1024;
+  static_assert((size_t)kRing * kStage >= (size_t)BN * kTileP * 4, "the fp32 tile lies over the ring");
+
+  static auto kernel() { return product_split_kernel<A_MN, B_MN, BN>; }
+
+  // (the same on every device that the library runs on)
+  static int clusters(int S) {
+    static std::atomic<int> known[kMaxSplit + 1];
+    int n = known[S].load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = S;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(S);
+      cfg.blockDim = dim3(kLinThreads);
+      cfg.dynamicSmemBytes = kSmem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&n, kernel(), &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = -1;
+      } else {
+        // the query counts one CTA of a kernel with TMEM per SM; two run (at BN = 16, 256 CTAs take
+        // the time of one round: 9.9 us)
+        n *= kPerSm;
+      }
+      known[S].store(n, std::memory_order_relaxed);
+    }
+    return n;
+  }
+
+  static cudaError_t launch(const ProductArgs& a, const Epi& e, int S, int steps, int seg, int* status,
+                            cudaStream_t st) {
+    CUtensorMap ta, tb;
+    if (!operand_map(&ta, a.a, A_MN, a.P, a.K, kTileP) || !operand_map(&tb, a.b, B_MN, a.Q, a.K, BN))
+      return cudaErrorInvalidValue;
+    SplitP p{};
+    p.e = e;
+    p.steps = steps;
+    p.seg = seg;
+    p.status = status;
+    p.stage_bytes = kStage;
+    p.ring = kRing;
+    cudaError_t rc = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (rc != cudaSuccess) return rc;
+    const dim3 grid(S, (unsigned)((a.P + kTileP - 1) / kTileP), (unsigned)((a.Q + BN - 1) / BN));
+    return launch_cluster(kernel(), grid, S, kSmem, st, ta, tb, p);
+  }
+
+  static SplitForm form() { return {&clusters, &launch}; }
+};
 
 template <bool A_MN, bool B_MN>
-cudaError_t launch_split_bn(int bn, const ProductArgs& a, const Epi& e, int S, int steps, int seg, int* status,
-                            cudaStream_t st) {
+SplitForm split_form(int bn) {
   if constexpr (!B_MN) {
-    if (bn == 16) return launch_split<A_MN, B_MN, 16>(a, e, S, steps, seg, status, st);
-    if (bn == 32) return launch_split<A_MN, B_MN, 32>(a, e, S, steps, seg, status, st);
+    if (bn == 16) return Split<A_MN, B_MN, 16>::form();
+    if (bn == 32) return Split<A_MN, B_MN, 32>::form();
   }
-  if (bn <= 64) return launch_split<A_MN, B_MN, 64>(a, e, S, steps, seg, status, st);
-  if (bn == 128) return launch_split<A_MN, B_MN, 128>(a, e, S, steps, seg, status, st);
-  return launch_split<A_MN, B_MN, 256>(a, e, S, steps, seg, status, st);
+  if (bn <= 64) return Split<A_MN, B_MN, 64>::form();
+  if (bn == 128) return Split<A_MN, B_MN, 128>::form();
+  return Split<A_MN, B_MN, 256>::form();
+}
+
+// Time of a split in us: rounds of clusters, each with a start and an end beside the
+// stages of a part, and from 128 CTAs on the memory shared by more of them.  Measured at
+// K = 4096: 128 CTAs of BN = 16 9.9 us (32 CTAs without a split 22.8), BN = 64 12.0 (24.6),
+// BN = 128 12.6 (27.3), BN = 256 15.7 (33.7).
+double split_us(int bn, int64_t tiles, int at_once, int S, int steps) {
+  const double stage = bn <= 32 ? 0.27 : (bn <= 64 ? 0.29 : (bn == 128 ? 0.31 : 0.375));
+  const double ends = bn <= 32 ? 5.6 : (bn <= 64 ? 6.3 : (bn == 128 ? 7.7 : 9.7));
+  const int64_t rounds = (tiles + at_once - 1) / at_once;
+  const double ctas = (double)(tiles < at_once ? tiles : at_once) * S;
+  return rounds * ((steps + S - 1) / S * stage * (ctas > 128 ? ctas / 128 : 1.0) + ends);
 }
 
 // Tiles of 256 x 256 that the pairs take whole: where half of the pairs or more would idle
@@ -924,39 +1000,39 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
   e.Q = a.Q;
   const char* env = getenv("MOE_LINEAR_FORM");
   const char form = env ? env[0] : 0;
-  if (!a.a_mn && !a.b_mn && a.Q <= 4 && (!form || form == 'r')) {
-    constexpr int R = 2;
-    int W = 1;  // warps per row: enough of them to fill the SMs, four loads for each at least
-    while (W < kRowsWarps && a.P / R * W < (int64_t)sms * 24 && a.K / 8 > 64 * W) W *= 2;
-    const int64_t per = kRowsWarps / W * R;
-    auto kern = a.Q == 1 ? product_rows_kernel<1, R> : (a.Q == 2 ? product_rows_kernel<2, R> : product_rows_kernel<4, R>);
-    return launch_kernel(kern, dim3((unsigned)((a.P + per - 1) / per)), dim3(kRowsWarps * 32), 0, st,
+  if (!a.a_mn && !a.b_mn && a.Q == 1 && (!form || form == 't')) {
+    int W = 1;  // warps per row: enough of them to fill the SMs, two loads for each at least
+    while (W < kRowsWarps && a.P / kRowsR * W < (int64_t)sms * 48 && a.K / 8 > 64 * W) W *= 2;
+    const int64_t per = kRowsWarps / W * kRowsR;
+    return launch_kernel(product_token_kernel, dim3((unsigned)((a.P + per - 1) / per)), dim3(kRowsWarps * 32), 0, st,
                          static_cast<const bf16*>(a.a), static_cast<const bf16*>(a.b), a.K, W, e);
   }
   const int steps = (int)((a.K + kStepK - 1) / kStepK);
   const int seg = a.out_f32 ? kSegSteps : 1 << 30;
   int bn = 16;
   while (bn < a.Q && bn < 256) bn *= 2;
-  // The split with the least time in units of stages: waves of CTAs times the
-  // stages of a part and about six more for its start and end.
-  const int64_t tiles = ((a.P + kTileP - 1) / kTileP) * ((a.Q + bn - 1) / bn);
-  const int slots = bn <= 64 ? 2 * sms : sms;
-  int S = 1;
-  int64_t best = 0;
-  for (int s = 1; s <= 8 && s <= steps; ++s) {
-    const int64_t cost = (tiles * s + slots - 1) / slots * ((steps + s - 1) / s + 6);
-    if (s == 1 || cost < best) {
-      best = cost;
+  const SplitForm split = a.a_mn ? (a.b_mn ? split_form<true, true>(bn) : split_form<true, false>(bn))
+                                 : split_form<false, false>(bn);
+  const int64_t tiles = (a.P + kTileP - 1) / kTileP * ((a.Q + bn - 1) / bn);
+  int S = 0;
+  double best = 0;
+  for (int s = 1; s <= kMaxSplit && s <= steps; ++s) {
+    const int at_once = split.clusters(s);
+    if (at_once < 1) continue;
+    const double us = split_us(bn, tiles, at_once, s, steps);
+    if (S == 0 || us < best) {
+      best = us;
       S = s;
     }
   }
-  // Pairs: rounds of tiles (a half one takes a little more than half of the time), in the same
-  // units (a stage of 128 x 256 per SM).
+  // The pairs' time, likewise: rounds of whole and of half tiles.  512 x 4096 x 4096 21.7 us
+  // (halves), 700 x 4096 x 2048 16.1, 1024 x 4096 x 4096 25.3; split 21.8, 22.5, 32.1.
   const int64_t pt = (a.Q + 255) / 256 * ((a.P + 255) / 256);
   const int pairs = sms / 2;
   const int64_t whole = pair_whole(pt, pairs), halves = 2 * (pt - whole);
-  const double pair_cost = ((double)((whole + pairs - 1) / pairs) + 0.55 * ((halves + pairs - 1) / pairs)) * steps;
-  const bool pair = form ? form == 'p' : pair_cost + 8 < (bn <= 64 ? 0.5 : bn == 128 ? 0.6 : 1.2) * best;
+  const double pair_us =
+      5.7 + steps * (0.306 * ((whole + pairs - 1) / pairs) + 0.245 * ((halves + pairs - 1) / pairs));
+  const bool pair = S == 0 || (form ? form == 'p' : pair_us < best);
   if (pair) {
     const bool keep = a.out_f32 && steps > kSegSteps;
 #define MOE_PAIR(A, B)                                                                              \
@@ -968,9 +1044,7 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
     MOE_PAIR(false, false);
 #undef MOE_PAIR
   }
-  if (a.a_mn && a.b_mn) return launch_split_bn<true, true>(bn, a, e, S, steps, seg, status, st);
-  if (a.a_mn) return launch_split_bn<true, false>(bn, a, e, S, steps, seg, status, st);
-  return launch_split_bn<false, false>(bn, a, e, S, steps, seg, status, st);
+  return split.launch(a, e, S, steps, seg, status, st);
 }
 
 cudaError_t launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t st) {

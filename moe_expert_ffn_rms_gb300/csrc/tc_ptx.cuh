@@ -456,12 +456,13 @@ MOE_DEV void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint
       : "memory");
 }
 
-// Arrives on `bar` in both CTAs once every MMA issued so far by this thread is done.
-MOE_DEV void mma_commit_pair(uint64_t* bar) {
+// Arrives on `bar` in the CTAs of the cluster that `mask` names (the pair's) once every MMA
+// issued so far by this thread is done.
+MOE_DEV void mma_commit_pair(uint64_t* bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"(mask)
       : "memory");
 }
 
