@@ -36,16 +36,17 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 }
 
 // Few columns per CTA (many threads on each) as long as all CTAs run at once: 608 rows of
-// 4096 columns 9.6 us with 8 threads per column and 128 CTAs, below 3 with 64.
+// 4096 columns 9.6 us with 8 threads per column and 128 CTAs, below 3 with 64.  By the
+// pitch, so that a call that leaves out the second output adds the first in the same order.
 inline cudaError_t launch_column_sum(const float* part, int n, int64_t pitch, int64_t cols, int64_t split, float* out0,
                                      float* out1, int sms, cudaStream_t st) {
   auto kern = column_sum_kernel<16>;
   int per = 16;
-  if (cols > (int64_t)per * 2 * sms) {
+  if (pitch > (int64_t)per * 2 * sms) {
     kern = column_sum_kernel<32>;
     per = 32;
   }
-  if (cols > (int64_t)per * 2 * sms) {
+  if (pitch > (int64_t)per * 2 * sms) {
     kern = column_sum_kernel<64>;
     per = 64;
   }

@@ -783,10 +783,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 // --------------------------------------------------------- activation gradient --
 // A CTA takes 64 x 8 columns and a share of the rows: thread (x, y) of 64 x 4 the
-// columns 8 x .. 8 x + 7 of rows y, y + 4, ...; the column sums of the CTA go to
-// row blockIdx.y of the partial sums.
+// columns 8 x .. 8 x + 7 of rows y, y + 4, ..., four of them (two of fp32) on their way at
+// a time; the column sums of the CTA go to row blockIdx.y of the partial sums.
+constexpr int kActCtas = 3;  // per SM
+
 template <int ACT, bool DF32>
-__global__ void __launch_bounds__(256) act_grad_kernel(const ActGradArgs a, int rows_per) {
+__global__ void __launch_bounds__(256, kActCtas) act_grad_kernel(const ActGradArgs a, int rows_per) {
   __shared__ float red[4][64][9];
   pdl_trigger();
   pdl_wait();
@@ -796,19 +798,41 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradArgs a, int 
   const int64_t m1 = m0 + rows_per < a.M ? m0 + rows_per : a.M;
   float s[8] = {};
   if (c < a.N) {
-#pragma unroll 4
-    for (int64_t m = m0 + y; m < m1; m += 4) {
-      float d[8];
-      load8(a.dout, DF32, (size_t)(m * a.N + c), d);
-      if (ACT != kActNone) {
-        float z[8];
-        load8(a.pre, false, (size_t)(m * a.N + c), z);
+    constexpr int W = DF32 ? 2 : 1, kActRows = DF32 ? 2 : 4;
+    for (int64_t m = m0 + y; m < m1; m += 4 * kActRows) {
+      uint4 d[kActRows][W], z[kActRows];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= act_slope(z[i], ACT);
+      for (int r = 0; r < kActRows; ++r) {
+        if (m + 4 * r < m1) {
+          const int64_t at = (m + 4 * r) * a.N + c;
+          const uint4* from = reinterpret_cast<const uint4*>(static_cast<const char*>(a.dout) + at * (DF32 ? 4 : 2));
+#pragma unroll
+          for (int i = 0; i < W; ++i) d[r][i] = from[i];
+          if (ACT != kActNone) z[r] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.pre) + at);
+        }
       }
-      if (a.dpre) store8_bf16(static_cast<bf16*>(a.dpre) + m * a.N + c, d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] += d[i];
+      for (int r = 0; r < kActRows; ++r) {
+        if (m + 4 * r >= m1) break;
+        float f[8];
+        if constexpr (DF32) {
+          f[0] = __uint_as_float(d[r][0].x); f[1] = __uint_as_float(d[r][0].y);
+          f[2] = __uint_as_float(d[r][0].z); f[3] = __uint_as_float(d[r][0].w);
+          f[4] = __uint_as_float(d[r][1].x); f[5] = __uint_as_float(d[r][1].y);
+          f[6] = __uint_as_float(d[r][1].z); f[7] = __uint_as_float(d[r][1].w);
+        } else {
+          unpack8_bf16(d[r][0], f);
+        }
+        if (ACT != kActNone) {
+          float v[8];
+          unpack8_bf16(z[r], v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= act_slope(v[i], ACT);
+        }
+        if (a.dpre) store8_bf16(static_cast<bf16*>(a.dpre) + (m + 4 * r) * a.N + c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += f[i];
+      }
     }
   }
   if (!a.db) return;
@@ -1048,9 +1072,9 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
 }
 
 cudaError_t launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t st) {
-  // row shares so that the grid fills the SMs a few times over
+  // row shares: one round of CTAs
   const int64_t strips = (a.N + 511) / 512;
-  int64_t shares = (8 * sms + strips - 1) / strips;
+  int64_t shares = kActCtas * sms / strips;
   if (shares > (a.M + 15) / 16) shares = (a.M + 15) / 16;
   if (shares > kActGradRows) shares = kActGradRows;
   if (shares < 1) shares = 1;
