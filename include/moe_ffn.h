@@ -550,7 +550,8 @@ moe_status moe_quantize_fp8_blocks(const void* x, int32_t N, int32_t K, int32_t 
  *               without a row (dropped: nothing is read and nothing added); one
  *               >= T*k counts as such and is flagged in the device status word
  *   topk_w      fp32 [T, k], or NULL: all 1
- *   residual    [T, H] bf16 or fp32 (residual_f32), or NULL; may be out
+ *   residual    [T, H] bf16 or fp32 (residual_f32), or NULL; may be out when both
+ *               have one type
  *   out         [T, H] bf16 or fp32 (out_f32)
  * T = 0 returns MOE_OK without looking at the tensor pointers (this and the next
  * two).  Errors of the three: INVALID_ARG (null or misaligned pointers);
@@ -580,7 +581,8 @@ moe_status moe_unpermute_backward(const void* dout, int32_t dout_f32, const void
 /* Gradient of moe_permute's gather xp[r] = x[row_src[r] / k]:
  *   dx[t, :] = dres[t, :] + sum_{j=0..k-1} dxp[row_of_pair[t*k+j], :]
  * dxp [T*k, H] bf16 (dxp_bf16 = 1) or fp32; dres [T, H] (dres_f32) the gradient
- * that reaches x past the experts, or NULL, may be dx; dx [T, H] (dx_f32).
+ * that reaches x past the experts, or NULL, may be dx when both have one type; dx
+ * [T, H] (dx_f32).
  * row_of_pair as in moe_unpermute. */
 moe_status moe_permute_backward(const void* dxp, int32_t dxp_bf16, const int32_t* row_of_pair,
                                 int32_t T, int32_t k, int32_t H, const void* dres, int32_t dres_f32,

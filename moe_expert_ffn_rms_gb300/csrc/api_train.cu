@@ -48,6 +48,8 @@ moe_status unpermute(const void* y, int y_bf16, const int32_t* row_of_pair, cons
   MOE_REQ(aligned(y, 16) && aligned(residual, 16) && aligned(out, 16) && aligned(row_of_pair, 4) &&
               aligned(topk_w, 4),
           MOE_ERR_INVALID_ARG, "misaligned pointer");
+  MOE_REQ(residual != out || (residual_f32 != 0) == (out_f32 != 0), MOE_ERR_INVALID_ARG,
+          "the row that is added may be the output only when both have one type");
   int sms = 0, *status = nullptr;
   if ((rc = moe::api_device(&sms, &status)) != MOE_OK) return rc;
   moe::UnpermuteArgs a{};
@@ -83,6 +85,7 @@ moe_status norm_grad(moe::NormGradArgs& a, size_t workspace_bytes, moe_stream_t 
     MOE_REQ(aligned(a.dy, 16) && aligned(a.x, 16) && aligned(a.w, 16) && aligned(a.dx, 16) &&
                 aligned(a.dres, 16) && aligned(a.mean, 4) && aligned(a.rstd, 4),
             MOE_ERR_INVALID_ARG, "misaligned pointer");
+    MOE_REQ(a.dx != a.dy || a.x_f32 == a.dy_f32, MOE_ERR_INVALID_ARG, "dx may be dy only when both have one type");
     const size_t need = moe::norm_grad_workspace_bytes(a.T, a.H);
     MOE_REQ(workspace_bytes >= need && a.workspace, MOE_ERR_WORKSPACE_TOO_SMALL,
             "norm backward workspace %zu < %zu bytes", workspace_bytes, need);
@@ -171,6 +174,7 @@ moe_status moe_layernorm(const void* x, int32_t x_f32, const void* w, const void
   MOE_REQ(aligned(x, 16) && aligned(w, 16) && aligned(b, 16) && aligned(y, 16) && aligned(mean, 4) &&
               aligned(rstd, 4),
           MOE_ERR_INVALID_ARG, "misaligned pointer");
+  MOE_REQ(x != y || (x_f32 != 0) == (y_f32 != 0), MOE_ERR_INVALID_ARG, "y may be x only when both have one type");
   int sms = 0, *status = nullptr;
   if ((rc = moe::api_device(&sms, &status)) != MOE_OK) return rc;
   moe::LayerNormArgs a{};

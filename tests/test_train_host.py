@@ -27,7 +27,7 @@ ROWS = [(dict(T=-1), 2), (dict(k=0), 2), (dict(k=9), 2), (dict(H=0), 2), (dict(H
 
 @pytest.mark.parametrize("kw,code", ROWS + [
     (dict(y=None), 1), (dict(row=None), 1), (dict(out=None), 1), (dict(y=FAKE + 8), 1), (dict(row=FAKE + 2), 1),
-    (dict(w=FAKE + 2), 1), (dict(res=FAKE + 4), 1), (dict(out=FAKE + 8), 1)])
+    (dict(w=FAKE + 2), 1), (dict(res=FAKE + 4), 1), (dict(out=FAKE + 8), 1), (dict(res_f32=1), 1)])
 def test_unpermute(M, kw, code):
     args = dict(y=FAKE, y_bf16=1, row=FAKE, w=FAKE, T=4, k=2, H=256, res=FAKE, res_f32=0, out=FAKE, out_f32=0, st=None)
     refused(M, "moe_unpermute", args, kw, code)
@@ -53,7 +53,8 @@ NORM = [(dict(T=-1), 2), (dict(H=0), 2), (dict(H=252), 2), (dict(H=16392), 2), (
 
 @pytest.mark.parametrize("kw,code", NORM + [
     (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(y=None), 1), (dict(mean=None), 1), (dict(rstd=None), 1),
-    (dict(b=FAKE + 8), 1), (dict(y=FAKE + 8), 1), (dict(mean=FAKE + 2), 1), (dict(rstd=FAKE + 2), 1)])
+    (dict(b=FAKE + 8), 1), (dict(y=FAKE + 8), 1), (dict(mean=FAKE + 2), 1), (dict(rstd=FAKE + 2), 1),
+    (dict(y_f32=1), 1)])
 def test_layernorm(M, kw, code):
     args = dict(x=FAKE, x_f32=0, w=FAKE, b=FAKE, w_f32=0, T=4, H=256, eps=1e-6, y=FAKE, y_f32=0, mean=FAKE, rstd=FAKE,
                 st=None)
@@ -62,7 +63,7 @@ def test_layernorm(M, kw, code):
 
 GRAD = NORM + [(dict(dy=None), 1), (dict(dx=None), 1), (dict(dw=None), 1), (dict(dy=FAKE + 8), 1),
                (dict(dx=FAKE + 8), 1), (dict(dres=FAKE + 8), 1), (dict(dw=FAKE + 2), 1), (dict(ws=None), 4),
-               (dict(ws=FAKE + 16), 1), (dict(wsb=100), 4)]
+               (dict(ws=FAKE + 16), 1), (dict(wsb=100), 4), (dict(dy_f32=1), 1)]
 
 
 @pytest.mark.parametrize("kw,code", GRAD + [(dict(mean=None), 1), (dict(rstd=None), 1), (dict(db=FAKE + 2), 1),
