@@ -84,11 +84,13 @@ __global__ void __launch_bounds__(kRowsThreads) unpermute_kernel(const Unpermute
   store8(a.out, a.out_f32, (size_t)t * a.H + v * 8, f);
 }
 
-// 32 blockDim.x / 32 lanes take one (token, slot) pair, so each row's dot product stays
-// with its warps; the k pairs of a token lie in one CTA (blockDim.y = k x tokens) and
-// read its dout row from L1.  Four chunks (two of fp32) of both rows are in flight per lane.
+// blockDim.x lanes take PP consecutive slots of a token, so each row's dot product stays with
+// its warps and dout's row is loaded once for them; the slots of a token lie in one CTA
+// (blockDim.y = groups of slots x tokens).  N chunks of dout and of each slot's row are in
+// flight per lane: four with one slot, two of fp32 or with four slots (short rows, of which a
+// lane has no more: T = 8192, H = 512, k = 8 45.2 us with one).
 // (A CTA per token with all k rows in flight per thread, at T = 4096, H = 4096, k = 8:
-// 123 registers, 113 us.)
+// 123 registers, 113 us; so 91.)
 constexpr int kGradThreads = 1024;
 
 // Eight columns as they are in memory.
@@ -112,21 +114,19 @@ struct Raw {
   }
 };
 
-template <bool YF32, bool DF32, int N>
-__global__ void __launch_bounds__(kGradThreads) unpermute_grad_kernel(const UnpermuteGradArgs a, int* status) {
-  __shared__ float red[kGradThreads / 32];
-  __shared__ float s_dw[kGradThreads / 32], s_w[kGradThreads / 32];
-  __shared__ int s_id[kGradThreads / 32];
+template <bool YF32, bool DF32, int N, int PP>
+__global__ void __launch_bounds__(PP == 1 ? kGradThreads : 256) unpermute_grad_kernel(const UnpermuteGradArgs a, int groups,
+                                                                      int* status) {
+  __shared__ float red[kGradThreads / 32][PP];
+  __shared__ float s_dw[kGradThreads / 32][kMaxTopK], s_w[kGradThreads / 32][kMaxTopK];
+  __shared__ int s_id[kGradThreads / 32][kMaxTopK];
   pdl_trigger();
   pdl_wait();
   const int nv = a.H >> 3, tx = threadIdx.x, ty = threadIdx.y, nt = blockDim.x;
-  const int64_t pair = (int64_t)blockIdx.x * blockDim.y + ty;
-  const bool on = pair < (int64_t)a.T * a.k;
-  const int64_t t = pair / a.k;
-  const int j = (int)(pair - t * a.k);
+  const int local = ty / groups, group = ty - local * groups, j0 = group * PP;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.y / groups) + local;
+  const bool on = t < a.T;
   const bool dots = a.dw || a.dlogits;
-  int row = -1, id = -1;
-  float w = 0.f, dot = 0.f;
   const size_t at_d = (size_t)t * a.H;
   Raw<DF32> d[N];
   auto load_dout = [&](int v0) {
@@ -134,67 +134,101 @@ __global__ void __launch_bounds__(kGradThreads) unpermute_grad_kernel(const Unpe
     for (int i = 0; i < N; ++i)
       if (v0 + i * nt < nv) d[i].load(a.dout, at_d + (v0 + i * nt) * 8);
   };
-  if (on) {
-    load_dout(tx);  // (does not wait for the row's index)
-    row = pair_row(a.row_of_pair, pair, a.T * a.k, tx == 0, status);
-    w = a.w[pair];
-    if (a.dlogits && tx == 0) id = a.ids[pair];
+  int row[PP], id[PP];
+  float w[PP], dot[PP];
+  bool any = false;
+#pragma unroll
+  for (int p = 0; p < PP; ++p) {
+    row[p] = id[p] = -1;
+    w[p] = dot[p] = 0.f;
   }
-  if (row >= 0) {
-    const size_t at_y = (size_t)row * a.H;
+  if (on) {
+    load_dout(tx);  // (does not wait for the rows' indices)
+#pragma unroll
+    for (int p = 0; p < PP; ++p) {
+      if (j0 + p < a.k) {
+        const int64_t pair = t * a.k + j0 + p;
+        row[p] = pair_row(a.row_of_pair, pair, a.T * a.k, tx == 0, status);
+        w[p] = a.w[pair];
+        if (a.dlogits && tx == 0) id[p] = a.ids[pair];
+        any |= row[p] >= 0;
+      }
+    }
+  }
+  if (any) {
     for (int v0 = tx; v0 < nv; v0 += nt * N) {
-      Raw<YF32> y[N];
+      Raw<YF32> y[PP][N];
       if (dots) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (v0 + i * nt < nv) y[i].load(a.y, at_y + (v0 + i * nt) * 8);
+        for (int p = 0; p < PP; ++p)
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (row[p] >= 0 && v0 + i * nt < nv) y[p][i].load(a.y, (size_t)row[p] * a.H + (v0 + i * nt) * 8);
       }
       if (v0 != tx) load_dout(v0);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int v = v0 + i * nt;
         if (v >= nv) break;
-        float f[8], g[8];
+        float f[8];
         d[i].get(f);
-        if (dots) {
-          y[i].get(g);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dot = fmaf(f[q], g[q], dot);
-        }
-        if (a.dy) {
+        for (int p = 0; p < PP; ++p) {
+          if (row[p] < 0) continue;
+          if (dots) {
+            float g[8];
+            y[p][i].get(g);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) f[q] *= w;
-          store8(a.dy, YF32, at_y + v * 8, f);
+            for (int q = 0; q < 8; ++q) dot[p] = fmaf(f[q], g[q], dot[p]);
+          }
+          if (a.dy) {
+            float g[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) g[q] = f[q] * w[p];
+            store8(a.dy, YF32, (size_t)row[p] * a.H + v * 8, g);
+          }
         }
       }
     }
   }
   if (!dots) return;
-  dot = warp_sum(dot);
+#pragma unroll
+  for (int p = 0; p < PP; ++p) dot[p] = warp_sum(dot[p]);
   const int wp = nt >> 5;
   if (wp > 1) {
-    if ((tx & 31) == 0) red[ty * wp + (tx >> 5)] = dot;
+    if ((tx & 31) == 0) {
+#pragma unroll
+      for (int p = 0; p < PP; ++p) red[ty * wp + (tx >> 5)][p] = dot[p];
+    }
     __syncthreads();
-    dot = 0.f;
-    for (int i = 0; i < wp; ++i) dot += red[ty * wp + i];
+#pragma unroll
+    for (int p = 0; p < PP; ++p) {
+      dot[p] = 0.f;
+      for (int i = 0; i < wp; ++i) dot[p] += red[ty * wp + i][p];
+    }
   }
-  if (tx == 0 && on && a.dw) a.dw[pair] = dot;
-  if (!a.dlogits) return;
   if (tx == 0 && on) {
-    if (id < 0 || id >= a.E) flag_status(status, MOE_ERR_INVALID_ARG);
-    s_dw[ty] = dot;
-    s_w[ty] = w;
-    s_id[ty] = id;
+#pragma unroll
+    for (int p = 0; p < PP; ++p) {
+      if (j0 + p >= a.k) continue;
+      if (a.dw) a.dw[t * a.k + j0 + p] = dot[p];
+      if (a.dlogits) {
+        if (id[p] < 0 || id[p] >= a.E) flag_status(status, MOE_ERR_INVALID_ARG);
+        s_dw[local][j0 + p] = dot[p];
+        s_w[local][j0 + p] = w[p];
+        s_id[local][j0 + p] = id[p];
+      }
+    }
   }
+  if (!a.dlogits) return;
   __syncthreads();
   if (!on) return;
-  const int y0 = ty - j;  // the token's first pair
   float s = 0.f;
-  for (int i = 0; i < a.k; ++i) s = fmaf(s_w[y0 + i], s_dw[y0 + i], s);
-  for (int e = j * nt + tx; e < a.E; e += a.k * nt) {
+  for (int i = 0; i < a.k; ++i) s = fmaf(s_w[local][i], s_dw[local][i], s);
+  for (int e = group * nt + tx; e < a.E; e += groups * nt) {
     float g = 0.f;
     for (int i = 0; i < a.k; ++i)
-      if (s_id[y0 + i] == e) g += s_w[y0 + i] * (s_dw[y0 + i] - s);
+      if (s_id[local][i] == e) g += s_w[local][i] * (s_dw[local][i] - s);
     a.dlogits[t * a.E + e] = g;
   }
 }
@@ -236,15 +270,16 @@ cudaError_t launch_unpermute_grad(const UnpermuteGradArgs& a, int sms, int* stat
   const int64_t pairs = (int64_t)a.T * a.k;
   int wp = 1;
   while (wp < 4 && wp * 64 < nv && pairs * wp < (int64_t)sms * 16) wp *= 2;
-  int tokens = 8 / (a.k * wp);
+  const bool four = nv <= 64 && a.k > 2 && !a.y_f32 && !a.dout_f32 && pairs >= (int64_t)sms * 16;
+  const int groups = four ? (a.k + 3) / 4 : a.k;
+  int tokens = 8 / (groups * wp);
   if (tokens < 1) tokens = 1;
-  // chunks of a row in flight per lane: two of fp32 or of short rows (fewer registers, more warps)
-  const bool two = nv <= 64 * wp;
-  auto kern = a.y_f32        ? (a.dout_f32 ? unpermute_grad_kernel<true, true, 2> : unpermute_grad_kernel<true, false, 2>)
-              : a.dout_f32   ? unpermute_grad_kernel<false, true, 2>
-              : two          ? unpermute_grad_kernel<false, false, 2>
-                             : unpermute_grad_kernel<false, false, 4>;
-  return launch_kernel(kern, dim3((a.T + tokens - 1) / tokens), dim3(32 * wp, a.k * tokens), 0, st, a, status);
+  auto kern = a.y_f32      ? (a.dout_f32 ? unpermute_grad_kernel<true, true, 2, 1> : unpermute_grad_kernel<true, false, 2, 1>)
+              : a.dout_f32 ? unpermute_grad_kernel<false, true, 2, 1>
+              : four       ? unpermute_grad_kernel<false, false, 2, 4>
+                           : unpermute_grad_kernel<false, false, 4, 1>;
+  return launch_kernel(kern, dim3((a.T + tokens - 1) / tokens), dim3(32 * wp, groups * tokens), 0, st, a, groups,
+                       status);
 }
 
 }  // namespace moe

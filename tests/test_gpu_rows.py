@@ -76,7 +76,7 @@ def check_sum(d, out, w):
 
 
 SHAPES = [(1, 8, 1), (1, 4096, 8), (3, 24, 2), (7, 264, 3), (33, 2944, 6), (257, 256, 8), (65, 2056, 5),
-          (130, 7168, 4), (5, 32768, 8), (1000, 512, 7)]
+          (130, 7168, 4), (5, 32768, 8), (1000, 512, 7), (900, 264, 3), (640, 96, 8)]
 TYPES = [(BF, BF), (BF, F32), (F32, BF), (F32, F32)]
 
 
