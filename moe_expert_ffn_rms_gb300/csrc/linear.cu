@@ -10,7 +10,21 @@
 //   dx       a = W  stored [K, P]  b = dpre [M, N]
 //   dW       a = x  stored [K, P]  b = dpre stored [K, Q]
 // The tensor cores take both layouts from shared memory (tcgen05 descriptors), so
-// nothing is transposed.
+// nothing is transposed.  Three forms, chosen in launch_product by their measured times: a
+// kernel for one token, clusters that split K, and pairs of CTAs.  Device time per call,
+// inputs not in L2, against bytes at 6794 GB/s or FLOPs at 1952 TFLOP/s:
+//   M x N x K                 us      of the floor
+//   8192 x 8192 x 8192        539     1.05   pairs
+//   4096 x 12288 x 4096       217     0.97   pairs; GELU and kept values 235, 0.90
+//     dx, dW of it            236, 217  0.90, 0.97
+//   1024 x 4096 x 4096        25      0.70   pairs, one round of 64 of 76
+//   256 x 4096 x 4096         15.7    0.35   split, 128 CTAs
+//   61 x 7168 x 2048          10.5    0.44   split
+//   16 x 4096 x 4096          10.3    0.48   split
+//   1 x 12288 x 4096          17.7    0.84   one token
+//   1 x 4096 x 4096           7.3     0.67   one token
+// Small ones are a launch (1.7 us for one token, 3.4 with TMEM and a cluster), the ramp of the
+// loads and the reduction over the cluster; large ones the tensor pipe.
 #include <cuda.h>
 #include <stdlib.h>
 
