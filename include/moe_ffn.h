@@ -654,7 +654,7 @@ typedef enum {
  *   bf16 or fp32 (out_f32).
  * Products accumulate in the tensor cores' fp32, whose additions truncate: a sum of
  * K terms is off by about 1.1e-9 K of its magnitude.  With fp32 outputs no more
- * than 1024 terms are added that way, and those sums in fp32 rounded to nearest.
+ * than 768 terms are added that way, and those sums in fp32 rounded to nearest.
  * The activation takes the unrounded z.  Nothing of the result depends on what else runs.
  * M = 0 returns MOE_OK without looking at the tensor pointers.
  * Errors: INVALID_ARG (null or misaligned pointers, act); UNSUPPORTED_SHAPE unless N and K

@@ -52,8 +52,9 @@ constexpr int kEpiWarps = 8;
 // fp32 results: the tensor cores' fp32 additions truncate, which over K terms leaves
 // about 1.1e-9 K of the sum's magnitude (measured: 9e-7 at K = 1024, 1.9e-5 at
 // 16384).  Sums longer than this many stages go through registers, rounded to
-// nearest, every kSegSteps stages.
-constexpr int kSegSteps = 16;
+// nearest, every kSegSteps stages, which leaves about 7e-7 (16 stages 1e-6, 8 stages 5e-7;
+// 4096 x 12288 x 4096 249 us, 238 and 263).
+constexpr int kSegSteps = 12;
 
 // ------------------------------------------------------------- activations --
 // sigmoid(z); exp overflows to infinity for z < -88, which gives 0.
