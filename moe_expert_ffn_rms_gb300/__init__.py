@@ -568,46 +568,51 @@ def moe_quantize_fp8_blocks(x, q, scale, block_rows, stream=None):
 _cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _arg(t, name, shape, dtypes, device):
-    """Pointer of a checked tensor."""
-    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+def _arg(t, name, shape, dtypes, index):
+    """Pointer of a checked tensor on CUDA device `index`."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
-    _check_tensor(t, name, shape, dtypes, device)
+    _check_tensor(t, name, shape, dtypes, torch.device("cuda", index))
     return t.data_ptr()
 
 
-def _queue(device, stream):
-    """The call's stream; ValueError unless the device is the current one."""
-    if device.type != "cuda" or device.index != _cur_device():
-        _check_current(device)
+def _queue(t, stream):
+    """Device index of t and the call's stream; ValueError unless t is on the current device."""
+    index = t.get_device()
+    if index < 0 or index != _cur_device():
+        _check_current(t.device)
     if stream is None and _raw_stream is not None:
-        return _raw_stream(device.index)
-    return _stream(stream)
+        return index, _raw_stream(index)
+    return index, _stream(stream)
 
 
-def _ws(workspace, device):
-    if workspace.device != device:
-        raise ValueError(f"workspace: on {workspace.device}, need {device}")
-    return _ws_ptr(workspace), _ws_bytes(workspace)
+def _ws(workspace, index):
+    if workspace.get_device() != index:
+        raise ValueError(f"workspace: on {workspace.device}, need cuda:{index}")
+    if not workspace.is_contiguous():
+        return _ws_ptr(workspace), _ws_bytes(workspace)
+    p = workspace.data_ptr()
+    q = (p + 255) & ~255
+    return q, max(0, workspace.numel() - (q - p))
 
 
-def _pairs(row_of_pair, n, device):
+def _pairs(row_of_pair, n, index):
     if row_of_pair.numel() != n:
         raise ValueError(f"row_of_pair: {row_of_pair.numel()} entries, need {n}")
-    return _arg(row_of_pair, "row_of_pair", row_of_pair.shape, _I32S, device)
+    return _arg(row_of_pair, "row_of_pair", row_of_pair.shape, _I32S, index)
 
 
 def moe_unpermute(y, row_of_pair, out, T, k, topk_w=None, residual=None, stream=None):
     """out = residual + each token's expert rows times their routing weights.  y bf16 / fp32
     [T*k, H] in expert order, row_of_pair int32 [T*k] of moe_permute (negative: dropped), topk_w
     fp32 [T, k] (None: all 1), residual and out bf16 / fp32 [T, H]; residual may be out."""
-    H, device = y.shape[-1], y.device
-    st = _queue(device, stream)
+    H = y.shape[-1]
+    index, st = _queue(y, stream)
     _check(lib.moe_unpermute(
-        _arg(y, "y", (T * k, H), _FLOATS, device), y.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, device),
-        None if topk_w is None else _arg(topk_w, "topk_w", (T, k), _F32S, device), T, k, H,
-        None if residual is None else _arg(residual, "residual", (T, H), _FLOATS, device),
-        residual is not None and residual.dtype == torch.float32, _arg(out, "out", (T, H), _FLOATS, device),
+        _arg(y, "y", (T * k, H), _FLOATS, index), y.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, index),
+        None if topk_w is None else _arg(topk_w, "topk_w", (T, k), _F32S, index), T, k, H,
+        None if residual is None else _arg(residual, "residual", (T, H), _FLOATS, index),
+        residual is not None and residual.dtype == torch.float32, _arg(out, "out", (T, H), _FLOATS, index),
         out.dtype == torch.float32, st))
     return out
 
@@ -617,8 +622,8 @@ def moe_unpermute_backward(dout, y, row_of_pair, topk_w, T, k, dy=None, dw=None,
     """Gradients of moe_unpermute from dout bf16 / fp32 [T, H]: dy [T*k, H] (y's type, bf16 or fp32
     without y; rows that no pair owns are left as they were), dw fp32 [T, k], and with ids int32 [T, k] the
     router's dlogits fp32 [T, E].  y is needed for dw and dlogits; dy may be y."""
-    H, device = dout.shape[-1], dout.device
-    st = _queue(device, stream)
+    H = dout.shape[-1]
+    index, st = _queue(dout, stream)
     yt = y if y is not None else dy
     if dy is not None and y is not None and dy.dtype != y.dtype:
         raise ValueError(f"dy: dtype {dy.dtype}, need {y.dtype}")
@@ -626,25 +631,25 @@ def moe_unpermute_backward(dout, y, row_of_pair, topk_w, T, k, dy=None, dw=None,
         raise ValueError("dlogits: must be [T, E]")
     E = 0 if dlogits is None else dlogits.shape[1]
     _check(lib.moe_unpermute_backward(
-        _arg(dout, "dout", (T, H), _FLOATS, device), dout.dtype == torch.float32,
-        None if y is None else _arg(y, "y", (T * k, H), _FLOATS, device), yt is None or yt.dtype == torch.bfloat16,
-        _pairs(row_of_pair, T * k, device), _arg(topk_w, "topk_w", (T, k), _F32S, device),
-        None if ids is None else _arg(ids, "ids", (T, k), _I32S, device), T, k, H, E,
-        None if dy is None else _arg(dy, "dy", (T * k, H), _FLOATS, device),
-        None if dw is None else _arg(dw, "dw", (T, k), _F32S, device),
-        None if dlogits is None else _arg(dlogits, "dlogits", (T, E), _F32S, device), st))
+        _arg(dout, "dout", (T, H), _FLOATS, index), dout.dtype == torch.float32,
+        None if y is None else _arg(y, "y", (T * k, H), _FLOATS, index), yt is None or yt.dtype == torch.bfloat16,
+        _pairs(row_of_pair, T * k, index), _arg(topk_w, "topk_w", (T, k), _F32S, index),
+        None if ids is None else _arg(ids, "ids", (T, k), _I32S, index), T, k, H, E,
+        None if dy is None else _arg(dy, "dy", (T * k, H), _FLOATS, index),
+        None if dw is None else _arg(dw, "dw", (T, k), _F32S, index),
+        None if dlogits is None else _arg(dlogits, "dlogits", (T, E), _F32S, index), st))
 
 
 def moe_permute_backward(dxp, row_of_pair, dx, T, k, dres=None, stream=None):
     """Gradient of moe_permute's gather: dx = dres + the sum of each token's rows of dxp (bf16 / fp32
     [T*k, H], expert order).  dres and dx bf16 / fp32 [T, H]; dres may be dx."""
-    H, device = dxp.shape[-1], dxp.device
-    st = _queue(device, stream)
+    H = dxp.shape[-1]
+    index, st = _queue(dxp, stream)
     _check(lib.moe_permute_backward(
-        _arg(dxp, "dxp", (T * k, H), _FLOATS, device), dxp.dtype == torch.bfloat16,
-        _pairs(row_of_pair, T * k, device), T, k, H,
-        None if dres is None else _arg(dres, "dres", (T, H), _FLOATS, device),
-        dres is not None and dres.dtype == torch.float32, _arg(dx, "dx", (T, H), _FLOATS, device),
+        _arg(dxp, "dxp", (T * k, H), _FLOATS, index), dxp.dtype == torch.bfloat16,
+        _pairs(row_of_pair, T * k, index), T, k, H,
+        None if dres is None else _arg(dres, "dres", (T, H), _FLOATS, index),
+        dres is not None and dres.dtype == torch.float32, _arg(dx, "dx", (T, H), _FLOATS, index),
         dx.dtype == torch.float32, st))
     return dx
 
@@ -652,16 +657,16 @@ def moe_permute_backward(dxp, row_of_pair, dx, T, k, dres=None, stream=None):
 def moe_layernorm(x, w, eps, y, b=None, mean=None, rstd=None, stream=None):
     """y = (x - mean) * rstd * w + b over the rows of x bf16 / fp32 [T, H]; w, b bf16 / fp32 [H] of one
     type; y bf16 / fp32 [T, H]; mean, rstd fp32 [T] for the backward pass."""
-    shape, device = x.shape, x.device
+    shape = x.shape
     T, H = shape
-    st = _queue(device, stream)
+    index, st = _queue(x, stream)
     wt = w.dtype
     _check(lib.moe_layernorm(
-        _arg(x, "x", shape, _FLOATS, device), x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, device),
-        None if b is None else _arg(b, "b", (H,), (wt,), device), wt == torch.float32, T, H, eps,
-        _arg(y, "y", shape, _FLOATS, device), y.dtype == torch.float32,
-        None if mean is None else _arg(mean, "mean", (T,), _F32S, device),
-        None if rstd is None else _arg(rstd, "rstd", (T,), _F32S, device), st))
+        _arg(x, "x", shape, _FLOATS, index), x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, index),
+        None if b is None else _arg(b, "b", (H,), (wt,), index), wt == torch.float32, T, H, eps,
+        _arg(y, "y", shape, _FLOATS, index), y.dtype == torch.float32,
+        None if mean is None else _arg(mean, "mean", (T,), _F32S, index),
+        None if rstd is None else _arg(rstd, "rstd", (T,), _F32S, index), st))
     return y
 
 
@@ -676,30 +681,30 @@ def moe_layernorm_backward(dy, x, w, mean, rstd, dx, dw, workspace, db=None, dre
     """Gradients of moe_layernorm: dx [T, H] of x's type (plus dres, of the same type), dw and db fp32
     [H]; mean and rstd of the forward call, workspace of moe_norm_backward_workspace_size(T, H) bytes.
     dx may be x, dres, or dy of the same type."""
-    shape, device, xt = x.shape, x.device, (x.dtype,)
+    shape, xt = x.shape, (x.dtype,)
     T, H = shape
-    st = _queue(device, stream)
+    index, st = _queue(x, stream)
     _check(lib.moe_layernorm_backward(
-        _arg(dy, "dy", shape, _FLOATS, device), dy.dtype == torch.float32, _arg(x, "x", shape, _FLOATS, device),
-        x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, device), w.dtype == torch.float32,
-        _arg(mean, "mean", (T,), _F32S, device), _arg(rstd, "rstd", (T,), _F32S, device),
-        None if dres is None else _arg(dres, "dres", shape, xt, device), T, H, _arg(dx, "dx", shape, xt, device),
-        _arg(dw, "dw", (H,), _F32S, device), None if db is None else _arg(db, "db", (H,), _F32S, device),
-        *_ws(workspace, device), st))
+        _arg(dy, "dy", shape, _FLOATS, index), dy.dtype == torch.float32, _arg(x, "x", shape, _FLOATS, index),
+        x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, index), w.dtype == torch.float32,
+        _arg(mean, "mean", (T,), _F32S, index), _arg(rstd, "rstd", (T,), _F32S, index),
+        None if dres is None else _arg(dres, "dres", shape, xt, index), T, H, _arg(dx, "dx", shape, xt, index),
+        _arg(dw, "dw", (H,), _F32S, index), None if db is None else _arg(db, "db", (H,), _F32S, index),
+        *_ws(workspace, index), st))
     return dx
 
 
 def moe_rmsnorm_backward(dy, x, w, eps, dx, dw, workspace, dres=None, stream=None):
     """Gradients of moe_rmsnorm: dx [T, H] of x's type (plus dres), dw fp32 [H]; the rest as
     moe_layernorm_backward."""
-    shape, device, xt = x.shape, x.device, (x.dtype,)
+    shape, xt = x.shape, (x.dtype,)
     T, H = shape
-    st = _queue(device, stream)
+    index, st = _queue(x, stream)
     _check(lib.moe_rmsnorm_backward(
-        _arg(dy, "dy", shape, _FLOATS, device), dy.dtype == torch.float32, _arg(x, "x", shape, _FLOATS, device),
-        x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, device), w.dtype == torch.float32, eps,
-        None if dres is None else _arg(dres, "dres", shape, xt, device), T, H, _arg(dx, "dx", shape, xt, device),
-        _arg(dw, "dw", (H,), _F32S, device), *_ws(workspace, device), st))
+        _arg(dy, "dy", shape, _FLOATS, index), dy.dtype == torch.float32, _arg(x, "x", shape, _FLOATS, index),
+        x.dtype == torch.float32, _arg(w, "w", (H,), _FLOATS, index), w.dtype == torch.float32, eps,
+        None if dres is None else _arg(dres, "dres", shape, xt, index), T, H, _arg(dx, "dx", shape, xt, index),
+        _arg(dw, "dw", (H,), _F32S, index), *_ws(workspace, index), st))
     return dx
 
 
@@ -707,19 +712,18 @@ def moe_linear(x, w, out, bias=None, residual=None, act=ACT_NONE, pre=None, stre
     """out = residual + act(x w^T + bias).  x bf16 [M, K], w bf16 [N, K], bias bf16 / fp32 [N], residual
     and out bf16 / fp32 [M, N] (residual may be out), act one of the ACT_ constants; pre bf16 [M, N]
     receives the values before the activation."""
-    device = x.device
-    st = _queue(device, stream)
+    index, st = _queue(x, stream)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: must be [M, K] and [N, K]")
     (m, k), n = x.shape, w.shape[0]
     _check(lib.moe_linear(
-        _arg(x, "x", (m, k), _BF16, device), _arg(w, "w", (n, k), _BF16, device),
-        None if bias is None else _arg(bias, "bias", (n,), _FLOATS, device),
+        _arg(x, "x", (m, k), _BF16, index), _arg(w, "w", (n, k), _BF16, index),
+        None if bias is None else _arg(bias, "bias", (n,), _FLOATS, index),
         bias is not None and bias.dtype == torch.float32,
-        None if residual is None else _arg(residual, "residual", (m, n), _FLOATS, device),
+        None if residual is None else _arg(residual, "residual", (m, n), _FLOATS, index),
         residual is not None and residual.dtype == torch.float32, m, n, k, act,
-        None if pre is None else _arg(pre, "pre", (m, n), _BF16, device),
-        _arg(out, "out", (m, n), _FLOATS, device), out.dtype == torch.float32, st))
+        None if pre is None else _arg(pre, "pre", (m, n), _BF16, index),
+        _arg(out, "out", (m, n), _FLOATS, index), out.dtype == torch.float32, st))
     return out
 
 
@@ -734,16 +738,15 @@ def moe_linear_backward(dout, x, w, workspace, dx=None, dw=None, db=None, pre=No
     """Gradients of moe_linear from dout bf16 / fp32 [M, N]: dx bf16 [M, K], dw bf16 / fp32 [N, K], db fp32
     [N], each where it is given; pre of the forward call with an activation; workspace of
     moe_linear_backward_workspace_size(M, N, K) bytes."""
-    device = dout.device
-    st = _queue(device, stream)
+    index, st = _queue(dout, stream)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: must be [M, K] and [N, K]")
     (m, k), n = x.shape, w.shape[0]
     _check(lib.moe_linear_backward(
-        _arg(dout, "dout", (m, n), _FLOATS, device), dout.dtype == torch.float32,
-        None if pre is None else _arg(pre, "pre", (m, n), _BF16, device), _arg(x, "x", (m, k), _BF16, device),
-        _arg(w, "w", (n, k), _BF16, device), m, n, k, act,
-        None if dx is None else _arg(dx, "dx", (m, k), _BF16, device),
-        None if dw is None else _arg(dw, "dw", (n, k), _FLOATS, device),
-        dw is not None and dw.dtype == torch.float32, None if db is None else _arg(db, "db", (n,), _F32S, device),
-        *_ws(workspace, device), st))
+        _arg(dout, "dout", (m, n), _FLOATS, index), dout.dtype == torch.float32,
+        None if pre is None else _arg(pre, "pre", (m, n), _BF16, index), _arg(x, "x", (m, k), _BF16, index),
+        _arg(w, "w", (n, k), _BF16, index), m, n, k, act,
+        None if dx is None else _arg(dx, "dx", (m, k), _BF16, index),
+        None if dw is None else _arg(dw, "dw", (n, k), _FLOATS, index),
+        dw is not None and dw.dtype == torch.float32, None if db is None else _arg(db, "db", (n,), _F32S, index),
+        *_ws(workspace, index), st))
