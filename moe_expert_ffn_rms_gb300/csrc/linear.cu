@@ -165,6 +165,30 @@ struct SplitP {
   int* status;
 };
 
+// Units (four columns of a row) u0 .. u1 - 1 of the tile, added over the S CTAs in rank order.
+// (256 x 4096 x 64, no split: 7.6 us, 11.6 with S as a variable and predicated steps up to eight;
+// 256 x 4096 x 4096, four CTAs: 15.7 us, 19.6 with 32 bytes per lane and load.)
+template <int S>
+MOE_DEV void split_store(const Epi& e, uint32_t base, int u0, int u1, int64_t p0, int64_t q0) {
+  uint32_t at[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) at[r] = S == 1 ? base : cluster_addr(base, r);
+#pragma unroll 2
+  for (int u = u0 + threadIdx.x; u < u1; u += kLinThreads) {
+    const int64_t pc = p0 + (u & 31) * 4;
+    if (pc >= e.P) continue;
+    float4 w[S];
+#pragma unroll
+    for (int r = 0; r < S; ++r) w[r] = S == 1 ? shared_ld4(at[r] + u * 16) : cluster_ld4(at[r] + u * 16);
+    float v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+    for (int r = 1; r < S; ++r) {
+      v[0] += w[r].x; v[1] += w[r].y; v[2] += w[r].z; v[3] += w[r].w;
+    }
+    epilogue4(e, q0 + (u >> 5), pc, v);
+  }
+}
+
 template <bool A_MN, bool B_MN, int BN>
 __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
     product_split_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -347,24 +371,14 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
   {
     const int rows = (int)(p.e.Q - q0 < BN ? p.e.Q - q0 : BN);
     const int units = rows * (kTileP / 4);
-    const int u1 = (int)((int64_t)units * (rank + 1) / S);
+    const int u0 = (int)((int64_t)units * rank / S), u1 = (int)((int64_t)units * (rank + 1) / S);
     const uint32_t base = smem_u32(ring);
-    for (int u = (int)((int64_t)units * rank / S) + threadIdx.x; u < u1; u += kLinThreads) {
-      const int64_t pc = p0 + (u & 31) * 4;
-      if (pc >= p.e.P) continue;
-      float4 w[kMaxSplit];
-#pragma unroll
-      for (uint32_t r = 0; r < kMaxSplit; ++r)
-        if (r < S) w[r] = cluster_ld4(cluster_addr(base + u * 16, r));
-      float v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-#pragma unroll
-      for (uint32_t r = 1; r < kMaxSplit; ++r) {
-        if (r < S) {
-          v[0] += w[r].x; v[1] += w[r].y; v[2] += w[r].z; v[3] += w[r].w;
-        }
-      }
-      epilogue4(p.e, q0 + (u >> 5), pc, v);
+#define MOE_S(N) \
+  case N: split_store<N>(p.e, base, u0, u1, p0, q0); break
+    switch (S) {
+      MOE_S(1); MOE_S(2); MOE_S(3); MOE_S(4); MOE_S(5); MOE_S(6); MOE_S(7); MOE_S(8);
     }
+#undef MOE_S
   }
   cluster_sync();  // the others have read this CTA's tile
   tc_fence_after();
@@ -974,16 +988,18 @@ SplitForm split_form(int bn) {
   return Split<A_MN, B_MN, 256>::form();
 }
 
-// Time of a split in us: rounds of clusters, each with a start and an end beside the
-// stages of a part, and from 128 CTAs on the memory shared by more of them.  Measured at
-// K = 4096: 128 CTAs of BN = 16 9.9 us (32 CTAs without a split 22.8), BN = 64 12.0 (24.6),
-// BN = 128 12.6 (27.3), BN = 256 15.7 (33.7).
+// Time of a split in us: rounds of clusters, each with a start and an end beside the stages of
+// a part; a stage takes longer beside many other CTAs (they share L2), and with two on
+// an SM.  Fitted to (us, S = 1 / S = 4, 32 tiles): one stage BN = 16 3.7 / 4.0, 128 5.4 / 6.1, 256
+// 7.6 / 8.3; K = 4096 BN = 16 22.8 / 9.9, 64 24.6 / 12.0, 128 25.3 / 12.6, 256 30 / 15.7.
 double split_us(int bn, int64_t tiles, int at_once, int S, int steps) {
-  const double stage = bn <= 32 ? 0.27 : (bn <= 64 ? 0.29 : (bn == 128 ? 0.31 : 0.375));
-  const double ends = bn <= 32 ? 5.6 : (bn <= 64 ? 6.3 : (bn == 128 ? 7.7 : 9.7));
+  const double stage = bn == 256 ? 0.375 : 0.31;
+  const double ends = (bn <= 32 ? 3.5 : (bn <= 64 ? 4.0 : (bn == 128 ? 5.1 : 7.3))) + (S > 1 ? 0.4 : 0.0);
   const int64_t rounds = (tiles + at_once - 1) / at_once;
   const double ctas = (double)(tiles < at_once ? tiles : at_once) * S;
-  return rounds * ((steps + S - 1) / S * stage * (ctas > 128 ? ctas / 128 : 1.0) + ends);
+  double shared = 1 + 0.35 * (ctas < 32 ? 0.0 : (ctas > 96 ? 1.0 : (ctas - 32) / 64));
+  if (ctas > 140) shared *= ctas / 140;
+  return rounds * ((steps + S - 1) / S * stage * shared + ends);
 }
 
 // Tiles of 256 x 256 that the pairs take whole: where half of the pairs or more would idle
@@ -1064,13 +1080,15 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
       S = s;
     }
   }
-  // The pairs' time, likewise: rounds of whole and of half tiles.  512 x 4096 x 4096 21.7 us
-  // (halves), 700 x 4096 x 2048 16.1, 1024 x 4096 x 4096 25.3; split 21.8, 22.5, 32.1.
+  // The pairs' time, likewise: rounds of whole and of half tiles, none shorter than its
+  // epilogue.  256 x 4096 x 64 4.6 us, 512 x 4096 x 4096 21.7 (halves), 700 x 4096 x 2048 16.1,
+  // 1024 x 4096 x 4096 25.3, 4096 x 12288 x 64 29.7; split 7.6, 21.8, 22.5, 32.1, over 100.
   const int64_t pt = (a.Q + 255) / 256 * ((a.P + 255) / 256);
   const int pairs = sms / 2;
   const int64_t whole = pair_whole(pt, pairs), halves = 2 * (pt - whole);
-  const double pair_us =
-      5.7 + steps * (0.306 * ((whole + pairs - 1) / pairs) + 0.245 * ((halves + pairs - 1) / pairs));
+  auto round = [&](double stage) { return steps * stage > 2.3 ? steps * stage : 2.3; };
+  const double pair_us = (steps < 8 ? 2.4 : 4.4) + round(0.31) * ((whole + pairs - 1) / pairs) +
+                         round(0.255) * ((halves + pairs - 1) / pairs);
   const bool pair = S == 0 || (form ? form == 'p' : pair_us < best);
   if (pair) {
     const bool keep = a.out_f32 && steps > kSegSteps;

@@ -389,6 +389,15 @@ MOE_DEV float4 cluster_ld4(uint32_t caddr) {
   return v;
 }
 
+MOE_DEV float4 shared_ld4(uint32_t saddr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(saddr)
+               : "memory");
+  return v;
+}
+
 MOE_DEV void cluster_mbar_arrive(uint32_t caddr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
