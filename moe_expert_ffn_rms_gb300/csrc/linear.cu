@@ -57,19 +57,58 @@ constexpr int kEpiWarps = 8;
 constexpr int kSegSteps = 12;
 
 // ------------------------------------------------------------- activations --
-// sigmoid(z); exp overflows to infinity for z < -88, which gives 0.
-MOE_DEV float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// The epilogues run under the next tile's products, and with short K they are what
+// takes the time, so each activation is a few products around one 2^x and one reciprocal
+// (both within two units in the last place; results below 2^-126 are 0).
+MOE_DEV float exp2_f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+MOE_DEV float recip_f(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// 0.5 z (1 + tanh(u)) = z sigmoid(2 u): no difference of near values.
+// 1 / (1 + 2^u); 0 where 2^u is infinite.
+MOE_DEV float sigmoid2_f(float u) { return recip_f(1.0f + exp2_f(u)); }
+
+// 0.5 (1 + tanh(a (z + b z^3))) = sigmoid(2 a (z + b z^3)): no difference of near values.
+MOE_DEV float gelu_tanh_gate(float z) {
+  return sigmoid2_f(z * fmaf(z * z, -2.0f * kGeluA * kGeluB * kLog2E, -2.0f * kGeluA * kLog2E));
+}
+
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2).
+// Phi(-|z|) = e t (p0 + ... + p7 t^7), t = 1 / (1 + 0.3 |z|): the polynomial is a fit to
+// exp(z^2 / 2) Phi(-|z|) / t on 0 <= |z| <= 13.4 by least squares, weighted until the
+// largest relative error was least, 1.3e-7; past that e is 0.  So the lower tail keeps its
+// relative precision but for the rounding of z^2, as exp does.
+MOE_DEV float normal_cdf(float z, float& e) {
+  const float t = recip_f(fmaf(fabsf(z), 0.3f, 1.0f));
+  e = exp2_f(z * z * (-0.5f * kLog2E));
+  float p = fmaf(t, 0.035966480f, -0.158421054f);
+  p = fmaf(t, p, 0.208457217f);
+  p = fmaf(t, p, -0.055625346f);
+  p = fmaf(t, p, 0.129592260f);
+  p = fmaf(t, p, 0.099599972f);
+  p = fmaf(t, p, 0.120804417f);
+  p = fmaf(t, p, 0.119625991f);
+  const float q = t * p * e;
+  return z > 0.f ? 1.0f - q : q;
+}
+
 MOE_DEV float act_f(float z, int act) {
+  float e;
   switch (act) {
     case kActRelu: return z < 0.f ? 0.f : z;
-    case kActSilu: return z * sigmoid_f(z);
-    case kActGelu: return z * normcdff(z);
-    case kActGeluTanh: return z * sigmoid_f(2.0f * kGeluA * (z + kGeluB * z * z * z));
+    case kActSilu: return z * sigmoid2_f(z * -kLog2E);
+    case kActGelu: return z * normal_cdf(z, e);
+    case kActGeluTanh: return z * gelu_tanh_gate(z);
     default: return z;
   }
 }
@@ -95,14 +134,18 @@ MOE_DEV float act_slope(float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
     case kActSilu: {
-      const float p = sigmoid_f(z);
+      const float p = sigmoid2_f(z * -kLog2E);
       return p * fmaf(z, 1.0f - p, 1.0f);
     }
-    case kActGelu: return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), normcdff(z));
+    case kActGelu: {
+      float e;
+      const float c = normal_cdf(z, e);
+      return e == 0.f ? c : fmaf(z * 0.3989422804014327f, e, c);
+    }
     case kActGeluTanh: {
-      const float s = sigmoid_f(2.0f * kGeluA * (z + kGeluB * z * z * z));
+      const float s = gelu_tanh_gate(z);
       const float t = s * (1.0f - s);  // 0 where z^3 is past the exponent's range
-      return t == 0.f ? s : fmaf(z * t, 2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z), s);
+      return t == 0.f ? s : fmaf(z * t, 2.0f * kGeluA * fmaf(z * z, 3.0f * kGeluB, 1.0f), s);
     }
     default: return 1.f;
   }

@@ -266,6 +266,42 @@ def test_special_values_stay_where_they_belong(M, form):
         assert ok[z.abs() >= 20].all(), (act, db)
 
 
+@pytest.mark.parametrize("act", ["SILU", "GELU", "GELU_TANH"])
+def test_activations_keep_their_relative_precision(M, act):
+    """Over the whole range, the lower tail included, z given exactly by the bias.  An exponent of size u has three
+    roundings (3 U u relative in the result); the factors around it, 1 / (1 + .) and a polynomial within 1.3e-7,
+    have less than 16 more.  Results below 2^-126 may be 0."""
+    n = 4096
+    z = torch.linspace(-13.0, 13.0, n, device=DEV).to(BF)
+    zd = z.double()
+    one, zero = torch.zeros((1, 8), device=DEV, dtype=BF), torch.zeros((n, 8), device=DEV, dtype=BF)
+    a = getattr(M, "ACT_" + act)
+    f, db = torch.empty((1, n), device=DEV), torch.empty(n, device=DEV)
+    M.moe_linear(one, zero, f, bias=z.float(), act=a)
+    M.moe_linear_backward(torch.ones((1, n), device=DEV), one, zero,
+                          M.alloc_workspace(M.moe_linear_backward_workspace_size(1, n, 8)), db=db, pre=z[None], act=a)
+    c = 2 * math.sqrt(2 / math.pi)
+    if act == "SILU":
+        u, gate = zd.abs(), torch.sigmoid(zd)
+        parts = gate, zd * gate * torch.sigmoid(-zd)
+        loss = (zd * gate).abs()
+    elif act == "GELU":
+        u, gate = zd * zd / 2, 0.5 * torch.erfc(-zd / math.sqrt(2))
+        parts = gate, zd * torch.exp(-u) / math.sqrt(2 * math.pi)
+        loss = 0 * zd
+    else:
+        u = (c * (zd + 0.044715 * zd ** 3)).abs()
+        gate, rise = torch.sigmoid(u * zd.sign()), zd * c * (1 + 3 * 0.044715 * zd * zd)
+        parts = gate, rise * gate * torch.sigmoid(-u * zd.sign())
+        loss = (rise * gate).abs()
+    rel, least = U * (16 + 3 * u), 2.0 ** -126 * (1 + zd.abs() ** 3)
+    want = zd * gate
+    assert ((f[0].double() - want).abs() <= rel * want.abs() + least).all()
+    # the slope: its two terms' errors, and that of 1 - gate, two roundings of 1, times what stands before it
+    size = parts[0] + parts[1].abs()
+    assert ((db.double() - parts[0] - parts[1]).abs() <= 2 * rel * size + 2 * U * loss + least).all()
+
+
 def test_streams_graphs_shared_workspace_and_empty_batches(M, form):
     m, n, k = 130, 1032, 520
     rn = gen(4)
