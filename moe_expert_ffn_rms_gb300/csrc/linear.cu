@@ -15,11 +15,13 @@
 // inputs not in L2, against bytes at 6794 GB/s or FLOPs at 1952 TFLOP/s:
 //   M x N x K                 us      of the floor
 //   8192 x 8192 x 8192        539     1.05   pairs
-//   4096 x 12288 x 4096       217     0.97   pairs; GELU and kept values 235, 0.90
-//     dx, dW of it            236, 217  0.90, 0.97
+//   4096 x 12288 x 4096       217     0.97   pairs; GELU and kept values 241, 0.88;
+//                                            with the tanh form 230, 0.92
+//     dx, dW of it            235, 217  0.90, 0.97
 //   1024 x 4096 x 4096        25      0.70   pairs, one round of 64 of 76
 //   256 x 4096 x 4096         15.7    0.35   split, 128 CTAs
-//   61 x 7168 x 2048          10.5    0.44   split
+//   512 x 1024 x 1024         7.4     0.08   split, 64 columns, four CTAs a tile
+//   61 x 7168 x 2048          10.6    0.44   split
 //   16 x 4096 x 4096          10.3    0.48   split
 //   1 x 12288 x 4096          17.7    0.84   one token
 //   1 x 4096 x 4096           7.3     0.67   one token
@@ -198,7 +200,8 @@ MOE_DEV void epilogue4(const Epi& e, int64_t q, int64_t p, float (&v)[4]) {
 // of K.  Each leaves its fp32 tile in its shared memory (over the ring), then
 // every CTA adds a share of the tile's elements over the cluster in rank order and
 // runs the epilogue on them: no workspace, no atomics, the same bits every time.
-constexpr int kMaxSplit = 8;  // CTAs of a cluster
+// Few tiles with a long K are what bounds it: so the tile's width is chosen with S (below).
+constexpr int kMaxSplit = 16;  // CTAs of a cluster: 1 to 8, or 16
 
 struct SplitP {
   Epi e;
@@ -216,7 +219,7 @@ MOE_DEV void split_store(const Epi& e, uint32_t base, int u0, int u1, int64_t p0
   uint32_t at[S];
 #pragma unroll
   for (int r = 0; r < S; ++r) at[r] = S == 1 ? base : cluster_addr(base, r);
-#pragma unroll 2
+#pragma unroll S > 8 ? 1 : 2
   for (int u = u0 + threadIdx.x; u < u1; u += kLinThreads) {
     const int64_t pc = p0 + (u & 31) * 4;
     if (pc >= e.P) continue;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
 #define MOE_S(N) \
   case N: split_store<N>(p.e, base, u0, u1, p0, q0); break
     switch (S) {
-      MOE_S(1); MOE_S(2); MOE_S(3); MOE_S(4); MOE_S(5); MOE_S(6); MOE_S(7); MOE_S(8);
+      MOE_S(1); MOE_S(2); MOE_S(3); MOE_S(4); MOE_S(5); MOE_S(6); MOE_S(7); MOE_S(8); MOE_S(16);
     }
 #undef MOE_S
   }
@@ -986,6 +989,7 @@ struct Split {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       if (cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
+          cudaFuncSetAttribute(kernel(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
           cudaOccupancyMaxActiveClusters(&n, kernel(), &cfg) != cudaSuccess || n < 1) {
         (void)cudaGetLastError();
         n = -1;
@@ -1012,6 +1016,7 @@ struct Split {
     p.stage_bytes = kStage;
     p.ring = kRing;
     cudaError_t rc = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (rc == cudaSuccess && S > 8) rc = cudaFuncSetAttribute(kernel(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (rc != cudaSuccess) return rc;
     const dim3 grid(S, (unsigned)((a.P + kTileP - 1) / kTileP), (unsigned)((a.Q + BN - 1) / BN));
     return launch_cluster(kernel(), grid, S, kSmem, st, ta, tb, p);
@@ -1032,17 +1037,21 @@ SplitForm split_form(int bn) {
 }
 
 // Time of a split in us: rounds of clusters, each with a start and an end beside the stages of
-// a part; a stage takes longer beside many other CTAs (they share L2), and with two on
-// an SM.  Fitted to (us, S = 1 / S = 4, 32 tiles): one stage BN = 16 3.7 / 4.0, 128 5.4 / 6.1, 256
-// 7.6 / 8.3; K = 4096 BN = 16 22.8 / 9.9, 64 24.6 / 12.0, 128 25.3 / 12.6, 256 30 / 15.7.
-double split_us(int bn, int64_t tiles, int at_once, int S, int steps) {
-  const double stage = bn == 256 ? 0.375 : 0.31;
-  const double ends = (bn <= 32 ? 3.5 : (bn <= 64 ? 4.0 : (bn == 128 ? 5.1 : 7.3))) + (S > 1 ? 0.4 : 0.0);
+// a part; a stage takes longer beside many other CTAs (they share L2), and where two are on
+// an SM its loads bound it, 105 bytes a ns.  `least` is the time of the operands from memory.
+// Against 5000 times of 270 products it picks one 1.5% above the best: us with the widest tile and clusters of up
+// to eight, the best, and its BN and S: 512 x 1024 x 1024 9.3 7.4 64 4; 64 x 256 x 8192 9.6 6.9 32 16;
+// 128 x 256 x 256 5.2 3.9 16 2; 256 x 4096 x 4096 15.6 15.6 256 4; dW 256 x 256 over 65536 rows 54 28 128 16.
+double split_us(int bn, int64_t tiles, int at_once, int S, int steps, int sms, double least) {
+  const double ends = (bn == 16 ? 3.45 : (bn == 32 ? 4.0 : (bn == 64 ? 4.9 : (bn == 128 ? 5.3 : 7.5)))) +
+                      (S > 1 ? 0.05 : 0.0) + (S > 8 ? 0.3 : 0.0) + 0.01 * S;
   const int64_t rounds = (tiles + at_once - 1) / at_once;
   const double ctas = (double)(tiles < at_once ? tiles : at_once) * S;
-  double shared = 1 + 0.35 * (ctas < 32 ? 0.0 : (ctas > 96 ? 1.0 : (ctas - 32) / 64));
-  if (ctas > 140) shared *= ctas / 140;
-  return rounds * ((steps + S - 1) / S * stage * shared + ends);
+  double stage = (bn == 256 ? 0.33 : 0.275) * (1 + 0.4 * (ctas < 32 ? 0.0 : (ctas > 96 ? 1.0 : (ctas - 32) / 64)));
+  const double loads = 2 * (kTileP + bn) * kStepK * 2 / 105e3;
+  if (ctas > sms && stage < loads) stage = loads;
+  const double us = rounds * ((steps + S - 1) / S) * stage;
+  return (us > least ? us : least) + rounds * ends;
 }
 
 // Tiles of 256 x 256 that the pairs take whole: where half of the pairs or more would idle
@@ -1107,30 +1116,36 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
   }
   const int steps = (int)((a.K + kStepK - 1) / kStepK);
   const int seg = a.out_f32 ? kSegSteps : 1 << 30;
-  int bn = 16;
-  while (bn < a.Q && bn < 256) bn *= 2;
-  const SplitForm split = a.a_mn ? (a.b_mn ? split_form<true, true>(bn) : split_form<true, false>(bn))
-                                 : split_form<false, false>(bn);
-  const int64_t tiles = (a.P + kTileP - 1) / kTileP * ((a.Q + bn - 1) / bn);
   int S = 0;
   double best = 0;
-  for (int s = 1; s <= kMaxSplit && s <= steps; ++s) {
-    const int at_once = split.clusters(s);
-    if (at_once < 1) continue;
-    const double us = split_us(bn, tiles, at_once, s, steps);
-    if (S == 0 || us < best) {
-      best = us;
-      S = s;
+  SplitForm split{};
+  const double least = (double)(a.P + a.Q) * a.K * 2 / 6.8e6;
+  int widest = 16;
+  while (widest < a.Q && widest < 256) widest *= 2;
+  for (int bn = a.b_mn && widest < 64 ? 64 : widest; bn >= (a.b_mn ? 64 : 16); bn /= 2) {
+    const SplitForm f = a.a_mn ? (a.b_mn ? split_form<true, true>(bn) : split_form<true, false>(bn))
+                               : split_form<false, false>(bn);
+    const int64_t tiles = (a.P + kTileP - 1) / kTileP * ((a.Q + bn - 1) / bn);
+    if ((a.Q + bn - 1) / bn > 65535) break;
+    for (int s = 1; s <= kMaxSplit && s <= steps; s += s < 8 ? 1 : 8) {
+      const int at_once = f.clusters(s);
+      if (at_once < 1) continue;
+      const double us = split_us(bn, tiles, at_once, s, steps, sms, least);
+      if (S == 0 || us < best) {
+        best = us;
+        S = s;
+        split = f;
+      }
     }
   }
   // The pairs' time, likewise: rounds of whole and of half tiles, none shorter than its
-  // epilogue.  256 x 4096 x 64 4.6 us, 512 x 4096 x 4096 21.7 (halves), 700 x 4096 x 2048 16.1,
-  // 1024 x 4096 x 4096 25.3, 4096 x 12288 x 64 29.7; split 7.6, 21.8, 22.5, 32.1, over 100.
+  // epilogue.  256 x 4096 x 64 4.8 us, 512 x 4096 x 4096 21.7 (halves), 700 x 4096 x 2048 15.7,
+  // 1024 x 4096 x 4096 25.4, 4096 x 12288 x 64 29.8; split 4.8, 21.3, 19.8, 32.4, 87.
   const int64_t pt = (a.Q + 255) / 256 * ((a.P + 255) / 256);
   const int pairs = sms / 2;
   const int64_t whole = pair_whole(pt, pairs), halves = 2 * (pt - whole);
   auto round = [&](double stage) { return steps * stage > 2.3 ? steps * stage : 2.3; };
-  const double pair_us = (steps < 8 ? 2.4 : 4.4) + round(0.31) * ((whole + pairs - 1) / pairs) +
+  const double pair_us = 2.4 + (steps < 7 ? 0.3 * steps : 2.0) + round(0.31) * ((whole + pairs - 1) / pairs) +
                          round(0.255) * ((halves + pairs - 1) / pairs);
   const bool pair = S == 0 || (form ? form == 'p' : pair_us < best);
   if (pair) {

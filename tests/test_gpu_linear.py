@@ -198,6 +198,20 @@ def test_backward_activations(M, m, n, k, act, form):
             backward(M, m, n, k, act=act, dout=dout, dw=dw)
 
 
+# few tiles and a long K (clusters of up to sixteen, tiles narrower than the rows), in each product
+LONG = [(1, 64, 16384), (16, 128, 16392), (25, 456, 4024), (64, 256, 8192), (100, 72, 5000), (128, 256, 256),
+        (200, 136, 12288), (512, 1024, 1024), (700, 264, 2056)]
+
+
+@pytest.mark.parametrize("m,n,k", LONG)
+def test_few_tiles_and_long_sums(M, m, n, k, form):
+    forward(M, m, n, k, act="GELU", bias=F32, res=BF, pre=True)
+    forward(M, m, n, k, out=F32)
+    backward(M, m, k, n, which="dx")
+    backward(M, max(k, 16), n, max(m // 8 * 8, 8), which="dw")
+    backward(M, max(k, 16), n, max(m // 8 * 8, 8), dw=F32, which="dw")
+
+
 @pytest.mark.parametrize("act", ["SILU", "GELU", "GELU_TANH"])
 def test_backward_against_differences(M, act):
     """Gradients against central differences of the forward in 64 bits at the kept bf16 values."""
