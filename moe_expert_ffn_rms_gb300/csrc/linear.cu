@@ -14,7 +14,7 @@
 // kernel for one token, clusters that split K, and pairs of CTAs.  Device time per call,
 // inputs not in L2, against bytes at 6794 GB/s or FLOPs at 1952 TFLOP/s:
 //   M x N x K                 us      of the floor
-//   8192 x 8192 x 8192        539     1.05   pairs
+//   8192 x 8192 x 8192        539-582 0.97-1.05  pairs (under the power limit)
 //   4096 x 12288 x 4096       217     0.97   pairs; GELU and kept values 241, 0.88;
 //                                            with the tanh form 230, 0.92
 //     dx, dW of it            235, 217  0.90, 0.97
