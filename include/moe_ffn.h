@@ -653,8 +653,10 @@ typedef enum {
  *   one type; pre bf16 [M, N] or NULL: receives z for the backward pass; out [M, N]
  *   bf16 or fp32 (out_f32).
  * Products accumulate in the tensor cores' fp32, whose additions truncate: a sum of
- * K terms is off by about 1.1e-9 K of its magnitude.  With fp32 outputs no more
- * than 768 terms are added that way, and those sums in fp32 rounded to nearest.
+ * n terms is off by about 1.1e-9 n of its magnitude, up to 6e-9 n where all terms have
+ * one sign.  No more than 16384 terms (at most 1e-4, a fortieth of half a bf16 step) are
+ * added that way, 768 with fp32 outputs (1.3e-6), and those sums in fp32 rounded to
+ * nearest.
  * The activation takes the unrounded z.  Nothing of the result depends on what else runs.
  * M = 0 returns MOE_OK without looking at the tensor pointers.
  * Errors: INVALID_ARG (null or misaligned pointers, act); UNSUPPORTED_SHAPE unless N and K

@@ -51,12 +51,18 @@ constexpr int kMaxRing = 12;
 constexpr int kBoxBytes = 64 * 128;  // an MN-major box: 64 K rows of 64 elements
 constexpr int kLinThreads = 320;     // producer, MMA issuer, eight epilogue warps
 constexpr int kEpiWarps = 8;
-// fp32 results: the tensor cores' fp32 additions truncate, which over K terms leaves
-// about 1.1e-9 K of the sum's magnitude (measured: 9e-7 at K = 1024, 1.9e-5 at
-// 16384).  Sums longer than this many stages go through registers, rounded to
-// nearest, every kSegSteps stages, which leaves about 7e-7 (16 stages 1e-6, 8 stages 5e-7;
-// 4096 x 12288 x 4096 249 us, 238 and 263).
+// The tensor cores' fp32 additions truncate.  Over n terms of mixed signs that leaves about 1.1e-9 n
+// of the sum (measured: 9e-7 at n = 1024, 1.9e-5 at 16384), over terms of one sign, where
+// it adds up, 1.7e-9 n to 6e-9 n (1.3e-6 at 768, 8e-5 at 16384, 1.6e-3 at 262144).
+// fp32 results: sums longer than kSegSteps stages go through registers, rounded to nearest,
+// every kSegSteps stages, which leaves about 7e-7, 1.3e-6 with one sign (16 stages 1e-6, 8 stages
+// 5e-7; 4096 x 12288 x 4096 249 us, 238 and 263).
+// bf16 results: half a step is 2^-8 of the value.  What a CTA adds up over kLongSteps stages (16384
+// terms) is off by a fiftieth of that at most and is taken whole; longer sums go through
+// registers every kLongSeg stages.
 constexpr int kSegSteps = 12;
+constexpr int kLongSteps = 256;
+constexpr int kLongSeg = 64;
 
 // ------------------------------------------------------------- activations --
 // The epilogues run under the next tile's products, and with short K they are what
@@ -530,7 +536,7 @@ struct PairP {
   int tq, tp;       // tiles of 256 x 256 along q and p
   int whole;        // tiles taken whole; those after them in two halves of 128 columns
   int group;        // row tiles of a raster group
-  int seg;          // KEEP: stages added up in the tensor cores
+  int seg;          // KEEP: stages added up in the tensor cores at a time
   int* status;
 };
 
@@ -554,20 +560,27 @@ MOE_DEV void pair_unit(const PairP& p, int u, int& q, int& c, int& half) {
   }
 }
 
-// A warp's 32 rows x 128 bytes on their way out: each lane writes its row's words in
-// 16-byte chunks at the places of the 128-byte swizzle, and one lane hands them
-// to a TMA store, which writes whole lines and drops what lies outside the matrix.
+// A warp's 32 rows x W words (128 bytes; 32 of bf16 results beside 128 kept sums, which leave few
+// registers: 128 bytes of them spill so, 356 with 64-byte rows) on their way out: each lane
+// writes its row's words in 16-byte chunks at the places of the 128-byte (32-byte) swizzle, and one lane hands them to a TMA store, which writes whole lines and drops
+// what lies outside the matrix.
 // (Straight from registers, 32 bytes of 32 rows at a time: 38.6 us instead of 29.7
 // at 4096 x 12288 x 64.)
 constexpr int kStoreBytes = 32 * 128;
 
-MOE_DEV void store_box(unsigned char* stage, int lane, const uint32_t (&w)[32], const CUtensorMap* map, int x,
+// Columns of a store.
+constexpr int pair_box(bool f32, bool keep) { return f32 ? 32 : (keep ? 16 : 64); }
+
+template <int W>
+MOE_DEV void store_box(unsigned char* stage, int lane, const uint32_t (&w)[W], const CUtensorMap* map, int x,
                        int y) {
+  static_assert(W == 32 || W == 8, "a row of 128 or 32 bytes");
+  const int swizzle = W == 32 ? lane & 7 : (lane >> 2) & 1;
   if (lane == 0) bulk_wait_read<0>();
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+  for (int j = 0; j < W / 4; ++j)
+    *reinterpret_cast<uint4*>(stage + lane * (4 * W) + ((j ^ swizzle) << 4)) =
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   fence_proxy_async_shared();
   __syncwarp();
@@ -577,13 +590,13 @@ MOE_DEV void store_box(unsigned char* stage, int lane, const uint32_t (&w)[32], 
   }
 }
 
-// Columns p .. p + N - 1 (N = 64 for bf16 outputs, 32 for fp32) of the warp's 32 rows,
+// Columns p .. p + N - 1 of the warp's 32 rows,
 // one row per lane (q: this lane's, q0: the first); the first column is below P, a
 // multiple of 8.  Rows from Q on hold values of no row and are dropped.
-template <bool F32>
+template <bool F32, int N>
 MOE_DEV void epilogue_box(const Epi& e, int64_t q, int64_t q0, int64_t p, float* v, unsigned char* stage, int lane,
                           const CUtensorMap* tout, const CUtensorMap* tpre) {
-  constexpr int N = F32 ? 32 : 64;
+  constexpr int W = F32 ? N : N / 2;
   const int groups = (int)min((int64_t)(N / 8), (e.P - p) >> 3);
   if (e.bias) {
 #pragma unroll
@@ -596,7 +609,7 @@ MOE_DEV void epilogue_box(const Epi& e, int64_t q, int64_t q0, int64_t p, float*
       }
     }
   }
-  uint32_t w[32];
+  uint32_t w[W];
   if (e.pre) {
     if constexpr (F32) {  // half a box of bf16: straight out
       if (q < e.Q) {
@@ -606,7 +619,7 @@ MOE_DEV void epilogue_box(const Epi& e, int64_t q, int64_t q0, int64_t p, float*
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < W; ++i) w[i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
       store_box(stage, lane, w, tpre, (int)p, (int)q0);
     }
   }
@@ -623,7 +636,7 @@ MOE_DEV void epilogue_box(const Epi& e, int64_t q, int64_t q0, int64_t p, float*
     }
   }
 #pragma unroll
-  for (int i = 0; i < 32; ++i) w[i] = F32 ? __float_as_uint(v[i]) : pack2_bf16(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < W; ++i) w[i] = F32 ? __float_as_uint(v[i]) : pack2_bf16(v[2 * i], v[2 * i + 1]);
   store_box(stage, lane, w, tout, (int)p, (int)q0);
 }
 
@@ -776,7 +789,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue --
-    constexpr int N = F32 ? 32 : 64;  // columns of a store
+    constexpr int N = pair_box(F32, KEEP);
     const int quarter = warp & 3, side = (warp - 2) >> 2;
     unsigned char* stage = ring + (size_t)p.ring * p.stage_bytes + (warp - 2) * kStoreBytes;
     const uint32_t lead0 = cluster_addr(smem_u32(&tempty[0]), 0), lead1 = cluster_addr(smem_u32(&tempty[1]), 0);
@@ -819,7 +832,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
           for (int i = 0; i < 128; i += N)
             if (i < half && c0 + i < p.e.P)
-              epilogue_box<F32>(p.e, q0 + lane, q0, c0 + i, acc + i, stage, lane, &tout, &tpre);
+              epilogue_box<F32, N>(p.e, q0 + lane, q0, c0 + i, acc + i, stage, lane, &tout, &tpre);
         }
       } else {
         if (!(ok = mbar_wait(&tfull[buf], bph, &s_abort))) break;
@@ -837,7 +850,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (lane == 0) cluster_mbar_arrive(buf ? lead1 : lead0);
           }
           if (rows && c0 + i < p.e.P)
-            epilogue_box<F32>(p.e, q0 + lane, q0, c0 + i, v, stage, lane, &tout, &tpre);
+            epilogue_box<F32, N>(p.e, q0 + lane, q0, c0 + i, v, stage, lane, &tout, &tpre);
         }
         if (++buf == 2) {
           buf = 0;
@@ -1064,11 +1077,13 @@ int pair_whole(int64_t tiles, int pairs) {
 template <bool A_MN, bool B_MN, bool F32, bool KEEP>
 cudaError_t launch_pair(const ProductArgs& a, const Epi& e, int steps, int sms, int* status, cudaStream_t st) {
   CUtensorMap ta, tb, to, tp;  // the pair's rows are q (b of the product), its columns p (a)
+  constexpr int box = pair_box(F32, KEEP);
+  constexpr auto swizzle = F32 || !KEEP ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B;
   const auto out_type = F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   if (!operand_map(&ta, a.b, A_MN, a.Q, a.K, kTileP) || !operand_map(&tb, a.a, B_MN, a.P, a.K, 64) ||
-      !encode_map(&to, a.out, out_type, F32 ? 4 : 2, a.Q, a.P, F32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(&tp, a.pre ? a.pre : a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.Q, a.P, 64, 32,
-                  CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_map(&to, a.out, out_type, F32 ? 4 : 2, a.Q, a.P, box, 32, swizzle) ||
+      !encode_map(&tp, a.pre ? a.pre : a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.Q, a.P, F32 ? 64 : box, 32,
+                  F32 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle))
     return cudaErrorInvalidValue;
   const int64_t tiles = (a.Q + 255) / 256 * ((a.P + 255) / 256);
   PairP p{};
@@ -1078,7 +1093,7 @@ cudaError_t launch_pair(const ProductArgs& a, const Epi& e, int steps, int sms, 
   p.tp = (int)((a.P + 255) / 256);
   p.whole = pair_whole(tiles, sms / 2);
   p.group = 8;
-  p.seg = kSegSteps;
+  p.seg = F32 ? kSegSteps : kLongSeg;
   p.status = status;
   p.stage_bytes = 2 * kTileP * 128;
   p.ring = (kSmemMax - 1024 - kEpiWarps * kStoreBytes) / p.stage_bytes;
@@ -1115,7 +1130,6 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
                          static_cast<const bf16*>(a.a), static_cast<const bf16*>(a.b), a.K, W, e);
   }
   const int steps = (int)((a.K + kStepK - 1) / kStepK);
-  const int seg = a.out_f32 ? kSegSteps : 1 << 30;
   int S = 0;
   double best = 0;
   SplitForm split{};
@@ -1149,16 +1163,20 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
                          round(0.255) * ((halves + pairs - 1) / pairs);
   const bool pair = S == 0 || (form ? form == 'p' : pair_us < best);
   if (pair) {
-    const bool keep = a.out_f32 && steps > kSegSteps;
-#define MOE_PAIR(A, B)                                                                              \
-  return keep        ? launch_pair<A, B, true, true>(a, e, steps, sms, status, st)                  \
-         : a.out_f32 ? launch_pair<A, B, true, false>(a, e, steps, sms, status, st)                 \
-                     : launch_pair<A, B, false, false>(a, e, steps, sms, status, st)
-    if (a.a_mn && a.b_mn) MOE_PAIR(true, true);
-    if (a.a_mn) return launch_pair<false, true, false, false>(a, e, steps, sms, status, st);  // (dx is bf16)
-    MOE_PAIR(false, false);
+    const bool keep = steps > (a.out_f32 ? kSegSteps : kLongSteps);
+#define MOE_PAIR(A, B, F32)                                                    \
+  return keep ? launch_pair<A, B, F32, true>(a, e, steps, sms, status, st)     \
+              : launch_pair<A, B, F32, false>(a, e, steps, sms, status, st)
+    if (a.a_mn && a.b_mn) {
+      if (a.out_f32) MOE_PAIR(true, true, true);
+      MOE_PAIR(true, true, false);
+    }
+    if (a.a_mn) MOE_PAIR(false, true, false);  // (dx is bf16)
+    if (a.out_f32) MOE_PAIR(false, false, true);
+    MOE_PAIR(false, false, false);
 #undef MOE_PAIR
   }
+  const int seg = a.out_f32 ? kSegSteps : ((steps + S - 1) / S > kLongSteps ? kLongSeg : 1 << 30);
   return split.launch(a, e, S, steps, seg, status, st);
 }
 
