@@ -30,11 +30,10 @@
 #include <cuda.h>
 #include <stdlib.h>
 
-#include <atomic>
-
 #include "block_tail.cuh"
 #include "column_sum.cuh"
 #include "common.cuh"
+#include "device_counts.h"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
 #include "train.h"
@@ -968,10 +967,10 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, size_
 
 constexpr int kSmemMax = 226 * 1024 - 1024;  // dynamic; the static part and the reserve beside it
 
-// One instance of the split kernel: how many of its clusters of S CTAs run at once, and its
-// launch.
+// One instance of the split kernel: how many of its clusters of S CTAs run at once on a device (the
+// current one), and its launch.
 struct SplitForm {
-  int (*clusters)(int S);
+  int (*clusters)(int device, int S);
   cudaError_t (*launch)(const ProductArgs& a, const Epi& e, int S, int steps, int seg, int* status, cudaStream_t st);
 };
 
@@ -986,11 +985,9 @@ struct Split {
 
   static auto kernel() { return product_split_kernel<A_MN, B_MN, BN>; }
 
-  // (the same on every device that the library runs on)
-  static int clusters(int S) {
-    static std::atomic<int> known[kMaxSplit + 1];
-    int n = known[S].load(std::memory_order_relaxed);
-    if (n == 0) {
+  static int clusters(int device, int S) {
+    static DeviceCounts<kMaxSplit + 1> known;
+    return known.get(device, S, [S] {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1001,19 +998,18 @@ struct Split {
       cfg.dynamicSmemBytes = kSmem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      if (cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
-          cudaFuncSetAttribute(kernel(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-          cudaOccupancyMaxActiveClusters(&n, kernel(), &cfg) != cudaSuccess || n < 1) {
+      int n = 0;
+      cudaError_t e = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel(), &cfg);
+      if (e != cudaSuccess) {
         (void)cudaGetLastError();
-        n = -1;
-      } else {
-        // the query counts one CTA of a kernel with TMEM per SM; two run (at BN = 16, 256 CTAs take
-        // the time of one round: 9.9 us)
-        n *= kPerSm;
+        return e == cudaErrorInvalidClusterSize ? 0 : -1;
       }
-      known[S].store(n, std::memory_order_relaxed);
-    }
-    return n;
+      // the query counts one CTA of a kernel with TMEM per SM; two run (at BN = 16, 256 CTAs take
+      // the time of one round: 9.9 us)
+      return n * kPerSm;
+    });
   }
 
   static cudaError_t launch(const ProductArgs& a, const Epi& e, int S, int steps, int seg, int* status,
@@ -1130,6 +1126,9 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
                          static_cast<const bf16*>(a.a), static_cast<const bf16*>(a.b), a.K, W, e);
   }
   const int steps = (int)((a.K + kStepK - 1) / kStepK);
+  int device = 0;
+  const cudaError_t rc = cudaGetDevice(&device);
+  if (rc != cudaSuccess) return rc;
   int S = 0;
   double best = 0;
   SplitForm split{};
@@ -1142,7 +1141,7 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
     const int64_t tiles = (a.P + kTileP - 1) / kTileP * ((a.Q + bn - 1) / bn);
     if ((a.Q + bn - 1) / bn > 65535) break;
     for (int s = 1; s <= kMaxSplit && s <= steps; s += s < 8 ? 1 : 8) {
-      const int at_once = f.clusters(s);
+      const int at_once = f.clusters(device, s);
       if (at_once < 1) continue;
       const double us = split_us(bn, tiles, at_once, s, steps, sms, least);
       if (S == 0 || us < best) {
