@@ -2,6 +2,7 @@
 // argument checks and launches.
 #include <stdarg.h>
 #include <stdio.h>
+#include <stdlib.h>
 
 #include "api_internal.h"
 #include "common.cuh"
@@ -104,6 +105,15 @@ moe_status check_linear(int M, int N, int K, int act) {
               K <= kLinearMaxNK && K % 8 == 0,
           MOE_ERR_UNSUPPORTED_SHAPE, "M=%d N=%d K=%d (M <= 2^23; N, K multiples of 8, <= 2^20)", M, N, K);
   MOE_REQ(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, MOE_ERR_INVALID_ARG, "act=%d", act);
+  return MOE_OK;
+}
+
+// MOE_LINEAR_FORM, read once per call.  `token`: whether the one-token kernel can run it.
+moe_status read_form(bool token, moe::LinearForm* form) {
+  const char* name = getenv("MOE_LINEAR_FORM");
+  MOE_REQ(moe::linear_form(name, form), MOE_ERR_INVALID_ARG, "MOE_LINEAR_FORM=%.32s: token, split or pair", name);
+  MOE_REQ(token || *form != moe::kFormToken, MOE_ERR_INVALID_ARG,
+          "MOE_LINEAR_FORM=token: for moe_linear of one row alone");
   return MOE_OK;
 }
 
@@ -257,6 +267,8 @@ moe_status moe_linear(const void* x, const void* w, const void* bias, int32_t bi
           MOE_ERR_INVALID_ARG, "misaligned pointer");
   MOE_REQ(residual != out || (residual_f32 != 0) == (out_f32 != 0), MOE_ERR_INVALID_ARG,
           "residual may be out only when both have one type");
+  moe::LinearForm form;
+  if ((rc = read_form(M == 1, &form)) != MOE_OK) return rc;
   int sms = 0, *status = nullptr;
   if ((rc = moe::api_device(&sms, &status)) != MOE_OK) return rc;
   moe::ProductArgs a{};
@@ -273,6 +285,7 @@ moe_status moe_linear(const void* x, const void* w, const void* bias, int32_t bi
   a.bias_f32 = bias_f32 != 0;
   a.res_f32 = residual_f32 != 0;
   a.out_f32 = out_f32 != 0;
+  a.form = form;
   MOE_CUDA(moe::launch_product(a, sms, status, (cudaStream_t)stream), "linear launch");
   return MOE_OK;
 }
@@ -301,6 +314,8 @@ moe_status moe_linear_backward(const void* dout, int32_t dout_f32, const void* p
             "linear backward workspace %zu < %zu bytes", workspace_bytes, need);
     MOE_REQ(aligned(workspace, 256), MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   }
+  moe::LinearForm form = moe::kFormAuto;
+  if (M > 0 && (rc = read_form(!dx && !dw, &form)) != MOE_OK) return rc;
   int sms = 0, *status = nullptr;
   if ((rc = moe::api_device(&sms, &status)) != MOE_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
@@ -333,6 +348,7 @@ moe_status moe_linear_backward(const void* dout, int32_t dout_f32, const void* p
     a.Q = M;
     a.K = N;
     a.out = dx;
+    a.form = form;
     MOE_CUDA(moe::launch_product(a, sms, status, st), "linear backward launch (dx)");
   }
   if (dw) {
@@ -346,6 +362,7 @@ moe_status moe_linear_backward(const void* dout, int32_t dout_f32, const void* p
     a.K = M;
     a.out = dw;
     a.out_f32 = dw_f32 != 0;
+    a.form = form;
     MOE_CUDA(moe::launch_product(a, sms, status, st), "linear backward launch (dw)");
   }
   return MOE_OK;

@@ -28,7 +28,7 @@
 // Small ones are a launch (1.7 us for one token, 3.4 with TMEM and a cluster), the ramp of the
 // loads and the reduction over the cluster; large ones the tensor pipe.
 #include <cuda.h>
-#include <stdlib.h>
+#include <string.h>
 
 #include "block_tail.cuh"
 #include "column_sum.cuh"
@@ -1104,6 +1104,19 @@ cudaError_t launch_pair(const ProductArgs& a, const Epi& e, int steps, int sms, 
 
 }  // namespace
 
+bool linear_form(const char* name, LinearForm* form) {
+  static const struct {
+    const char* name;
+    LinearForm form;
+  } forms[] = {{"", kFormAuto}, {"token", kFormToken}, {"split", kFormSplit}, {"pair", kFormPair}};
+  for (const auto& f : forms)
+    if (strcmp(name ? name : "", f.name) == 0) {
+      *form = f.form;
+      return true;
+    }
+  return false;
+}
+
 cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStream_t st) {
   Epi e{};
   e.bias = a.bias;
@@ -1116,9 +1129,7 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
   e.out_f32 = a.out_f32;
   e.P = a.P;
   e.Q = a.Q;
-  const char* env = getenv("MOE_LINEAR_FORM");
-  const char form = env ? env[0] : 0;
-  if (!a.a_mn && !a.b_mn && a.Q == 1 && (!form || form == 't')) {
+  if (!a.a_mn && !a.b_mn && a.Q == 1 && (a.form == kFormAuto || a.form == kFormToken)) {
     int W = 1;  // warps per row: enough of them to fill the SMs, two loads for each at least
     while (W < kRowsWarps && a.P / kRowsR * W < (int64_t)sms * 48 && a.K / 8 > 64 * W) W *= 2;
     const int64_t per = kRowsWarps / W * kRowsR;
@@ -1160,7 +1171,7 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
   auto round = [&](double stage) { return steps * stage > 2.3 ? steps * stage : 2.3; };
   const double pair_us = 2.4 + (steps < 7 ? 0.3 * steps : 2.0) + round(0.31) * ((whole + pairs - 1) / pairs) +
                          round(0.255) * ((halves + pairs - 1) / pairs);
-  const bool pair = S == 0 || (form ? form == 'p' : pair_us < best);
+  const bool pair = S == 0 || (a.form == kFormAuto ? pair_us < best : a.form == kFormPair);
   if (pair) {
     const bool keep = steps > (a.out_f32 ? kSegSteps : kLongSteps);
 #define MOE_PAIR(A, B, F32)                                                    \

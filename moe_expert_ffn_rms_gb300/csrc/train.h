@@ -75,6 +75,11 @@ cudaError_t launch_norm_grad(const NormGradArgs& a, int sms, int* status, cudaSt
 // ---------------------------------------------------------------- linear.cu --
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
+// The form of a product: chosen by its size, or the one that MOE_LINEAR_FORM names.
+enum LinearForm { kFormAuto = 0, kFormToken, kFormSplit, kFormPair };
+// What `name` (NULL and "": kFormAuto) says; false if no form has that name.
+bool linear_form(const char* name, LinearForm* form);
+
 // One product D[q, p] = sum_k a[p, k] b[q, k] with p the contiguous index of the
 // output, and its epilogue out = residual + act(D + bias).  a_mn: a is stored [K, P]
 // instead of [P, K]; b_mn likewise.
@@ -89,6 +94,7 @@ struct ProductArgs {
   void* out;             // [Q, P]
   int act;
   bool bias_f32, res_f32, out_f32;
+  LinearForm form;  // kFormToken: Q = 1, a and b K-major
 };
 cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStream_t st);
 
