@@ -568,6 +568,17 @@ def moe_quantize_fp8_blocks(x, q, scale, block_rows, stream=None):
 _cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+_INT32 = 0x7fffffff
+
+
+def _fits(*sizes):
+    """ValueError unless each fits the int32 of the C entry points; ctypes would cut it off without a word.  (The calls
+    below look at the sizes' bits together first: an or of two or three costs a tenth of this.)"""
+    for v in sizes:
+        if not -_INT32 <= v <= _INT32:
+            raise ValueError(f"size {v}: does not fit an int32")
+
+
 def _arg(t, name, shape, dtypes, index):
     """Pointer of a checked tensor on CUDA device `index`."""
     if t.dtype in dtypes and t.shape == shape and t.get_device() == index and t.is_contiguous():
@@ -607,6 +618,8 @@ def moe_unpermute(y, row_of_pair, out, T, k, topk_w=None, residual=None, stream=
     [T*k, H] in expert order, row_of_pair int32 [T*k] of moe_permute (negative: dropped), topk_w
     fp32 [T, k] (None: all 1), residual and out bf16 / fp32 [T, H]; residual may be out."""
     H = y.shape[-1]
+    if T | k | H > _INT32:
+        _fits(T, k, H)
     index, st = _queue(y, stream)
     _check(lib.moe_unpermute(
         _arg(y, "y", (T * k, H), _FLOATS, index), y.dtype == torch.bfloat16, _pairs(row_of_pair, T * k, index),
@@ -623,13 +636,15 @@ def moe_unpermute_backward(dout, y, row_of_pair, topk_w, T, k, dy=None, dw=None,
     without y; rows that no pair owns are left as they were), dw fp32 [T, k], and with ids int32 [T, k] the
     router's dlogits fp32 [T, E].  y is needed for dw and dlogits; dy may be y."""
     H = dout.shape[-1]
-    index, st = _queue(dout, stream)
     yt = y if y is not None else dy
     if dy is not None and y is not None and dy.dtype != y.dtype:
         raise ValueError(f"dy: dtype {dy.dtype}, need {y.dtype}")
     if dlogits is not None and dlogits.dim() != 2:
         raise ValueError("dlogits: must be [T, E]")
     E = 0 if dlogits is None else dlogits.shape[1]
+    if T | k | H | E > _INT32:
+        _fits(T, k, H, E)
+    index, st = _queue(dout, stream)
     _check(lib.moe_unpermute_backward(
         _arg(dout, "dout", (T, H), _FLOATS, index), dout.dtype == torch.float32,
         None if y is None else _arg(y, "y", (T * k, H), _FLOATS, index), yt is None or yt.dtype == torch.bfloat16,
@@ -644,6 +659,8 @@ def moe_permute_backward(dxp, row_of_pair, dx, T, k, dres=None, stream=None):
     """Gradient of moe_permute's gather: dx = dres + the sum of each token's rows of dxp (bf16 / fp32
     [T*k, H], expert order).  dres and dx bf16 / fp32 [T, H]; dres may be dx."""
     H = dxp.shape[-1]
+    if T | k | H > _INT32:
+        _fits(T, k, H)
     index, st = _queue(dxp, stream)
     _check(lib.moe_permute_backward(
         _arg(dxp, "dxp", (T * k, H), _FLOATS, index), dxp.dtype == torch.bfloat16,
@@ -659,6 +676,8 @@ def moe_layernorm(x, w, eps, y, b=None, mean=None, rstd=None, stream=None):
     type; y bf16 / fp32 [T, H]; mean, rstd fp32 [T] for the backward pass."""
     shape = x.shape
     T, H = shape
+    if T | H > _INT32:
+        _fits(T, H)
     index, st = _queue(x, stream)
     wt = w.dtype
     _check(lib.moe_layernorm(
@@ -671,6 +690,7 @@ def moe_layernorm(x, w, eps, y, b=None, mean=None, rstd=None, stream=None):
 
 
 def moe_norm_backward_workspace_size(T, H) -> int:
+    _fits(T, H)
     n = lib.moe_norm_backward_workspace_size(T, H)
     if n == 0:
         raise MoeError(2, last_error())
@@ -683,6 +703,8 @@ def moe_layernorm_backward(dy, x, w, mean, rstd, dx, dw, workspace, db=None, dre
     dx may be x, dres, or dy of the same type."""
     shape, xt = x.shape, (x.dtype,)
     T, H = shape
+    if T | H > _INT32:
+        _fits(T, H)
     index, st = _queue(x, stream)
     _check(lib.moe_layernorm_backward(
         _arg(dy, "dy", shape, _FLOATS, index), dy.dtype == torch.float32, _arg(x, "x", shape, _FLOATS, index),
@@ -699,6 +721,8 @@ def moe_rmsnorm_backward(dy, x, w, eps, dx, dw, workspace, dres=None, stream=Non
     moe_layernorm_backward."""
     shape, xt = x.shape, (x.dtype,)
     T, H = shape
+    if T | H > _INT32:
+        _fits(T, H)
     index, st = _queue(x, stream)
     _check(lib.moe_rmsnorm_backward(
         _arg(dy, "dy", shape, _FLOATS, index), dy.dtype == torch.float32, _arg(x, "x", shape, _FLOATS, index),
@@ -712,10 +736,12 @@ def moe_linear(x, w, out, bias=None, residual=None, act=ACT_NONE, pre=None, stre
     """out = residual + act(x w^T + bias).  x bf16 [M, K], w bf16 [N, K], bias bf16 / fp32 [N], residual
     and out bf16 / fp32 [M, N] (residual may be out), act one of the ACT_ constants; pre bf16 [M, N]
     receives the values before the activation."""
-    index, st = _queue(x, stream)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: must be [M, K] and [N, K]")
     (m, k), n = x.shape, w.shape[0]
+    if m | n | k | act > _INT32:
+        _fits(m, n, k, act)
+    index, st = _queue(x, stream)
     _check(lib.moe_linear(
         _arg(x, "x", (m, k), _BF16, index), _arg(w, "w", (n, k), _BF16, index),
         None if bias is None else _arg(bias, "bias", (n,), _FLOATS, index),
@@ -728,6 +754,7 @@ def moe_linear(x, w, out, bias=None, residual=None, act=ACT_NONE, pre=None, stre
 
 
 def moe_linear_backward_workspace_size(M, N, K) -> int:
+    _fits(M, N, K)
     n = lib.moe_linear_backward_workspace_size(M, N, K)
     if n == 0:
         raise MoeError(2, last_error())
@@ -738,10 +765,12 @@ def moe_linear_backward(dout, x, w, workspace, dx=None, dw=None, db=None, pre=No
     """Gradients of moe_linear from dout bf16 / fp32 [M, N]: dx bf16 [M, K], dw bf16 / fp32 [N, K], db fp32
     [N], each where it is given; pre of the forward call with an activation; workspace of
     moe_linear_backward_workspace_size(M, N, K) bytes."""
-    index, st = _queue(dout, stream)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: must be [M, K] and [N, K]")
     (m, k), n = x.shape, w.shape[0]
+    if m | n | k | act > _INT32:
+        _fits(m, n, k, act)
+    index, st = _queue(dout, stream)
     _check(lib.moe_linear_backward(
         _arg(dout, "dout", (m, n), _FLOATS, index), dout.dtype == torch.float32,
         None if pre is None else _arg(pre, "pre", (m, n), _BF16, index), _arg(x, "x", (m, k), _BF16, index),
