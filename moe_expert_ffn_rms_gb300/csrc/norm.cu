@@ -32,6 +32,7 @@
 #include "block_tail.cuh"
 #include "column_sum.cuh"
 #include "common.cuh"
+#include "norm_stages.h"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
 #include "train.h"
@@ -46,8 +47,6 @@ constexpr int kNarrowMaxV = 64;      // 8-column chunks of a row that a warp tak
 constexpr int kNarrowGradV = 32;     // and backward (16384 x 512: 25.2 us so, 21.7 streamed)
 constexpr int kNarrowWarps = 8;      // rows at a time of a CTA then
 constexpr int kNarrowCtas = 2;       // of them per SM, backward
-constexpr int kNormStages = 8;       // rows on their way at most
-constexpr int kNormSmem = 212 << 10; // per SM, for the stages
 constexpr int kMaxSms = 160;         // the workspace's size goes by it
 
 // Sums of N values over the CTA of at most NW warps; every thread gets them.  `red` is
@@ -295,9 +294,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32) layernorm_narrow_kernel(con
 
 // CTA-wide forms: kRowVpt chunks per thread, so that the reductions' instructions, which every
 // warp repeats, are few beside the row's own (8192 x 7168 bf16 with two chunks: 69 us).
-constexpr int kRowVpt = 2;
 constexpr int kRowNw = 32;
-constexpr int kRowThreadsPerSm = 1024;  // of the streaming form: 64 registers each
 
 template <bool XF32, bool KEPT>
 __global__ void __launch_bounds__(kRowNw * 32) layernorm_row_kernel(const LayerNormArgs a) {
@@ -333,6 +330,7 @@ __global__ void __launch_bounds__(kRowThreadsPerSm)
     layernorm_stream_kernel(const LayerNormArgs a, int S, int* status) {
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ float red[2][1][kRowNw];
+  static_assert(sizeof(red) + kNormStages * 8 + 16 <= kCtaSmem - 1024, "the static part that the stages leave room for");
   __shared__ uint64_t full[kNormStages];
   __shared__ int s_abort;
   __shared__ int64_t s_last;  // row sent for last
@@ -573,9 +571,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradA
   norm_grad_part<VPT>(a, tid, nt, dw, db);
 }
 
-constexpr int kGradVpt = 2;
-constexpr int kGradNw = 16;
-
 // The stages of layernorm_stream_kernel, each with the row's x, dy and dres.  The
 // parts are in registers when the reduction has passed, so a stage is sent for again
 // then.
@@ -584,6 +579,7 @@ __global__ void __launch_bounds__(kGradNw * 32) norm_grad_stream_kernel(const No
   constexpr int V = kGradVpt;
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ float red[2][2][kGradNw];
+  static_assert(sizeof(red) + kNormStages * 8 + 16 <= kCtaSmem - 1024, "the static part that the stages leave room for");
   __shared__ uint64_t full[kNormStages];
   __shared__ int s_abort;
   __shared__ int64_t s_last;  // row sent for last
@@ -664,18 +660,6 @@ __global__ void __launch_bounds__(kGradNw * 32) norm_grad_stream_kernel(const No
   stream_end(ok, full, S, s_last, status);
 }
 
-int row_threads(int nv) { return (nv + 31) / 32 * 32; }
-
-// CTAs per SM: the forward kernels have at most 64 registers, the backward ones 128.
-int row_ctas(int nv) {
-  const int n = kRowThreadsPerSm / row_threads((nv + kRowVpt - 1) / kRowVpt);
-  return n < 1 ? 1 : (n < 16 ? n : 16);
-}
-int grad_ctas(int nv) {
-  const int n = kGradNw * 32 / row_threads((nv + kGradVpt - 1) / kGradVpt);
-  return n < 8 ? n : 8;
-}
-
 // CTAs (rows of partial sums) of the backward pass on `sms` SMs.
 int norm_grad_ctas(int T, int H, int sms) {
   const int nv = H >> 3;
@@ -713,8 +697,7 @@ cudaError_t launch_layernorm(const LayerNormArgs& a, int sms, int* status, cudaS
         a.x_f32 ? (a.w_f32 ? layernorm_row_kernel<true, false> : layernorm_row_kernel<true, true>)
                 : (a.w_f32 ? layernorm_row_kernel<false, false> : layernorm_row_kernel<false, true>),
         dim3(a.T), dim3(threads), 0, st, a);
-  int S = (int)(kNormSmem / ctas / bytes);
-  if (S > kNormStages) S = kNormStages;
+  const int S = norm_stages(ctas, bytes);
   auto kern = a.x_f32 ? (a.w_f32 ? layernorm_stream_kernel<true, false> : layernorm_stream_kernel<true, true>)
                       : (a.w_f32 ? layernorm_stream_kernel<false, false> : layernorm_stream_kernel<false, true>);
   // the same limit in every call: another thread's launch may lie between this and ours
@@ -746,8 +729,7 @@ cudaError_t launch_norm_grad(const NormGradArgs& a, int sms, int* status, cudaSt
     } else if (nv <= kGradVpt * kGradNw * 32) {
       const int threads = row_threads((nv + kGradVpt - 1) / kGradVpt);
       const int64_t bytes = (int64_t)a.H * ((a.x_f32 ? 4 : 2) * (a.dres ? 2 : 1) + (a.dy_f32 ? 4 : 2));
-      int S = (int)(kNormSmem / grad_ctas(nv) / bytes);
-      if (S > kNormStages) S = kNormStages;
+      const int S = norm_stages(grad_ctas(nv), bytes);
       auto pick = [&](auto r) {
         constexpr bool R = decltype(r)::value;
         return a.x_f32 ? (a.dy_f32 ? norm_grad_stream_kernel<R, true, true> : norm_grad_stream_kernel<R, true, false>)
