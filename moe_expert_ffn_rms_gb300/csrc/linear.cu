@@ -200,15 +200,12 @@ MOE_DEV void epilogue4(const Epi& e, int64_t q, int64_t p, float (&v)[4]) {
         make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
 }
 
-// A wait may run out in one lane and pass in the others, and what follows it (elect.sync, tcgen05
-// instructions, __syncwarp) needs the whole warp, without a limit: no lane may leave its role alone.
-// An epilogue warp votes on each wait.  In a producer or an MMA issuer, whose stages a vote each would slow by 1 to
-// 3%, a lane whose wait ran out goes on to the end of the loop, without waiting any more, and issues nothing.
+// The warp's wait: false in all lanes if it ran out in one of them.  What follows a wait (elect.sync, tcgen05
+// instructions, __syncwarp) needs the whole warp, without a limit, and a lane that left its role alone
+// would never reach it.  (The vote is also what a stage's lanes meet at: with a __syncwarp beside it
+// large products take 1.5% longer; one thread per role instead of a warp, 30%.)
 MOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-}
-MOE_DEV bool still(bool ok, uint64_t* bar, uint32_t parity, int* abort) {
-  return ok && mbar_wait(bar, parity, abort);
 }
 
 // ------------------------------------------------------- cluster split-K form --
@@ -300,8 +297,8 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
     uint32_t ph = 0, armed = 0, armed_ph = 0;
     bool ok = true;
     for (int k = k0; k < k1; ++k) {
-      ok = still(ok, &empty[s], ph ^ 1, &s_abort);
-      if (elect_one() && ok) {
+      if (!(ok = warp_wait(&empty[s], ph ^ 1, &s_abort))) break;
+      if (elect_one()) {
         unsigned char* a = ring + (size_t)s * p.stage_bytes;
         unsigned char* b = a + kTileP * 128;
         mbar_arrive_expect_tx(&full[s], kTileP * 128 + (B_MN ? kBBoxes * kBoxBytes : BN * 128));
@@ -317,17 +314,16 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
           tma_load_2d_plain(b, &tb, &full[s], k * kStepK, (int)q0);
         }
       }
-      __syncwarp();
-      armed |= (ok ? 1u : 0u) << s;
-      if (ok) armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
+      armed |= 1u << s;
+      armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
       if (++s == p.ring) {
         s = 0;
         ph ^= 1;
       }
     }
-    ok = ok && producer_tail(empty, p.ring, s, ph, &s_abort);
+    if (ok) ok = __all_sync(0xffffffffu, producer_tail(empty, p.ring, s, ph, &s_abort));
     if (!ok) {
-      flag_status(p.status, MOE_ERR_TIMEOUT);
+      if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
       drain_armed(full, p.ring, armed, armed_ph);
     }
   } else if (warp == 1) {
@@ -338,14 +334,14 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
     bool ok = true, issued = false;
     for (int k = k0; k < k1; ++k) {
       if (n == 0) {
-        ok = still(ok, &tempty[buf], bph ^ 1, &s_abort);
+        if (!(ok = warp_wait(&tempty[buf], bph ^ 1, &s_abort))) break;
         tc_fence_after();
       }
-      ok = still(ok, &full[s], ph, &s_abort);
+      if (!(ok = warp_wait(&full[s], ph, &s_abort))) break;
       tc_fence_after();
       const uint32_t a = smem_u32(ring + (size_t)s * p.stage_bytes), b = a + kTileP * 128;
       const bool last = k + 1 == k1 || n + 1 == p.seg;
-      if (elect_one() && ok) {
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const uint64_t ad = A_MN ? sw128_mn_desc(a + kk * 2048, 64) : sw128_desc(a + kk * 32);
@@ -355,7 +351,6 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
         mma_commit(&empty[s]);
         if (last) mma_commit(&tfull[buf]);
       }
-      __syncwarp();
       issued = true;
       if (++s == p.ring) {
         s = 0;
@@ -370,9 +365,9 @@ __global__ void __launch_bounds__(kLinThreads, BN <= 64 ? 2 : 1)
         }
       }
     }
-    ok = __all_sync(0xffffffffu, ok && accumulator_tail(tempty, buf, bph, &s_abort));
+    if (ok) ok = __all_sync(0xffffffffu, accumulator_tail(tempty, buf, bph, &s_abort));
     if (!ok) {
-      flag_status(p.status, MOE_ERR_TIMEOUT);
+      if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
       if (issued) {  // issued MMAs complete before TMEM is released
         if (elect_one()) mma_commit(&drain);
         __syncwarp();
@@ -697,7 +692,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int s = 0;
     uint32_t ph = 0, armed = 0, armed_ph = 0;
     bool ok = true;
-    for (int u = first; u < units; u += stride) {
+    for (int u = first; ok && u < units; u += stride) {
       int a0, b0, half;
       pair_unit(p, u, a0, b0, half);
       if (half == 0) continue;
@@ -705,8 +700,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       b0 += (int)rank * half;
       const uint32_t bytes = 2 * (kTileP * 128 + half * 128);
       for (int k = 0; k < p.steps; ++k) {
-        ok = still(ok, &empty[s], ph ^ 1, &s_abort);
-        if (elect_one() && ok) {
+        if (!(ok = warp_wait(&empty[s], ph ^ 1, &s_abort))) break;
+        if (elect_one()) {
           unsigned char* a = ring + (size_t)s * p.stage_bytes;
           unsigned char* b = a + kTileP * 128;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
@@ -721,18 +716,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             else tma_load_2d_pair(b + i * 128, &tb, bar, k * kStepK, b0 + i);
           }
         }
-        __syncwarp();
-        armed |= (ok ? 1u : 0u) << s;
-        if (ok) armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
+        armed |= 1u << s;
+        armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
         if (++s == p.ring) {
           s = 0;
           ph ^= 1;
         }
       }
     }
-    ok = ok && producer_tail(empty, p.ring, s, ph, &s_abort);
+    if (ok) ok = __all_sync(0xffffffffu, producer_tail(empty, p.ring, s, ph, &s_abort));
     if (!ok) {
-      flag_status(p.status, MOE_ERR_TIMEOUT);
+      if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
       if (rank == 0) drain_armed(full, p.ring, armed, armed_ph);
       // copies of the pair's other CTA that no barrier of this one was armed for
       const long long t0 = clock64();
@@ -745,21 +739,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int s = 0, buf = 0;
       uint32_t ph = 0, bph = 0;
       bool ok = true, issued = false;
-      for (int u = first; u < units; u += stride) {
+      for (int u = first; ok && u < units; u += stride) {
         int q, c, half, n = 0;
         pair_unit(p, u, q, c, half);
         if (half == 0) continue;
         const uint32_t idesc = make_idesc_major(256, 2 * half, A_MN, B_MN);
         for (int k = 0; k < p.steps; ++k) {
           if (n == 0) {
-            ok = still(ok, &tempty[buf], bph ^ 1, &s_abort);
+            if (!(ok = warp_wait(&tempty[buf], bph ^ 1, &s_abort))) break;
             tc_fence_after();
           }
-          ok = still(ok, &full[s], ph, &s_abort);
+          if (!(ok = warp_wait(&full[s], ph, &s_abort))) break;
           tc_fence_after();
           const uint32_t a = smem_u32(ring + (size_t)s * p.stage_bytes), b = a + kTileP * 128;
           const bool last = k + 1 == p.steps || (KEEP && n + 1 == p.seg);
-          if (elect_one() && ok) {
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint64_t ad = A_MN ? sw128_mn_desc(a + kk * 2048, 64) : sw128_desc(a + kk * 32);
@@ -769,7 +763,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             mma_commit_pair(&empty[s], 3);
             if (last) mma_commit_pair(&tfull[buf], 3);
           }
-          __syncwarp();
           issued = true;
           if (++s == p.ring) {
             s = 0;
@@ -785,9 +778,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         }
       }
-      ok = __all_sync(0xffffffffu, ok && accumulator_tail(tempty, buf, bph, &s_abort));
+      if (ok) ok = __all_sync(0xffffffffu, accumulator_tail(tempty, buf, bph, &s_abort));
       if (!ok) {
-        flag_status(p.status, MOE_ERR_TIMEOUT);
+        if (lane == 0) flag_status(p.status, MOE_ERR_TIMEOUT);
         if (issued) {
           if (elect_one()) mma_commit_pair(&drain, 3);
           __syncwarp();

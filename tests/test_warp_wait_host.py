@@ -3,8 +3,7 @@
 The lanes poll an mbarrier one by one.  A lane may reach its limit just before the phase completes, while the others see it
 complete.  What follows a wait (elect.sync, tcgen05.ld, __syncwarp) needs every lane of the warp: if a lane leaves its loop
 alone, it waits at the __syncwarp behind the role for lanes that wait for it at elect.sync, with no limit.  A vote over
-the wait's result makes the lanes leave together (the epilogue warps); a lane that goes on to the end of the loop without
-waiting keeps them together too (producers and MMA issuers)."""
+the wait's result makes the lanes leave together."""
 import random
 import re
 from pathlib import Path
@@ -14,7 +13,7 @@ import pytest
 CSRC = Path(__file__).parent.parent / "moe_expert_ffn_rms_gb300" / "csrc"
 
 
-def run(stages, lanes, seed, rule):
+def run(stages, lanes, seed, vote):
     """"done" or "stuck" for one warp, each lane a coroutine that yields what it waits for."""
     rng = random.Random(seed)
     lands = [rng.randint(0, 12) for _ in range(stages)]  # polls until a stage's phase completes
@@ -33,14 +32,12 @@ def run(stages, lanes, seed, rule):
         return
 
     def lane():
-        ok = True
         for k in range(stages):
-            if ok:
-                yield from wait(k, rng.choice((3, 8, 100)))
-                ok = clock[0] >= sum(lands[:k + 1])
-            if rule == "vote":
-                ok = yield ("vote", ok)
-            if not ok and rule != "go on":
+            yield from wait(k, rng.choice((3, 8, 100)))
+            passed = clock[0] >= sum(lands[:k + 1])
+            if vote:
+                passed = yield ("vote", passed)
+            if not passed:
                 break
             yield "elect"
         yield "syncwarp"
@@ -70,24 +67,17 @@ def run(stages, lanes, seed, rule):
     return "stuck"
 
 
-@pytest.mark.parametrize("rule", ["vote", "go on"])
 @pytest.mark.parametrize("stages,lanes", [(1, 2), (4, 4), (9, 8)])
-def test_lanes_stay_together(stages, lanes, rule):
-    assert all(run(stages, lanes, seed, rule) == "done" for seed in range(400))
+def test_lanes_that_vote_leave_together(stages, lanes):
+    assert all(run(stages, lanes, seed, vote=True) == "done" for seed in range(400))
 
 
 def test_lanes_that_leave_alone_get_stuck():
-    assert any(run(4, 4, seed, "leave") == "stuck" for seed in range(400))
+    assert any(run(4, 4, seed, vote=False) == "stuck" for seed in range(400))
 
 
-def test_the_products_wait_by_these_rules():
+def test_every_wait_of_a_warp_in_the_products_is_voted_on():
     src = (CSRC / "linear.cu").read_text()
-    waits = re.findall(r".*\bmbar_wait\(.*", src)
-    assert len(waits) == 2 and "__all_sync" in waits[0] and "return ok && " in waits[1]
-    # issuers and producers: no way out of the loop, and nothing issued once a wait ran out
-    for body in re.findall(r"- producer --\n(.*?)- epilogue --", src, re.S):
-        assert "break" not in body and "warp_wait" not in body and body.count("= still(ok, ") == 3
-        assert body.count("if (elect_one() && ok) {") == 2
-        # what needs the warp after the loop goes by a vote
-        assert "ok = __all_sync(0xffffffffu, ok && accumulator_tail(" in body
-    assert src.count("if (!(ok = warp_wait(&tfull[buf], bph, &s_abort))) break;") == 3
+    waits = re.findall(r".*\b(?:mbar_wait|producer_tail|accumulator_tail)\(.*", src)
+    assert len(waits) == 5 and all("__all_sync(0xffffffffu, " in w for w in waits), waits
+    assert len(re.findall(r"\bok = warp_wait\(", src)) == 9
