@@ -15,15 +15,18 @@
 // inputs not in L2, against bytes at 6794 GB/s or FLOPs at 1952 TFLOP/s:
 //   M x N x K                 us      of the floor
 //   8192 x 8192 x 8192        539-582 0.97-1.05  pairs (under the power limit)
-//   4096 x 12288 x 4096       217     0.97   pairs; GELU and kept values 241, 0.88;
-//                                            with the tanh form 230, 0.92
-//     dx, dW of it            235, 217  0.90, 0.97
+//   4096 x 12288 x 4096       216-224 0.94-0.98  pairs; GELU and kept values 238, 0.89, with the
+//                                            tanh form 227-234, 0.90-0.93 (257, 0.82, back to back
+//                                            under the power limit); fp32 output 243-251
+//     dx, dW of it            233, 216  0.90, 0.97
+//     its gradient, SiLU, db  492-512   0.83-0.86  (550, 0.77, back to back); fp32 dout and dW 545
+//     16, 64, 256 rows of 4096 x 4096   31, 33, 38 us, 0.3: four launches
 //   1024 x 4096 x 4096        25      0.70   pairs, one round of 64 of 76
-//   256 x 4096 x 4096         15.7    0.35   split, 128 CTAs
+//   256 x 4096 x 4096         15.8    0.35   split, 128 CTAs
 //   512 x 1024 x 1024         7.4     0.08   split, 64 columns, four CTAs a tile
-//   61 x 7168 x 2048          10.6    0.44   split
+//   61 x 7168 x 2048          10.7    0.43   split
 //   16 x 4096 x 4096          10.3    0.48   split
-//   1 x 12288 x 4096          17.7    0.84   one token
+//   1 x 12288 x 4096          17.7-18.6  0.80-0.84   one token
 //   1 x 4096 x 4096           7.3     0.67   one token
 // Small ones are a launch (1.7 us for one token, 3.4 with TMEM and a cluster), the ramp of the
 // loads and the reduction over the cluster; large ones the tensor pipe.
@@ -986,6 +989,11 @@ struct Split {
   static constexpr int kRing = kRoom / kStage < kMaxRing ? kRoom / kStage : kMaxRing;
   static constexpr size_t kSmem = (size_t)kRing * kStage + 1024;
   static_assert((size_t)kRing * kStage >= (size_t)BN * kTileP * 4, "the fp32 tile lies over the ring");
+  // No allocation of TMEM waits for a CTA that waits for another: what fits on an SM together never wants
+  // more than its 512 columns.  (The library's kernels that allocate all 512 have 145 KB of its 228.)
+  static_assert(kPerSm * 2 * (BN < 32 ? 32 : BN) <= 512 && kSmem + (145 << 10) > (228 << 10) &&
+                    (kPerSm + 1) * kSmem > (228 << 10),
+                "tensor memory of the CTAs that share an SM");
 
   static auto kernel() { return product_split_kernel<A_MN, B_MN, BN>; }
 
@@ -1053,7 +1061,7 @@ SplitForm split_form(int bn) {
 // a part; a stage takes longer beside many other CTAs (they share L2), and where two are on
 // an SM its loads bound it, 105 bytes a ns.  `least` is the time of the operands from memory.
 // Against 5000 times of 270 products it picks one 1.5% above the best: us with the widest tile and clusters of up
-// to eight, the best, and its BN and S: 512 x 1024 x 1024 9.3 7.4 64 4; 64 x 256 x 8192 9.6 6.9 32 16;
+// to eight, the best, and its BN and S: 512 x 1024 x 1024 9.3 7.4 64 4; 64 x 256 x 8192 9.6 7.4 32 16;
 // 128 x 256 x 256 5.2 3.9 16 2; 256 x 4096 x 4096 15.6 15.6 256 4; dW 256 x 256 over 65536 rows 54 28 128 16.
 double split_us(int bn, int64_t tiles, int at_once, int S, int steps, int sms, double least) {
   const double ends = (bn == 16 ? 3.45 : (bn == 32 ? 4.0 : (bn == 64 ? 4.9 : (bn == 128 ? 5.3 : 7.5)))) +
@@ -1167,7 +1175,7 @@ cudaError_t launch_product(const ProductArgs& a, int sms, int* status, cudaStrea
     }
   }
   // The pairs' time, likewise: rounds of whole and of half tiles, none shorter than its
-  // epilogue.  256 x 4096 x 64 4.8 us, 512 x 4096 x 4096 21.7 (halves), 700 x 4096 x 2048 15.7,
+  // epilogue.  256 x 4096 x 64 4.9 us, 512 x 4096 x 4096 22.6 (halves), 700 x 4096 x 2048 15.9,
   // 1024 x 4096 x 4096 25.4, 4096 x 12288 x 64 29.8; split 4.8, 21.3, 19.8, 32.4, 87.
   const int64_t pt = (a.Q + 255) / 256 * ((a.P + 255) / 256);
   const int pairs = sms / 2;

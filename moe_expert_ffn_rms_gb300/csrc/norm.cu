@@ -23,9 +23,15 @@
 //   16384  1024  17       58%    31       64%
 //   16384  256   5.7      43%    12.5     40%
 //   8192   4096                                                62 us   79%
-//   16     4096  1.8      (launch and two reductions)
+//   16     4096  1.8      (launch and two reductions)  4.4 (two launches)        4.6
+//   2047   5120                                                                24.5   63%
+//   4096   12288 42       71%    150   39%                                     128    58%
+//   2048   16384                 98    40%                                     82     60%
 // The forward form is bound by instruction issue (62% of the slots), the backward
-// one by DRAM on long rows and by latency on short ones.
+// one by DRAM on long rows and by latency on short ones: a CTA's threads take one row through its
+// reduction with few others beside it (512 threads per SM at most, one CTA of 320 at 5120 columns).
+// Rows above 8192 columns have no copies ahead, and 64 registers for two chunks per thread, which
+// spill (216 bytes, rms_norm 40).  Short rows' forward grids are more CTAs than are resident, in rounds.
 // The backward pass keeps a thread on the same columns for all of its rows and adds
 // their part of dw and db in registers; each CTA leaves one row of partial sums,
 // and a second kernel adds those in their order.
